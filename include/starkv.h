@@ -14,6 +14,9 @@
  *   paged decode        : single-query attention computed straight from the
  *                         codes, never materialising full keys or values;
  *   chunked prefill     : causal attention of prompt chunks over the codes;
+ *   rotary append       : compress-and-append of rotated keys, with the queries;
+ *   shared-prefix decode: decode of groups that share their first pages;
+ *   cross attention     : many query rows over another sequence's pages;
  * plus host helpers for rank selection and cache capacity.
  *
  * Formulation (head_dim d, H query heads, Hkv KV heads with query head h
@@ -75,6 +78,7 @@ typedef enum {
 #define STARKV_FLAG_BAD_BLOCK_ID 0x1  /* block id outside [0, num_blocks) */
 #define STARKV_FLAG_BAD_SEQ_LEN 0x2   /* seq_len < 0 or > max_blocks_per_seq*16 or > max_seq_len */
 #define STARKV_FLAG_TIMEOUT 0x4       /* a pipeline wait exceeded its bound */
+#define STARKV_FLAG_BAD_ROW_OFFSET 0x8 /* row_offsets not starting at 0, falling, or above the row count */
 /* Bits 8..15 accompany STARKV_FLAG_TIMEOUT and name the internal wait(s) that
  * ran out (diagnostic only; the numbering is not part of the stable ABI). */
 
@@ -141,6 +145,65 @@ starkv_status starkv_compress_store(const starkv_layer_desc* desc, int32_t n_tok
                                     const void* v, const void* A_K, const void* A_V,
                                     const int32_t* slot_mapping, void* k_cache, void* v_cache,
                                     int32_t* status, void* stream);
+
+/*
+ * A rotary position embedding: `cos_sin` is a DEVICE fp32 table
+ * [max_position][rot_dim], 16-byte aligned, whose row p holds the rot_dim / 2
+ * cosines and then the rot_dim / 2 sines of position p's angles.  The first
+ * rot_dim elements of every head are rotated in pairs, the rest are kept:
+ *   (x[i], x[i + rot_dim/2])   with interleaved == 0,
+ *   (x[2i], x[2i + 1])         with interleaved == 1,     i < rot_dim / 2:
+ *   (a, b) -> (a cos - b sin, b cos + a sin).
+ * rot_dim is a multiple of 16 and at most head_dim.
+ */
+typedef struct {
+  const float* cos_sin;
+  int32_t max_position;
+  int32_t rot_dim;
+  int32_t interleaved;
+} starkv_rope;
+
+/*
+ * starkv_rope_compress_append -- starkv_compress_append with the rotary
+ * position embedding applied on the way, and the new tokens' queries rotated
+ * in the same launch.
+ *
+ *   c_K[b,j,:] = Rot(positions[b]) k[b,j,:] . A_K[j]      c_V[b,:] = v[b,:] . A_V
+ *   q_out[b,h,:] = Rot(positions[b]) q[b,h,:]
+ *
+ * The rotated key is not rounded before its code is formed (fp32 throughout, one
+ * rounding to fp16); q_out is rounded to fp16 and is what starkv_paged_decode
+ * and its kin take as q.
+ *
+ *   rope          host struct, see above
+ *   q             fp16 [batch][H][d], or NULL: no queries to rotate
+ *   q_out         fp16 [batch][H][d]; may be q itself (rotated in place), must
+ *                 not overlap it otherwise; ignored when q is NULL
+ *   the rest      as in starkv_compress_append
+ *
+ * A position outside [0, max_position) skips the row's codes (flagged
+ * STARKV_FLAG_BAD_SEQ_LEN) and leaves its q_out row as it was; a position the
+ * block table does not cover or a bad block id skips the codes only.
+ * STARKV_ERR_UNSUPPORTED for a rot_dim that is no multiple of 16 or above
+ * head_dim.  The method pages do not say where the rotation is applied; with
+ * codes of rotated keys, the cache needs no position at decode.
+ */
+starkv_status starkv_rope_compress_append(const starkv_layer_desc* desc, const starkv_rope* rope, int32_t batch,
+                                          const void* q, const void* k, const void* v, const void* A_K,
+                                          const void* A_V, const int32_t* block_tables, const int32_t* positions,
+                                          void* k_cache, void* v_cache, void* q_out, int32_t* status, void* stream);
+
+/*
+ * starkv_rope_compress_store -- the same for n_tokens rows at explicit slots
+ * (a prompt chunk): positions[i] rotates row i and slot_mapping[i] =
+ * page * 16 + offset places its codes, as in starkv_compress_store.  A slot
+ * outside [0, num_blocks*16) skips the row's codes (a padding row may carry
+ * slot -1 and any position).
+ */
+starkv_status starkv_rope_compress_store(const starkv_layer_desc* desc, const starkv_rope* rope, int32_t n_tokens,
+                                         const void* q, const void* k, const void* v, const void* A_K,
+                                         const void* A_V, const int32_t* positions, const int32_t* slot_mapping,
+                                         void* k_cache, void* v_cache, void* q_out, int32_t* status, void* stream);
 
 /*
  * starkv_decode_workspace_bytes -- device scratch needed by starkv_paged_decode
@@ -268,6 +331,82 @@ starkv_status starkv_paged_prefill(const starkv_layer_desc* desc, int32_t n_seqs
                                    const void* k_cache, const void* v_cache, const int32_t* block_tables,
                                    const int32_t* starts, const int32_t* row_offsets, float scale,
                                    void* workspace, size_t workspace_bytes, void* out, void* stream);
+
+/*
+ * starkv_paged_decode_shared -- starkv_paged_decode for a batch whose sequences
+ * come in groups with the same first pages (one system prompt, several samples
+ * or beams of one prompt): a group's shared pages are read once for all of its
+ * rows.  The result is that of starkv_paged_decode with the same q, tables and
+ * seq_lens.
+ *
+ *   n_groups      groups; group g holds rows row_offsets[g] ..
+ *                 row_offsets[g+1] - 1 of q, out, block_tables and seq_lens
+ *   shared_lens   int32 [n_groups] (device): tokens that all rows of the group
+ *                 have in common.  Only whole pages are shared: with s =
+ *                 shared_lens[g] / 16, the first s entries of the block tables
+ *                 of the group's rows must agree (those of its first row are
+ *                 read); tokens from 16 s on are read through each row's own
+ *                 table.
+ *   row_offsets   int32 [n_groups + 1] (device), non-decreasing from 0.  Rows
+ *                 from row_offsets[n_groups] on belong to no group: nothing of
+ *                 theirs is read and their out rows are left as they were.
+ *   max_shared_len  host-side upper bound of every shared_lens[g]
+ *   max_own_len     host-side upper bound of every seq_lens[b] - 16 s
+ *   workspace     at least starkv_shared_workspace_bytes(desc, n_groups, batch,
+ *                 max_shared_len, max_own_len) bytes, 256-byte aligned
+ *   the rest      as in starkv_paged_decode
+ *
+ * A row whose seq_lens[b] is below the shared length attends over its own
+ * seq_lens[b] tokens only; 0 gives a zero output row.  Groups of one row,
+ * empty groups and shared lengths of 0 are allowed.  Values out of range are
+ * clamped and flagged in the status word (STARKV_FLAG_BAD_SEQ_LEN,
+ * STARKV_FLAG_BAD_ROW_OFFSET, STARKV_FLAG_BAD_BLOCK_ID; the affected rows are
+ * undefined).  Accumulation is fp32; attention weights enter the V contraction
+ * as fp16.  Calls that share a workspace must be ordered on one stream.  At
+ * most 2^20 rows.  The method pages have no counterpart to this entry point.
+ */
+size_t starkv_shared_workspace_bytes(const starkv_layer_desc* desc, int32_t n_groups, int32_t batch,
+                                     int32_t max_shared_len, int32_t max_own_len);
+starkv_status starkv_paged_decode_shared(const starkv_layer_desc* desc, int32_t n_groups, int32_t batch,
+                                         int32_t max_shared_len, int32_t max_own_len, const void* q,
+                                         const void* B_K, const void* B_V, const void* k_cache,
+                                         const void* v_cache, const int32_t* block_tables,
+                                         const int32_t* seq_lens, const int32_t* shared_lens,
+                                         const int32_t* row_offsets, float scale, void* workspace,
+                                         size_t workspace_bytes, void* out, void* stream);
+
+/*
+ * starkv_paged_cross -- attention of query rows over all cached tokens of
+ * another sequence, without a causal limit: a decoder's rows over an encoder's
+ * states, whose codes starkv_compress_store has put into the pages.  Row
+ * row_offsets[s] + i of q (i-th query row of sequence s) attends over the
+ * tokens 0 .. seq_lens[s] - 1 of the pages block_tables[s]; each page is read
+ * once for all rows of its sequence.
+ *
+ *   n_seqs        sequences
+ *   n_rows        query rows in total (host value)
+ *   max_seq_len   host-side upper bound of every seq_lens[s]
+ *   q             fp16 [n_rows][H][d]
+ *   block_tables  int32 [n_seqs][max_blocks_per_seq]
+ *   seq_lens      int32 [n_seqs] (device)
+ *   row_offsets   int32 [n_seqs + 1] (device), non-decreasing from 0; rows from
+ *                 row_offsets[n_seqs] on are left as they were
+ *   workspace     at least starkv_cross_workspace_bytes(desc, n_seqs, n_rows,
+ *                 max_seq_len) bytes, 256-byte aligned
+ *   out           fp16 [n_rows][H][d]
+ *
+ * seq_lens[s] == 0 gives zero rows.  Errors, flags and rounding as in
+ * starkv_paged_decode_shared.  The work per (row, token) is that of the codes'
+ * ranks: beyond about v_rank x Hkv x d / (H x (v_rank - 2 d)) rows per sequence
+ * attention over rebuilt keys and values would need fewer operations.
+ */
+size_t starkv_cross_workspace_bytes(const starkv_layer_desc* desc, int32_t n_seqs, int32_t n_rows,
+                                    int32_t max_seq_len);
+starkv_status starkv_paged_cross(const starkv_layer_desc* desc, int32_t n_seqs, int32_t n_rows,
+                                 int32_t max_seq_len, const void* q, const void* B_K, const void* B_V,
+                                 const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                                 const int32_t* seq_lens, const int32_t* row_offsets, float scale,
+                                 void* workspace, size_t workspace_bytes, void* out, void* stream);
 
 /*
  * starkv_paged_decode_profiled -- starkv_paged_decode that also records CUDA

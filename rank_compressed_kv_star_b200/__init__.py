@@ -22,6 +22,7 @@ STATUS = {
     6: "STARKV_ERR_TIMEOUT",
 }
 FLAG_BAD_BLOCK_ID, FLAG_BAD_SEQ_LEN, FLAG_TIMEOUT = 1, 2, 4
+FLAG_BAD_ROW_OFFSET = 8
 
 EXPORTED = (
     "starkv_compress_append", "starkv_compress_store", "starkv_decode_workspace_bytes",
@@ -30,6 +31,8 @@ EXPORTED = (
     "starkv_decode_check", "starkv_decode_workspace_layout", "starkv_status_string",
     "starkv_rank_from_spectrum", "starkv_version", "starkv_kv_bytes_per_token", "starkv_num_blocks",
     "starkv_prefill_workspace_bytes", "starkv_paged_prefill", "starkv_set_wait_test_hook",
+    "starkv_rope_compress_append", "starkv_rope_compress_store", "starkv_shared_workspace_bytes",
+    "starkv_paged_decode_shared", "starkv_cross_workspace_bytes", "starkv_paged_cross",
 )
 
 
@@ -56,6 +59,25 @@ class WorkspaceLayout(ctypes.Structure):
                 ("v_ctas", ctypes.c_int32), ("v_slots", ctypes.c_int32),
                 ("n_rranges", ctypes.c_int32), ("r_range", ctypes.c_int32),
                 ("k_tensor", ctypes.c_int32), ("qth_off", ctypes.c_size_t)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("max_position", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+def rope_table(cos_sin, interleaved: bool = False, max_position: int | None = None, rot_dim: int | None = None) -> Rope:
+    """``cos_sin``: fp32 device tensor [max_position][rot_dim] (cosines, then sines), or an address with both sizes.
+
+    The tensor is kept alive by the returned object.
+    """
+    if not isinstance(cos_sin, int):
+        if str(cos_sin.dtype) != "torch.float32" or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous float32 [max_position][rot_dim] tensor")
+        max_position, rot_dim = cos_sin.shape
+    rope = Rope(_ptr(cos_sin), max_position, rot_dim, int(interleaved))
+    rope.tensor = cos_sin
+    return rope
 
 
 def layer_desc(num_heads, head_dim, k_rank, v_rank, num_blocks, max_blocks_per_seq,
@@ -106,6 +128,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                          ctypes.c_size_t, P, P]
     lib.starkv_paged_prefill.restype = ctypes.c_int
     lib.starkv_paged_decode_static.restype = ctypes.c_int
+    RP = ctypes.POINTER(Rope)
+    lib.starkv_rope_compress_append.argtypes = [DP, RP, I32, P, P, P, P, P, P, P, P, P, P, P, P]
+    lib.starkv_rope_compress_append.restype = ctypes.c_int
+    lib.starkv_rope_compress_store.argtypes = [DP, RP, I32, P, P, P, P, P, P, P, P, P, P, P, P]
+    lib.starkv_rope_compress_store.restype = ctypes.c_int
+    lib.starkv_shared_workspace_bytes.argtypes = [DP, I32, I32, I32, I32]
+    lib.starkv_shared_workspace_bytes.restype = SZ
+    lib.starkv_paged_decode_shared.argtypes = [DP, I32, I32, I32, I32, P, P, P, P, P, P, P, P, P, ctypes.c_float, P,
+                                               SZ, P, P]
+    lib.starkv_paged_decode_shared.restype = ctypes.c_int
+    lib.starkv_cross_workspace_bytes.argtypes = [DP, I32, I32, I32]
+    lib.starkv_cross_workspace_bytes.restype = SZ
+    lib.starkv_paged_cross.argtypes = [DP, I32, I32, I32, P, P, P, P, P, P, P, P, ctypes.c_float, P, SZ, P, P]
+    lib.starkv_paged_cross.restype = ctypes.c_int
     lib.starkv_decode_check.argtypes = [P, P, ctypes.POINTER(ctypes.c_int32)]
     lib.starkv_decode_check.restype = ctypes.c_int
     lib.starkv_decode_workspace_layout.argtypes = [DP, I32, I32, ctypes.POINTER(WorkspaceLayout)]
@@ -273,6 +309,64 @@ def starkv_paged_decode_static(desc: LayerDesc, batch: int, max_seq_len: int, q,
         _ptr(v_cache), _ptr(block_tables), _ptr(seq_lens), float(scale), _ptr(out), _stream(stream))
     if check:
         _check(st, "starkv_paged_decode_static")
+    return st
+
+
+def starkv_rope_compress_append(desc: LayerDesc, rope: Rope, batch: int, q, k, v, A_K, A_V, block_tables, positions,
+                                k_cache, v_cache, q_out, stream=None, check: bool = True, status=None) -> int:
+    """compress-append of the rotated keys; ``q`` (or None) is rotated into ``q_out``."""
+    st = load_library().starkv_rope_compress_append(
+        _desc_ref(desc), _desc_ref(rope), batch, _ptr(q), _ptr(k), _ptr(v), _ptr(A_K), _ptr(A_V), _ptr(block_tables),
+        _ptr(positions), _ptr(k_cache), _ptr(v_cache), _ptr(q_out), _ptr(status), _stream(stream))
+    if check:
+        _check(st, "starkv_rope_compress_append")
+    return st
+
+
+def starkv_rope_compress_store(desc: LayerDesc, rope: Rope, n_tokens: int, q, k, v, A_K, A_V, positions, slot_mapping,
+                               k_cache, v_cache, q_out, stream=None, check: bool = True, status=None) -> int:
+    st = load_library().starkv_rope_compress_store(
+        _desc_ref(desc), _desc_ref(rope), n_tokens, _ptr(q), _ptr(k), _ptr(v), _ptr(A_K), _ptr(A_V), _ptr(positions),
+        _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache), _ptr(q_out), _ptr(status), _stream(stream))
+    if check:
+        _check(st, "starkv_rope_compress_store")
+    return st
+
+
+def starkv_shared_workspace_bytes(desc: LayerDesc, n_groups: int, batch: int, max_shared_len: int,
+                                  max_own_len: int) -> int:
+    return int(load_library().starkv_shared_workspace_bytes(_desc_ref(desc), n_groups, batch, max_shared_len,
+                                                            max_own_len))
+
+
+def starkv_paged_decode_shared(desc: LayerDesc, n_groups: int, batch: int, max_shared_len: int, max_own_len: int, q,
+                               B_K, B_V, k_cache, v_cache, block_tables, seq_lens, shared_lens, row_offsets,
+                               scale: float, workspace, workspace_bytes: int, out, stream=None,
+                               check: bool = True) -> int:
+    """Paged decode of groups of rows whose tables agree on the first ``shared_lens[g] // 16`` pages."""
+    st = load_library().starkv_paged_decode_shared(
+        _desc_ref(desc), n_groups, batch, max_shared_len, max_own_len, _ptr(q), _ptr(B_K), _ptr(B_V), _ptr(k_cache),
+        _ptr(v_cache), _ptr(block_tables), _ptr(seq_lens), _ptr(shared_lens), _ptr(row_offsets), float(scale),
+        _ptr(workspace), int(workspace_bytes), _ptr(out), _stream(stream))
+    if check:
+        _check(st, "starkv_paged_decode_shared")
+    return st
+
+
+def starkv_cross_workspace_bytes(desc: LayerDesc, n_seqs: int, n_rows: int, max_seq_len: int) -> int:
+    return int(load_library().starkv_cross_workspace_bytes(_desc_ref(desc), n_seqs, n_rows, max_seq_len))
+
+
+def starkv_paged_cross(desc: LayerDesc, n_seqs: int, n_rows: int, max_seq_len: int, q, B_K, B_V, k_cache, v_cache,
+                       block_tables, seq_lens, row_offsets, scale: float, workspace, workspace_bytes: int, out,
+                       stream=None, check: bool = True) -> int:
+    """Attention of ragged query rows over all cached tokens of their sequences (no causal limit)."""
+    st = load_library().starkv_paged_cross(
+        _desc_ref(desc), n_seqs, n_rows, max_seq_len, _ptr(q), _ptr(B_K), _ptr(B_V), _ptr(k_cache), _ptr(v_cache),
+        _ptr(block_tables), _ptr(seq_lens), _ptr(row_offsets), float(scale), _ptr(workspace), int(workspace_bytes),
+        _ptr(out), _stream(stream))
+    if check:
+        _check(st, "starkv_paged_cross")
     return st
 
 

@@ -36,12 +36,18 @@ struct AppendTarget {
   const int32_t* positions;
   int MB, NB;
   int32_t* status;         // optional: flags of skipped targets are OR-ed in
+  const int32_t* rope_positions;   // rows whose position is outside [0, rope_max) are skipped too (null: not checked)
+  int rope_max;
 };
 
 // Physical row (page*16 + slot) of row b's target, or a negated STARKV_FLAG_*
 // naming why the target is skipped: -STARKV_FLAG_BAD_SEQ_LEN for a position
-// outside the block table, -STARKV_FLAG_BAD_BLOCK_ID for a page outside the pool.
+// outside the block table (or the rotation's table), -STARKV_FLAG_BAD_BLOCK_ID for a page outside the pool.
 __device__ __forceinline__ int64_t append_row(const AppendTarget& a, int b) {
+  if (a.rope_positions) {
+    const int32_t rp = a.rope_positions[b];
+    if (rp < 0 || rp >= a.rope_max) return -STARKV_FLAG_BAD_SEQ_LEN;
+  }
   if (a.slots) {
     const int32_t sl = a.slots[b];
     return (sl < 0 || sl >= a.NB * 16) ? -STARKV_FLAG_BAD_BLOCK_ID : static_cast<int64_t>(sl);

@@ -15,6 +15,8 @@
 #include "../../include/starkv.h"
 #include "append_kernels.cuh"
 #include "decode_kernels.cuh"
+#include "group_kernels.cuh"
+#include "rope_kernels.cuh"
 
 // Launch-shape defaults (overridable at build time for tuning sweeps).
 #ifndef STARKV_K_CTAS_PER_SM
@@ -1412,6 +1414,375 @@ starkv_status starkv_paged_decode_static(const starkv_layer_desc* desc, int32_t 
   if (!ws) return STARKV_ERR_CUDA;
   return decode_impl(desc, batch, max_seq_len, q, B_K, B_V, k_cache, v_cache, block_tables, seq_lens, scale, ws,
                      STARKV_STATIC_WS_BYTES, out, stream, nullptr);
+}
+
+// ------------------------------------------------- rotary compress-and-append
+namespace {
+starkv_status rope_impl(const starkv_layer_desc* desc, const starkv_rope* rope, int32_t n, const void* q, const void* k,
+                        const void* v, const void* A_K, const void* A_V, const int32_t* positions, AppendTarget tgt,
+                        void* k_cache, void* v_cache, void* q_out, void* stream) {
+  starkv_status st = check_desc(desc);
+  if (st != STARKV_OK) return st;
+  if (!rope || n < 0 || rope->rot_dim <= 0 || rope->max_position <= 0 || (rope->interleaved & ~1))
+    return STARKV_ERR_INVALID_ARG;
+  if (rope->rot_dim % 16 != 0 || rope->rot_dim > desc->head_dim) return STARKV_ERR_UNSUPPORTED;
+  if (n == 0) return STARKV_OK;
+  if (!rope->cos_sin || !aligned16(rope->cos_sin) || !positions || (reinterpret_cast<uintptr_t>(positions) & 3u) ||
+      (reinterpret_cast<uintptr_t>(tgt.status) & 3u))
+    return STARKV_ERR_INVALID_ARG;
+  if (q && (!q_out || !aligned16(q) || !aligned16(q_out))) return STARKV_ERR_INVALID_ARG;
+  tgt.rope_positions = positions;
+  tgt.rope_max = rope->max_position;
+  AppendPlan ap{};
+  st = plan_append(desc, n, k, v, A_K, A_V, tgt, k_cache, v_cache, &ap);
+  if (st != STARKV_OK) return st;
+  RopeParams rp{};
+  rp.rope.cos_sin = rope->cos_sin;
+  rp.rope.positions = positions;
+  rp.rope.max_position = rope->max_position;
+  rp.rope.rot = rope->rot_dim;
+  rp.rope.interleaved = rope->interleaved;
+  rp.v = ap.vp;
+  rp.k = ap.kp;
+  rp.q = static_cast<const __half*>(q);
+  rp.q_out = static_cast<__half*>(q_out);
+  rp.n = n;
+  rp.H = desc->num_heads;
+  rp.d = desc->head_dim;
+  const int KS = ap.KS;
+  rp.k.tile = kRopeKB;
+  rp.v_mt = ap.v_mt;
+  rp.v_cols = ap.v_cols;
+  rp.k_items = rp.k.H * ((n + rp.k.tile - 1) / rp.k.tile);
+  rp.k_cols = (rp.k_items + KS - 1) / KS;
+  const int64_t units = static_cast<int64_t>(n) * rp.H * rope_units(rp.d, rp.rope.rot, rp.rope.interleaved);
+  rp.q_items = q ? static_cast<int>((units + kRopeQUnits - 1) / kRopeQUnits) : 0;
+  const size_t k_smem = static_cast<size_t>(rp.d) * rp.k.r * 2 + static_cast<size_t>(rp.k.tile) * rp.d * 4;
+  const size_t smem = (ap.v_smem > k_smem ? ap.v_smem : k_smem) + 1024;
+  if (!set_smem(rope_append_kernel, smem)) return STARKV_ERR_CUDA;
+  const dim3 grid(rp.v_cols + rp.k_cols + (rp.q_items + KS - 1) / KS, KS);
+  return launch(rope_append_kernel, grid, dim3(kPrepThreads), smem, static_cast<cudaStream_t>(stream), KS, ap.amap,
+                ap.vmap, rp) == cudaSuccess ? STARKV_OK : STARKV_ERR_CUDA;
+}
+}  // namespace
+
+starkv_status starkv_rope_compress_append(const starkv_layer_desc* desc, const starkv_rope* rope, int32_t batch,
+                                          const void* q, const void* k, const void* v, const void* A_K,
+                                          const void* A_V, const int32_t* block_tables, const int32_t* positions,
+                                          void* k_cache, void* v_cache, void* q_out, int32_t* status, void* stream) {
+  AppendTarget tgt{nullptr, block_tables, positions, desc ? desc->max_blocks_per_seq : 0, desc ? desc->num_blocks : 0,
+                   status};
+  return rope_impl(desc, rope, batch, q, k, v, A_K, A_V, positions, tgt, k_cache, v_cache, q_out, stream);
+}
+
+starkv_status starkv_rope_compress_store(const starkv_layer_desc* desc, const starkv_rope* rope, int32_t n_tokens,
+                                         const void* q, const void* k, const void* v, const void* A_K,
+                                         const void* A_V, const int32_t* positions, const int32_t* slot_mapping,
+                                         void* k_cache, void* v_cache, void* q_out, int32_t* status, void* stream) {
+  AppendTarget tgt{slot_mapping, nullptr, nullptr, desc ? desc->max_blocks_per_seq : 0, desc ? desc->num_blocks : 0,
+                   status};
+  return rope_impl(desc, rope, n_tokens, q, k, v, A_K, A_V, positions, tgt, k_cache, v_cache, q_out, stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------- groups of rows over the same pages
+namespace {
+// fp16 [rows][heads][inner] as a 3-D tensor map with boxes of 64 values x
+// box_heads x box_rows and the 128-byte swizzle (values past the end read as zero).
+bool encode_rows_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t heads, uint64_t rows,
+                     uint32_t box_heads, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {inner, heads, rows};
+  cuuint64_t strides[2] = {inner * 2, heads * inner * 2};
+  cuuint32_t box[3] = {64, box_heads, box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct GroupPlan {
+  GroupGeom g;
+  // K pass
+  int kb, ksteps, qbox, nq, k_stages, k_ctas;
+  uint32_t a_bytes, q_bytes, k_tmem;
+  size_t k_smem;
+  // V pass
+  int v_stages, v_ctas;
+  size_t v_smem;
+  // up-projection
+  int up_mt, up_rows, up_tiles, up_npad, up_ks, up_kpc, up_stages;
+  uint32_t up_stage_bytes, up_tmem;
+  size_t up_smem;
+  // absorption
+  int abs_tile;
+  // workspace
+  size_t ent_off, kpre_off, vpre_off, row_ent_off, row_lim_off, used_off, mrow_off, lpart_off[2], qh_off, ql_off,
+      p_off[2], z_off[2], carry_off, zh_off, zl_off, total;
+};
+
+starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n_groups, int32_t n_rows,
+                              int32_t max0, int32_t max1, GroupPlan* gp) {
+  starkv_status st = check_desc(d);
+  if (st != STARKV_OK) return st;
+  const int64_t cap = static_cast<int64_t>(d->max_blocks_per_seq) * 16;
+  if (n_groups < 0 || n_rows < 0 || max0 < 0 || max1 < 0) return STARKV_ERR_INVALID_ARG;
+  if ((shared ? max0 / 16 * 16 : max0) > cap || max1 > cap) return STARKV_ERR_INVALID_ARG;   // whole pages are shared
+  if (n_rows > (1 << 20) || n_groups > (1 << 20)) return STARKV_ERR_UNSUPPORTED;
+  GroupPlan& p = *gp;
+  std::memset(&p, 0, sizeof(p));
+  GroupGeom& g = p.g;
+  g.H = d->num_heads; g.Hkv = kv_heads(d); g.d = d->head_dim; g.r = d->k_rank; g.R = d->v_rank;
+  while ((g.Hkv << g.log2G) < g.H) ++g.log2G;
+  const int G = 1 << g.log2G;
+  g.MB = d->max_blocks_per_seq; g.NB = d->num_blocks;
+  g.n_rows = n_rows; g.n_groups = n_groups; g.shared = shared ? 1 : 0;
+  g.E = n_groups + (shared ? n_rows : 0);
+  g.max_len[0] = max0; g.max_len[1] = max1;
+  g.t_pad[0] = max0 > 0 ? (max0 + 127) / 128 * 128 : 128;
+  g.t_pad[1] = max1 > 0 ? (max1 + 127) / 128 * 128 : 128;
+  g.n_rt = (g.R + kGVTile - 1) / kGVTile;
+  const int sms = device_sm_count();
+
+  // K pass: 128 columns per tile, 64 where the query tile of a large rank would
+  // leave no room for a ring; two query slots where three stages still fit
+  p.kb = (g.r + 63) / 64;
+  p.ksteps = (g.r + 15) / 16;
+  g.ncol = p.kb <= 2 ? 128 : 64;
+  p.qbox = G > 16 ? G : 16;
+  p.a_bytes = static_cast<uint32_t>(p.kb) * 16384u;
+  p.q_bytes = static_cast<uint32_t>(p.kb) * 2u * g.ncol * 128u;
+  const uint32_t budget = 200u * 1024u;
+  p.nq = budget >= 2u * p.q_bytes + 3u * p.a_bytes ? 2 : 1;
+  p.k_stages = static_cast<int>((budget - p.nq * p.q_bytes) / p.a_bytes);
+  if (p.k_stages > 8) p.k_stages = 8;
+  p.k_smem = 1024 + static_cast<size_t>(p.nq) * p.q_bytes + static_cast<size_t>(p.k_stages) * p.a_bytes +
+             (2 * p.k_stages + 4 + 2 * kGKAcc + 2) * sizeof(uint64_t);
+  p.k_tmem = static_cast<uint32_t>(kGKAcc * g.ncol);
+  p.k_ctas = sms;
+  {
+    // tokens per item: enough items for every CTA, each long enough to hide its start
+    const int per = g.ncol / G;
+    const int64_t tiles = n_groups + n_rows / per;
+    const int64_t blocks = (tiles < n_rows ? tiles : n_rows) * g.Hkv * (g.t_pad[0] / 128) +
+                           (shared ? static_cast<int64_t>(n_rows) * g.Hkv * (g.t_pad[1] / 128) : 0);
+    int64_t n = blocks / (4 * static_cast<int64_t>(sms));
+    n = n < 1 ? 1 : (n > 8 ? 8 : n);
+    g.chunk = static_cast<int>(n) * 128;
+  }
+  for (int s = 0; s < 2; ++s) g.n_ch[s] = (g.t_pad[s] + g.chunk - 1) / g.chunk;
+
+  // V pass: one CTA per SM, three 64 KiB stages
+  p.v_stages = 3;
+  p.v_ctas = sms;
+  p.v_smem = 1024 + static_cast<size_t>(p.v_stages) * (kGVABytes + kGVBBytes) + (2 * p.v_stages + 5) * sizeof(uint64_t);
+
+  // up-projection
+  p.up_mt = (g.d + 127) / 128;
+  p.up_rows = 256 / G < n_rows ? 256 / G : (n_rows > 0 ? n_rows : 1);
+  p.up_tiles = n_rows > 0 ? (n_rows + p.up_rows - 1) / p.up_rows : 1;
+  p.up_npad = (p.up_rows * G + 15) / 16 * 16;
+  p.up_stage_bytes = 16384u + 2u * p.up_npad * 128u;
+  p.up_stages = static_cast<int>(200u * 1024u / p.up_stage_bytes);
+  if (p.up_stages > 6) p.up_stages = 6;
+  {
+    size_t ring = static_cast<size_t>(p.up_stages) * p.up_stage_bytes;
+    if (ring < static_cast<size_t>(p.up_npad) * 512) ring = static_cast<size_t>(p.up_npad) * 512;
+    p.up_smem = 1024 + ring + (2 * p.up_stages + 1) * sizeof(uint64_t);
+  }
+  p.up_ks = 1;
+  while (p.up_ks < 8 && static_cast<int64_t>(g.Hkv) * p.up_mt * p.up_tiles * p.up_ks * 2 <= sms && g.R / 64 >= p.up_ks * 2)
+    p.up_ks *= 2;
+  p.up_kpc = (g.R + p.up_ks * 64 - 1) / (p.up_ks * 64) * 64;
+  p.up_tmem = static_cast<uint32_t>(pow2_ceil(p.up_npad < 32 ? 32 : p.up_npad));
+
+  p.abs_tile = g.H * ((n_rows + 15) / 16) <= 2 * sms ? 16 : kAbsBT;
+
+  const size_t N = static_cast<size_t>(n_rows), rh = N * g.H;
+  size_t off = 256;   // the status word
+  auto take = [&](size_t bytes) { const size_t o = off; off = align_up(off + bytes, 256); return o; };
+  p.ent_off = take(static_cast<size_t>(g.E) * sizeof(GroupEntry));
+  p.kpre_off = take((static_cast<size_t>(g.E) + 1) * 8);
+  p.vpre_off = take((static_cast<size_t>(g.E) + 1) * 8);
+  p.row_ent_off = take(N * 4);
+  p.row_lim_off = take(N * 4);
+  p.used_off = take(4);
+  p.mrow_off = take(rh * 4);
+  p.qh_off = take(rh * g.r * 2);
+  p.ql_off = take(rh * g.r * 2);
+  for (int s = 0; s < (shared ? 2 : 1); ++s) {
+    p.lpart_off[s] = take(rh * g.n_ch[s] * 4);
+    p.p_off[s] = take(rh * g.t_pad[s] * 2);
+    p.z_off[s] = take(rh * g.R * 4);
+  }
+  p.carry_off = take(static_cast<size_t>(p.v_ctas) * kGVTile * kGVTile * 4);
+  p.zh_off = take(rh * g.R * 2);
+  p.zl_off = take(rh * g.R * 2);
+  p.total = off;
+  return STARKV_OK;
+}
+
+template <bool kWeights>
+cudaError_t launch_group_kpass(const GroupPlan& pl, const CUtensorMap& kmap, const CUtensorMap& qhmap,
+                               const CUtensorMap& qlmap, const GroupKParams& kp, cudaStream_t s) {
+  if (!set_smem(group_kpass_kernel<kWeights>, pl.k_smem)) return cudaErrorInvalidValue;
+  return launch(group_kpass_kernel<kWeights>, dim3(pl.k_ctas), dim3(kGKThreads), pl.k_smem, s, 1, kmap, qhmap, qlmap, kp);
+}
+
+starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_groups, int32_t n_rows, int32_t max0,
+                         int32_t max1, const void* q, const void* B_K, const void* B_V, const void* k_cache,
+                         const void* v_cache, const int32_t* block_tables, const int32_t* seq_lens,
+                         const int32_t* shared_lens, const int32_t* row_offsets, float scale, void* workspace,
+                         size_t workspace_bytes, void* out, void* stream) {
+  GroupPlan pl{};
+  starkv_status st = make_group_plan(desc, shared, n_groups, n_rows, max0, max1, &pl);
+  if (st != STARKV_OK) return st;
+  if (!(std::isfinite(scale) && scale > 0.f)) return STARKV_ERR_INVALID_ARG;
+  if (n_rows == 0 || n_groups == 0) return clear_status(workspace, workspace_bytes, stream);
+  if (!q || !B_K || !B_V || !k_cache || !v_cache || !block_tables || !seq_lens || !row_offsets || !out ||
+      (shared && !shared_lens))
+    return STARKV_ERR_INVALID_ARG;
+  const void* ints[] = {block_tables, seq_lens, shared_lens, row_offsets};
+  for (const void* x : ints)
+    if (reinterpret_cast<uintptr_t>(x) & 3u) return STARKV_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(B_K) || !aligned16(B_V) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+    return STARKV_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < pl.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return STARKV_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  GroupGeom& g = pl.g;
+  g.status = reinterpret_cast<int32_t*>(ws);
+  g.ent = reinterpret_cast<GroupEntry*>(ws + pl.ent_off);
+  g.kpre = reinterpret_cast<int64_t*>(ws + pl.kpre_off);
+  g.vpre = reinterpret_cast<int64_t*>(ws + pl.vpre_off);
+  g.row_ent = reinterpret_cast<int32_t*>(ws + pl.row_ent_off);
+  g.row_lim = reinterpret_cast<int32_t*>(ws + pl.row_lim_off);
+  g.n_used = reinterpret_cast<int32_t*>(ws + pl.used_off);
+  g.mrow = reinterpret_cast<float*>(ws + pl.mrow_off);
+  const int n_src = shared ? 2 : 1;
+  __half* P[2];
+  float* Z[2];
+  for (int i = 0; i < 2; ++i) {   // an unused second source stands for the first
+    const int s0 = i < n_src ? i : 0;
+    g.lpart[i] = reinterpret_cast<float*>(ws + pl.lpart_off[s0]);
+    P[i] = reinterpret_cast<__half*>(ws + pl.p_off[s0]);
+    Z[i] = reinterpret_cast<float*>(ws + pl.z_off[s0]);
+  }
+  __half* qh = reinterpret_cast<__half*>(ws + pl.qh_off);
+  __half* ql = reinterpret_cast<__half*>(ws + pl.ql_off);
+  __half* zh = reinterpret_cast<__half*>(ws + pl.zh_off);
+  __half* zl = reinterpret_cast<__half*>(ws + pl.zl_off);
+  float* carry = reinterpret_cast<float*>(ws + pl.carry_off);
+  const uint32_t G = 1u << g.log2G;
+  const uint64_t rh = static_cast<uint64_t>(n_rows) * g.H;
+
+  CUtensorMap kmap, qhmap, qlmap, vmap, pmap[2], bvmap, zhmap, zlmap;
+  if (!encode_kpool_map(&kmap, k_cache, g.r, g.Hkv, g.NB, 1, 16) ||
+      !encode_rows_map(&qhmap, qh, g.r, g.H, n_rows, G, static_cast<uint32_t>(pl.qbox) / G) ||
+      !encode_rows_map(&qlmap, ql, g.r, g.H, n_rows, G, static_cast<uint32_t>(pl.qbox) / G) ||
+      !encode_vpool_map(&vmap, v_cache, g.R, g.NB, 4) ||
+      !encode_2d_map(&pmap[0], P[0], g.t_pad[0], rh, 64, kGVPBox) ||
+      !encode_2d_map(&pmap[1], P[1], g.t_pad[n_src - 1], rh, 64, kGVPBox) ||
+      !encode_2d_map(&bvmap, B_V, static_cast<uint64_t>(g.Hkv) * g.d, g.R, 64, 64) ||
+      !encode_rows_map(&zhmap, zh, g.R, g.H, n_rows, G, static_cast<uint32_t>(pl.up_rows)) ||
+      !encode_rows_map(&zlmap, zl, g.R, g.H, n_rows, G, static_cast<uint32_t>(pl.up_rows)))
+    return STARKV_ERR_CUDA;
+
+  GroupAbsorbParams ap{};
+  ap.su.g = g;
+  ap.su.row_offsets = row_offsets;
+  ap.su.seq_lens = seq_lens;
+  ap.su.shared_lens = shared_lens;
+  ap.q = static_cast<const __half*>(q);
+  ap.B_K = static_cast<const __half*>(B_K);
+  ap.qh = qh; ap.ql = ql;
+  ap.coef = scale * kLog2e;
+  ap.tile = pl.abs_tile;
+  const size_t abs_smem = (static_cast<size_t>(g.d) * g.r + static_cast<size_t>(ap.tile) * g.d) * 2;
+  const int abs_ctas = 1 + g.H * ((n_rows + ap.tile - 1) / ap.tile);
+  if (!set_smem(group_absorb_kernel, abs_smem)) return STARKV_ERR_CUDA;
+  if (launch(group_absorb_kernel, dim3(abs_ctas), dim3(kPrepThreads), abs_smem, s, 1, ap) != cudaSuccess)
+    return STARKV_ERR_CUDA;
+
+  GroupKParams kp{};
+  kp.g = g;
+  kp.tables = block_tables;
+  kp.P[0] = P[0]; kp.P[1] = P[1];
+  kp.kb = pl.kb; kp.ksteps = pl.ksteps; kp.qbox = pl.qbox; kp.nq = pl.nq; kp.stages = pl.k_stages;
+  kp.a_bytes = pl.a_bytes; kp.q_bytes = pl.q_bytes; kp.tmem_cols = pl.k_tmem;
+  if (launch_group_kpass<false>(pl, kmap, qhmap, qlmap, kp, s) != cudaSuccess ||
+      launch_group_kpass<true>(pl, kmap, qhmap, qlmap, kp, s) != cudaSuccess)
+    return STARKV_ERR_CUDA;
+
+  GroupVParams vp{};
+  vp.g = g;
+  vp.tables = block_tables;
+  vp.Z[0] = Z[0]; vp.Z[1] = Z[1];
+  vp.zcarry = carry;
+  vp.stages = pl.v_stages;
+  vp.stage_bytes = kGVABytes + kGVBBytes;
+  if (!set_smem(group_vpass_kernel, pl.v_smem)) return STARKV_ERR_CUDA;
+  if (launch(group_vpass_kernel, dim3(pl.v_ctas), dim3(kGVThreads), pl.v_smem, s, 1, vmap, pmap[0], pmap[1], vp) !=
+      cudaSuccess)
+    return STARKV_ERR_CUDA;
+
+  GroupCombineParams cp{};
+  cp.g = g;
+  cp.Z[0] = Z[0]; cp.Z[1] = Z[1];
+  cp.zcarry = carry;
+  cp.zh = zh; cp.zl = zl;
+  cp.v_grid = pl.v_ctas;
+  const int64_t warps = static_cast<int64_t>(rh) * g.n_rt;
+  if (launch(group_combine_kernel, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, s, 1, cp) != cudaSuccess)
+    return STARKV_ERR_CUDA;
+
+  GroupUpParams up{};
+  up.g = g;
+  up.out = static_cast<__half*>(out);
+  up.n_mt = pl.up_mt; up.rows_tile = pl.up_rows; up.npad = pl.up_npad; up.k_per_cta = pl.up_kpc;
+  up.stages = pl.up_stages; up.stage_bytes = pl.up_stage_bytes; up.tmem_cols = pl.up_tmem;
+  if (!set_smem(group_up_kernel, pl.up_smem)) return STARKV_ERR_CUDA;
+  if (launch(group_up_kernel, dim3(g.Hkv * pl.up_mt * pl.up_tiles, pl.up_ks), dim3(kGUThreads), pl.up_smem, s, pl.up_ks,
+             bvmap, zhmap, zlmap, up) != cudaSuccess)
+    return STARKV_ERR_CUDA;
+  return STARKV_OK;
+}
+}  // namespace
+
+extern "C" {
+
+size_t starkv_shared_workspace_bytes(const starkv_layer_desc* desc, int32_t n_groups, int32_t batch,
+                                     int32_t max_shared_len, int32_t max_own_len) {
+  GroupPlan pl{};
+  return make_group_plan(desc, true, n_groups, batch, max_shared_len, max_own_len, &pl) == STARKV_OK ? pl.total : 0;
+}
+
+starkv_status starkv_paged_decode_shared(const starkv_layer_desc* desc, int32_t n_groups, int32_t batch,
+                                         int32_t max_shared_len, int32_t max_own_len, const void* q,
+                                         const void* B_K, const void* B_V, const void* k_cache, const void* v_cache,
+                                         const int32_t* block_tables, const int32_t* seq_lens,
+                                         const int32_t* shared_lens, const int32_t* row_offsets, float scale,
+                                         void* workspace, size_t workspace_bytes, void* out, void* stream) {
+  return group_impl(desc, true, n_groups, batch, max_shared_len, max_own_len, q, B_K, B_V, k_cache, v_cache,
+                    block_tables, seq_lens, shared_lens, row_offsets, scale, workspace, workspace_bytes, out, stream);
+}
+
+size_t starkv_cross_workspace_bytes(const starkv_layer_desc* desc, int32_t n_seqs, int32_t n_rows,
+                                    int32_t max_seq_len) {
+  GroupPlan pl{};
+  return make_group_plan(desc, false, n_seqs, n_rows, max_seq_len, 0, &pl) == STARKV_OK ? pl.total : 0;
+}
+
+starkv_status starkv_paged_cross(const starkv_layer_desc* desc, int32_t n_seqs, int32_t n_rows, int32_t max_seq_len,
+                                 const void* q, const void* B_K, const void* B_V, const void* k_cache,
+                                 const void* v_cache, const int32_t* block_tables, const int32_t* seq_lens,
+                                 const int32_t* row_offsets, float scale, void* workspace, size_t workspace_bytes,
+                                 void* out, void* stream) {
+  return group_impl(desc, false, n_seqs, n_rows, max_seq_len, 0, q, B_K, B_V, k_cache, v_cache, block_tables, seq_lens,
+                    nullptr, row_offsets, scale, workspace, workspace_bytes, out, stream);
 }
 
 starkv_status starkv_decode_check(const void* workspace, void* stream, int32_t* flags_out) {

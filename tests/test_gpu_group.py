@@ -1,0 +1,201 @@
+"""Shared-prefix decode and cross attention against the fp64 oracle (GPU).
+
+Bounds are derived in group_common.  Unused slots of the pools are NaN and
+workspaces start as NaN bytes, so no result may depend on either.
+"""
+import numpy as np
+import pytest
+import torch
+
+import rank_compressed_kv_star_b200 as S
+from group_common import (Layer, UNTOUCHED, call, check_case, dev, make_cross, make_shared, reference, to_device)
+from gpu_common import load
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built(cuda_ok):
+    load()
+
+
+LAYERS = {
+    "mha4": (4, 4, 64, 16, 64), "gqa32": (32, 8, 128, 64, 512), "one": (1, 1, 64, 80, 64), "mqa8": (8, 1, 32, 48, 192),
+    "wide": (16, 4, 256, 256, 320), "gqa64": (64, 4, 128, 128, 576), "mqa64": (64, 1, 64, 160, 128),
+    "mha32": (32, 32, 128, 64, 2048),
+}
+
+
+@pytest.mark.parametrize("tokens,rows", [(1, 1), (15, 2), (16, 1), (17, 3), (63, 1), (64, 5), (65, 1), (127, 2), (128, 1),
+                                         (129, 4), (300, 9), (1111, 2)])
+def test_cross_lengths(tokens, rows):
+    L = Layer(1, *LAYERS["mha4"])
+    check_case(L, make_cross(L, [(tokens, rows)]))
+
+
+@pytest.mark.parametrize("layer", sorted(LAYERS))
+def test_cross_layers(layer):
+    L = Layer(2, *LAYERS[layer])
+    check_case(L, make_cross(L, [(70, 3), (0, 2), (211, 1), (16, 0), (33, 7)], pad_rows=3))
+
+
+@pytest.mark.parametrize("layer", sorted(LAYERS))
+def test_shared_layers(layer):
+    L = Layer(3, *LAYERS[layer])
+    check_case(L, make_shared(L, [(100, [5, 0, 33]), (64, [16]), (0, [20, 1])], pad_rows=2))
+
+
+@pytest.mark.parametrize("shared,owns", [
+    (0, [1]), (1, [3, 1]), (15, [16, 2]), (16, [1, 0]), (17, [40]), (130, [0, 0, 0]), (1000, [17, 250, 3, 64, 65, 1]),
+    (64, [-1, 5, -64, -20, 0, 9]),      # rows shorter than the shared length, one of no tokens
+    (48, [-48, -48])])
+def test_shared_lengths(shared, owns):
+    L = Layer(4, *LAYERS["gqa32"])
+    check_case(L, make_shared(L, [(shared, owns)]))
+
+
+@pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 31, 33, 64, 65, 130, 300])
+def test_many_rows_share_pages(rows):
+    """Every column tile width, several tiles per entry, all rows checked at a small layer."""
+    L = Layer(5, 8, 2, 64, 48, 192)
+    check_case(L, make_cross(L, [(90, rows), (40, 2)]))
+    check_case(L, make_shared(L, [(70, [1 + b % 3 for b in range(rows)])]))
+
+
+def test_long_shared_prefix_splits_tiles():
+    """Tiles carried over several CTAs; a sample of rows is checked."""
+    L = Layer(6, *LAYERS["gqa32"])
+    c = make_shared(L, [(5003, [200, 11, 77] * 3)])
+    check_case(L, c, rows=[0, 4, 8])
+    c = make_cross(L, [(4099, 1)])
+    check_case(L, c)
+
+
+def test_shared_equals_paged_decode():
+    """The same q, tables and lengths through starkv_paged_decode."""
+    L = Layer(7, *LAYERS["mha32"])
+    c = make_shared(L, [(200, [9, 30, 1]), (50, [64])])
+    g, got = check_case(L, c)
+    T = int(c["seq_lens"].max())
+    wsb = S.starkv_decode_workspace_bytes(g["desc"], c["n"], T)
+    ws = torch.empty(wsb, dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(g["out"])
+    S.starkv_paged_decode(g["desc"], c["n"], T, g["q"], g["B_K"], g["B_V"], g["k"], g["v"], g["tables"], g["seq_lens"],
+                          L.scale, ws, wsb, out)
+    ref, bound = reference(L, c)
+    want = out.float().cpu().numpy()
+    for b in range(c["n"]):
+        assert (np.abs(got[b] - want[b]) <= 2 * bound[b]).all()
+
+
+def test_peaked_and_flat_rows():
+    """Logits of a few hundred (one token takes all) and of zero (a plain mean)."""
+    for q_scale in (60.0, 0.0):
+        L = Layer(8, *LAYERS["gqa32"], q_scale=q_scale)
+        check_case(L, make_shared(L, [(320, [40, 7])]))
+        check_case(L, make_cross(L, [(333, 5)]))
+
+
+def test_infinite_and_nan_codes_reach_only_their_rows():
+    L = Layer(9, *LAYERS["mha4"])
+    c = make_shared(L, [(64, [10, 12]), (32, [5])])
+    bad = c["tables"][0, 4]                       # row 0's own page
+    c["v"][bad, 3] = np.inf
+    c["k"][bad, 2] = np.nan
+    g = to_device(L, c)
+    call(L, c, g)
+    got = g["out"].float().cpu().numpy()
+    assert np.isnan(got[0]).any()
+    ref, bound = reference(L, c, rows=[1, 2])
+    for b in (1, 2):
+        assert (np.abs(got[b] - ref[b]) <= bound[b]).all()
+
+
+def test_repeatable_and_on_another_stream():
+    L = Layer(10, *LAYERS["gqa32"])
+    c = make_shared(L, [(777, [30, 90, 200, 1, 5]), (0, [64])])
+    g, first = check_case(L, c)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(3):
+            g["out"].fill_(UNTOUCHED)
+            call(L, c, g, stream=s)
+    s.synchronize()
+    assert np.array_equal(g["out"].float().cpu().numpy(), first)
+
+
+def test_captured_graphs_with_changed_inputs():
+    """A captured call replayed after the lengths, the row counts and the queries change (within its bounds)."""
+    L = Layer(11, *LAYERS["gqa32"])
+    c = make_shared(L, [(150, [30, 90, 20]), (64, [5, 6])])
+    d = make_cross(L, [(100, 4), (64, 3)])
+    gc, gd = to_device(L, c), to_device(L, d)
+    call(L, c, gc), call(L, d, gd)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(L, c, gc)
+        call(L, d, gd)
+    q2 = L.f(c["n"], L.H, L.d, a=1.0)
+    gc["q"].copy_(dev(q2))
+    c["q"] = q2
+    c["seq_lens"] = (c["seq_lens"] - np.array([3, 50, 0, 1, 0])).astype(np.int32)
+    gc["seq_lens"].copy_(dev(c["seq_lens"]))
+    d["row_offsets"] = np.array([0, 2, 5], np.int32)     # rows 5 and 6 now belong to no sequence
+    gd["row_offsets"].copy_(dev(d["row_offsets"]))
+    d["used"] = 5
+    gc["out"].fill_(UNTOUCHED), gd["out"].fill_(UNTOUCHED)
+    graph.replay()
+    torch.cuda.synchronize()
+    for x, g in ((c, gc), (d, gd)):
+        assert S.starkv_decode_check(g["ws"]) == (0, 0)
+        ref, bound = reference(L, x)
+        got = g["out"].float().cpu().numpy()
+        for b in ref:
+            assert (np.abs(got[b] - ref[b]) <= bound[b]).all()
+        assert (got[x["used"]:] == UNTOUCHED).all()
+
+
+def test_out_of_range_values_are_flagged_and_other_groups_stand():
+    L = Layer(12, *LAYERS["gqa32"])
+    base = make_shared(L, [(64, [10, 12]), (32, [5, 8])])
+
+    def flags(**change):
+        c = dict(base)
+        c.update(change)
+        g = to_device(L, c)
+        call(L, c, g)
+        return S.starkv_decode_check(g["ws"])[1], g["out"].float().cpu().numpy()
+
+    ref, bound = reference(L, base, rows=[0, 1])
+    t = base["tables"].copy()
+    t[2, 1] = base["nb"]                                   # a shared page of group 1
+    t[3, 1] = -1
+    for change, flag in ((dict(tables=t), S.FLAG_BAD_BLOCK_ID),
+                         (dict(seq_lens=np.array([74, 76, -1, 40], np.int32)), S.FLAG_BAD_SEQ_LEN),
+                         (dict(seq_lens=np.array([74, 76, 37, 90], np.int32)), S.FLAG_BAD_SEQ_LEN),
+                         (dict(shared_lens=np.array([64, 1 << 20], np.int32)), S.FLAG_BAD_SEQ_LEN),
+                         (dict(row_offsets=np.array([0, 2, 9], np.int32)), S.FLAG_BAD_ROW_OFFSET)):
+        got_flags, got = flags(**change)
+        assert got_flags & flag, (change, got_flags)
+        for b in (0, 1):
+            assert (np.abs(got[b] - ref[b]) <= bound[b]).all()
+    for offsets in ([0, 3, 2], [1, 2, 4], [-5, 2, 4]):
+        assert flags(row_offsets=np.array(offsets, np.int32))[0] & S.FLAG_BAD_ROW_OFFSET
+
+
+def test_rows_in_no_group_and_empty_calls():
+    L = Layer(13, *LAYERS["mha4"])
+    c = make_cross(L, [(50, 2)], pad_rows=4)
+    g, _ = check_case(L, c)
+    # no sequence at all: nothing is written but the status word
+    g["out"].fill_(UNTOUCHED)
+    st = S.starkv_paged_cross(g["desc"], 0, 6, 50, g["q"], g["B_K"], g["B_V"], g["k"], g["v"], g["tables"], g["seq_lens"],
+                              g["row_offsets"], L.scale, g["ws"], g["bytes"], g["out"])
+    assert st == 0 and S.starkv_decode_check(g["ws"]) == (0, 0)
+    assert (g["out"] == UNTOUCHED).all()
+    # bounds of zero: rows without tokens
+    c = make_shared(L, [(0, [0, 0])])
+    g, got = check_case(L, c)
+    assert (got == 0).all()
