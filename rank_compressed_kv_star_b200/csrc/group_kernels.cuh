@@ -8,17 +8,15 @@
 // a row b and query head h, with g(h) = h / (H / Hkv) and the tokens t of the
 // row's one or two entries,
 //   s[b,h,t] = log2(e) scale q[b,h] . B_K[g(h)]^T . c_K[t,g(h)]
-//   M[b,h]   = max_t s          w[b,h,t] = fp16(exp2(s - M))        L = sum_t w
-//   out[b,h] = (sum_t w c_V[t] / L) . B_V[:, g(h) d : (g(h)+1) d]
-// The maximum is taken over both entries before any weight is formed, so the
-// partial sums of a row simply add up.  Launches, all on the caller's stream:
-//   1. group_absorb  q~ = log2(e) scale q . B_K^T in fp16 hi + lo halves; the
-//                    entry tables (one extra CTA); M = -inf
-//   2. group_kpass<max>      S = c_K . q~ on tcgen05, maxima only
-//   3. group_kpass<weights>  S again, w to the P matrix, L per token chunk
-//   4. group_vpass   Z = P . c_V on tcgen05, partial sums per (tile, CTA)
-//   5. group_combine Z / L over the partials, in fp16 hi + lo halves
-//   6. group_up      out = Z / L . B_V on tcgen05
+//   out[b,h] = (sum_t exp2(s - M) c_V[t] / sum_t exp2(s - M)) . B_V[:, g(h) d : (g(h)+1) d]
+// Launches, all on the caller's stream:
+//   1. group_absorb   q~ = log2(e) scale q . B_K^T in fp16 hi + lo halves, and
+//                     the entry tables (one extra CTA)
+//   2. group_attend   per segment (a run of tokens of one column tile): the
+//                     maxima m of its logits, w = fp16(exp2(s - m)), l = sum w
+//                     and Z = sum w c_V, all on tcgen05
+//   3. group_combine  M = max m, Z / L over a row's segments, in hi + lo halves
+//   4. group_up       out = Z / L . B_V on tcgen05
 // All rows of an entry share every load of its pages: the codes of a page are
 // read from HBM once per entry, whatever the number of rows.
 #pragma once
@@ -35,45 +33,67 @@ namespace starkv {
 
 // One run of rows over one list of pages: rows row0 .. row0 + nrows - 1 over
 // tokens 0 .. len - 1, token t in slot t % 16 of page tables[tab][page0 + t / 16].
+// Its columns are the (KV head j, row, query head of j) triples in that order.
 struct alignas(16) GroupEntry {
   int32_t row0, nrows, len, page0;
   int32_t tab, src;   // src 0: a group's (or sequence's) pages; 1: a row's own pages
-  int32_t minlim;     // fewest tokens that any of the rows attends over
-  int32_t pad;
+  int32_t pad0, pad1;
 };
 
 struct GroupGeom {
   int H, Hkv, log2G, d, r, R, MB, NB;
   int n_rows, n_groups, E;     // E = n_groups entries, plus n_rows own entries when shared
   int shared;                  // 1: shared-prefix decode, 0: cross attention
-  int ncol;                    // K pass: query columns per tile (rows per tile x G)
-  int chunk;                   // K pass: tokens per item, a multiple of 128
-  int n_rt;                    // V pass: 256-row tiles of R
-  int t_pad[2];                // P row length by source, a multiple of 128
-  int n_ch[2];                 // chunks per P row by source
+  int ncap;                    // columns per tile at most
+  int n_slab, C, nch;          // R in n_slab slabs, each over the C CTAs of a cluster, 64 nch codes per CTA
+  int weight[2];               // cost of a 128-token block of a tile by source
   int max_len[2];              // host bounds of the entries' lengths by source
   GroupEntry* ent;             // [E]
-  int64_t* kpre;               // [E + 1] K items before each entry
-  int64_t* vpre;               // [E + 1] V units before each entry
+  int64_t* pre;                // [E + 1] cost of the tiles before each entry
   int32_t* row_ent;            // [n_rows] the row's group, or -1
-  int32_t* row_lim;            // [n_rows] tokens of the group's pages that the row attends over
+  int32_t* row_use;            // [n_rows] 1: the row attends over its group's pages
   int32_t* n_used;             // rows that belong to groups (row_offsets[n_groups])
-  float* mrow;                 // [n_rows][H] maxima
-  float* lpart[2];             // [n_rows][H][n_ch] sums of weights per chunk
   int32_t* status;
 };
 
-constexpr int kGVTile = 256;    // V pass: columns (row, head) and rows of R per tile
-constexpr int kGVTok = 64;      // V pass: tokens per unit
+constexpr int kGTok = 128;      // tokens per block
 
-// Column tiles of an entry with `cols` (row, head) columns, and their width.
-__device__ __forceinline__ int gv_tiles(int cols) { return (cols + kGVTile - 1) / kGVTile; }
-__device__ __forceinline__ int gv_width(int cols, int nt) { return ((cols + nt - 1) / nt + 15) / 16 * 16; }
-// Row tiles of the K pass and rows per tile.
-__device__ __forceinline__ int gk_tiles(int nrows, const GroupGeom& g) {
-  const int per = g.ncol >> g.log2G;
-  return (nrows + per - 1) / per;
+// The column tiles of an entry: whole KV heads (hpt of them, width = hpt * m
+// columns) while the m = nrows * G columns of a head fit a tile, else runs of cw
+// columns of one head (split runs per head).
+struct TileShape {
+  int m, nt, hpt, split, cw;
+};
+__device__ __forceinline__ TileShape tile_shape(int nrows, const GroupGeom& g) {
+  TileShape t;
+  t.m = nrows << g.log2G;
+  if (t.m <= g.ncap) {
+    const int most = g.ncap / t.m;
+    t.nt = (g.Hkv + most - 1) / most;
+    t.hpt = (g.Hkv + t.nt - 1) / t.nt;
+    t.nt = (g.Hkv + t.hpt - 1) / t.hpt;
+    t.split = 1;
+    t.cw = t.m;
+  } else {
+    t.hpt = 1;
+    const int n = (t.m + g.ncap - 1) / g.ncap;
+    t.cw = ((t.m + n - 1) / n + 7) / 8 * 8;
+    t.split = (t.m + t.cw - 1) / t.cw;
+    t.nt = g.Hkv * t.split;
+  }
+  return t;
 }
+// Tile of the column `within` of KV head j, and the column's place in the tile.
+__device__ __forceinline__ int tile_of(const TileShape& t, int j, int within, int* place) {
+  if (t.split == 1) {
+    *place = (j % t.hpt) * t.m + within;
+    return j / t.hpt;
+  }
+  *place = within % t.cw;
+  return j * t.split + within / t.cw;
+}
+
+__device__ __forceinline__ int64_t entry_blocks(const GroupEntry& en) { return (en.len + kGTok - 1) / kGTok; }
 
 // Largest e with pre[e] <= x (0 <= x < pre[E]; empty entries are skipped).
 __device__ __forceinline__ int32_t entry_of(const int64_t* pre, int32_t E, int64_t x) {
@@ -99,105 +119,103 @@ __device__ __forceinline__ int clamp_flag(int x, int lo, int hi, int32_t* bad, i
   return x;
 }
 
+// Rows [r0, r0 + n) of group e: the caller's offsets, clamped to the rows there are.
+__device__ __forceinline__ void group_rows(const GroupSetupParams& p, int e, int* r0, int* n) {
+  const int a = min(max(p.row_offsets[e], 0), p.g.n_rows), b = min(max(p.row_offsets[e + 1], 0), p.g.n_rows);
+  *r0 = a;
+  *n = b > a ? b - a : 0;
+}
+// Group of row b (and the group's rows), or -1: behind the last group, or the
+// offsets are out of order.
+__device__ __forceinline__ int group_of_row(const GroupSetupParams& p, int b, int* r0, int* n) {
+  if (b >= p.row_offsets[p.g.n_groups]) return -1;
+  int lo = 0, hi = p.g.n_groups - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.row_offsets[mid] <= b) lo = mid; else hi = mid - 1;
+  }
+  group_rows(p, lo, r0, n);
+  return b >= *r0 && b < *r0 + *n ? lo : -1;
+}
+
 // One CTA of 256 threads.  Every value read from the caller's arrays is clamped
 // (and flagged) here, so that the later kernels index in range whatever they hold.
 __device__ __forceinline__ void group_setup(const GroupSetupParams& p) {
   const GroupGeom& g = p.g;
   __shared__ int32_t bad;
-  __shared__ int64_t sk[256], sv[256];
-  const int tid = threadIdx.x;
+  __shared__ int64_t warp_sum[8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) bad = 0;
   __syncthreads();
-  if (tid == 0)
-    *g.n_used = g.n_groups > 0 ? clamp_flag(p.row_offsets[g.n_groups], 0, g.n_rows, &bad, STARKV_FLAG_BAD_ROW_OFFSET) : 0;
-  for (int e = tid; e < g.n_groups; e += 256) {
+  if (tid == 0) *g.n_used = clamp_flag(p.row_offsets[g.n_groups], 0, g.n_rows, &bad, STARKV_FLAG_BAD_ROW_OFFSET);
+  // thread t makes the entries [t per, (t + 1) per) and keeps their cost
+  const int per = (g.E + 255) / 256;
+  const int e0 = tid * per, e1 = min(g.E, e0 + per);
+  int64_t mine = 0;
+  auto cost = [&](const GroupEntry& en) {
+    return en.nrows > 0 ? static_cast<int64_t>(tile_shape(en.nrows, g).nt) * g.n_slab * entry_blocks(en) * g.weight[en.src]
+                        : static_cast<int64_t>(0);
+  };
+  for (int e = e0; e < e1; ++e) {
     GroupEntry en{};
-    const int r0 = clamp_flag(p.row_offsets[e], 0, g.n_rows, &bad, STARKV_FLAG_BAD_ROW_OFFSET);
-    const int r1 = clamp_flag(p.row_offsets[e + 1], 0, g.n_rows, &bad, STARKV_FLAG_BAD_ROW_OFFSET);
-    if (r1 < r0 || (e == 0 && r0 != 0)) atomicOr(&bad, STARKV_FLAG_BAD_ROW_OFFSET);
-    en.row0 = r0;
-    en.nrows = r1 > r0 ? r1 - r0 : 0;
-    const int len = clamp_flag(g.shared ? p.shared_lens[e] : p.seq_lens[e], 0, g.max_len[0], &bad, STARKV_FLAG_BAD_SEQ_LEN);
-    en.len = g.shared ? len / kBlock * kBlock : len;   // whole pages are shared
-    en.tab = g.shared ? (r0 < g.n_rows ? r0 : 0) : e;
-    en.minlim = en.len;
-    g.ent[e] = en;
-  }
-  __syncthreads();
-  const int used = *g.n_used;
-  for (int b = tid; b < g.n_rows; b += 256) {
-    int e = -1;
-    if (b < used) {
-      int lo = 0, hi = g.n_groups - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.row_offsets[mid] <= b) lo = mid; else hi = mid - 1;
-      }
-      if (b >= g.ent[lo].row0 && b < g.ent[lo].row0 + g.ent[lo].nrows) e = lo;   // else the offsets are out of order
-    }
-    int lim = e >= 0 ? g.ent[e].len : 0;
-    if (g.shared) {
-      GroupEntry en{};
+    if (e < g.n_groups) {
+      const int a = p.row_offsets[e], b = p.row_offsets[e + 1];
+      if (a < 0 || a > b || b > g.n_rows || (e == 0 && a != 0)) atomicOr(&bad, STARKV_FLAG_BAD_ROW_OFFSET);
+      group_rows(p, e, &en.row0, &en.nrows);
+      const int len =
+          clamp_flag(g.shared ? p.shared_lens[e] : p.seq_lens[e], 0, g.max_len[0], &bad, STARKV_FLAG_BAD_SEQ_LEN);
+      en.len = g.shared ? len / kBlock * kBlock : len;   // whole pages are shared
+      en.tab = g.shared ? min(en.row0, g.n_rows - 1) : e;
+    } else {
+      const int b = e - g.n_groups;
+      int r0, n;
+      const int grp = group_of_row(p, b, &r0, &n);
       en.row0 = b;
       en.src = 1;
       en.tab = b;
-      if (e >= 0) {
+      int use = 0;
+      if (grp >= 0) {
+        const int common = min(max(p.shared_lens[grp], 0), g.max_len[0]) / kBlock * kBlock;
         const int T = clamp_flag(p.seq_lens[b], 0, g.MB * kBlock, &bad, STARKV_FLAG_BAD_SEQ_LEN);
-        const int own = T > lim ? T - lim : 0;
         en.nrows = 1;
-        en.page0 = lim / kBlock;
-        en.len = clamp_flag(own, 0, g.max_len[1], &bad, STARKV_FLAG_BAD_SEQ_LEN);
-        en.minlim = en.len;
-        if (T < lim) {
-          lim = T;
-          atomicMin(&g.ent[e].minlim, T);
+        if (T >= common) {
+          use = common > 0;
+          en.page0 = common / kBlock;
+          en.len = clamp_flag(T - common, 0, g.max_len[1], &bad, STARKV_FLAG_BAD_SEQ_LEN);
+        } else {
+          en.len = T;   // shorter than the shared pages: the row reads all of its tokens by itself
         }
       }
-      g.ent[g.n_groups + b] = en;
+      g.row_ent[b] = grp;
+      g.row_use[b] = use;
     }
-    g.row_ent[b] = e;
-    g.row_lim[b] = lim;
+    g.ent[e] = en;
+    mine += cost(en);
   }
+  if (!g.shared)
+    for (int b = tid; b < g.n_rows; b += 256) {
+      int r0, n;
+      const int grp = group_of_row(p, b, &r0, &n);
+      g.row_ent[b] = grp;
+      g.row_use[b] = grp >= 0 ? 1 : 0;
+    }
+  // exclusive prefix sums of the costs
+  int64_t v = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  if (lane == 31) warp_sum[warp] = v;
   __syncthreads();
-  // exclusive prefix sums of the K items and V units over the entries
-  const int per = (g.E + 255) / 256;
-  const int e0 = tid * per;
-  int64_t nk = 0, nv = 0;
-  auto counts = [&](int e, int64_t* k, int64_t* v) {
-    const GroupEntry en = g.ent[e];
-    const int cols = en.nrows * g.H;
-    const bool live = en.nrows > 0 && en.len > 0;
-    *k = live ? static_cast<int64_t>(gk_tiles(en.nrows, g)) * g.Hkv * ((en.len + g.chunk - 1) / g.chunk) : 0;
-    *v = live ? static_cast<int64_t>(gv_tiles(cols)) * g.n_rt * ((en.len + kGVTok - 1) / kGVTok) : 0;
-  };
-  for (int e = e0; e < e0 + per && e < g.E; ++e) {
-    int64_t k, v;
-    counts(e, &k, &v);
-    nk += k;
-    nv += v;
-  }
-  sk[tid] = nk;
-  sv[tid] = nv;
-  __syncthreads();
-  for (int o = 1; o < 256; o <<= 1) {
-    const int64_t a = tid >= o ? sk[tid - o] : 0, b = tid >= o ? sv[tid - o] : 0;
-    __syncthreads();
-    sk[tid] += a;
-    sv[tid] += b;
-    __syncthreads();
-  }
-  int64_t ak = sk[tid] - nk, av = sv[tid] - nv;
-  for (int e = e0; e < e0 + per && e < g.E; ++e) {
-    int64_t k, v;
-    counts(e, &k, &v);
-    g.kpre[e] = ak;
-    g.vpre[e] = av;
-    ak += k;
-    av += v;
+  int64_t at = v - mine;
+  for (int w = 0; w < warp; ++w) at += warp_sum[w];
+  for (int e = e0; e < e1; ++e) {
+    g.pre[e] = at;
+    at += cost(g.ent[e]);
   }
   if (tid == 255) {
-    g.kpre[g.E] = sk[255];
-    g.vpre[g.E] = sv[255];
+    g.pre[g.E] = at;
     *g.status = bad;
   }
 }
@@ -207,8 +225,8 @@ struct GroupAbsorbParams {
   GroupSetupParams su;
   const __half* q;     // [n_rows][H][d]
   const __half* B_K;   // [Hkv][r][d]
-  __half* qh;          // [n_rows * H][r] fp16 of q~
-  __half* ql;          // [n_rows * H][r] fp16 of its remainder
+  __half* qh[2];       // by source, [n_rows * H][r] in the order of the entries' columns: fp16 of q~
+  __half* ql[2];       // fp16 of its remainder
   float coef;          // scale * log2(e)
   int tile;            // rows per item
 };
@@ -217,6 +235,7 @@ struct GroupAbsorbParams {
 __global__ void __launch_bounds__(kPrepThreads)
 group_absorb_kernel(GroupAbsorbParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ int32_t s_row0[kAbsBT], s_n[kAbsBT];
   griddep_wait();
   griddep_launch_dependents();
   if (blockIdx.x == 0) {
@@ -230,7 +249,12 @@ group_absorb_kernel(GroupAbsorbParams p) {
   const int nb = min(p.tile, g.n_rows - b0);
   __half* Ws = reinterpret_cast<__half*>(smem_raw);   // [d][r]: B_K[g(h)] transposed
   __half* qs = Ws + static_cast<size_t>(D) * r;       // [tile][d]
-  for (int b = tid; b < nb; b += kPrepThreads) g.mrow[static_cast<size_t>(b0 + b) * g.H + h] = -INFINITY;
+  if (tid < nb) {
+    int r0 = 0, n = 0;
+    const int e = group_of_row(p.su, b0 + tid, &r0, &n);
+    s_row0[tid] = r0;
+    s_n[tid] = e >= 0 ? n : 0;
+  }
   const __half* bk = p.B_K + static_cast<size_t>(h >> g.log2G) * r * D;
   for (int x = tid; x < r * (D / 8); x += kPrepThreads) {
     const int i = x % r, jb = x / r;
@@ -245,81 +269,124 @@ group_absorb_kernel(GroupAbsorbParams p) {
         reinterpret_cast<const uint4*>(p.q + (static_cast<size_t>(b0 + bb) * g.H + h) * D)[c];
   }
   __syncthreads();
+  const int j = h >> g.log2G, gg = h & ((1 << g.log2G) - 1);
   small_proj(Ws, qs, nb, D, r, [&](int bb, int i, float v0, float v1) {
     v0 *= p.coef;
     v1 *= p.coef;
-    const size_t o = (static_cast<size_t>(b0 + bb) * g.H + h) * r + i;
     const __half2 hi = __floats2half2_rn(v0, v1);
     const float2 hf = __half22float2(hi);
-    *reinterpret_cast<__half2*>(p.qh + o) = hi;
-    *reinterpret_cast<__half2*>(p.ql + o) = __floats2half2_rn(v0 - hf.x, v1 - hf.y);
+    const __half2 lo = __floats2half2_rn(v0 - hf.x, v1 - hf.y);
+    const int n = s_n[bb], row = b0 + bb;
+    if (n == 0) return;   // in no group
+    const size_t o0 = (static_cast<size_t>(s_row0[bb]) * g.H + ((static_cast<size_t>(j) * n + row - s_row0[bb]) << g.log2G) + gg) * r + i;
+    *reinterpret_cast<__half2*>(p.qh[0] + o0) = hi;
+    *reinterpret_cast<__half2*>(p.ql[0] + o0) = lo;
+    if (g.shared) {
+      const size_t o1 = (static_cast<size_t>(row) * g.H + h) * r + i;
+      *reinterpret_cast<__half2*>(p.qh[1] + o1) = hi;
+      *reinterpret_cast<__half2*>(p.ql[1] + o1) = lo;
+    }
   });
 }
 
-// ================================================================== K pass
-// An item is one KV head, one tile of rows and one chunk of tokens of an entry.
-// Per block of 128 tokens, D[token, column] = c_K . (q~ hi + q~ lo) with the
-// tokens on the 128 TMEM lanes (A: one 16-token x 64-code TMA box per page,
-// K-major with the 128-byte swizzle) and the tile's (row, query head of the KV
-// head) pairs as columns.  Warp 0 issues the copies, warp 1 the MMAs into a
-// ring of accumulators, warps 2..9 drain them: each takes one lane quarter and
-// every other block of 16 columns.  The weights pass forms S a second time
-// rather than keeping it: r / R of the V pass's products against 8 bytes of
-// traffic per logit.
-struct GroupKParams {
+// ================================================================== attend
+// One cluster of C CTAs works on one segment at a time: a run of 128-token
+// blocks of one column tile (up to ncap (KV head, row, query head) columns of an
+// entry).  CTA c accumulates Z for its own 64 nch codes of R in tensor memory;
+// the logits of (block, KV head) units go round the CTAs, each unit computed by
+// one CTA and its fp16 weights copied to all of them through distributed shared
+// memory.  So the K codes, the exponentials and the V codes are each read and
+// computed once per tile, and no logit or weight leaves the SMs.
+//   phase A  S = c_K . (q~ hi + q~ lo) per unit; column maxima, exchanged
+//   phase B  S again; w = fp16(exp2(s - m)) into the P block of every CTA;
+//            Z += P . c_V as blocks complete
+// Costs of all tiles are laid end to end and cluster i of n takes the blocks
+// that begin in [i P / n, (i+1) P / n).  The sums of a tile that begins in a
+// cluster's range go to the tile's own place, those of a tile carried over from
+// the cluster before to the cluster's carry slot: fixed places, fixed order.
+//
+// Warps: 0 loads q~ and K tiles, 1 issues the S products, 2 loads V tiles, 3
+// issues the Z products, 4..11 take the maxima, form the weights and store Z.
+struct GroupAttendParams {
   GroupGeom g;
   const int32_t* tables;     // rows of g.MB entries
-  __half* P[2];              // [n_rows * H][t_pad] by source
+  float* Z[2];               // by source, [n_rows * H][R]
+  float* m[2];               // by source, [n_slab][n_rows * H]
+  float* l[2];               // by source, [n_slab][n_rows * H][C]
+  float* zcarry;             // [clusters][ncap][R]
+  float* mcarry;             // [clusters][ncap]
+  float* lcarry;             // [clusters][ncap][C]
   int kb, ksteps;            // 64-code blocks and 16-code steps of r
-  int qbox;                  // columns per query box, max(16, G)
-  int nq, stages;            // query slots, ring stages
-  uint32_t a_bytes, q_bytes; // ring stage, query slot (hi then lo)
-  uint32_t tmem_cols;
+  int k_stages, v_stages;
+  uint32_t v_stage_bytes;    // 2 pages x 16 tokens x 64 nch codes
 };
 
-constexpr int kGKThreads = 320;
-constexpr int kGKEpi = kGKThreads - 64;
-constexpr int kGKAcc = 4;
+constexpr int kGAThreads = 384;
+constexpr int kGAEpi = kGAThreads - 128;
+constexpr int kGAVTok = 32;        // tokens per V stage
+constexpr int kGAQBox = 32;        // columns per query box
+constexpr int kGAMaxC = 8;
 
-struct KItem {
+struct Segment {
   GroupEntry en;
-  int j, row0, nrow, c, t0, t1;   // KV head, rows of the tile, chunk, tokens [t0, t1)
+  TileShape ts;
+  int ct, slab;
+  int col0, ncols;     // first column (of the entry's) and columns of the tile
+  int nh, mt, j0;      // KV heads in the tile, columns per head, first head
+  int b0, b1;          // blocks
+  bool first;          // the tile begins here
 };
 
-// Walks the items [i0, i1) of a CTA in order.
-struct KWalk {
+struct SegWalk {
   const GroupGeom& g;
-  int64_t it, end, ebeg, eend;
+  int64_t x, end, ebeg, eend;   // cost positions
   int32_t e;
   GroupEntry en;
-  __device__ KWalk(const GroupGeom& g_, int64_t i0, int64_t i1) : g(g_), it(i0), end(i1), ebeg(0), eend(0), e(0) {
-    if (it < end) {
-      e = entry_of(g.kpre, g.E, it);
-      load();
+  __device__ SegWalk(const GroupGeom& g_, int64_t a, int64_t b) : g(g_), x(a), end(b), ebeg(0), eend(0), e(0) {
+    if (x < end) {
+      e = entry_of(g.pre, g.E, x);
+      ebeg = g.pre[e];
+      eend = g.pre[e + 1];
+      en = g.ent[e];
     }
   }
-  __device__ void load() {
-    ebeg = g.kpre[e];
-    eend = g.kpre[e + 1];
-    en = g.ent[e];
-  }
-  __device__ bool next(KItem* x) {
-    if (it >= end) return false;
-    while (it >= eend) { ++e; ebeg = eend; eend = g.kpre[e + 1]; if (it < eend) en = g.ent[e]; }
-    const int64_t local = it - ebeg;
-    const int nt = gk_tiles(en.nrows, g);
-    x->en = en;
-    x->j = static_cast<int>(local % g.Hkv);
-    const int rest = static_cast<int>(local / g.Hkv);
-    const int rt = rest % nt;
-    x->c = rest / nt;
-    const int per = (en.nrows + nt - 1) / nt;
-    x->row0 = en.row0 + rt * per;
-    x->nrow = min(per, en.row0 + en.nrows - x->row0);
-    x->t0 = x->c * g.chunk;
-    x->t1 = min(en.len, x->t0 + g.chunk);
-    ++it;
-    return true;
+  // The next run of blocks that begin in [x, end); blocks of an entry of weight
+  // w begin at ebeg + w i.
+  __device__ bool next(Segment* s) {
+    for (;;) {
+      if (x >= end) return false;
+      while (x >= eend) { ++e; ebeg = eend; eend = g.pre[e + 1]; if (x < eend) en = g.ent[e]; }
+      const int w = g.weight[en.src];
+      const int64_t i = (x - ebeg + w - 1) / w;                       // first block that begins at or after x
+      const int64_t stop = ((end < eend ? end : eend) - ebeg + w - 1) / w;   // first block not taken
+      if (i >= stop) { x = end < eend ? end : eend; continue; }
+      const int64_t blocks = entry_blocks(en);
+      const int64_t tile = i / blocks;
+      s->en = en;
+      s->ts = tile_shape(en.nrows, g);
+      s->ct = static_cast<int>(tile / g.n_slab);
+      s->slab = static_cast<int>(tile % g.n_slab);
+      const TileShape& t = s->ts;
+      if (t.split == 1) {
+        s->j0 = s->ct * t.hpt;
+        s->nh = min(t.hpt, g.Hkv - s->j0);
+        s->mt = t.m;
+        s->col0 = s->j0 * t.m;
+      } else {
+        s->j0 = s->ct / t.split;
+        s->nh = 1;
+        const int c = (s->ct % t.split) * t.cw;
+        s->mt = min(t.cw, t.m - c);
+        s->col0 = s->j0 * t.m + c;
+      }
+      s->ncols = s->nh * s->mt;
+      s->b0 = static_cast<int>(i - tile * blocks);
+      const int64_t left = stop - i;
+      s->b1 = static_cast<int>(left < blocks - s->b0 ? s->b0 + left : blocks);
+      s->first = s->b0 == 0;
+      x = ebeg + (i + s->b1 - s->b0) * w;
+      return true;
+    }
   }
 };
 
@@ -337,344 +404,76 @@ __device__ __forceinline__ float lane_sum16(float (&a)[16], int lane) {
   return a[0] + __shfl_xor_sync(0xffffffffu, a[0], 1);
 }
 
-template <bool kWeights>
-__global__ void __launch_bounds__(kGKThreads, 1)
-group_kpass_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qhmap,
-                   const __grid_constant__ CUtensorMap qlmap, GroupKParams p) {
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = align_smem_1024(smem_raw);
-  const GroupGeom& g = p.g;
-  const int S = p.stages;
-  uint8_t* qslot = smem + static_cast<size_t>(S) * p.a_bytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(qslot + static_cast<size_t>(p.nq) * p.q_bytes);
-  uint64_t* empty = full + S;
-  uint64_t* qfull = empty + S;
-  uint64_t* qempty = qfull + 2;
-  uint64_t* tfull = qempty + 2;
-  uint64_t* tempty = tfull + kGKAcc;
-  uint64_t* mmadone = tempty + kGKAcc;
-  uint64_t* ebar = mmadone + 1;
-  __shared__ uint32_t taddr_s;
-  __shared__ volatile int32_t abort_flag;
-  __shared__ int64_t s_off[128];
-  __shared__ int32_t s_lim[128];
-  __shared__ __align__(16) float s_m[128];
-  __shared__ float s_red[4][128];
-
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-    for (int s = 0; s < S; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-    for (int a = 0; a < 2; ++a) { mbar_init(&qfull[a], 1); mbar_init(&qempty[a], 1); }
-    for (int a = 0; a < kGKAcc; ++a) { mbar_init(&tfull[a], 1); mbar_init(&tempty[a], kGKEpi / 32); }
-    mbar_init(mmadone, 1);
-    mbar_init(ebar, kGKEpi);
-    abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == 1) {
-    tmem_alloc(&taddr_s, p.tmem_cols);
-    tmem_relinquish();
-    tc_fence_before();
-  }
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t taddr = taddr_s;
-  griddep_wait();
-  griddep_launch_dependents();
-  const int64_t total = g.kpre[g.E];
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * total / gridDim.x;
-  const int64_t i1 = static_cast<int64_t>(blockIdx.x + 1) * total / gridDim.x;
-  const int G = 1 << g.log2G;
-  const uint32_t half_q = p.q_bytes / 2;
-
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      prefetch_tensormap(&kmap);
-      prefetch_tensormap(&qhmap);
-      prefetch_tensormap(&qlmap);
-      const uint64_t keep = policy_evict_last();
-      uint32_t k = 0, qi = 0;
-      bool ok = true;
-      KWalk walk(g, i0, i1);
-      KItem x;
-      while (ok && walk.next(&x)) {
-        const int qs = static_cast<int>(qi % p.nq);
-        if (qi >= static_cast<uint32_t>(p.nq) && !mbar_wait(&qempty[qs], ((qi / p.nq) - 1) & 1)) { ok = false; break; }
-        const int cols = x.nrow << g.log2G;
-        const int nbox = (cols + p.qbox - 1) / p.qbox;
-        const int rows_box = p.qbox >> g.log2G;
-        uint8_t* qd = qslot + static_cast<size_t>(qs) * p.q_bytes;
-        mbar_arrive_expect_tx(&qfull[qs], static_cast<uint32_t>(2 * p.kb * nbox * p.qbox) * 128u);
-        for (int a = 0; a < p.kb; ++a)
-          for (int b = 0; b < nbox; ++b) {
-            const uint32_t o = static_cast<uint32_t>(a * g.ncol + b * p.qbox) * 128u;
-            tma_load_3d(qd + o, &qhmap, a * 64, x.j << g.log2G, x.row0 + b * rows_box, &qfull[qs], keep);
-            tma_load_3d(qd + half_q + o, &qlmap, a * 64, x.j << g.log2G, x.row0 + b * rows_box, &qfull[qs], keep);
-          }
-        ++qi;
-        const int32_t* trow = p.tables + static_cast<size_t>(x.en.tab) * g.MB + x.en.page0;
-        for (int t = x.t0; t < x.t1; t += 128, ++k) {
-          const int s = static_cast<int>(k % S);
-          if (k >= static_cast<uint32_t>(S) && !mbar_wait(&empty[s], ((k / S) - 1) & 1)) { ok = false; break; }
-          const int np = (min(128, x.t1 - t) + kBlock - 1) / kBlock;
-          uint8_t* st = smem + static_cast<size_t>(s) * p.a_bytes;
-          mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(np * p.kb) * 2048u);
-          for (int c = 0; c < np; ++c) {
-            int32_t phys = trow[t / kBlock + c];
-            if (phys < 0 || phys >= g.NB) { set_flag(g.status, STARKV_FLAG_BAD_BLOCK_ID); phys = 0; }
-            for (int a = 0; a < p.kb; ++a)
-              tma_load_3d(st + a * 16384 + c * 2048, &kmap, a * 64, x.j, phys * kBlock, &full[s], keep);
-          }
-        }
-      }
-      if (!ok) {
-        set_timeout(g.status, kSiteKEmpty);
-        abort_flag = 1;
-      }
-      // copies still in flight land before the CTA can exit
-      const uint32_t f0 = k >= static_cast<uint32_t>(S) ? k - S : 0u;
-      for (uint32_t kk = f0; kk < k; ++kk) mbar_wait(&full[kk % S], (kk / S) & 1);
-      const uint32_t q0 = qi >= static_cast<uint32_t>(p.nq) ? qi - p.nq : 0u;
-      for (uint32_t kk = q0; kk < qi; ++kk) mbar_wait(&qfull[kk % p.nq], (kk / p.nq) & 1);
-    }
-  } else if (warp == 1) {
-    // ----------------------------------------------------------------- MMA
-    if (lane == 0) {
-      uint32_t k = 0, qi = 0;
-      bool ok = true;
-      KWalk walk(g, i0, i1);
-      KItem x;
-      while (ok && walk.next(&x)) {
-        const int qs = static_cast<int>(qi % p.nq);
-        if (!mbar_wait(&qfull[qs], (qi / p.nq) & 1)) { ok = false; break; }
-        const int nmma = ((x.nrow << g.log2G) + 15) / 16 * 16;
-        const uint32_t idesc = idesc_f16_f32(128, nmma, /*a_mn_major=*/false, /*b_mn_major=*/false);
-        const uint32_t sq = smem_u32(qslot + static_cast<size_t>(qs) * p.q_bytes);
-        for (int t = x.t0; t < x.t1; t += 128, ++k) {
-          const int s = static_cast<int>(k % S), a = static_cast<int>(k % kGKAcc);
-          if (k >= kGKAcc && !mbar_wait(&tempty[a], ((k / kGKAcc) - 1) & 1)) { ok = false; break; }
-          if (!mbar_wait(&full[s], (k / S) & 1) || abort_flag) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smem + static_cast<size_t>(s) * p.a_bytes);
-          const uint32_t dst = taddr + static_cast<uint32_t>(a * g.ncol);
-          for (int ks = 0; ks < p.ksteps; ++ks) {
-            const uint32_t blk = ks >> 2, off = (ks & 3) * 32u;
-            const uint64_t ad = smem_desc(sa + blk * 16384u + off, 16u, 1024u, kSwizzle128B);
-            const uint32_t bo = sq + blk * static_cast<uint32_t>(g.ncol) * 128u + off;
-            umma_f16_ss(dst, ad, smem_desc(bo, 16u, 1024u, kSwizzle128B), idesc, ks > 0 ? 1u : 0u);
-            umma_f16_ss(dst, ad, smem_desc(bo + half_q, 16u, 1024u, kSwizzle128B), idesc, 1u);
-          }
-          umma_commit(&empty[s]);
-          umma_commit(&tfull[a]);
-        }
-        umma_commit(&qempty[qs]);
-        ++qi;
-      }
-      if (!ok) { set_timeout(g.status, kSiteKFull); abort_flag = 1; }
-      umma_commit(mmadone);
-      mbar_wait(mmadone, 0);
-    }
-  } else {
-    // ------------------------------------------------------------ epilogue
-    const int et = tid - 64;
-    const int q = warp & 3, hf = (warp - 2) >> 2;
-    const uint32_t tq = taddr + (static_cast<uint32_t>(q * 32) << 16);
-    uint32_t k = 0, phase = 0;
-    bool ok = true;
-    KWalk walk(g, i0, i1);
-    KItem x;
-    while (ok && walk.next(&x)) {
-      const int cols = x.nrow << g.log2G;
-      const int ncb = (cols + 15) / 16;
-      const int t_pad = g.t_pad[x.en.src];
-      __half* P = kWeights ? p.P[x.en.src] : nullptr;
-      // per column: its (row, head), token limit, maximum and P row
-      if (!group_sync(ebar, phase)) { ok = false; break; }
-      if (et < 128) {
-        const int row = x.row0 + (et >> g.log2G);
-        const bool live = et < cols;
-        const size_t rh = static_cast<size_t>(live ? row : x.row0) * g.H + (x.j << g.log2G) + (et & (G - 1));
-        s_lim[et] = live ? (x.en.src ? x.en.len : g.row_lim[row]) : 0;
-        s_off[et] = static_cast<int64_t>(rh) * t_pad;
-        s_m[et] = kWeights && live ? g.mrow[rh] : 0.f;
-      }
-      if (!group_sync(ebar, phase)) { ok = false; break; }
-      float run[4][16];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int u = 0; u < 16; ++u) run[i][u] = kWeights ? 0.f : -INFINITY;
-      for (int tb = x.t0; tb < x.t1; tb += 128, ++k) {
-        const int a = static_cast<int>(k % kGKAcc);
-        const bool ready = mbar_wait(&tfull[a], (k / kGKAcc) & 1);
-        if (!__all_sync(0xffffffffu, ready && !abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        const int t = tb + q * 32 + lane;
-        const bool all_in = tb + 128 <= x.en.minlim;   // no limit inside the block
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int cb = hf + 2 * i;
-          if (cb < ncb) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x16(tq + static_cast<uint32_t>(a * g.ncol + cb * 16), v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int u = 0; u < 16; ++u) {
-              const int c = cb * 16 + u;
-              const float s = __uint_as_float(v[u]);
-              const bool in = all_in || t < s_lim[c];
-              if constexpr (kWeights) {
-                const __half w = __float2half_rn(in ? ex2_approx(s - s_m[c]) : 0.f);
-                run[i][u] += __half2float(w);
-                if (c < cols) P[s_off[c] + t] = w;
-              } else {
-                run[i][u] = fmaxf(run[i][u], in ? s : -INFINITY);
-              }
-            }
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty[a]);
-      }
-      if (!ok) break;
-      if constexpr (kWeights) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int cb = hf + 2 * i;
-          if (cb < ncb) {
-            const float sum = lane_sum16(run[i], lane);
-            if ((lane & 1) == 0) s_red[q][cb * 16 + (lane >> 1)] = sum;
-          }
-        }
-        if (!group_sync(ebar, phase)) { ok = false; break; }
-        if (et < cols) {
-          const float L = ((s_red[0][et] + s_red[1][et]) + s_red[2][et]) + s_red[3][et];
-          const size_t rh = static_cast<size_t>(x.row0 + (et >> g.log2G)) * g.H + (x.j << g.log2G) + (et & (G - 1));
-          g.lpart[x.en.src][rh * g.n_ch[x.en.src] + x.c] = L;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int cb = hf + 2 * i;
-          if (cb < ncb) {
-            float mine = -INFINITY;
-#pragma unroll
-            for (int u = 0; u < 16; ++u) {
-              const float m = warp_max_f32(run[i][u]);
-              if (lane == u) mine = m;
-            }
-            const int c = cb * 16 + lane;
-            if (lane < 16 && c < cols && mine > -INFINITY) {
-              const size_t rh = static_cast<size_t>(x.row0 + (c >> g.log2G)) * g.H + (x.j << g.log2G) + (c & (G - 1));
-              atomic_max_f32(&g.mrow[rh], mine);
-            }
-          }
-        }
-      }
-    }
-    if (!ok) { set_timeout(g.status, kSiteKFull); abort_flag = 1; }
-  }
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(taddr, p.tmem_cols);
-  }
+// Shared-memory layout of the attend kernel (bytes from the 1024-aligned base).
+struct AttendSmem {
+  uint32_t v, q, k, p, mx, stat, bars, total;
+};
+__host__ __device__ __forceinline__ AttendSmem attend_smem(int ncap, int kb, int k_stages, int v_stages, uint32_t v_stage_bytes) {
+  AttendSmem s;
+  s.v = 0;
+  s.q = s.v + ((v_stages * v_stage_bytes + 1023u) & ~1023u);
+  s.k = s.q + static_cast<uint32_t>(kb * 2 * ncap) * 128u;
+  s.p = s.k + static_cast<uint32_t>(k_stages) * 16384u;
+  s.mx = s.p + 2u * static_cast<uint32_t>(ncap) * 256u;               // maxima of every CTA: [2][C][ncap]
+  s.stat = s.mx + 2u * kGAMaxC * static_cast<uint32_t>(ncap) * 4u;    // m [ncap], per quarter max [4][ncap], sum [4][ncap]
+  s.bars = s.stat + 9u * static_cast<uint32_t>(ncap) * 4u;
+  s.total = s.bars + 8u * static_cast<uint32_t>(2 * k_stages + 3 * v_stages + 32);
+  return s;
 }
 
-// ================================================================== V pass
-// Z^T (256 rows of R x up to 256 columns) += C_V^T . P^T over the tokens of an
-// entry, 64 tokens (4 pages) per stage: A = the pages' codes (MN-major, one TMA
-// box of 256 codes x 16 tokens per page), B = the P rows of the tile's (row,
-// head) columns (K-major).  A unit is one stage of one tile; the units of all
-// tiles are laid end to end and CTA i of n takes [floor(i U / n), floor((i+1)
-// U / n)).  The sum of a tile that begins in a CTA's range goes to the Z matrix
-// of its source, that of a tile carried over from the CTA before goes to the
-// CTA's carry slot, so a tile's partial sums have fixed places and order.
-struct GroupVParams {
-  GroupGeom g;
-  const int32_t* tables;
-  float* Z[2];          // [n_rows * H][R] by source
-  float* zcarry;        // [CTAs][256 columns][256]
-  int stages;
-  uint32_t stage_bytes;
-};
-
-constexpr int kGVThreads = 192;
-constexpr uint32_t kGVABytes = 4u * 8192u;         // 4 pages x 16 tokens x 256 codes
-constexpr uint32_t kGVBBytes = kGVTile * 128u;     // 256 columns x 64 tokens
-constexpr int kGVPBox = 32;                        // P rows per TMA box
-
-struct VSeg {
-  GroupEntry en;
-  int nt, rt, col0, ncols, n;    // column tile, R tile, first column, columns, UMMA N
-  int u0, u1;                    // units of the tile taken by this CTA
-  bool first, last;              // the tile begins / ends here
-};
-
-struct VWalk {
-  const GroupGeom& g;
-  int64_t u, end, ebeg, eend;
-  int32_t e;
-  GroupEntry en;
-  __device__ VWalk(const GroupGeom& g_, int64_t a, int64_t b) : g(g_), u(a), end(b), ebeg(0), eend(0), e(0) {
-    if (u < end) {
-      e = entry_of(g.vpre, g.E, u);
-      ebeg = g.vpre[e];
-      eend = g.vpre[e + 1];
-      en = g.ent[e];
-    }
-  }
-  __device__ bool next(VSeg* s) {
-    if (u >= end) return false;
-    while (u >= eend) { ++e; ebeg = eend; eend = g.vpre[e + 1]; if (u < eend) en = g.ent[e]; }
-    const int units = (en.len + kGVTok - 1) / kGVTok;
-    const int64_t local = u - ebeg;
-    const int64_t tile = local / units;
-    const int cols = en.nrows * g.H;
-    const int width = gv_width(cols, gv_tiles(cols));
-    s->en = en;
-    s->nt = static_cast<int>(tile / g.n_rt);
-    s->rt = static_cast<int>(tile % g.n_rt);
-    s->col0 = s->nt * width;
-    s->ncols = min(width, cols - s->col0);
-    s->n = (s->ncols + 15) / 16 * 16;
-    s->u0 = static_cast<int>(local - tile * units);
-    const int64_t left = end - u;
-    s->u1 = left < units - s->u0 ? s->u0 + static_cast<int>(left) : units;
-    s->first = s->u0 == 0;
-    s->last = s->u1 == units;
-    u += s->u1 - s->u0;
-    return true;
-  }
-};
-
-__global__ void __launch_bounds__(kGVThreads, 1)
-group_vpass_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap pmap0,
-                   const __grid_constant__ CUtensorMap pmap1, GroupVParams p) {
+__global__ void __launch_bounds__(kGAThreads, 1)
+group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                    const __grid_constant__ CUtensorMap qhmap0, const __grid_constant__ CUtensorMap qlmap0,
+                    const __grid_constant__ CUtensorMap qhmap1, const __grid_constant__ CUtensorMap qlmap1,
+                    GroupAttendParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
   const GroupGeom& g = p.g;
-  const int S = p.stages;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(S) * p.stage_bytes);
-  uint64_t* empty = full + S;
-  uint64_t* zdone = empty + S;     // a segment's products are complete
-  uint64_t* tfree = zdone + 1;     // its accumulator has been stored
-  uint64_t* fixreq = tfree + 1;    // a partly filled page has landed
-  uint64_t* fixed = fixreq + 1;    // its rows past the end are zero
-  uint64_t* mmadone = fixed + 1;
+  const AttendSmem lay = attend_smem(g.ncap, p.kb, p.k_stages, p.v_stages, p.v_stage_bytes);
+  const int KS = p.k_stages, VS = p.v_stages, C = g.C, ncap = g.ncap;
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + lay.bars);
+  uint64_t* kempty = kfull + KS;
+  uint64_t* vfull = kempty + KS;
+  uint64_t* vempty = vfull + VS;
+  uint64_t* vfix = vempty + VS;       // [VS] the stage's partly filled page has been zeroed behind its end
+  uint64_t* qfull = vfix + VS;
+  uint64_t* qempty = qfull + 1;
+  uint64_t* tfull = qempty + 1;       // [2] logits ready
+  uint64_t* tempty = tfull + 2;       // [2] logits read
+  uint64_t* pfull = tempty + 2;       // [2] weights of a block complete, from all CTAs
+  uint64_t* pempty = pfull + 2;       // [2] weights consumed, by all CTAs
+  uint64_t* mxbar = pempty + 2;       // [2] maxima of all CTAs
+  uint64_t* zdone = mxbar + 2;
+  uint64_t* zfree = zdone + 1;
+  uint64_t* sdone = zfree + 1;        // every S / Z product issued has completed
+  uint64_t* mdone = sdone + 1;
+  uint64_t* ebar = mdone + 1;
+  float* s_mx = reinterpret_cast<float*>(smem + lay.mx);
+  float* s_m = reinterpret_cast<float*>(smem + lay.stat);
+  float* s_qmax = s_m + ncap;
+  float* s_qsum = s_qmax + 4 * ncap;
   __shared__ uint32_t taddr_s;
   __shared__ volatile int32_t abort_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int c = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   if (tid == 0) {
-    for (int s = 0; s < S; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int s = 0; s < KS; ++s) { mbar_init(&kfull[s], 1); mbar_init(&kempty[s], 1); }
+    for (int s = 0; s < VS; ++s) { mbar_init(&vfull[s], 1); mbar_init(&vempty[s], 1); mbar_init(&vfix[s], 1); }
+    mbar_init(qfull, 1);
+    mbar_init(qempty, 1);
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], kGAEpi / 32);
+      mbar_init(&pfull[a], 1);
+      mbar_init(&pempty[a], C);
+      mbar_init(&mxbar[a], 1);
+    }
     mbar_init(zdone, 1);
-    mbar_init(tfree, 4);
-    mbar_init(fixreq, 1);
-    mbar_init(fixed, 128);
-    mbar_init(mmadone, 1);
+    mbar_init(zfree, kGAEpi / 32);
+    mbar_init(sdone, 1);
+    mbar_init(mdone, 1);
+    mbar_init(ebar, kGAEpi);
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -684,160 +483,406 @@ group_vpass_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_consta
     tc_fence_before();
   }
   __syncthreads();
+  if (C > 1) cluster_sync();     // every CTA's barriers exist before anyone signals them
   tc_fence_after();
   const uint32_t taddr = taddr_s;
   griddep_wait();
   griddep_launch_dependents();
   Partition pt;
-  pt.P = g.vpre[g.E];
-  pt.G = static_cast<int32_t>(pt.P < gridDim.x ? pt.P : gridDim.x);
-  const int cta = blockIdx.x;
-  const bool live = cta < pt.G;
-  const int64_t u0 = live ? part_begin(cta, pt) : 0, u1 = live ? part_begin(cta + 1, pt) : 0;
+  pt.P = g.pre[g.E];
+  pt.G = static_cast<int32_t>(gridDim.x);   // clusters lie along y
+  const int cl = blockIdx.x;
+  const int64_t x0 = part_begin(cl, pt), x1 = part_begin(cl + 1, pt);
 
   if (warp == 0) {
-    // ------------------------------------------------------------ producer
+    // ------------------------------------------------------- q~ and K tiles
     if (lane == 0) {
-      prefetch_tensormap(&vmap);
-      prefetch_tensormap(&pmap0);
-      prefetch_tensormap(&pmap1);
-      const uint64_t pol_once = policy_evict_first(), pol_keep = policy_evict_last();
-      uint32_t k = 0;
+      prefetch_tensormap(&kmap);
+      prefetch_tensormap(&qhmap0);
+      prefetch_tensormap(&qlmap0);
+      const uint64_t keep = policy_evict_last();
+      uint32_t k = 0, seg = 0;
       bool ok = true;
-      VWalk walk(g, u0, u1);
-      VSeg x;
+      SegWalk walk(g, x0, x1);
+      Segment x;
       while (ok && walk.next(&x)) {
-        const int32_t* trow = p.tables + static_cast<size_t>(x.en.tab) * g.MB + x.en.page0;
-        const int nbox = (x.n + kGVPBox - 1) / kGVPBox;
-        const int prow = x.en.row0 * g.H + x.col0;
-        const uint64_t pol = x.en.src ? pol_once : pol_keep;
-        for (int u = x.u0; u < x.u1; ++u, ++k) {
-          const int s = static_cast<int>(k % S);
-          if (k >= static_cast<uint32_t>(S) && !mbar_wait(&empty[s], ((k / S) - 1) & 1)) { ok = false; break; }
-          const int t0 = u * kGVTok;
-          const int np = (min(kGVTok, x.en.len - t0) + kBlock - 1) / kBlock;
-          uint8_t* st = smem + static_cast<size_t>(s) * p.stage_bytes;
-          mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(np) * 8192u + static_cast<uint32_t>(nbox) * kGVPBox * 128u);
-          for (int c = 0; c < np; ++c) {
-            int32_t phys = trow[t0 / kBlock + c];
-            if (phys < 0 || phys >= g.NB) { set_flag(g.status, STARKV_FLAG_BAD_BLOCK_ID); phys = 0; }
-            tma_load_3d(st + c * 8192, &vmap, 0, phys * kBlock, x.rt * 4, &full[s], pol);
+        if (seg > 0 && !mbar_wait(qempty, (seg - 1) & 1)) { ok = false; break; }
+        ++seg;
+        const int nbox = (x.ncols + kGAQBox - 1) / kGAQBox;
+        const int row = x.en.row0 * g.H + x.col0;
+        mbar_arrive_expect_tx(qfull, static_cast<uint32_t>(2 * p.kb * nbox * kGAQBox) * 128u);
+        for (int a = 0; a < p.kb; ++a)
+          for (int b = 0; b < nbox; ++b) {
+            uint8_t* d = smem + lay.q + static_cast<uint32_t>(a * ncap + b * kGAQBox) * 128u;
+            tma_load_2d(d, x.en.src ? &qhmap1 : &qhmap0, a * 64, row + b * kGAQBox, qfull, keep);
+            tma_load_2d(d + static_cast<uint32_t>(p.kb * ncap) * 128u, x.en.src ? &qlmap1 : &qlmap0, a * 64,
+                        row + b * kGAQBox, qfull, keep);
           }
-          for (int b = 0; b < nbox; ++b)
-            tma_load_2d(st + kGVABytes + b * kGVPBox * 128, x.en.src ? &pmap1 : &pmap0, t0, prow + b * kGVPBox, &full[s],
-                        pol);
-        }
+        const int32_t* trow = p.tables + static_cast<size_t>(x.en.tab) * g.MB + x.en.page0;
+        const int units = (x.b1 - x.b0) * x.nh;
+        for (int pass = 0; pass < 2 && ok; ++pass)
+          for (int i = c; i < units && ok; i += C) {
+            const int b = x.b0 + i / x.nh, j = x.j0 + i % x.nh;
+            const int np = (min(kGTok, x.en.len - b * kGTok) + kBlock - 1) / kBlock;
+            for (int a = 0; a < p.kb; ++a, ++k) {
+              const int s = static_cast<int>(k % KS);
+              if (k >= static_cast<uint32_t>(KS) && !mbar_wait(&kempty[s], ((k / KS) - 1) & 1)) { ok = false; break; }
+              uint8_t* st = smem + lay.k + s * 16384u;
+              mbar_arrive_expect_tx(&kfull[s], static_cast<uint32_t>(np) * 2048u);
+              for (int t = 0; t < np; ++t) {
+                int32_t phys = trow[b * (kGTok / kBlock) + t];
+                if (phys < 0 || phys >= g.NB) { set_flag(g.status, STARKV_FLAG_BAD_BLOCK_ID); phys = 0; }
+                tma_load_3d(st + t * 2048, &kmap, a * 64, j, phys * kBlock, &kfull[s], keep);
+              }
+            }
+          }
       }
+      if (!ok) {
+        set_timeout(g.status, kSiteKEmpty);
+        abort_flag = 1;
+      }
+      // copies still in flight land before the CTA can exit
+      for (uint32_t i = k >= static_cast<uint32_t>(KS) ? k - KS : 0u; i < k; ++i) mbar_wait(&kfull[i % KS], (i / KS) & 1);
+      if (seg > 0) mbar_wait(qfull, (seg - 1) & 1);
+    }
+  } else if (warp == 1) {
+    // ----------------------------------------------------------- S products
+    if (lane == 0) {
+      uint32_t k = 0, seg = 0, u = 0;
+      bool ok = true;
+      SegWalk walk(g, x0, x1);
+      Segment x;
+      while (ok && walk.next(&x)) {
+        if (!mbar_wait(qfull, seg & 1)) { ok = false; break; }
+        ++seg;
+        const int units = (x.b1 - x.b0) * x.nh;
+        for (int pass = 0; pass < 2 && ok; ++pass)
+          for (int i = c; i < units && ok; i += C, ++u) {
+            // the head's columns, widened to whole groups of eight q~ rows
+            const int f = (i % x.nh) * x.mt, w0 = f & ~7;
+            const int n = (f + x.mt - w0 + 15) / 16 * 16;
+            const uint32_t idesc = idesc_f16_f32(128, n, /*a_mn_major=*/false, /*b_mn_major=*/false);
+            const int a = u & 1;
+            if (u >= 2 && !mbar_wait(&tempty[a], ((u / 2) - 1) & 1)) { ok = false; break; }
+            const uint32_t dst = taddr + 256u + a * 128u;
+            int ks = 0;
+            for (int kbi = 0; kbi < p.kb; ++kbi, ++k) {
+              const int s = static_cast<int>(k % KS);
+              if (!mbar_wait(&kfull[s], (k / KS) & 1) || abort_flag) { ok = false; break; }
+              tc_fence_after();
+              const uint32_t sa = smem_u32(smem + lay.k + s * 16384u);
+              const uint32_t sq = smem_u32(smem + lay.q) + static_cast<uint32_t>(kbi * ncap + w0) * 128u;
+              for (int kk = 0; kk < 4 && ks < p.ksteps; ++kk, ++ks) {
+                const uint64_t ad = smem_desc(sa + kk * 32u, 16u, 1024u, kSwizzle128B);
+                const uint32_t bo = sq + kk * 32u;
+                umma_f16_ss(dst, ad, smem_desc(bo, 16u, 1024u, kSwizzle128B), idesc, ks > 0 ? 1u : 0u);
+                umma_f16_ss(dst, ad, smem_desc(bo + static_cast<uint32_t>(p.kb * ncap) * 128u, 16u, 1024u, kSwizzle128B),
+                            idesc, 1u);
+              }
+              umma_commit(&kempty[s]);
+            }
+            if (ok) umma_commit(&tfull[a]);
+          }
+        umma_commit(qempty);
+      }
+      if (!ok) { set_timeout(g.status, kSiteKFull); abort_flag = 1; }
+      umma_commit(sdone);
+      if (!mbar_wait(sdone, 0)) set_timeout(g.status, kSiteVMdone);
+    }
+  } else if (warp == 2) {
+    // -------------------------------------------------------------- V tiles
+    // The whole warp walks; lane 0 issues the copies.  A page that the entry's
+    // end leaves partly filled is zeroed behind it, so that whatever its unused
+    // slots hold contributes exactly 0.
+    if (lane == 0) prefetch_tensormap(&vmap);
+    const uint64_t pol_once = policy_evict_first(), pol_keep = policy_evict_last();
+    uint32_t k = 0;
+    bool ok = true;
+    SegWalk walk(g, x0, x1);
+    Segment x;
+    while (ok && walk.next(&x)) {
+      const int32_t* trow = p.tables + static_cast<size_t>(x.en.tab) * g.MB + x.en.page0;
+      const int chunk0 = (x.slab * C + c) * g.nch;
+      const uint64_t pol = x.en.src ? pol_once : pol_keep;
+      const int tend = min(x.en.len, x.b1 * kGTok);
+      for (int t0 = x.b0 * kGTok; t0 < tend && ok; t0 += kGAVTok, ++k) {
+        const int s = static_cast<int>(k % VS);
+        const int nt = min(kGAVTok, tend - t0), np = (nt + kBlock - 1) / kBlock;
+        uint8_t* st = smem + lay.v + static_cast<size_t>(s) * p.v_stage_bytes;
+        if (lane == 0) {
+          if (k >= static_cast<uint32_t>(VS) && !mbar_wait(&vempty[s], ((k / VS) - 1) & 1)) {
+            ok = false;
+          } else {
+            mbar_arrive_expect_tx(&vfull[s], static_cast<uint32_t>(np * g.nch) * 2048u);
+            for (int t = 0; t < np; ++t) {
+              int32_t phys = trow[t0 / kBlock + t];
+              if (phys < 0 || phys >= g.NB) { set_flag(g.status, STARKV_FLAG_BAD_BLOCK_ID); phys = 0; }
+              tma_load_3d(st + t * g.nch * 2048, &vmap, 0, phys * kBlock, chunk0, &vfull[s], pol);
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        const int ntl = nt & (kBlock - 1);
+        if (ok && ntl) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&vfull[s], (k / VS) & 1))) { ok = false; break; }
+          uint8_t* pg = st + (np - 1) * g.nch * 2048;
+          const int nz = kBlock - ntl;
+          for (int y = lane; y < g.nch * nz * 8; y += 32) {
+            const int ch = y / (nz * 8), rem = y % (nz * 8);
+            *reinterpret_cast<uint4*>(pg + ch * 2048 + (ntl + rem / 8) * 128 + (rem % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (ok && lane == 0) mbar_arrive(&vfix[s]);
+      }
+    }
+    if (lane == 0) {
       if (!ok) {
         set_timeout(g.status, kSiteVEmpty);
         abort_flag = 1;
       }
-      const uint32_t f0 = k >= static_cast<uint32_t>(S) ? k - S : 0u;
-      for (uint32_t kk = f0; kk < k; ++kk) mbar_wait(&full[kk % S], (kk / S) & 1);
+      for (uint32_t i = k >= static_cast<uint32_t>(VS) ? k - VS : 0u; i < k; ++i) mbar_wait(&vfull[i % VS], (i / VS) & 1);
     }
-  } else if (warp == 1) {
-    // ----------------------------------------------------------------- MMA
+  } else if (warp == 3) {
+    // ----------------------------------------------------------- Z products
     if (lane == 0) {
-      uint32_t k = 0, seg = 0, fix = 0;
+      uint32_t k = 0, seg = 0, blk = 0;
       bool ok = true;
-      VWalk walk(g, u0, u1);
-      VSeg x;
+      SegWalk walk(g, x0, x1);
+      Segment x;
       while (ok && walk.next(&x)) {
-        const uint32_t idesc = idesc_f16_f32(128, x.n, /*a_mn_major=*/true, /*b_mn_major=*/false);
-        const int mts = x.rt * kGVTile + 128 < g.R ? 2 : 1;
-        if (seg > 0 && !mbar_wait(tfree, (seg - 1) & 1)) { ok = false; break; }
-        uint32_t acc = 0;
-        for (int u = x.u0; u < x.u1; ++u, ++k) {
-          const int s = static_cast<int>(k % S);
-          if (!mbar_wait(&full[s], (k / S) & 1) || abort_flag) { ok = false; break; }
-          const int nt = min(kGVTok, x.en.len - u * kGVTok);
-          if (nt & (kBlock - 1)) {   // a page that ends inside: its rows past the end are zeroed first
-            mbar_arrive(fixreq);
-            if (!mbar_wait(fixed, fix & 1)) { ok = false; break; }
-            ++fix;
-          }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smem + static_cast<size_t>(s) * p.stage_bytes);
-          const int np = (nt + kBlock - 1) / kBlock;
-          for (int c = 0; c < np; ++c) {
-            const uint64_t bd = smem_desc(sa + kGVABytes + c * 32u, 16u, 1024u, kSwizzle128B);
-            for (int m = 0; m < mts; ++m)
-              umma_f16_ss(taddr + m * 256u, smem_desc(sa + c * 8192u + m * 4096u, 2048u, 1024u, kSwizzle128B), bd, idesc,
-                          acc);
-            acc = 1;
-          }
-          umma_commit(&empty[s]);
-        }
-        if (!ok) break;
-        umma_commit(zdone);
+        const int n = (x.ncols + 15) / 16 * 16;
+        const uint32_t idesc = idesc_f16_f32(128, n, /*a_mn_major=*/true, /*b_mn_major=*/false);
+        const int codes = g.R - (x.slab * C + c) * g.nch * 64;          // codes of R left for this CTA
+        const int mts = (min(codes, g.nch * 64) + 127) / 128;           // 128-row tiles (<= 0: none)
+        if (seg > 0 && !mbar_wait(zfree, (seg - 1) & 1)) { ok = false; break; }
         ++seg;
+        uint32_t acc = 0;
+        for (int b = x.b0; b < x.b1 && ok; ++b, ++blk) {
+          const int a = blk & 1;
+          if (!mbar_wait(&pfull[a], (blk / 2) & 1) || abort_flag) { ok = false; break; }
+          const uint32_t sp = smem_u32(smem + lay.p) + a * static_cast<uint32_t>(ncap) * 256u;
+          const int nt = min(kGTok, x.en.len - b * kGTok);
+          for (int t = 0; t < nt; t += kGAVTok, ++k) {
+            const int s = static_cast<int>(k % VS);
+            if (!mbar_wait(&vfull[s], (k / VS) & 1) || !mbar_wait(&vfix[s], (k / VS) & 1) || abort_flag) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t sv = smem_u32(smem + lay.v + static_cast<size_t>(s) * p.v_stage_bytes);
+            const int np = (min(kGAVTok, nt - t) + kBlock - 1) / kBlock;
+            for (int pg = 0; pg < np; ++pg) {
+              const int tk = t + pg * kBlock;
+              const uint64_t bd = smem_desc(sp + (tk >> 6) * static_cast<uint32_t>(ncap) * 128u + (tk & 63) * 2u, 16u, 1024u,
+                                            kSwizzle128B);
+              for (int m = 0; m < mts; ++m)
+                umma_f16_ss(taddr + m * 128u, smem_desc(sv + pg * g.nch * 2048u + m * 4096u, 2048u, 1024u, kSwizzle128B), bd,
+                            idesc, acc);
+              acc = 1;
+            }
+            umma_commit(&vempty[s]);
+          }
+          if (!ok) break;
+          if (C > 1) umma_commit_multicast(&pempty[a], static_cast<uint16_t>((1u << C) - 1u));
+          else umma_commit(&pempty[a]);
+        }
+        if (ok) umma_commit(zdone);
       }
       if (!ok) { set_timeout(g.status, kSiteVFull); abort_flag = 1; }
-      umma_commit(mmadone);
-      if (!mbar_wait(mmadone, 0)) set_timeout(g.status, kSiteVMdone);
+      umma_commit(mdone);
+      if (!mbar_wait(mdone, 0)) set_timeout(g.status, kSiteVMdone);
     }
   } else {
-    // ------------------------------------------------------------ epilogue
-    const int et = tid - 64, q = warp & 3, i4 = lane & 3;
-    uint32_t seg = 0, fix = 0, k = 0;
-    const uint64_t keep = policy_evict_last();   // partial sums: read back by the combine kernel
-    VWalk walk(g, u0, u1);
-    VSeg x;
-    while (walk.next(&x)) {
-      k += static_cast<uint32_t>(x.u1 - x.u0);
-      const int ntl = x.en.len & (kBlock - 1);
-      if (x.last && ntl) {
-        if (!__all_sync(0xffffffffu, mbar_wait(fixreq, fix & 1))) { set_timeout(g.status, kSiteVPready); abort_flag = 1; break; }
-        ++fix;
-        const int c = ((x.en.len - 1) / kBlock) & 3;
-        uint8_t* pg = smem + static_cast<size_t>((k - 1) % S) * p.stage_bytes + c * 8192;
-        const int nz = kBlock - ntl;
-        for (int y = et; y < 4 * nz * 8; y += 128) {
-          const int ch = y / (nz * 8), rem = y % (nz * 8);
-          *reinterpret_cast<uint4*>(pg + ch * 2048 + (ntl + rem / 8) * 128 + (rem % 8) * 16) = make_uint4(0, 0, 0, 0);
+    // -------------------------------------------- maxima, weights, Z stores
+    const int et = tid - 128;
+    const int q = warp & 3, hf = (warp - 4) >> 2;     // TMEM lane quarter; which blocks of 16 columns
+    const uint32_t tq = taddr + (static_cast<uint32_t>(q * 32) << 16);
+    const uint64_t keep = policy_evict_last();
+    uint32_t u = 0, seg = 0, blk = 0, phase = 0;
+    bool ok = true;
+    SegWalk walk(g, x0, x1);
+    Segment x;
+    while (ok && walk.next(&x)) {
+      const int units = (x.b1 - x.b0) * x.nh;
+      for (int y = et; y < 4 * ncap; y += kGAEpi) { s_qmax[y] = -INFINITY; s_qsum[y] = 0.f; }
+      if (!group_sync(ebar, phase)) { ok = false; break; }
+      // ---- phase A
+      for (int i = c; i < units; i += C, ++u) {
+        const int a = u & 1;
+        const bool ready = mbar_wait(&tfull[a], (u / 2) & 1);
+        if (!__all_sync(0xffffffffu, ready && !abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const int f = (i % x.nh) * x.mt, w0 = f & ~7, fe = f + x.mt;
+        // all ones for a token of the entry; a mask and not a condition, so that no
+        // loop around the warp-wide loads below is split by lane
+        const uint32_t in = (x.b0 + i / x.nh) * kGTok + q * 32 + lane < x.en.len ? 0xffffffffu : 0u;
+        for (int cb = w0 + hf * 16; cb < fe; cb += 32) {
+          __syncwarp();
+          uint32_t v[32];
+          tmem_ld_32x32b_x16(tq + 256u + a * 128u + (cb - w0), v);
+          tmem_ld_wait();
+          float mine = -INFINITY;
+#pragma unroll
+          for (int y = 0; y < 16; ++y) {
+            const float m = warp_max_f32(__uint_as_float((v[y] & in) | (~in & 0xff800000u)));   // -inf behind the end
+            if (lane == y) mine = m;
+          }
+          const int tc = cb + lane;
+          if (lane < 16 && tc >= f && tc < fe) s_qmax[q * ncap + tc] = fmaxf(s_qmax[q * ncap + tc], mine);
         }
-        fence_proxy_async_smem();
-        mbar_arrive(fixed);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[a]);
       }
-      if (!__all_sync(0xffffffffu, mbar_wait(zdone, seg & 1) && !abort_flag)) {
-        set_timeout(g.status, kSiteVZdone);
-        abort_flag = 1;
+      if (!ok) break;
+      if (!group_sync(ebar, phase)) { ok = false; break; }
+      // ---- the tile's maxima over all CTAs of the cluster
+      const int par = seg & 1;
+      float* mx = s_mx + par * kGAMaxC * ncap;
+      if (et < ncap)
+        mx[c * ncap + et] =
+            fmaxf(fmaxf(s_qmax[et], s_qmax[ncap + et]), fmaxf(s_qmax[2 * ncap + et], s_qmax[3 * ncap + et]));
+      if (C > 1) {
+        fence_proxy_async_smem();
+        if (!group_sync(ebar, phase)) { ok = false; break; }
+        if (et == 0) {
+          mbar_arrive_expect_tx(&mxbar[par], static_cast<uint32_t>((C - 1) * ncap) * 4u);
+          for (int o = 1; o < C; ++o) {
+            const uint32_t to = static_cast<uint32_t>(c + o < C ? c + o : c + o - C);
+            bulk_s2cluster(mx + c * ncap, to, static_cast<uint32_t>(ncap) * 4u, &mxbar[par]);
+          }
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(&mxbar[par], (seg / 2) & 1) && !abort_flag)) { ok = false; break; }
+      } else if (!group_sync(ebar, phase)) {
+        ok = false;
         break;
       }
       ++seg;
-      tc_fence_after();
-      float* dst;
-      size_t stride;
-      if (x.first) {
-        dst = p.Z[x.en.src] + (static_cast<size_t>(x.en.row0) * g.H + x.col0) * g.R + x.rt * kGVTile;
-        stride = g.R;
-      } else {
-        dst = p.zcarry + static_cast<size_t>(cta) * kGVTile * kGVTile;
-        stride = kGVTile;
+      if (et < ncap) {
+        float m = mx[et];
+        for (int o = 1; o < C; ++o) m = fmaxf(m, mx[o * ncap + et]);
+        s_m[et] = m;
       }
+      if (!group_sync(ebar, phase)) { ok = false; break; }
+      // ---- phase B
+      int i = c;
+      for (int b = x.b0; b < x.b1; ++b, ++blk) {
+        const int a2 = blk & 1;
+        if (blk >= 2) {
+          const bool free2 = mbar_wait(&pempty[a2], ((blk / 2) - 1) & 1);
+          if (!__all_sync(0xffffffffu, free2 && !abort_flag)) { ok = false; break; }
+        }
+        uint8_t* pb = smem + lay.p + a2 * static_cast<uint32_t>(ncap) * 256u;
+        const int t = q * 32 + lane;                          // token of the block
+        const uint32_t in = b * kGTok + t < x.en.len ? 0xffffffffu : 0u;
+        uint8_t* prow = pb + (t >> 6) * static_cast<uint32_t>(ncap) * 128u + (t & 7) * 2;
+        const uint32_t tchunk = static_cast<uint32_t>(t & 63) >> 3;
+        int own = 0;
+        const int stop = (b + 1 - x.b0) * x.nh;
+        for (; i < stop; i += C, ++u, ++own) {
+          const int a = u & 1;
+          const bool ready = mbar_wait(&tfull[a], (u / 2) & 1);
+          if (!__all_sync(0xffffffffu, ready && !abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const int f = (i % x.nh) * x.mt, w0 = f & ~7, fe = f + x.mt;
+          for (int cb = w0 + hf * 16; cb < fe; cb += 32) {
+            __syncwarp();
+            uint32_t v[32];
+            tmem_ld_32x32b_x16(tq + 256u + a * 128u + (cb - w0), v);
+            tmem_ld_wait();
+            float w[16];
+#pragma unroll
+            for (int y = 0; y < 16; ++y) {
+              const int tc = cb + y;
+              // a weight in (0, 1], rounded to fp16 for the products; the sum takes the rounded weights
+              const float e = ex2_approx(__uint_as_float(v[y]) - s_m[tc < ncap ? tc : 0]);
+              const __half hw = __float2half_rn(__uint_as_float(__float_as_uint(e) & in));   // 0 behind the end
+              w[y] = __half2float(hw);
+              if (tc >= f && tc < fe)
+                *reinterpret_cast<__half*>(prow + tc * 128 + ((tchunk ^ (static_cast<uint32_t>(tc) & 7u)) << 4)) = hw;
+            }
+            const float sum = lane_sum16(w, lane);
+            const int tc = cb + (lane >> 1);
+            if ((lane & 1) == 0 && tc >= f && tc < fe) s_qsum[q * ncap + tc] += sum;
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[a]);
+          fence_proxy_async_smem();
+          if (!group_sync(ebar, phase)) { ok = false; break; }
+          // the unit's columns to the other CTAs, two halves of 64 tokens each: one
+          // lane of every warp takes the next destination
+          if (C > 1 && lane == 0) {
+            for (int o = warp - 3; o < C; o += kGAEpi / 32) {
+              const uint32_t to = static_cast<uint32_t>(c + o < C ? c + o : c + o - C);
+              bulk_s2cluster(pb + f * 128, to, static_cast<uint32_t>(x.mt) * 128u, &pfull[a2]);
+              bulk_s2cluster(pb + static_cast<uint32_t>(ncap) * 128u + f * 128, to, static_cast<uint32_t>(x.mt) * 128u,
+                             &pfull[a2]);
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        // armed after this CTA's own units: it now waits for the others' bytes only
+        if (et == 0) mbar_arrive_expect_tx(&pfull[a2], static_cast<uint32_t>((x.nh - own) * x.mt) * 256u);
+      }
+      if (!ok) break;
+      // ---- Z, m and l of the segment
+      const bool done = mbar_wait(zdone, (seg - 1) & 1);
+      if (!__all_sync(0xffffffffu, done && !abort_flag)) { ok = false; break; }
+      tc_fence_after();
+      const size_t idx = static_cast<size_t>(x.en.row0) * g.H + x.col0;     // the tile's first column
+      const size_t rh = static_cast<size_t>(g.n_rows) * g.H;
+      const int code0 = (x.slab * C + c) * g.nch * 64;
+      float* dst = (x.first ? p.Z[x.en.src] + idx * g.R : p.zcarry + static_cast<size_t>(cl) * ncap * g.R) + code0;
+      const int codes = min(g.R - code0, g.nch * 64);
+      const int i4 = lane & 3;
+      const int npad = (x.ncols + 15) / 16 * 16;
       for (int m = 0; m < 2; ++m) {
-        const int j0 = m * 128 + q * 32;                  // the warp's first row of the R tile
-        if (x.rt * kGVTile + j0 >= g.R) break;            // warp-uniform (R is a multiple of 64)
+        const int j0 = m * 128 + q * 32;
+        if (j0 >= codes) break;      // warp-uniform (codes is a multiple of 64)
         float* zq = dst + j0 + 4 * (lane >> 2);
-        for (int h0 = 0; h0 < x.n; h0 += 16) {
+        for (int h0 = hf * 16; h0 < npad; h0 += 32) {
+          __syncwarp();
           uint32_t v[32];
-          tmem_ld_32x32b_x16(taddr + (static_cast<uint32_t>(q * 32) << 16) + m * 256u + h0, v);
+          tmem_ld_32x32b_x16(tq + m * 128u + h0, v);
           tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float4 f = quad_transpose(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1]),
-                                            __uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3]), i4);
-            const int col = h0 + 4 * c + i4;
-            if (col < x.ncols) st_global_hint_free(reinterpret_cast<float4*>(zq + col * stride), f, keep);
+          for (int y = 0; y < 4; ++y) {
+            const float4 z = quad_transpose(__uint_as_float(v[4 * y]), __uint_as_float(v[4 * y + 1]),
+                                            __uint_as_float(v[4 * y + 2]), __uint_as_float(v[4 * y + 3]), i4);
+            const int col = h0 + 4 * y + i4;
+            if (col < x.ncols) st_global_hint_free(reinterpret_cast<float4*>(zq + static_cast<size_t>(col) * g.R), z, keep);
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(tfree);
+      if (lane == 0) mbar_arrive(zfree);
+      if (et < x.ncols) {
+        const float sum = ((s_qsum[et] + s_qsum[ncap + et]) + s_qsum[2 * ncap + et]) + s_qsum[3 * ncap + et];
+        if (x.first) {
+          const size_t o = static_cast<size_t>(x.slab) * rh + idx + et;
+          p.l[x.en.src][o * C + c] = sum;
+          if (c == 0) p.m[x.en.src][o] = s_m[et];
+        } else {
+          const size_t o = static_cast<size_t>(cl) * ncap + et;
+          p.lcarry[o * C + c] = sum;
+          if (c == 0) p.mcarry[o] = s_m[et];
+        }
+      }
+      if (!group_sync(ebar, phase)) { ok = false; break; }   // the sums are read before the next segment clears them
     }
+    if (!ok) { set_timeout(g.status, kSiteVPready); abort_flag = 1; }
   }
   __syncthreads();
+  if (C > 1) {
+    cluster_sync();   // nobody leaves while others may still copy to it or signal it
+    if (abort_flag) { // after a timeout copies may still be on their way here
+      const uint64_t t0 = globaltimer_ns();
+      for (uint32_t i = 0; i < (1u << 20) && globaltimer_ns() - t0 < 50000; ++i) {}
+    }
+    cluster_sync();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(taddr, 512);
@@ -845,81 +890,95 @@ group_vpass_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_consta
 }
 
 // ================================================================= combine
-// Z / L of every (row, head): the partial sums of its one or two entries in a
-// fixed order, as fp16 hi + lo halves (about 22 bits).  One warp per (row,
-// head, 256-code tile of R).  A row without tokens gives zeros.
+// Z / L of every (row, head): with M the largest of its segments' maxima, the
+// segments' sums scaled by exp2(m - M) and added in a fixed order, as fp16 hi +
+// lo halves (about 22 bits).  One warp per (row, head, 256 codes of R).  A row
+// without tokens gives zeros.
 struct GroupCombineParams {
   GroupGeom g;
   const float* Z[2];
+  const float* m[2];
+  const float* l[2];
   const float* zcarry;
+  const float* mcarry;
+  const float* lcarry;
   __half* zh;            // [n_rows * H][R]
   __half* zl;
-  int v_grid;
+  int clusters;
 };
-
-__device__ __forceinline__ void add_partials(const GroupGeom& g, const Partition& pt, int e, const GroupEntry& en, int row,
-                                             int h, int rt, const float* Z, const float* zcarry, int lane, float (&acc)[8]) {
-  const int cols = en.nrows * g.H, nt = gv_tiles(cols), width = gv_width(cols, nt);
-  const int col = (row - en.row0) * g.H + h;
-  const int units = (en.len + kGVTok - 1) / kGVTok;
-  const int tile = col / width;
-  const int64_t a = g.vpre[e] + (static_cast<int64_t>(tile) * g.n_rt + rt) * units;
-  const int32_t i0 = part_owner(a, pt), i1 = part_owner(a + units - 1, pt);
-  const float* src = Z + (static_cast<size_t>(row) * g.H + h) * g.R + rt * kGVTile + lane * 8;
-  for (int32_t i = i0; i <= i1; ++i) {
-    const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + 4);
-    acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
-    acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
-    src = zcarry + (static_cast<size_t>(i + 1) * kGVTile + (col - tile * width)) * kGVTile + lane * 8;
-  }
-}
 
 __global__ void __launch_bounds__(256) group_combine_kernel(GroupCombineParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const GroupGeom& g = p.g;
   const int lane = threadIdx.x & 31;
+  const int n_rt = (g.R + 255) / 256;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (w >= static_cast<int64_t>(g.n_rows) * g.H * g.n_rt) return;
-  const int rt = static_cast<int>(w % g.n_rt);
-  const int64_t rh = w / g.n_rt;
-  const int row = static_cast<int>(rh / g.H), h = static_cast<int>(rh % g.H);
+  const int64_t rh = static_cast<int64_t>(g.n_rows) * g.H;
+  if (w >= rh * n_rt) return;
+  const int code = static_cast<int>(w % n_rt) * 256 + lane * 8;
+  const int64_t rhi = w / n_rt;
+  const int row = static_cast<int>(rhi / g.H), h = static_cast<int>(rhi % g.H);
   const int e = g.row_ent[row];
-  if (e < 0) return;
+  if (e < 0 || code >= g.R) return;
   Partition pt;
-  pt.P = g.vpre[g.E];
-  pt.G = static_cast<int32_t>(pt.P < p.v_grid ? pt.P : p.v_grid);
+  pt.P = g.pre[g.E];
+  pt.G = p.clusters;
+  const int slab = code / (g.C * g.nch * 64);
+  const int j = h >> g.log2G;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  float L = 0.f;
-  const bool in = rt * kGVTile + lane * 8 < g.R;
-  const int n_src = g.shared ? 2 : 1;
-  for (int s = 0; s < n_src; ++s) {
+  float M = -INFINITY, L = 0.f;
+  for (int s = 0; s < (g.shared ? 2 : 1); ++s) {
+    if (s == 0 && !g.row_use[row]) continue;
     const int es = s ? g.n_groups + row : e;
     const GroupEntry en = g.ent[es];
     if (en.len == 0) continue;
-    const int nc = (en.len + g.chunk - 1) / g.chunk;
-    for (int c = lane; c < nc; c += 32) L += g.lpart[s][rh * g.n_ch[s] + c];
-    if (in) add_partials(g, pt, es, en, row, h, rt, p.Z[s], p.zcarry, lane, acc);
-  }
+    const TileShape ts = tile_shape(en.nrows, g);
+    const int within = ((row - en.row0) << g.log2G) + (h & ((1 << g.log2G) - 1));
+    int place;
+    const int ct = tile_of(ts, j, within, &place);
+    const size_t idx = static_cast<size_t>(en.row0) * g.H + static_cast<size_t>(j) * ts.m + within;
+    const int64_t blocks = entry_blocks(en), wt = g.weight[s];
+    const int64_t first = g.pre[es] + (static_cast<int64_t>(ct) * g.n_slab + slab) * blocks * wt;
+    const int32_t i0 = part_owner(first, pt), i1 = part_owner(first + (blocks - 1) * wt, pt);
+    for (int32_t i = i0; i <= i1; ++i) {
+      // clusters whose range holds no block's beginning have no segment
+      if (i > i0) {
+        const int64_t b = (part_begin(i, pt) - first + wt - 1) / wt;
+        if (first + b * wt >= part_begin(i + 1, pt)) continue;
+      }
+      const size_t o = i == i0 ? static_cast<size_t>(slab) * rh + idx : static_cast<size_t>(i) * (g.ncap) + place;
+      const float* zp = (i == i0 ? p.Z[s] + idx * g.R : p.zcarry + o * g.R) + code;
+      const float m = i == i0 ? p.m[s][o] : p.mcarry[o];
+      const float* lp = (i == i0 ? p.l[s] : p.lcarry) + o * g.C;
+      const float4 z0 = *reinterpret_cast<const float4*>(zp), z1 = *reinterpret_cast<const float4*>(zp + 4);
+      float l = 0.f;
+      for (int c = 0; c < g.C; ++c) l += lp[c];
+      // a segment whose logits are all NaN or -inf has m = -inf and l = NaN
+      const float Mn = fmaxf(M, m);
+      const float a = M > -INFINITY ? ex2_approx(M - Mn) : 1.f;
+      const float f = m > -INFINITY ? ex2_approx(m - Mn) : l;
+      L = L * a + l * f;
+      const float zz[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  if (!in) return;
-  // no token at all: every sum is 0 and so is the result
-  const bool none = g.row_lim[row] == 0 && (!g.shared || g.ent[g.n_groups + row].len == 0);
-  const float il = none ? 0.f : 1.f / L;
+      for (int u = 0; u < 8; ++u) acc[u] = acc[u] * a + zz[u] * f;
+      M = Mn;
+    }
+  }
+  const float il = L == 0.f ? 0.f : 1.f / L;   // no token at all: L = 0 and the result is 0
   uint4 hv, lv;
   uint32_t* hw = reinterpret_cast<uint32_t*>(&hv);
   uint32_t* lw = reinterpret_cast<uint32_t*>(&lv);
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const float z0 = none ? 0.f : acc[2 * u] * il, z1 = none ? 0.f : acc[2 * u + 1] * il;
+    const float z0 = acc[2 * u] * il, z1 = acc[2 * u + 1] * il;
     const __half2 hh = __floats2half2_rn(z0, z1);
     const float2 f = __half22float2(hh);
     const __half2 ll = __floats2half2_rn(z0 - f.x, z1 - f.y);
     hw[u] = *reinterpret_cast<const uint32_t*>(&hh);
     lw[u] = *reinterpret_cast<const uint32_t*>(&ll);
   }
-  const size_t o = static_cast<size_t>(rh) * g.R + rt * kGVTile + lane * 8;
+  const size_t o = static_cast<size_t>(rhi) * g.R + code;
   *reinterpret_cast<uint4*>(p.zh + o) = hv;
   *reinterpret_cast<uint4*>(p.zl + o) = lv;
 }

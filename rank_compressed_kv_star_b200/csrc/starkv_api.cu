@@ -1505,13 +1505,10 @@ bool encode_rows_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_
 
 struct GroupPlan {
   GroupGeom g;
-  // K pass
-  int kb, ksteps, qbox, nq, k_stages, k_ctas;
-  uint32_t a_bytes, q_bytes, k_tmem;
-  size_t k_smem;
-  // V pass
-  int v_stages, v_ctas;
-  size_t v_smem;
+  // attend
+  int kb, ksteps, k_stages, v_stages, clusters;
+  uint32_t v_stage_bytes;
+  size_t at_smem;
   // up-projection
   int up_mt, up_rows, up_tiles, up_npad, up_ks, up_kpc, up_stages;
   uint32_t up_stage_bytes, up_tmem;
@@ -1519,9 +1516,40 @@ struct GroupPlan {
   // absorption
   int abs_tile;
   // workspace
-  size_t ent_off, kpre_off, vpre_off, row_ent_off, row_lim_off, used_off, mrow_off, lpart_off[2], qh_off, ql_off,
-      p_off[2], z_off[2], carry_off, zh_off, zl_off, total;
+  size_t ent_off, pre_off, row_ent_off, row_use_off, used_off, qh_off[2], ql_off[2], z_off[2], m_off[2], l_off[2],
+      zcarry_off, mcarry_off, lcarry_off, zh_off, zl_off, total;
 };
+
+// Clusters of C CTAs of the attend kernel that the device holds at once.
+int max_attend_clusters(int C, size_t smem) {
+  static std::mutex mu;
+  static std::map<std::tuple<int, int, size_t>, int> known;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) { cudaGetLastError(); return device_sm_count() / C; }
+  std::lock_guard<std::mutex> lock(mu);
+  const auto key = std::make_tuple(dev, C, smem);
+  auto it = known.find(key);
+  if (it != known.end()) return it->second;
+  int n = 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(device_sm_count()), static_cast<unsigned>(C));
+  cfg.blockDim = dim3(kGAThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = static_cast<unsigned>(C);
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (!set_smem(group_attend_kernel, smem) ||
+      cudaOccupancyMaxActiveClusters(&n, group_attend_kernel, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return device_sm_count() / C;   // no device: the host-side sizes only
+  }
+  known[key] = n;
+  return n;
+}
 
 starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n_groups, int32_t n_rows,
                               int32_t max0, int32_t max1, GroupPlan* gp) {
@@ -1541,43 +1569,23 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
   g.n_rows = n_rows; g.n_groups = n_groups; g.shared = shared ? 1 : 0;
   g.E = n_groups + (shared ? n_rows : 0);
   g.max_len[0] = max0; g.max_len[1] = max1;
-  g.t_pad[0] = max0 > 0 ? (max0 + 127) / 128 * 128 : 128;
-  g.t_pad[1] = max1 > 0 ? (max1 + 127) / 128 * 128 : 128;
-  g.n_rt = (g.R + kGVTile - 1) / kGVTile;
+  g.weight[0] = 2; g.weight[1] = 3;
   const int sms = device_sm_count();
 
-  // K pass: 128 columns per tile, 64 where the query tile of a large rank would
-  // leave no room for a ring; two query slots where three stages still fit
+  // attend: slabs of at most 2048 codes of R, each over a cluster of CTAs of at
+  // most 256 codes; as many columns as the query tile and the P blocks leave room for
+  g.n_slab = (g.R + 2047) / 2048;
+  g.C = (g.R + 256 * g.n_slab - 1) / (256 * g.n_slab);
+  g.nch = (g.R / 64 + g.n_slab * g.C - 1) / (g.n_slab * g.C);
   p.kb = (g.r + 63) / 64;
   p.ksteps = (g.r + 15) / 16;
-  g.ncol = p.kb <= 2 ? 128 : 64;
-  p.qbox = G > 16 ? G : 16;
-  p.a_bytes = static_cast<uint32_t>(p.kb) * 16384u;
-  p.q_bytes = static_cast<uint32_t>(p.kb) * 2u * g.ncol * 128u;
-  const uint32_t budget = 200u * 1024u;
-  p.nq = budget >= 2u * p.q_bytes + 3u * p.a_bytes ? 2 : 1;
-  p.k_stages = static_cast<int>((budget - p.nq * p.q_bytes) / p.a_bytes);
-  if (p.k_stages > 8) p.k_stages = 8;
-  p.k_smem = 1024 + static_cast<size_t>(p.nq) * p.q_bytes + static_cast<size_t>(p.k_stages) * p.a_bytes +
-             (2 * p.k_stages + 4 + 2 * kGKAcc + 2) * sizeof(uint64_t);
-  p.k_tmem = static_cast<uint32_t>(kGKAcc * g.ncol);
-  p.k_ctas = sms;
-  {
-    // tokens per item: enough items for every CTA, each long enough to hide its start
-    const int per = g.ncol / G;
-    const int64_t tiles = n_groups + n_rows / per;
-    const int64_t blocks = (tiles < n_rows ? tiles : n_rows) * g.Hkv * (g.t_pad[0] / 128) +
-                           (shared ? static_cast<int64_t>(n_rows) * g.Hkv * (g.t_pad[1] / 128) : 0);
-    int64_t n = blocks / (4 * static_cast<int64_t>(sms));
-    n = n < 1 ? 1 : (n > 8 ? 8 : n);
-    g.chunk = static_cast<int>(n) * 128;
-  }
-  for (int s = 0; s < 2; ++s) g.n_ch[s] = (g.t_pad[s] + g.chunk - 1) / g.chunk;
-
-  // V pass: one CTA per SM, three 64 KiB stages
-  p.v_stages = 3;
-  p.v_ctas = sms;
-  p.v_smem = 1024 + static_cast<size_t>(p.v_stages) * (kGVABytes + kGVBBytes) + (2 * p.v_stages + 5) * sizeof(uint64_t);
+  g.ncap = p.kb == 1 ? 128 : (p.kb == 2 ? 64 : 32);
+  p.k_stages = p.kb < 2 ? 2 : (p.kb == 3 ? 6 : 4);
+  p.v_stage_bytes = static_cast<uint32_t>(g.nch) * 4096u;
+  p.v_stages = 5;
+  p.at_smem = 1024 + attend_smem(g.ncap, p.kb, p.k_stages, p.v_stages, p.v_stage_bytes).total;
+  if (p.at_smem > 227u * 1024u) return STARKV_ERR_UNSUPPORTED;
+  p.clusters = max_attend_clusters(g.C, p.at_smem);
 
   // up-projection
   p.up_mt = (g.d + 127) / 128;
@@ -1604,31 +1612,25 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
   size_t off = 256;   // the status word
   auto take = [&](size_t bytes) { const size_t o = off; off = align_up(off + bytes, 256); return o; };
   p.ent_off = take(static_cast<size_t>(g.E) * sizeof(GroupEntry));
-  p.kpre_off = take((static_cast<size_t>(g.E) + 1) * 8);
-  p.vpre_off = take((static_cast<size_t>(g.E) + 1) * 8);
+  p.pre_off = take((static_cast<size_t>(g.E) + 1) * 8);
   p.row_ent_off = take(N * 4);
-  p.row_lim_off = take(N * 4);
+  p.row_use_off = take(N * 4);
   p.used_off = take(4);
-  p.mrow_off = take(rh * 4);
-  p.qh_off = take(rh * g.r * 2);
-  p.ql_off = take(rh * g.r * 2);
   for (int s = 0; s < (shared ? 2 : 1); ++s) {
-    p.lpart_off[s] = take(rh * g.n_ch[s] * 4);
-    p.p_off[s] = take(rh * g.t_pad[s] * 2);
+    p.qh_off[s] = take(rh * g.r * 2);
+    p.ql_off[s] = take(rh * g.r * 2);
     p.z_off[s] = take(rh * g.R * 4);
+    p.m_off[s] = take(rh * g.n_slab * 4);
+    p.l_off[s] = take(rh * g.n_slab * g.C * 4);
   }
-  p.carry_off = take(static_cast<size_t>(p.v_ctas) * kGVTile * kGVTile * 4);
+  const size_t carry = static_cast<size_t>(p.clusters) * g.ncap;
+  p.zcarry_off = take(carry * g.R * 4);
+  p.mcarry_off = take(carry * 4);
+  p.lcarry_off = take(carry * g.C * 4);
   p.zh_off = take(rh * g.R * 2);
   p.zl_off = take(rh * g.R * 2);
   p.total = off;
   return STARKV_OK;
-}
-
-template <bool kWeights>
-cudaError_t launch_group_kpass(const GroupPlan& pl, const CUtensorMap& kmap, const CUtensorMap& qhmap,
-                               const CUtensorMap& qlmap, const GroupKParams& kp, cudaStream_t s) {
-  if (!set_smem(group_kpass_kernel<kWeights>, pl.k_smem)) return cudaErrorInvalidValue;
-  return launch(group_kpass_kernel<kWeights>, dim3(pl.k_ctas), dim3(kGKThreads), pl.k_smem, s, 1, kmap, qhmap, qlmap, kp);
 }
 
 starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_groups, int32_t n_rows, int32_t max0,
@@ -1653,42 +1655,30 @@ starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_g
     return STARKV_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  auto f32 = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
+  auto f16 = [&](size_t off) { return reinterpret_cast<__half*>(ws + off); };
+  auto i32 = [&](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
   GroupGeom& g = pl.g;
-  g.status = reinterpret_cast<int32_t*>(ws);
+  g.status = i32(0);
   g.ent = reinterpret_cast<GroupEntry*>(ws + pl.ent_off);
-  g.kpre = reinterpret_cast<int64_t*>(ws + pl.kpre_off);
-  g.vpre = reinterpret_cast<int64_t*>(ws + pl.vpre_off);
-  g.row_ent = reinterpret_cast<int32_t*>(ws + pl.row_ent_off);
-  g.row_lim = reinterpret_cast<int32_t*>(ws + pl.row_lim_off);
-  g.n_used = reinterpret_cast<int32_t*>(ws + pl.used_off);
-  g.mrow = reinterpret_cast<float*>(ws + pl.mrow_off);
-  const int n_src = shared ? 2 : 1;
-  __half* P[2];
-  float* Z[2];
-  for (int i = 0; i < 2; ++i) {   // an unused second source stands for the first
-    const int s0 = i < n_src ? i : 0;
-    g.lpart[i] = reinterpret_cast<float*>(ws + pl.lpart_off[s0]);
-    P[i] = reinterpret_cast<__half*>(ws + pl.p_off[s0]);
-    Z[i] = reinterpret_cast<float*>(ws + pl.z_off[s0]);
-  }
-  __half* qh = reinterpret_cast<__half*>(ws + pl.qh_off);
-  __half* ql = reinterpret_cast<__half*>(ws + pl.ql_off);
-  __half* zh = reinterpret_cast<__half*>(ws + pl.zh_off);
-  __half* zl = reinterpret_cast<__half*>(ws + pl.zl_off);
-  float* carry = reinterpret_cast<float*>(ws + pl.carry_off);
+  g.pre = reinterpret_cast<int64_t*>(ws + pl.pre_off);
+  g.row_ent = i32(pl.row_ent_off);
+  g.row_use = i32(pl.row_use_off);
+  g.n_used = i32(pl.used_off);
+  const int second = shared ? 1 : 0;   // an unused second source stands for the first
   const uint32_t G = 1u << g.log2G;
   const uint64_t rh = static_cast<uint64_t>(n_rows) * g.H;
 
-  CUtensorMap kmap, qhmap, qlmap, vmap, pmap[2], bvmap, zhmap, zlmap;
+  CUtensorMap kmap, vmap, qhmap[2], qlmap[2], bvmap, zhmap, zlmap;
   if (!encode_kpool_map(&kmap, k_cache, g.r, g.Hkv, g.NB, 1, 16) ||
-      !encode_rows_map(&qhmap, qh, g.r, g.H, n_rows, G, static_cast<uint32_t>(pl.qbox) / G) ||
-      !encode_rows_map(&qlmap, ql, g.r, g.H, n_rows, G, static_cast<uint32_t>(pl.qbox) / G) ||
-      !encode_vpool_map(&vmap, v_cache, g.R, g.NB, 4) ||
-      !encode_2d_map(&pmap[0], P[0], g.t_pad[0], rh, 64, kGVPBox) ||
-      !encode_2d_map(&pmap[1], P[1], g.t_pad[n_src - 1], rh, 64, kGVPBox) ||
+      !encode_vpool_map(&vmap, v_cache, g.R, g.NB, static_cast<uint32_t>(g.nch)) ||
+      !encode_2d_map(&qhmap[0], ws + pl.qh_off[0], g.r, rh, 64, kGAQBox) ||
+      !encode_2d_map(&qlmap[0], ws + pl.ql_off[0], g.r, rh, 64, kGAQBox) ||
+      !encode_2d_map(&qhmap[1], ws + pl.qh_off[second], g.r, rh, 64, kGAQBox) ||
+      !encode_2d_map(&qlmap[1], ws + pl.ql_off[second], g.r, rh, 64, kGAQBox) ||
       !encode_2d_map(&bvmap, B_V, static_cast<uint64_t>(g.Hkv) * g.d, g.R, 64, 64) ||
-      !encode_rows_map(&zhmap, zh, g.R, g.H, n_rows, G, static_cast<uint32_t>(pl.up_rows)) ||
-      !encode_rows_map(&zlmap, zl, g.R, g.H, n_rows, G, static_cast<uint32_t>(pl.up_rows)))
+      !encode_rows_map(&zhmap, ws + pl.zh_off, g.R, g.H, n_rows, G, static_cast<uint32_t>(pl.up_rows)) ||
+      !encode_rows_map(&zlmap, ws + pl.zl_off, g.R, g.H, n_rows, G, static_cast<uint32_t>(pl.up_rows)))
     return STARKV_ERR_CUDA;
 
   GroupAbsorbParams ap{};
@@ -1698,7 +1688,10 @@ starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_g
   ap.su.shared_lens = shared_lens;
   ap.q = static_cast<const __half*>(q);
   ap.B_K = static_cast<const __half*>(B_K);
-  ap.qh = qh; ap.ql = ql;
+  for (int i = 0; i < 2; ++i) {
+    ap.qh[i] = f16(pl.qh_off[i ? second : 0]);
+    ap.ql[i] = f16(pl.ql_off[i ? second : 0]);
+  }
   ap.coef = scale * kLog2e;
   ap.tile = pl.abs_tile;
   const size_t abs_smem = (static_cast<size_t>(g.d) * g.r + static_cast<size_t>(ap.tile) * g.d) * 2;
@@ -1707,35 +1700,34 @@ starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_g
   if (launch(group_absorb_kernel, dim3(abs_ctas), dim3(kPrepThreads), abs_smem, s, 1, ap) != cudaSuccess)
     return STARKV_ERR_CUDA;
 
-  GroupKParams kp{};
-  kp.g = g;
-  kp.tables = block_tables;
-  kp.P[0] = P[0]; kp.P[1] = P[1];
-  kp.kb = pl.kb; kp.ksteps = pl.ksteps; kp.qbox = pl.qbox; kp.nq = pl.nq; kp.stages = pl.k_stages;
-  kp.a_bytes = pl.a_bytes; kp.q_bytes = pl.q_bytes; kp.tmem_cols = pl.k_tmem;
-  if (launch_group_kpass<false>(pl, kmap, qhmap, qlmap, kp, s) != cudaSuccess ||
-      launch_group_kpass<true>(pl, kmap, qhmap, qlmap, kp, s) != cudaSuccess)
-    return STARKV_ERR_CUDA;
+  // a launch of no more clusters than the call can have blocks
+  const int64_t tiles0 = (n_groups < n_rows ? n_groups : n_rows) + 2 * static_cast<int64_t>(rh) / g.ncap + 1;
+  const int64_t blocks = g.n_slab * (tiles0 * ((max0 + kGTok - 1) / kGTok) +
+                                     (shared ? n_rows * ((g.H + g.ncap - 1) / g.ncap) * static_cast<int64_t>((max1 + kGTok - 1) / kGTok + 1) : 0));
+  const int clusters = blocks < 1 ? 1 : (blocks < pl.clusters ? static_cast<int>(blocks) : pl.clusters);
 
-  GroupVParams vp{};
-  vp.g = g;
-  vp.tables = block_tables;
-  vp.Z[0] = Z[0]; vp.Z[1] = Z[1];
-  vp.zcarry = carry;
-  vp.stages = pl.v_stages;
-  vp.stage_bytes = kGVABytes + kGVBBytes;
-  if (!set_smem(group_vpass_kernel, pl.v_smem)) return STARKV_ERR_CUDA;
-  if (launch(group_vpass_kernel, dim3(pl.v_ctas), dim3(kGVThreads), pl.v_smem, s, 1, vmap, pmap[0], pmap[1], vp) !=
-      cudaSuccess)
+  GroupAttendParams tp{};
+  tp.g = g;
+  tp.tables = block_tables;
+  for (int i = 0; i < 2; ++i) {
+    const int x = i ? second : 0;
+    tp.Z[i] = f32(pl.z_off[x]); tp.m[i] = f32(pl.m_off[x]); tp.l[i] = f32(pl.l_off[x]);
+  }
+  tp.zcarry = f32(pl.zcarry_off); tp.mcarry = f32(pl.mcarry_off); tp.lcarry = f32(pl.lcarry_off);
+  tp.kb = pl.kb; tp.ksteps = pl.ksteps; tp.k_stages = pl.k_stages; tp.v_stages = pl.v_stages;
+  tp.v_stage_bytes = pl.v_stage_bytes;
+  if (!set_smem(group_attend_kernel, pl.at_smem)) return STARKV_ERR_CUDA;
+  if (launch(group_attend_kernel, dim3(clusters, g.C), dim3(kGAThreads), pl.at_smem, s, g.C, kmap, vmap, qhmap[0], qlmap[0],
+             qhmap[1], qlmap[1], tp) != cudaSuccess)
     return STARKV_ERR_CUDA;
 
   GroupCombineParams cp{};
   cp.g = g;
-  cp.Z[0] = Z[0]; cp.Z[1] = Z[1];
-  cp.zcarry = carry;
-  cp.zh = zh; cp.zl = zl;
-  cp.v_grid = pl.v_ctas;
-  const int64_t warps = static_cast<int64_t>(rh) * g.n_rt;
+  for (int i = 0; i < 2; ++i) { cp.Z[i] = tp.Z[i]; cp.m[i] = tp.m[i]; cp.l[i] = tp.l[i]; }
+  cp.zcarry = tp.zcarry; cp.mcarry = tp.mcarry; cp.lcarry = tp.lcarry;
+  cp.zh = f16(pl.zh_off); cp.zl = f16(pl.zl_off);
+  cp.clusters = clusters;
+  const int64_t warps = static_cast<int64_t>(rh) * ((g.R + 255) / 256);
   if (launch(group_combine_kernel, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, s, 1, cp) != cudaSuccess)
     return STARKV_ERR_CUDA;
 

@@ -73,9 +73,9 @@ def test_group_workspace_bytes():
     assert S.starkv_cross_workspace_bytes(d, 1, 4, 600 * 16 + 1) == 0
     a = S.starkv_shared_workspace_bytes(d, 1, 64, 8192, 256)
     assert a > 0 and a % 256 == 0
-    # grows with every bound
-    assert S.starkv_shared_workspace_bytes(d, 1, 64, 9000, 256) > a
-    assert S.starkv_shared_workspace_bytes(d, 1, 64, 8192, 512) > a
+    # never smaller for larger bounds, larger for more rows
+    assert S.starkv_shared_workspace_bytes(d, 1, 64, 9000, 256) >= a
+    assert S.starkv_shared_workspace_bytes(d, 1, 64, 8192, 512) >= a
     assert S.starkv_shared_workspace_bytes(d, 1, 80, 8192, 256) > a
     assert S.starkv_cross_workspace_bytes(d, 8, 64, 1500) > S.starkv_cross_workspace_bytes(d, 8, 32, 1500) > 0
 
