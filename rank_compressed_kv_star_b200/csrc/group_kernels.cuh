@@ -306,7 +306,8 @@ group_absorb_kernel(GroupAbsorbParams p) {
 // the cluster before to the cluster's carry slot: fixed places, fixed order.
 //
 // Warps: 0 loads q~ and K tiles, 1 issues the S products, 2 loads V tiles, 3
-// issues the Z products, 4..11 take the maxima, form the weights and store Z.
+// issues the Z products, 4..11 take the maxima, form the weights and store Z, 12
+// tells the other CTAs that a P block has been consumed here.
 struct GroupAttendParams {
   GroupGeom g;
   const int32_t* tables;     // rows of g.MB entries
@@ -321,8 +322,8 @@ struct GroupAttendParams {
   uint32_t v_stage_bytes;    // 2 pages x 16 tokens x 64 nch codes
 };
 
-constexpr int kGAThreads = 384;
-constexpr int kGAEpi = kGAThreads - 128;
+constexpr int kGAThreads = 416;
+constexpr int kGAEpi = 256;        // threads of warps 4..11
 constexpr int kGAVTok = 32;        // tokens per V stage
 constexpr int kGAQBox = 32;        // columns per query box
 constexpr int kGAMaxC = 8;
@@ -441,7 +442,8 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   uint64_t* tfull = qempty + 1;       // [2] logits ready
   uint64_t* tempty = tfull + 2;       // [2] logits read
   uint64_t* pfull = tempty + 2;       // [2] weights of a block complete, from all CTAs
-  uint64_t* pempty = pfull + 2;       // [2] weights consumed, by all CTAs
+  uint64_t* pdone = pfull + 2;        // [2] weights consumed by this CTA's products
+  uint64_t* pempty = pdone + 2;       // [2] weights consumed, by all CTAs
   uint64_t* mxbar = pempty + 2;       // [2] maxima of all CTAs
   uint64_t* zdone = mxbar + 2;
   uint64_t* zfree = zdone + 1;
@@ -466,6 +468,7 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], kGAEpi / 32);
       mbar_init(&pfull[a], 1);
+      mbar_init(&pdone[a], 1);
       mbar_init(&pempty[a], C);
       mbar_init(&mxbar[a], 1);
     }
@@ -682,8 +685,7 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             umma_commit(&vempty[s]);
           }
           if (!ok) break;
-          if (C > 1) umma_commit_multicast(&pempty[a], static_cast<uint16_t>((1u << C) - 1u));
-          else umma_commit(&pempty[a]);
+          umma_commit(&pdone[a]);
         }
         if (ok) umma_commit(zdone);
       }
@@ -691,6 +693,19 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       umma_commit(mdone);
       if (!mbar_wait(mdone, 0)) set_timeout(g.status, kSiteVMdone);
     }
+  } else if (warp == 12) {
+    // ------------------------------------------- consumed P blocks, to all CTAs
+    uint32_t blk = 0;
+    bool ok = true;
+    SegWalk walk(g, x0, x1);
+    Segment x;
+    while (ok && walk.next(&x))
+      for (int b = x.b0; b < x.b1; ++b, ++blk) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&pdone[blk & 1], (blk / 2) & 1) && !abort_flag)) { ok = false; break; }
+        if (lane < C) mbar_arrive_cluster(&pempty[blk & 1], static_cast<uint32_t>(lane));
+        __syncwarp();
+      }
+    if (!ok && lane == 0) { set_timeout(g.status, kSiteVTfree); abort_flag = 1; }
   } else {
     // -------------------------------------------- maxima, weights, Z stores
     const int et = tid - 128;

@@ -221,6 +221,13 @@ __device__ __forceinline__ void bulk_s2cluster(const void* src, uint32_t rank, u
                : "memory");
 }
 
+// Arrival on the barrier at `bar`'s offset in CTA `rank` of the cluster (this CTA included).
+__device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank) {
+  uint32_t rb;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rb) : "r"(smem_u32(bar)), "r"(rank));
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(rb) : "memory");
+}
+
 // Generic-proxy writes to shared memory become visible to the async proxy
 // (TMA engine, tensor cores) after this fence.
 __device__ __forceinline__ void fence_proxy_async_smem() {
@@ -294,15 +301,6 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    smem_u32(bar))
                : "memory");
-}
-
-// The same arrival on the barrier at `bar`'s offset in every CTA of the cluster whose bit of `mask` is set.
-__device__ __forceinline__ void umma_commit_multicast(uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"(mask)
-      : "memory");
 }
 
 // 32 lanes x 32 consecutive 32-bit columns: thread i gets lane (base+i), columns c..c+31.

@@ -44,9 +44,9 @@ class Layer:
         k = np.full((nb, PAGE, self.Hkv, self.r), np.nan, np.float16)
         v = np.full((nb, PAGE, self.R), np.nan, np.float16)
         for pg, n in tables_used:
-            for t in range(n):
-                k[pg[t // PAGE], t % PAGE] = self.f(self.Hkv, self.r, a=0.8)
-                v[pg[t // PAGE], t % PAGE] = self.f(self.R, a=0.8)
+            t = np.arange(n)
+            k[pg[t // PAGE], t % PAGE] = self.f(n, self.Hkv, self.r, a=0.8)
+            v[pg[t // PAGE], t % PAGE] = self.f(n, self.R, a=0.8)
         return k, v, nb
 
 

@@ -71,6 +71,13 @@ def test_long_shared_prefix_splits_tiles():
     check_case(L, c)
 
 
+@pytest.mark.parametrize("layer,tokens", [("gqa32", 30011), ("mha32", 9001), ("wide", 40003), ("mqa64", 50021)])
+def test_long_sequences_run_many_blocks_per_cluster(layer, tokens):
+    """More 128-token blocks than clusters, so that one cluster reuses its weight blocks many times."""
+    L = Layer(14, *LAYERS[layer])
+    check_case(L, make_cross(L, [(tokens, 2), (700, 1)]), rows=[1, 2])
+
+
 def test_shared_equals_paged_decode():
     """The same q, tables and lengths through starkv_paged_decode."""
     L = Layer(7, *LAYERS["mha32"])
