@@ -8,15 +8,16 @@
 // a row b and query head h, with g(h) = h / (H / Hkv) and the tokens t of the
 // row's one or two entries,
 //   s[b,h,t] = log2(e) scale q[b,h] . B_K[g(h)]^T . c_K[t,g(h)]
-//   out[b,h] = (sum_t exp2(s - M) c_V[t] / sum_t exp2(s - M)) . B_V[:, g(h) d : (g(h)+1) d]
-// Launches, all on the caller's stream:
-//   1. group_absorb   q~ = log2(e) scale q . B_K^T in fp16 hi + lo halves, and
-//                     the entry tables (one extra CTA)
-//   2. group_attend   per segment (a run of tokens of one column tile): the
-//                     maxima m of its logits, w = fp16(exp2(s - m)), l = sum w
-//                     and Z = sum w c_V, all on tcgen05
-//   3. group_combine  M = max m, Z / L over a row's segments, in hi + lo halves
-//   4. group_up       out = Z / L . B_V on tcgen05
+//   M[b,h]   = max_t s          w[b,h,t] = fp16(exp2(s - M))        L = sum_t w
+//   out[b,h] = (sum_t w c_V[t] / L) . B_V[:, g(h) d : (g(h)+1) d]
+// The maximum is taken over both entries before any weight is formed, so the
+// partial sums of a row simply add up.  Launches, all on the caller's stream:
+//   1. group_absorb           q~ = log2(e) scale q . B_K^T in fp16 hi + lo
+//                             halves; the entry tables (one extra CTA); M = -inf
+//   2. group_kpass<maxima>    S = c_K . q~ on tcgen05, column maxima only
+//   3. group_kpass<weights>   S again, w to the P matrix, L per token chunk
+//   4. group_vpass            Z = P . c_V on tcgen05, partial sums per (tile, CTA)
+//   5. group_finish           Z / L over the partials, out = Z / L . B_V on tcgen05
 // All rows of an entry share every load of its pages: the codes of a page are
 // read from HBM once per entry, whatever the number of rows.
 #pragma once
@@ -33,76 +34,58 @@ namespace starkv {
 
 // One run of rows over one list of pages: rows row0 .. row0 + nrows - 1 over
 // tokens 0 .. len - 1, token t in slot t % 16 of page tables[tab][page0 + t / 16].
-// Its columns are the (KV head j, row, query head of j) triples in that order.
+// Its columns are the (row, query head) pairs in that order.
 struct alignas(16) GroupEntry {
   int32_t row0, nrows, len, page0;
-  int32_t tab, src;   // src 0: a group's (or sequence's) pages; 1: a row's own pages
-  int32_t pad0, pad1;
+  int32_t tab;
+  int32_t psrc, zsrc;  // which P and Z matrices it uses: 0 a group's (or sequence's), 1 a row's own
+  int32_t tile0;       // V tiles before it
 };
 
 struct GroupGeom {
   int H, Hkv, log2G, d, r, R, MB, NB;
   int n_rows, n_groups, E;     // E = n_groups entries, plus n_rows own entries when shared
   int shared;                  // 1: shared-prefix decode, 0: cross attention
-  int ncap;                    // columns per tile at most
-  int n_slab, C, nch;          // R in n_slab slabs, each over the C CTAs of a cluster, 64 nch codes per CTA
-  int weight[2];               // cost of a 128-token block of a tile by source
-  int max_len[2];              // host bounds of the entries' lengths by source
+  int ncol;                    // K pass: query columns per tile
+  int chunk_w, chunk_n;        // K pass: tokens per item of a wide / narrow entry
+  int n_rt;                    // V pass: 256-row tiles of R
+  int t_pad[2];                // P row length, a multiple of 128
+  int n_ch[2];                 // chunks per row of the sums of weights
+  int max_len[2];              // host bounds of the entries' lengths
   GroupEntry* ent;             // [E]
-  int64_t* pre;                // [E + 1] cost of the tiles before each entry
+  int32_t* kpre;               // [E + 1] K items before each entry
+  int32_t* vpre;               // [E + 1] V units before each entry
   int32_t* row_ent;            // [n_rows] the row's group, or -1
   int32_t* row_use;            // [n_rows] 1: the row attends over its group's pages
   int32_t* n_used;             // rows that belong to groups (row_offsets[n_groups])
+  int32_t* tfirst;             // [V tiles] first CTA of each tile
+  int32_t* tlast;              // [V tiles] last CTA
+  float* mrow;                 // [n_rows][H] maxima
+  float* lpart[2];             // by zsrc, [n_rows][H][n_ch] sums of weights per chunk
   int32_t* status;
 };
 
-constexpr int kGTok = 128;      // tokens per block
+constexpr int kGVTile = 256;    // V pass: columns (row, head) and rows of R per tile
+constexpr int kGVTok = 64;      // V pass: tokens per unit
+constexpr int kGNarrowCols = 128;
+constexpr int kGNarrowPer = 16;
 
-// The column tiles of an entry: whole KV heads (hpt of them, width = hpt * m
-// columns) while the m = nrows * G columns of a head fit a tile, else runs of cw
-// columns of one head (split runs per head).
-struct TileShape {
-  int m, nt, hpt, split, cw;
-};
-__device__ __forceinline__ TileShape tile_shape(int nrows, const GroupGeom& g) {
-  TileShape t;
-  t.m = nrows << g.log2G;
-  if (t.m <= g.ncap) {
-    const int most = g.ncap / t.m;
-    t.nt = (g.Hkv + most - 1) / most;
-    t.hpt = (g.Hkv + t.nt - 1) / t.nt;
-    t.nt = (g.Hkv + t.hpt - 1) / t.hpt;
-    t.split = 1;
-    t.cw = t.m;
-  } else {
-    t.hpt = 1;
-    const int n = (t.m + g.ncap - 1) / g.ncap;
-    t.cw = ((t.m + n - 1) / n + 7) / 8 * 8;
-    t.split = (t.m + t.cw - 1) / t.cw;
-    t.nt = g.Hkv * t.split;
-  }
-  return t;
+// Column tiles of an entry with `cols` (row, head) columns, and their width.
+__device__ __forceinline__ int gv_tiles(int cols) { return (cols + kGVTile - 1) / kGVTile; }
+__device__ __forceinline__ int gv_width(int cols, int nt) { return ((cols + nt - 1) / nt + 15) / 16 * 16; }
+
+// A narrow entry has so few columns that one tile holds those of all heads: its K
+// tiles are 128 code rows in page order (128 / Hkv tokens x Hkv heads, large
+// contiguous copies), and each row uses the columns of its own head; the
+// tensor cores compute the others too, which costs less than the copies.  A wide
+// entry's K tiles are 128 tokens of one head.
+__device__ __forceinline__ bool gk_narrow(int nrows, const GroupGeom& g) {
+  return nrows * g.H <= g.ncol && (nrows << g.log2G) <= kGNarrowPer;
 }
-// Tile of the column `within` of KV head j, and the column's place in the tile.
-__device__ __forceinline__ int tile_of(const TileShape& t, int j, int within, int* place) {
-  if (t.split == 1) {
-    *place = (j % t.hpt) * t.m + within;
-    return j / t.hpt;
-  }
-  *place = within % t.cw;
-  return j * t.split + within / t.cw;
-}
-
-__device__ __forceinline__ int64_t entry_blocks(const GroupEntry& en) { return (en.len + kGTok - 1) / kGTok; }
-
-// Largest e with pre[e] <= x (0 <= x < pre[E]; empty entries are skipped).
-__device__ __forceinline__ int32_t entry_of(const int64_t* pre, int32_t E, int64_t x) {
-  int32_t lo = 0, hi = E - 1;
-  while (lo < hi) {
-    const int32_t mid = (lo + hi + 1) >> 1;
-    if (pre[mid] <= x) lo = mid; else hi = mid - 1;
-  }
-  return lo;
+// Row tiles of a wide entry.
+__device__ __forceinline__ int gk_tiles(int nrows, const GroupGeom& g) {
+  const int per = g.ncol >> g.log2G;
+  return (nrows + per - 1) / per;
 }
 
 // ================================================================= tables
@@ -119,23 +102,15 @@ __device__ __forceinline__ int clamp_flag(int x, int lo, int hi, int32_t* bad, i
   return x;
 }
 
-// Rows [r0, r0 + n) of group e: the caller's offsets, clamped to the rows there are.
-__device__ __forceinline__ void group_rows(const GroupSetupParams& p, int e, int* r0, int* n) {
-  const int a = min(max(p.row_offsets[e], 0), p.g.n_rows), b = min(max(p.row_offsets[e + 1], 0), p.g.n_rows);
-  *r0 = a;
-  *n = b > a ? b - a : 0;
-}
-// Group of row b (and the group's rows), or -1: behind the last group, or the
-// offsets are out of order.
-__device__ __forceinline__ int group_of_row(const GroupSetupParams& p, int b, int* r0, int* n) {
+// Group of row b, or -1: behind the last group, or the offsets are out of order.
+__device__ __forceinline__ int group_of_row(const GroupSetupParams& p, int b) {
   if (b >= p.row_offsets[p.g.n_groups]) return -1;
   int lo = 0, hi = p.g.n_groups - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (p.row_offsets[mid] <= b) lo = mid; else hi = mid - 1;
   }
-  group_rows(p, lo, r0, n);
-  return b >= *r0 && b < *r0 + *n ? lo : -1;
+  return b >= p.row_offsets[lo] && b < p.row_offsets[lo + 1] ? lo : -1;
 }
 
 // One CTA of 256 threads.  Every value read from the caller's arrays is clamped
@@ -143,35 +118,40 @@ __device__ __forceinline__ int group_of_row(const GroupSetupParams& p, int b, in
 __device__ __forceinline__ void group_setup(const GroupSetupParams& p) {
   const GroupGeom& g = p.g;
   __shared__ int32_t bad;
-  __shared__ int64_t warp_sum[8];
+  __shared__ int32_t warp_sum[3][8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) bad = 0;
   __syncthreads();
   if (tid == 0) *g.n_used = clamp_flag(p.row_offsets[g.n_groups], 0, g.n_rows, &bad, STARKV_FLAG_BAD_ROW_OFFSET);
-  // thread t makes the entries [t per, (t + 1) per) and keeps their cost
+  // thread t makes the entries [t per, (t + 1) per)
   const int per = (g.E + 255) / 256;
   const int e0 = tid * per, e1 = min(g.E, e0 + per);
-  int64_t mine = 0;
-  auto cost = [&](const GroupEntry& en) {
-    return en.nrows > 0 ? static_cast<int64_t>(tile_shape(en.nrows, g).nt) * g.n_slab * entry_blocks(en) * g.weight[en.src]
-                        : static_cast<int64_t>(0);
+  int32_t mine[3] = {0, 0, 0};   // K items, V units, V tiles
+  auto counts = [&](const GroupEntry& en, int32_t (&c)[3]) {
+    c[0] = c[1] = c[2] = 0;
+    if (en.nrows == 0 || en.len == 0) return;
+    const int nt = gv_tiles(en.nrows * g.H) * g.n_rt;
+    c[0] = gk_narrow(en.nrows, g) ? (en.len + g.chunk_n - 1) / g.chunk_n
+                                  : gk_tiles(en.nrows, g) * g.Hkv * ((en.len + g.chunk_w - 1) / g.chunk_w);
+    c[1] = nt * ((en.len + kGVTok - 1) / kGVTok);
+    c[2] = nt;
   };
   for (int e = e0; e < e1; ++e) {
     GroupEntry en{};
     if (e < g.n_groups) {
       const int a = p.row_offsets[e], b = p.row_offsets[e + 1];
       if (a < 0 || a > b || b > g.n_rows || (e == 0 && a != 0)) atomicOr(&bad, STARKV_FLAG_BAD_ROW_OFFSET);
-      group_rows(p, e, &en.row0, &en.nrows);
+      en.row0 = min(max(a, 0), g.n_rows);
+      en.nrows = max(0, min(max(b, 0), g.n_rows) - en.row0);
       const int len =
           clamp_flag(g.shared ? p.shared_lens[e] : p.seq_lens[e], 0, g.max_len[0], &bad, STARKV_FLAG_BAD_SEQ_LEN);
       en.len = g.shared ? len / kBlock * kBlock : len;   // whole pages are shared
       en.tab = g.shared ? min(en.row0, g.n_rows - 1) : e;
     } else {
       const int b = e - g.n_groups;
-      int r0, n;
-      const int grp = group_of_row(p, b, &r0, &n);
+      const int grp = group_of_row(p, b);
       en.row0 = b;
-      en.src = 1;
+      en.psrc = en.zsrc = 1;
       en.tab = b;
       int use = 0;
       if (grp >= 0) {
@@ -183,39 +163,54 @@ __device__ __forceinline__ void group_setup(const GroupSetupParams& p) {
           en.page0 = common / kBlock;
           en.len = clamp_flag(T - common, 0, g.max_len[1], &bad, STARKV_FLAG_BAD_SEQ_LEN);
         } else {
-          en.len = T;   // shorter than the shared pages: the row reads all of its tokens by itself
+          // shorter than the shared pages: the row reads all of its tokens by
+          // itself and keeps its weights in its unused row of the group's P
+          en.len = T;
+          en.psrc = 0;
         }
       }
       g.row_ent[b] = grp;
       g.row_use[b] = use;
     }
     g.ent[e] = en;
-    mine += cost(en);
+    int32_t c[3];
+    counts(en, c);
+    for (int i = 0; i < 3; ++i) mine[i] += c[i];
   }
   if (!g.shared)
     for (int b = tid; b < g.n_rows; b += 256) {
-      int r0, n;
-      const int grp = group_of_row(p, b, &r0, &n);
+      const int grp = group_of_row(p, b);
       g.row_ent[b] = grp;
       g.row_use[b] = grp >= 0 ? 1 : 0;
     }
-  // exclusive prefix sums of the costs
-  int64_t v = mine;
+  // exclusive prefix sums
+  int32_t v[3] = {mine[0], mine[1], mine[2]};
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += y;
-  }
-  if (lane == 31) warp_sum[warp] = v;
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int32_t y = __shfl_up_sync(0xffffffffu, v[i], o);
+      if (lane >= o) v[i] += y;
+    }
+  if (lane == 31)
+    for (int i = 0; i < 3; ++i) warp_sum[i][warp] = v[i];
   __syncthreads();
-  int64_t at = v - mine;
-  for (int w = 0; w < warp; ++w) at += warp_sum[w];
+  int32_t at[3];
+  for (int i = 0; i < 3; ++i) {
+    at[i] = v[i] - mine[i];
+    for (int w = 0; w < warp; ++w) at[i] += warp_sum[i][w];
+  }
   for (int e = e0; e < e1; ++e) {
-    g.pre[e] = at;
-    at += cost(g.ent[e]);
+    int32_t c[3];
+    counts(g.ent[e], c);
+    g.kpre[e] = at[0];
+    g.vpre[e] = at[1];
+    g.ent[e].tile0 = at[2];
+    for (int i = 0; i < 3; ++i) at[i] += c[i];
   }
   if (tid == 255) {
-    g.pre[g.E] = at;
+    g.kpre[g.E] = at[0];
+    g.vpre[g.E] = at[1];
     *g.status = bad;
   }
 }
@@ -225,8 +220,8 @@ struct GroupAbsorbParams {
   GroupSetupParams su;
   const __half* q;     // [n_rows][H][d]
   const __half* B_K;   // [Hkv][r][d]
-  __half* qh[2];       // by source, [n_rows * H][r] in the order of the entries' columns: fp16 of q~
-  __half* ql[2];       // fp16 of its remainder
+  __half* qh;          // [n_rows * H][r] fp16 of q~
+  __half* ql;          // [n_rows * H][r] fp16 of its remainder
   float coef;          // scale * log2(e)
   int tile;            // rows per item
 };
@@ -235,7 +230,6 @@ struct GroupAbsorbParams {
 __global__ void __launch_bounds__(kPrepThreads)
 group_absorb_kernel(GroupAbsorbParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ int32_t s_row0[kAbsBT], s_n[kAbsBT];
   griddep_wait();
   griddep_launch_dependents();
   if (blockIdx.x == 0) {
@@ -249,12 +243,7 @@ group_absorb_kernel(GroupAbsorbParams p) {
   const int nb = min(p.tile, g.n_rows - b0);
   __half* Ws = reinterpret_cast<__half*>(smem_raw);   // [d][r]: B_K[g(h)] transposed
   __half* qs = Ws + static_cast<size_t>(D) * r;       // [tile][d]
-  if (tid < nb) {
-    int r0 = 0, n = 0;
-    const int e = group_of_row(p.su, b0 + tid, &r0, &n);
-    s_row0[tid] = r0;
-    s_n[tid] = e >= 0 ? n : 0;
-  }
+  for (int b = tid; b < nb; b += kPrepThreads) g.mrow[static_cast<size_t>(b0 + b) * g.H + h] = -INFINITY;
   const __half* bk = p.B_K + static_cast<size_t>(h >> g.log2G) * r * D;
   for (int x = tid; x < r * (D / 8); x += kPrepThreads) {
     const int i = x % r, jb = x / r;
@@ -269,125 +258,105 @@ group_absorb_kernel(GroupAbsorbParams p) {
         reinterpret_cast<const uint4*>(p.q + (static_cast<size_t>(b0 + bb) * g.H + h) * D)[c];
   }
   __syncthreads();
-  const int j = h >> g.log2G, gg = h & ((1 << g.log2G) - 1);
   small_proj(Ws, qs, nb, D, r, [&](int bb, int i, float v0, float v1) {
     v0 *= p.coef;
     v1 *= p.coef;
+    const size_t o = (static_cast<size_t>(b0 + bb) * g.H + h) * r + i;
     const __half2 hi = __floats2half2_rn(v0, v1);
     const float2 hf = __half22float2(hi);
-    const __half2 lo = __floats2half2_rn(v0 - hf.x, v1 - hf.y);
-    const int n = s_n[bb], row = b0 + bb;
-    if (n == 0) return;   // in no group
-    const size_t o0 = (static_cast<size_t>(s_row0[bb]) * g.H + ((static_cast<size_t>(j) * n + row - s_row0[bb]) << g.log2G) + gg) * r + i;
-    *reinterpret_cast<__half2*>(p.qh[0] + o0) = hi;
-    *reinterpret_cast<__half2*>(p.ql[0] + o0) = lo;
-    if (g.shared) {
-      const size_t o1 = (static_cast<size_t>(row) * g.H + h) * r + i;
-      *reinterpret_cast<__half2*>(p.qh[1] + o1) = hi;
-      *reinterpret_cast<__half2*>(p.ql[1] + o1) = lo;
-    }
+    *reinterpret_cast<__half2*>(p.qh + o) = hi;
+    *reinterpret_cast<__half2*>(p.ql + o) = __floats2half2_rn(v0 - hf.x, v1 - hf.y);
   });
 }
 
-// ================================================================== attend
-// One cluster of C CTAs works on one segment at a time: a run of 128-token
-// blocks of one column tile (up to ncap (KV head, row, query head) columns of an
-// entry).  CTA c accumulates Z for its own 64 nch codes of R in tensor memory;
-// the logits of (block, KV head) units go round the CTAs, each unit computed by
-// one CTA and its fp16 weights copied to all of them through distributed shared
-// memory.  So the K codes, the exponentials and the V codes are each read and
-// computed once per tile, and no logit or weight leaves the SMs.
-//   phase A  S = c_K . (q~ hi + q~ lo) per unit; column maxima, exchanged
-//   phase B  S again; w = fp16(exp2(s - m)) into the P block of every CTA;
-//            Z += P . c_V as blocks complete
-// Costs of all tiles are laid end to end and cluster i of n takes the blocks
-// that begin in [i P / n, (i+1) P / n).  The sums of a tile that begins in a
-// cluster's range go to the tile's own place, those of a tile carried over from
-// the cluster before to the cluster's carry slot: fixed places, fixed order.
-//
-// Warps: 0 loads q~ and K tiles, 1 issues the S products, 2 loads V tiles, 3
-// issues the Z products, 4..11 take the maxima, form the weights and store Z, 12
-// tells the other CTAs that a P block has been consumed here.
-struct GroupAttendParams {
+// The entry that holds position x of a prefix array (pre[e] <= x < pre[e + 1]),
+// looked up by the whole CTA at once; s_e is shared.  Call before a __syncthreads.
+__device__ __forceinline__ void find_entry(const int32_t* pre, int32_t E, int32_t x, int32_t* s_e) {
+  for (int e = threadIdx.x; e < E; e += blockDim.x)
+    if (pre[e] <= x && x < pre[e + 1]) *s_e = e;
+}
+
+// ================================================================== K pass
+// A step is one A tile of 128 code rows: D[row, column] = c_K . (q~ hi + q~ lo)
+// with the code rows on the 128 TMEM lanes (K-major, 128-byte swizzle).  An item
+// of a wide entry is one KV head, one tile of rows and one chunk of tokens, its
+// tiles 128 tokens of the head (one 16-token x 64-code box per page) and its
+// columns the tile's (row, query head of the KV head) pairs.  An item of a
+// narrow entry is one chunk of tokens of all heads (see gk_narrow).  Warp 0
+// issues the copies, warp 1 the MMAs into a ring of accumulators, warps 2..9
+// drain them: wide, each takes one lane quarter and every other block of 16
+// columns; narrow, four of them stage their quarter in shared memory and each
+// lane reads its own head's columns.  The weights pass forms S a second time
+// rather than keeping it: r / R of the V pass's products against 8 bytes of
+// traffic per logit.
+struct GroupKParams {
   GroupGeom g;
   const int32_t* tables;     // rows of g.MB entries
-  float* Z[2];               // by source, [n_rows * H][R]
-  float* m[2];               // by source, [n_slab][n_rows * H]
-  float* l[2];               // by source, [n_slab][n_rows * H][C]
-  float* zcarry;             // [clusters][ncap][R]
-  float* mcarry;             // [clusters][ncap]
-  float* lcarry;             // [clusters][ncap][C]
+  __half* P[2];              // [n_rows * H][t_pad] by psrc
   int kb, ksteps;            // 64-code blocks and 16-code steps of r
-  int k_stages, v_stages;
-  uint32_t v_stage_bytes;    // 2 pages x 16 tokens x 64 nch codes
+  int qbox;                  // wide: columns per query box, max(16, G)
+  int log2Hkv;
+  int nq, stages;            // query slots, ring stages
+  uint32_t a_bytes, q_bytes; // ring stage, query slot (hi then lo)
+  uint32_t tmem_cols;
 };
 
-constexpr int kGAThreads = 416;
-constexpr int kGAEpi = 256;        // threads of warps 4..11
-constexpr int kGAVTok = 32;        // tokens per V stage
-constexpr int kGAQBox = 32;        // columns per query box
-constexpr int kGAMaxC = 8;
+constexpr int kGKThreads = 320;
+constexpr int kGKEpi = kGKThreads - 64;
+constexpr int kGKAcc = 4;
+constexpr int kGKQBox = 32;          // narrow: columns per query box
 
-struct Segment {
+struct KItem {
   GroupEntry en;
-  TileShape ts;
-  int ct, slab;
-  int col0, ncols;     // first column (of the entry's) and columns of the tile
-  int nh, mt, j0;      // KV heads in the tile, columns per head, first head
-  int b0, b1;          // blocks
-  bool first;          // the tile begins here
+  bool narrow;
+  int j, row0, nrow, cols;        // KV head (wide), rows of the tile, columns
+  int c, t0, t1, step;            // chunk, tokens [t0, t1), tokens per step
 };
 
-struct SegWalk {
+// Walks the items [it, end) of a CTA in order, from entry e0 on.
+struct KWalk {
   const GroupGeom& g;
-  int64_t x, end, ebeg, eend;   // cost positions
-  int32_t e;
+  int32_t it, end, ebeg, eend, e;
   GroupEntry en;
-  __device__ SegWalk(const GroupGeom& g_, int64_t a, int64_t b) : g(g_), x(a), end(b), ebeg(0), eend(0), e(0) {
-    if (x < end) {
-      e = entry_of(g.pre, g.E, x);
-      ebeg = g.pre[e];
-      eend = g.pre[e + 1];
+  __device__ KWalk(const GroupGeom& g_, int32_t i0, int32_t i1, int32_t e0) : g(g_), it(i0), end(i1), ebeg(0), eend(0), e(e0) {
+    if (it < end) {
+      ebeg = g.kpre[e];
+      eend = g.kpre[e + 1];
       en = g.ent[e];
     }
   }
-  // The next run of blocks that begin in [x, end); blocks of an entry of weight
-  // w begin at ebeg + w i.
-  __device__ bool next(Segment* s) {
-    for (;;) {
-      if (x >= end) return false;
-      while (x >= eend) { ++e; ebeg = eend; eend = g.pre[e + 1]; if (x < eend) en = g.ent[e]; }
-      const int w = g.weight[en.src];
-      const int64_t i = (x - ebeg + w - 1) / w;                       // first block that begins at or after x
-      const int64_t stop = ((end < eend ? end : eend) - ebeg + w - 1) / w;   // first block not taken
-      if (i >= stop) { x = end < eend ? end : eend; continue; }
-      const int64_t blocks = entry_blocks(en);
-      const int64_t tile = i / blocks;
-      s->en = en;
-      s->ts = tile_shape(en.nrows, g);
-      s->ct = static_cast<int>(tile / g.n_slab);
-      s->slab = static_cast<int>(tile % g.n_slab);
-      const TileShape& t = s->ts;
-      if (t.split == 1) {
-        s->j0 = s->ct * t.hpt;
-        s->nh = min(t.hpt, g.Hkv - s->j0);
-        s->mt = t.m;
-        s->col0 = s->j0 * t.m;
-      } else {
-        s->j0 = s->ct / t.split;
-        s->nh = 1;
-        const int c = (s->ct % t.split) * t.cw;
-        s->mt = min(t.cw, t.m - c);
-        s->col0 = s->j0 * t.m + c;
-      }
-      s->ncols = s->nh * s->mt;
-      s->b0 = static_cast<int>(i - tile * blocks);
-      const int64_t left = stop - i;
-      s->b1 = static_cast<int>(left < blocks - s->b0 ? s->b0 + left : blocks);
-      s->first = s->b0 == 0;
-      x = ebeg + (i + s->b1 - s->b0) * w;
-      return true;
+  __device__ bool next(KItem* x) {
+    if (it >= end) return false;
+    while (it >= eend) { ++e; ebeg = eend; eend = g.kpre[e + 1]; if (it < eend) en = g.ent[e]; }
+    const uint32_t local = static_cast<uint32_t>(it - ebeg);
+    x->en = en;
+    x->narrow = gk_narrow(en.nrows, g);
+    if (x->narrow) {
+      x->j = 0;
+      x->row0 = en.row0;
+      x->nrow = en.nrows;
+      x->cols = en.nrows * g.H;
+      x->c = local;
+      x->t0 = x->c * g.chunk_n;
+      // whole pages: weights past the end are written as zeros
+      x->t1 = min((en.len + kBlock - 1) / kBlock * kBlock, x->t0 + g.chunk_n);
+      x->step = 128 / g.Hkv;
+    } else {
+      const uint32_t nt = gk_tiles(en.nrows, g);
+      x->j = local % static_cast<uint32_t>(g.Hkv);
+      const uint32_t rest = local / static_cast<uint32_t>(g.Hkv);
+      const int rt = rest % nt;
+      x->c = rest / nt;
+      const int per = (en.nrows + nt - 1) / nt;
+      x->row0 = en.row0 + rt * per;
+      x->nrow = min(per, en.row0 + en.nrows - x->row0);
+      x->cols = x->nrow << g.log2G;
+      x->t0 = x->c * g.chunk_w;
+      x->t1 = min(en.len, x->t0 + g.chunk_w);
+      x->step = 128;
     }
+    ++it;
+    return true;
   }
 };
 
@@ -405,606 +374,634 @@ __device__ __forceinline__ float lane_sum16(float (&a)[16], int lane) {
   return a[0] + __shfl_xor_sync(0xffffffffu, a[0], 1);
 }
 
-// Shared-memory layout of the attend kernel (bytes from the 1024-aligned base).
-struct AttendSmem {
-  uint32_t v, q, k, p, mx, stat, bars, total;
-};
-__host__ __device__ __forceinline__ AttendSmem attend_smem(int ncap, int kb, int k_stages, int v_stages, uint32_t v_stage_bytes) {
-  AttendSmem s;
-  s.v = 0;
-  s.q = s.v + ((v_stages * v_stage_bytes + 1023u) & ~1023u);
-  s.k = s.q + static_cast<uint32_t>(kb * 2 * ncap) * 128u;
-  s.p = s.k + static_cast<uint32_t>(k_stages) * 16384u;
-  s.mx = s.p + 2u * static_cast<uint32_t>(ncap) * 256u;               // maxima of every CTA: [2][C][ncap]
-  s.stat = s.mx + 2u * kGAMaxC * static_cast<uint32_t>(ncap) * 4u;    // m [ncap], per quarter max [4][ncap], sum [4][ncap]
-  s.bars = s.stat + 9u * static_cast<uint32_t>(ncap) * 4u;
-  s.total = s.bars + 8u * static_cast<uint32_t>(2 * k_stages + 3 * v_stages + 32);
-  return s;
-}
-
-__global__ void __launch_bounds__(kGAThreads, 1)
-group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                    const __grid_constant__ CUtensorMap qhmap0, const __grid_constant__ CUtensorMap qlmap0,
-                    const __grid_constant__ CUtensorMap qhmap1, const __grid_constant__ CUtensorMap qlmap1,
-                    GroupAttendParams p) {
+template <bool kWeights>
+__global__ void __launch_bounds__(kGKThreads, 1)
+group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_constant__ CUtensorMap knmap,
+                   const __grid_constant__ CUtensorMap qhwmap, const __grid_constant__ CUtensorMap qlwmap,
+                   const __grid_constant__ CUtensorMap qhnmap, const __grid_constant__ CUtensorMap qlnmap, GroupKParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
   const GroupGeom& g = p.g;
-  const AttendSmem lay = attend_smem(g.ncap, p.kb, p.k_stages, p.v_stages, p.v_stage_bytes);
-  const int KS = p.k_stages, VS = p.v_stages, C = g.C, ncap = g.ncap;
-  uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + lay.bars);
-  uint64_t* kempty = kfull + KS;
-  uint64_t* vfull = kempty + KS;
-  uint64_t* vempty = vfull + VS;
-  uint64_t* vfix = vempty + VS;       // [VS] the stage's partly filled page has been zeroed behind its end
-  uint64_t* qfull = vfix + VS;
-  uint64_t* qempty = qfull + 1;
-  uint64_t* tfull = qempty + 1;       // [2] logits ready
-  uint64_t* tempty = tfull + 2;       // [2] logits read
-  uint64_t* pfull = tempty + 2;       // [2] weights of a block complete, from all CTAs
-  uint64_t* pdone = pfull + 2;        // [2] weights consumed by this CTA's products
-  uint64_t* pempty = pdone + 2;       // [2] weights consumed, by all CTAs
-  uint64_t* mxbar = pempty + 2;       // [2] maxima of all CTAs
-  uint64_t* zdone = mxbar + 2;
-  uint64_t* zfree = zdone + 1;
-  uint64_t* sdone = zfree + 1;        // every S / Z product issued has completed
-  uint64_t* mdone = sdone + 1;
-  uint64_t* ebar = mdone + 1;
-  float* s_mx = reinterpret_cast<float*>(smem + lay.mx);
-  float* s_m = reinterpret_cast<float*>(smem + lay.stat);
-  float* s_qmax = s_m + ncap;
-  float* s_qsum = s_qmax + 4 * ncap;
+  const int S = p.stages;
+  uint8_t* qslot = smem + static_cast<size_t>(S) * p.a_bytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(qslot + static_cast<size_t>(p.nq) * p.q_bytes);
+  uint64_t* empty = full + S;
+  uint64_t* qfull = empty + S;
+  uint64_t* qempty = qfull + 2;
+  uint64_t* tfull = qempty + 2;
+  uint64_t* tempty = tfull + kGKAcc;
+  uint64_t* mmadone = tempty + kGKAcc;
+  uint64_t* ebar = mmadone + 1;
+  float* stage = reinterpret_cast<float*>(ebar + 1);   // [4 warps][32 lanes][ncol + 4]
   __shared__ uint32_t taddr_s;
   __shared__ volatile int32_t abort_flag;
+  __shared__ int32_t s_e0;
+  __shared__ int64_t s_off[128];   // P row of each column, or -1
+  __shared__ int32_t s_rh[128];    // its (row, query head), or -1
+  __shared__ float s_m[128];
+  __shared__ float s_red[4][128];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int c = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   if (tid == 0) {
-    for (int s = 0; s < KS; ++s) { mbar_init(&kfull[s], 1); mbar_init(&kempty[s], 1); }
-    for (int s = 0; s < VS; ++s) { mbar_init(&vfull[s], 1); mbar_init(&vempty[s], 1); mbar_init(&vfix[s], 1); }
-    mbar_init(qfull, 1);
-    mbar_init(qempty, 1);
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], kGAEpi / 32);
-      mbar_init(&pfull[a], 1);
-      mbar_init(&pdone[a], 1);
-      mbar_init(&pempty[a], C);
-      mbar_init(&mxbar[a], 1);
-    }
-    mbar_init(zdone, 1);
-    mbar_init(zfree, kGAEpi / 32);
-    mbar_init(sdone, 1);
-    mbar_init(mdone, 1);
-    mbar_init(ebar, kGAEpi);
+    for (int s = 0; s < S; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int a = 0; a < 2; ++a) { mbar_init(&qfull[a], 1); mbar_init(&qempty[a], 1); }
+    for (int a = 0; a < kGKAcc; ++a) { mbar_init(&tfull[a], 1); mbar_init(&tempty[a], kGKEpi / 32); }
+    mbar_init(mmadone, 1);
+    mbar_init(ebar, kGKEpi);
     abort_flag = 0;
     fence_mbar_init();
+    prefetch_tensormap(&kwmap);
+    prefetch_tensormap(&knmap);
+    prefetch_tensormap(&qhwmap);
+    prefetch_tensormap(&qlwmap);
+    prefetch_tensormap(&qhnmap);
+    prefetch_tensormap(&qlnmap);
   }
   if (warp == 1) {
-    tmem_alloc(&taddr_s, 512);
+    tmem_alloc(&taddr_s, p.tmem_cols);
     tmem_relinquish();
     tc_fence_before();
   }
-  __syncthreads();
-  if (C > 1) cluster_sync();     // every CTA's barriers exist before anyone signals them
-  tc_fence_after();
-  const uint32_t taddr = taddr_s;
   griddep_wait();
   griddep_launch_dependents();
-  Partition pt;
-  pt.P = g.pre[g.E];
-  pt.G = static_cast<int32_t>(gridDim.x);   // clusters lie along y
-  const int cl = blockIdx.x;
-  const int64_t x0 = part_begin(cl, pt), x1 = part_begin(cl + 1, pt);
+  const int64_t total = g.kpre[g.E];
+  const int32_t i0 = static_cast<int32_t>(blockIdx.x * total / gridDim.x);
+  const int32_t i1 = static_cast<int32_t>((blockIdx.x + 1) * total / gridDim.x);
+  if (i0 < i1) find_entry(g.kpre, g.E, i0, &s_e0);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t taddr = taddr_s;
+  const int32_t e0 = i0 < i1 ? s_e0 : 0;
+  const int G = 1 << g.log2G;
+  const uint32_t half_q = p.q_bytes / 2;
 
   if (warp == 0) {
-    // ------------------------------------------------------- q~ and K tiles
+    // ------------------------------------------------------------ producer
     if (lane == 0) {
-      prefetch_tensormap(&kmap);
-      prefetch_tensormap(&qhmap0);
-      prefetch_tensormap(&qlmap0);
       const uint64_t keep = policy_evict_last();
-      uint32_t k = 0, seg = 0;
+      uint32_t k = 0, qi = 0;
       bool ok = true;
-      SegWalk walk(g, x0, x1);
-      Segment x;
+      KWalk walk(g, i0, i1, e0);
+      KItem x;
       while (ok && walk.next(&x)) {
-        if (seg > 0 && !mbar_wait(qempty, (seg - 1) & 1)) { ok = false; break; }
-        ++seg;
-        const int nbox = (x.ncols + kGAQBox - 1) / kGAQBox;
-        const int row = x.en.row0 * g.H + x.col0;
-        mbar_arrive_expect_tx(qfull, static_cast<uint32_t>(2 * p.kb * nbox * kGAQBox) * 128u);
-        for (int a = 0; a < p.kb; ++a)
-          for (int b = 0; b < nbox; ++b) {
-            uint8_t* d = smem + lay.q + static_cast<uint32_t>(a * ncap + b * kGAQBox) * 128u;
-            tma_load_2d(d, x.en.src ? &qhmap1 : &qhmap0, a * 64, row + b * kGAQBox, qfull, keep);
-            tma_load_2d(d + static_cast<uint32_t>(p.kb * ncap) * 128u, x.en.src ? &qlmap1 : &qlmap0, a * 64,
-                        row + b * kGAQBox, qfull, keep);
-          }
+        const int qs = static_cast<int>(qi % p.nq);
+        if (qi >= static_cast<uint32_t>(p.nq) && !mbar_wait(&qempty[qs], ((qi / p.nq) - 1) & 1)) { ok = false; break; }
+        uint8_t* qd = qslot + static_cast<size_t>(qs) * p.q_bytes;
+        if (x.narrow) {
+          const int nbox = (x.cols + kGKQBox - 1) / kGKQBox;
+          mbar_arrive_expect_tx(&qfull[qs], static_cast<uint32_t>(2 * p.kb * nbox * kGKQBox) * 128u);
+          for (int a = 0; a < p.kb; ++a)
+            for (int b = 0; b < nbox; ++b) {
+              const uint32_t o = static_cast<uint32_t>(a * g.ncol + b * kGKQBox) * 128u;
+              tma_load_2d(qd + o, &qhnmap, a * 64, x.row0 * g.H + b * kGKQBox, &qfull[qs], keep);
+              tma_load_2d(qd + half_q + o, &qlnmap, a * 64, x.row0 * g.H + b * kGKQBox, &qfull[qs], keep);
+            }
+        } else {
+          const int nbox = (x.cols + p.qbox - 1) / p.qbox;
+          const int rows_box = p.qbox >> g.log2G;
+          mbar_arrive_expect_tx(&qfull[qs], static_cast<uint32_t>(2 * p.kb * nbox * p.qbox) * 128u);
+          for (int a = 0; a < p.kb; ++a)
+            for (int b = 0; b < nbox; ++b) {
+              const uint32_t o = static_cast<uint32_t>(a * g.ncol + b * p.qbox) * 128u;
+              tma_load_3d(qd + o, &qhwmap, a * 64, x.j << g.log2G, x.row0 + b * rows_box, &qfull[qs], keep);
+              tma_load_3d(qd + half_q + o, &qlwmap, a * 64, x.j << g.log2G, x.row0 + b * rows_box, &qfull[qs], keep);
+            }
+        }
+        ++qi;
         const int32_t* trow = p.tables + static_cast<size_t>(x.en.tab) * g.MB + x.en.page0;
-        const int units = (x.b1 - x.b0) * x.nh;
-        for (int pass = 0; pass < 2 && ok; ++pass)
-          for (int i = c; i < units && ok; i += C) {
-            const int b = x.b0 + i / x.nh, j = x.j0 + i % x.nh;
-            const int np = (min(kGTok, x.en.len - b * kGTok) + kBlock - 1) / kBlock;
-            for (int a = 0; a < p.kb; ++a, ++k) {
-              const int s = static_cast<int>(k % KS);
-              if (k >= static_cast<uint32_t>(KS) && !mbar_wait(&kempty[s], ((k / KS) - 1) & 1)) { ok = false; break; }
-              uint8_t* st = smem + lay.k + s * 16384u;
-              mbar_arrive_expect_tx(&kfull[s], static_cast<uint32_t>(np) * 2048u);
-              for (int t = 0; t < np; ++t) {
-                int32_t phys = trow[b * (kGTok / kBlock) + t];
-                if (phys < 0 || phys >= g.NB) { set_flag(g.status, STARKV_FLAG_BAD_BLOCK_ID); phys = 0; }
-                tma_load_3d(st + t * 2048, &kmap, a * 64, j, phys * kBlock, &kfull[s], keep);
-              }
+        const int tb = x.narrow ? min(kBlock, x.step) : kBlock;           // tokens per box
+        const uint32_t box = x.narrow ? static_cast<uint32_t>(tb * g.Hkv) * 128u : 2048u;
+        for (int t = x.t0; t < x.t1; t += x.step, ++k) {
+          const int s = static_cast<int>(k % S);
+          if (k >= static_cast<uint32_t>(S) && !mbar_wait(&empty[s], ((k / S) - 1) & 1)) { ok = false; break; }
+          const int nb = (min(x.step, x.t1 - t) + tb - 1) / tb;
+          uint8_t* st = smem + static_cast<size_t>(s) * p.a_bytes;
+          mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nb * p.kb) * box);
+          for (int c = 0; c < nb; ++c) {
+            const int tk = t + c * tb;
+            int32_t phys = trow[tk / kBlock];
+            if (phys < 0 || phys >= g.NB) { set_flag(g.status, STARKV_FLAG_BAD_BLOCK_ID); phys = 0; }
+            const int row = phys * kBlock + (tk & (kBlock - 1));
+            for (int a = 0; a < p.kb; ++a) {
+              if (x.narrow) tma_load_3d(st + a * 16384 + c * box, &knmap, a * 64, 0, row, &full[s], keep);
+              else tma_load_3d(st + a * 16384 + c * box, &kwmap, a * 64, x.j, row, &full[s], keep);
             }
           }
+        }
       }
       if (!ok) {
         set_timeout(g.status, kSiteKEmpty);
         abort_flag = 1;
       }
       // copies still in flight land before the CTA can exit
-      for (uint32_t i = k >= static_cast<uint32_t>(KS) ? k - KS : 0u; i < k; ++i) mbar_wait(&kfull[i % KS], (i / KS) & 1);
-      if (seg > 0) mbar_wait(qfull, (seg - 1) & 1);
+      const uint32_t f0 = k >= static_cast<uint32_t>(S) ? k - S : 0u;
+      for (uint32_t kk = f0; kk < k; ++kk) mbar_wait(&full[kk % S], (kk / S) & 1);
+      const uint32_t q0 = qi >= static_cast<uint32_t>(p.nq) ? qi - p.nq : 0u;
+      for (uint32_t kk = q0; kk < qi; ++kk) mbar_wait(&qfull[kk % p.nq], (kk / p.nq) & 1);
     }
   } else if (warp == 1) {
-    // ----------------------------------------------------------- S products
+    // ----------------------------------------------------------------- MMA
     if (lane == 0) {
-      uint32_t k = 0, seg = 0, u = 0;
+      uint32_t k = 0, qi = 0;
       bool ok = true;
-      SegWalk walk(g, x0, x1);
-      Segment x;
+      KWalk walk(g, i0, i1, e0);
+      KItem x;
       while (ok && walk.next(&x)) {
-        if (!mbar_wait(qfull, seg & 1)) { ok = false; break; }
-        ++seg;
-        const int units = (x.b1 - x.b0) * x.nh;
-        for (int pass = 0; pass < 2 && ok; ++pass)
-          for (int i = c; i < units && ok; i += C, ++u) {
-            // the head's columns, widened to whole groups of eight q~ rows
-            const int f = (i % x.nh) * x.mt, w0 = f & ~7;
-            const int n = (f + x.mt - w0 + 15) / 16 * 16;
-            const uint32_t idesc = idesc_f16_f32(128, n, /*a_mn_major=*/false, /*b_mn_major=*/false);
-            const int a = u & 1;
-            if (u >= 2 && !mbar_wait(&tempty[a], ((u / 2) - 1) & 1)) { ok = false; break; }
-            const uint32_t dst = taddr + 256u + a * 128u;
-            int ks = 0;
-            for (int kbi = 0; kbi < p.kb; ++kbi, ++k) {
-              const int s = static_cast<int>(k % KS);
-              if (!mbar_wait(&kfull[s], (k / KS) & 1) || abort_flag) { ok = false; break; }
-              tc_fence_after();
-              const uint32_t sa = smem_u32(smem + lay.k + s * 16384u);
-              const uint32_t sq = smem_u32(smem + lay.q) + static_cast<uint32_t>(kbi * ncap + w0) * 128u;
-              for (int kk = 0; kk < 4 && ks < p.ksteps; ++kk, ++ks) {
-                const uint64_t ad = smem_desc(sa + kk * 32u, 16u, 1024u, kSwizzle128B);
-                const uint32_t bo = sq + kk * 32u;
-                umma_f16_ss(dst, ad, smem_desc(bo, 16u, 1024u, kSwizzle128B), idesc, ks > 0 ? 1u : 0u);
-                umma_f16_ss(dst, ad, smem_desc(bo + static_cast<uint32_t>(p.kb * ncap) * 128u, 16u, 1024u, kSwizzle128B),
-                            idesc, 1u);
-              }
-              umma_commit(&kempty[s]);
-            }
-            if (ok) umma_commit(&tfull[a]);
+        const int qs = static_cast<int>(qi % p.nq);
+        if (!mbar_wait(&qfull[qs], (qi / p.nq) & 1)) { ok = false; break; }
+        const int nmma = (x.cols + 15) / 16 * 16;
+        const uint32_t idesc = idesc_f16_f32(128, nmma, /*a_mn_major=*/false, /*b_mn_major=*/false);
+        const uint32_t sq = smem_u32(qslot + static_cast<size_t>(qs) * p.q_bytes);
+        for (int t = x.t0; t < x.t1; t += x.step, ++k) {
+          const int s = static_cast<int>(k % S), a = static_cast<int>(k % kGKAcc);
+          if (k >= kGKAcc && !mbar_wait(&tempty[a], ((k / kGKAcc) - 1) & 1)) { ok = false; break; }
+          if (!mbar_wait(&full[s], (k / S) & 1) || abort_flag) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + static_cast<size_t>(s) * p.a_bytes);
+          const uint32_t dst = taddr + static_cast<uint32_t>(a * g.ncol);
+          for (int ks = 0; ks < p.ksteps; ++ks) {
+            const uint32_t blk = ks >> 2, off = (ks & 3) * 32u;
+            const uint64_t ad = smem_desc(sa + blk * 16384u + off, 16u, 1024u, kSwizzle128B);
+            const uint32_t bo = sq + blk * static_cast<uint32_t>(g.ncol) * 128u + off;
+            umma_f16_ss(dst, ad, smem_desc(bo, 16u, 1024u, kSwizzle128B), idesc, ks > 0 ? 1u : 0u);
+            umma_f16_ss(dst, ad, smem_desc(bo + half_q, 16u, 1024u, kSwizzle128B), idesc, 1u);
           }
-        umma_commit(qempty);
+          umma_commit(&empty[s]);
+          umma_commit(&tfull[a]);
+        }
+        umma_commit(&qempty[qs]);
+        ++qi;
       }
       if (!ok) { set_timeout(g.status, kSiteKFull); abort_flag = 1; }
-      umma_commit(sdone);
-      if (!mbar_wait(sdone, 0)) set_timeout(g.status, kSiteVMdone);
+      umma_commit(mmadone);
+      mbar_wait(mmadone, 0);
     }
-  } else if (warp == 2) {
-    // -------------------------------------------------------------- V tiles
-    // The whole warp walks; lane 0 issues the copies.  A page that the entry's
-    // end leaves partly filled is zeroed behind it, so that whatever its unused
-    // slots hold contributes exactly 0.
-    if (lane == 0) prefetch_tensormap(&vmap);
-    const uint64_t pol_once = policy_evict_first(), pol_keep = policy_evict_last();
-    uint32_t k = 0;
-    bool ok = true;
-    SegWalk walk(g, x0, x1);
-    Segment x;
-    while (ok && walk.next(&x)) {
-      const int32_t* trow = p.tables + static_cast<size_t>(x.en.tab) * g.MB + x.en.page0;
-      const int chunk0 = (x.slab * C + c) * g.nch;
-      const uint64_t pol = x.en.src ? pol_once : pol_keep;
-      const int tend = min(x.en.len, x.b1 * kGTok);
-      for (int t0 = x.b0 * kGTok; t0 < tend && ok; t0 += kGAVTok, ++k) {
-        const int s = static_cast<int>(k % VS);
-        const int nt = min(kGAVTok, tend - t0), np = (nt + kBlock - 1) / kBlock;
-        uint8_t* st = smem + lay.v + static_cast<size_t>(s) * p.v_stage_bytes;
-        if (lane == 0) {
-          if (k >= static_cast<uint32_t>(VS) && !mbar_wait(&vempty[s], ((k / VS) - 1) & 1)) {
-            ok = false;
-          } else {
-            mbar_arrive_expect_tx(&vfull[s], static_cast<uint32_t>(np * g.nch) * 2048u);
-            for (int t = 0; t < np; ++t) {
-              int32_t phys = trow[t0 / kBlock + t];
-              if (phys < 0 || phys >= g.NB) { set_flag(g.status, STARKV_FLAG_BAD_BLOCK_ID); phys = 0; }
-              tma_load_3d(st + t * g.nch * 2048, &vmap, 0, phys * kBlock, chunk0, &vfull[s], pol);
-            }
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        const int ntl = nt & (kBlock - 1);
-        if (ok && ntl) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&vfull[s], (k / VS) & 1))) { ok = false; break; }
-          uint8_t* pg = st + (np - 1) * g.nch * 2048;
-          const int nz = kBlock - ntl;
-          for (int y = lane; y < g.nch * nz * 8; y += 32) {
-            const int ch = y / (nz * 8), rem = y % (nz * 8);
-            *reinterpret_cast<uint4*>(pg + ch * 2048 + (ntl + rem / 8) * 128 + (rem % 8) * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        if (ok && lane == 0) mbar_arrive(&vfix[s]);
-      }
-    }
-    if (lane == 0) {
-      if (!ok) {
-        set_timeout(g.status, kSiteVEmpty);
-        abort_flag = 1;
-      }
-      for (uint32_t i = k >= static_cast<uint32_t>(VS) ? k - VS : 0u; i < k; ++i) mbar_wait(&vfull[i % VS], (i / VS) & 1);
-    }
-  } else if (warp == 3) {
-    // ----------------------------------------------------------- Z products
-    if (lane == 0) {
-      uint32_t k = 0, seg = 0, blk = 0;
-      bool ok = true;
-      SegWalk walk(g, x0, x1);
-      Segment x;
-      while (ok && walk.next(&x)) {
-        const int n = (x.ncols + 15) / 16 * 16;
-        const uint32_t idesc = idesc_f16_f32(128, n, /*a_mn_major=*/true, /*b_mn_major=*/false);
-        const int codes = g.R - (x.slab * C + c) * g.nch * 64;          // codes of R left for this CTA
-        const int mts = (min(codes, g.nch * 64) + 127) / 128;           // 128-row tiles (<= 0: none)
-        if (seg > 0 && !mbar_wait(zfree, (seg - 1) & 1)) { ok = false; break; }
-        ++seg;
-        uint32_t acc = 0;
-        for (int b = x.b0; b < x.b1 && ok; ++b, ++blk) {
-          const int a = blk & 1;
-          if (!mbar_wait(&pfull[a], (blk / 2) & 1) || abort_flag) { ok = false; break; }
-          const uint32_t sp = smem_u32(smem + lay.p) + a * static_cast<uint32_t>(ncap) * 256u;
-          const int nt = min(kGTok, x.en.len - b * kGTok);
-          for (int t = 0; t < nt; t += kGAVTok, ++k) {
-            const int s = static_cast<int>(k % VS);
-            if (!mbar_wait(&vfull[s], (k / VS) & 1) || !mbar_wait(&vfix[s], (k / VS) & 1) || abort_flag) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t sv = smem_u32(smem + lay.v + static_cast<size_t>(s) * p.v_stage_bytes);
-            const int np = (min(kGAVTok, nt - t) + kBlock - 1) / kBlock;
-            for (int pg = 0; pg < np; ++pg) {
-              const int tk = t + pg * kBlock;
-              const uint64_t bd = smem_desc(sp + (tk >> 6) * static_cast<uint32_t>(ncap) * 128u + (tk & 63) * 2u, 16u, 1024u,
-                                            kSwizzle128B);
-              for (int m = 0; m < mts; ++m)
-                umma_f16_ss(taddr + m * 128u, smem_desc(sv + pg * g.nch * 2048u + m * 4096u, 2048u, 1024u, kSwizzle128B), bd,
-                            idesc, acc);
-              acc = 1;
-            }
-            umma_commit(&vempty[s]);
-          }
-          if (!ok) break;
-          umma_commit(&pdone[a]);
-        }
-        if (ok) umma_commit(zdone);
-      }
-      if (!ok) { set_timeout(g.status, kSiteVFull); abort_flag = 1; }
-      umma_commit(mdone);
-      if (!mbar_wait(mdone, 0)) set_timeout(g.status, kSiteVMdone);
-    }
-  } else if (warp == 12) {
-    // ------------------------------------------- consumed P blocks, to all CTAs
-    uint32_t blk = 0;
-    bool ok = true;
-    SegWalk walk(g, x0, x1);
-    Segment x;
-    while (ok && walk.next(&x))
-      for (int b = x.b0; b < x.b1; ++b, ++blk) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&pdone[blk & 1], (blk / 2) & 1) && !abort_flag)) { ok = false; break; }
-        if (lane < C) mbar_arrive_cluster(&pempty[blk & 1], static_cast<uint32_t>(lane));
-        __syncwarp();
-      }
-    if (!ok && lane == 0) { set_timeout(g.status, kSiteVTfree); abort_flag = 1; }
   } else {
-    // -------------------------------------------- maxima, weights, Z stores
-    const int et = tid - 128;
-    const int q = warp & 3, hf = (warp - 4) >> 2;     // TMEM lane quarter; which blocks of 16 columns
+    // ------------------------------------------------------------ epilogue
+    const int et = tid - 64;
+    const int q = warp & 3, hf = (warp - 2) >> 2;
     const uint32_t tq = taddr + (static_cast<uint32_t>(q * 32) << 16);
-    const uint64_t keep = policy_evict_last();
-    uint32_t u = 0, seg = 0, blk = 0, phase = 0;
+    uint32_t k = 0, phase = 0;
     bool ok = true;
-    SegWalk walk(g, x0, x1);
-    Segment x;
+    KWalk walk(g, i0, i1, e0);
+    KItem x;
     while (ok && walk.next(&x)) {
-      const int units = (x.b1 - x.b0) * x.nh;
-      for (int y = et; y < 4 * ncap; y += kGAEpi) { s_qmax[y] = -INFINITY; s_qsum[y] = 0.f; }
+      const int t_pad = g.t_pad[x.en.psrc];
+      __half* P = kWeights ? p.P[x.en.psrc] : nullptr;
+      // per column: its P row (-1: the row does not attend over these pages) and maximum
       if (!group_sync(ebar, phase)) { ok = false; break; }
-      // ---- phase A
-      for (int i = c; i < units; i += C, ++u) {
-        const int a = u & 1;
-        const bool ready = mbar_wait(&tfull[a], (u / 2) & 1);
-        if (!__all_sync(0xffffffffu, ready && !abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        const int f = (i % x.nh) * x.mt, w0 = f & ~7, fe = f + x.mt;
-        // all ones for a token of the entry; a mask and not a condition, so that no
-        // loop around the warp-wide loads below is split by lane
-        const uint32_t in = (x.b0 + i / x.nh) * kGTok + q * 32 + lane < x.en.len ? 0xffffffffu : 0u;
-        for (int cb = w0 + hf * 16; cb < fe; cb += 32) {
-          __syncwarp();
-          uint32_t v[32];
-          tmem_ld_32x32b_x16(tq + 256u + a * 128u + (cb - w0), v);
-          tmem_ld_wait();
-          float mine = -INFINITY;
-#pragma unroll
-          for (int y = 0; y < 16; ++y) {
-            const float m = warp_max_f32(__uint_as_float((v[y] & in) | (~in & 0xff800000u)));   // -inf behind the end
-            if (lane == y) mine = m;
-          }
-          const int tc = cb + lane;
-          if (lane < 16 && tc >= f && tc < fe) s_qmax[q * ncap + tc] = fmaxf(s_qmax[q * ncap + tc], mine);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty[a]);
-      }
-      if (!ok) break;
-      if (!group_sync(ebar, phase)) { ok = false; break; }
-      // ---- the tile's maxima over all CTAs of the cluster
-      const int par = seg & 1;
-      float* mx = s_mx + par * kGAMaxC * ncap;
-      if (et < ncap)
-        mx[c * ncap + et] =
-            fmaxf(fmaxf(s_qmax[et], s_qmax[ncap + et]), fmaxf(s_qmax[2 * ncap + et], s_qmax[3 * ncap + et]));
-      if (C > 1) {
-        fence_proxy_async_smem();
-        if (!group_sync(ebar, phase)) { ok = false; break; }
-        if (et == 0) {
-          mbar_arrive_expect_tx(&mxbar[par], static_cast<uint32_t>((C - 1) * ncap) * 4u);
-          for (int o = 1; o < C; ++o) {
-            const uint32_t to = static_cast<uint32_t>(c + o < C ? c + o : c + o - C);
-            bulk_s2cluster(mx + c * ncap, to, static_cast<uint32_t>(ncap) * 4u, &mxbar[par]);
+      if (et < 128) {
+        int32_t rh = -1;
+        float m = 0.f;
+        if (et < x.cols) {
+          const int row = x.row0 + (x.narrow ? et / g.H : et >> g.log2G);
+          const int h = x.narrow ? et & (g.H - 1) : (x.j << g.log2G) + (et & (G - 1));
+          if (x.en.zsrc || g.row_use[row]) {
+            rh = row * g.H + h;
+            if (kWeights) m = g.mrow[rh];
           }
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(&mxbar[par], (seg / 2) & 1) && !abort_flag)) { ok = false; break; }
-      } else if (!group_sync(ebar, phase)) {
-        ok = false;
-        break;
-      }
-      ++seg;
-      if (et < ncap) {
-        float m = mx[et];
-        for (int o = 1; o < C; ++o) m = fmaxf(m, mx[o * ncap + et]);
+        s_rh[et] = rh;
+        s_off[et] = rh < 0 ? -1 : static_cast<int64_t>(rh) * t_pad;
         s_m[et] = m;
+        if (kWeights)
+          for (int u = 0; u < 4; ++u) s_red[u][et] = 0.f;
       }
       if (!group_sync(ebar, phase)) { ok = false; break; }
-      // ---- phase B
-      int i = c;
-      for (int b = x.b0; b < x.b1; ++b, ++blk) {
-        const int a2 = blk & 1;
-        if (blk >= 2) {
-          const bool free2 = mbar_wait(&pempty[a2], ((blk / 2) - 1) & 1);
-          if (!__all_sync(0xffffffffu, free2 && !abort_flag)) { ok = false; break; }
+      if (x.narrow) {
+        // lane: code row rho = q * 32 + lane of the step, i.e. token rho / Hkv, KV head
+        // rho % Hkv; value i is (row i / G of the entry, query head i % G of the head)
+        const int rho = q * 32 + lane, j = rho & (g.Hkv - 1), tl = rho >> p.log2Hkv;
+        const int ng = x.nrow << g.log2G;
+        float* st = stage + static_cast<size_t>(q * 32 + lane) * (g.ncol + 4);
+        float run[kGNarrowPer];
+#pragma unroll
+        for (int i = 0; i < kGNarrowPer; ++i) run[i] = kWeights ? 0.f : -INFINITY;
+        for (int tb = x.t0; tb < x.t1; tb += x.step, ++k) {
+          const int a = static_cast<int>(k % kGKAcc);
+          const bool ready = mbar_wait(&tfull[a], (k / kGKAcc) & 1);
+          if (!__all_sync(0xffffffffu, ready && !abort_flag)) { ok = false; break; }
+          if (hf == 0) {
+            tc_fence_after();
+            for (int cb = 0; cb < x.cols; cb += 16) {
+              __syncwarp();
+              uint32_t v[32];
+              tmem_ld_32x32b_x16(tq + static_cast<uint32_t>(a * g.ncol + cb), v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                *reinterpret_cast<uint4*>(st + cb + 4 * u) = make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+            }
+            tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[a]);
+          if (hf == 0) {
+            const int t = tb + tl;
+            const bool in = t < x.en.len;
+            const bool page = t < x.t1;
+#pragma unroll
+            for (int i = 0; i < kGNarrowPer; ++i) {
+              if (i < ng) {
+                const int col = (i >> g.log2G) * g.H + (j << g.log2G) + (i & (G - 1));
+                const float s = st[col];
+                if constexpr (kWeights) {
+                  const __half w = __float2half_rn(in ? ex2_approx(s - s_m[col]) : 0.f);
+                  run[i] += __half2float(w);
+                  if (page && s_off[col] >= 0) P[s_off[col] + t] = w;
+                } else {
+                  run[i] = fmaxf(run[i], in ? s : -INFINITY);
+                }
+              }
+            }
+          }
         }
-        uint8_t* pb = smem + lay.p + a2 * static_cast<uint32_t>(ncap) * 256u;
-        const int t = q * 32 + lane;                          // token of the block
-        const uint32_t in = b * kGTok + t < x.en.len ? 0xffffffffu : 0u;
-        uint8_t* prow = pb + (t >> 6) * static_cast<uint32_t>(ncap) * 128u + (t & 7) * 2;
-        const uint32_t tchunk = static_cast<uint32_t>(t & 63) >> 3;
-        int own = 0;
-        const int stop = (b + 1 - x.b0) * x.nh;
-        for (; i < stop; i += C, ++u, ++own) {
-          const int a = u & 1;
-          const bool ready = mbar_wait(&tfull[a], (u / 2) & 1);
+        if (!ok) break;
+        if (hf == 0) {
+          // lanes of the same KV head join: lane l < Hkv (or every lane) speaks for its head
+#pragma unroll
+          for (int i = 0; i < kGNarrowPer; ++i)
+            if (i < ng) {
+              for (int o = 16; o >= g.Hkv; o >>= 1) {
+                const float y = __shfl_xor_sync(0xffffffffu, run[i], o);
+                run[i] = kWeights ? run[i] + y : fmaxf(run[i], y);
+              }
+              const int col = (i >> g.log2G) * g.H + (j << g.log2G) + (i & (G - 1));
+              if (lane < g.Hkv) {
+                if constexpr (kWeights) s_red[q][col] = run[i];
+                else if (s_rh[col] >= 0 && run[i] > -INFINITY) atomic_max_f32(&g.mrow[s_rh[col]], run[i]);
+              }
+            }
+        }
+      } else {
+        const int ncb = (x.cols + 15) / 16;
+        float run[4][16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int u = 0; u < 16; ++u) run[i][u] = kWeights ? 0.f : -INFINITY;
+        for (int tb = x.t0; tb < x.t1; tb += 128, ++k) {
+          const int a = static_cast<int>(k % kGKAcc);
+          const bool ready = mbar_wait(&tfull[a], (k / kGKAcc) & 1);
           if (!__all_sync(0xffffffffu, ready && !abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const int f = (i % x.nh) * x.mt, w0 = f & ~7, fe = f + x.mt;
-          for (int cb = w0 + hf * 16; cb < fe; cb += 32) {
-            __syncwarp();
-            uint32_t v[32];
-            tmem_ld_32x32b_x16(tq + 256u + a * 128u + (cb - w0), v);
-            tmem_ld_wait();
-            float w[16];
+          const int t = tb + q * 32 + lane;
+          const uint32_t in = t < x.en.len ? 0xffffffffu : 0u;   // a mask: no loop around the warp-wide loads splits by lane
 #pragma unroll
-            for (int y = 0; y < 16; ++y) {
-              const int tc = cb + y;
-              // a weight in (0, 1], rounded to fp16 for the products; the sum takes the rounded weights
-              const float e = ex2_approx(__uint_as_float(v[y]) - s_m[tc < ncap ? tc : 0]);
-              const __half hw = __float2half_rn(__uint_as_float(__float_as_uint(e) & in));   // 0 behind the end
-              w[y] = __half2float(hw);
-              if (tc >= f && tc < fe)
-                *reinterpret_cast<__half*>(prow + tc * 128 + ((tchunk ^ (static_cast<uint32_t>(tc) & 7u)) << 4)) = hw;
+          for (int i = 0; i < 4; ++i) {
+            const int cb = hf + 2 * i;
+            if (cb < ncb) {
+              __syncwarp();
+              uint32_t v[32];
+              tmem_ld_32x32b_x16(tq + static_cast<uint32_t>(a * g.ncol + cb * 16), v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int u = 0; u < 16; ++u) {
+                const int c = cb * 16 + u;
+                if constexpr (kWeights) {
+                  const float e = ex2_approx(__uint_as_float(v[u]) - s_m[c]);
+                  const __half w = __float2half_rn(__uint_as_float(__float_as_uint(e) & in));
+                  run[i][u] += __half2float(w);
+                  const int64_t off = s_off[c];
+                  if (off >= 0) P[off + t] = w;
+                } else {
+                  run[i][u] = fmaxf(run[i][u], __uint_as_float((v[u] & in) | (~in & 0xff800000u)));
+                }
+              }
             }
-            const float sum = lane_sum16(w, lane);
-            const int tc = cb + (lane >> 1);
-            if ((lane & 1) == 0 && tc >= f && tc < fe) s_qsum[q * ncap + tc] += sum;
           }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&tempty[a]);
-          fence_proxy_async_smem();
-          if (!group_sync(ebar, phase)) { ok = false; break; }
-          // the unit's columns to the other CTAs, two halves of 64 tokens each: one
-          // lane of every warp takes the next destination
-          if (C > 1 && lane == 0) {
-            for (int o = warp - 3; o < C; o += kGAEpi / 32) {
-              const uint32_t to = static_cast<uint32_t>(c + o < C ? c + o : c + o - C);
-              bulk_s2cluster(pb + f * 128, to, static_cast<uint32_t>(x.mt) * 128u, &pfull[a2]);
-              bulk_s2cluster(pb + static_cast<uint32_t>(ncap) * 128u + f * 128, to, static_cast<uint32_t>(x.mt) * 128u,
-                             &pfull[a2]);
-            }
-          }
-          __syncwarp();
         }
         if (!ok) break;
-        // armed after this CTA's own units: it now waits for the others' bytes only
-        if (et == 0) mbar_arrive_expect_tx(&pfull[a2], static_cast<uint32_t>((x.nh - own) * x.mt) * 256u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int cb = hf + 2 * i;
+          if (cb < ncb) {
+            if constexpr (kWeights) {
+              const float sum = lane_sum16(run[i], lane);
+              if ((lane & 1) == 0) s_red[q][cb * 16 + (lane >> 1)] = sum;
+            } else {
+              float mine = -INFINITY;
+#pragma unroll
+              for (int u = 0; u < 16; ++u) {
+                const float m = warp_max_f32(run[i][u]);
+                if (lane == u) mine = m;
+              }
+              const int c = cb * 16 + (lane & 15);
+              if (lane < 16 && s_rh[c] >= 0 && mine > -INFINITY) atomic_max_f32(&g.mrow[s_rh[c]], mine);
+            }
+          }
+        }
       }
-      if (!ok) break;
-      // ---- Z, m and l of the segment
-      const bool done = mbar_wait(zdone, (seg - 1) & 1);
-      if (!__all_sync(0xffffffffu, done && !abort_flag)) { ok = false; break; }
+      if constexpr (kWeights) {
+        if (!group_sync(ebar, phase)) { ok = false; break; }
+        if (et < x.cols && s_rh[et] >= 0) {
+          const float L = ((s_red[0][et] + s_red[1][et]) + s_red[2][et]) + s_red[3][et];
+          g.lpart[x.en.zsrc][static_cast<size_t>(s_rh[et]) * g.n_ch[x.en.zsrc] + x.c] = L;
+        }
+      }
+    }
+    if (!ok) { set_timeout(g.status, kSiteKFull); abort_flag = 1; }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(taddr, p.tmem_cols);
+  }
+}
+
+// ================================================================== V pass
+// Z^T (256 rows of R x up to 256 columns) += C_V^T . P^T over the tokens of an
+// entry, 64 tokens (4 pages) per stage: A = the pages' codes (MN-major, one TMA
+// box of 256 codes x 16 tokens per page), B = the P rows of the tile's (row,
+// head) columns (K-major).  A unit is one stage of one tile; the units of all
+// tiles are laid end to end and CTA i of n takes [floor(i U / n), floor((i+1)
+// U / n)).  The sum of a tile that begins in a CTA's range goes to the Z matrix
+// of its source, that of a tile carried over from the CTA before goes to the
+// CTA's carry slot, so a tile's partial sums have fixed places and order.
+struct GroupVParams {
+  GroupGeom g;
+  const int32_t* tables;
+  float* Z[2];          // [n_rows * H][R] by zsrc
+  float* zcarry;        // [CTAs][256 columns][256]
+  int stages;
+  uint32_t stage_bytes;
+};
+
+constexpr int kGVThreads = 320;                    // warp 0 TMA, warp 1 MMA, warps 2..9 store
+constexpr int kGVEpi = kGVThreads - 64;
+constexpr uint32_t kGVABytes = 4u * 8192u;         // 4 pages x 16 tokens x 256 codes
+constexpr uint32_t kGVBBytes = kGVTile * 128u;     // 256 columns x 64 tokens
+constexpr int kGVPBox = 32;                        // P rows per TMA box
+constexpr int kGVMinUnits = 3;                     // units per CTA at least, in a call with few
+
+struct VSeg {
+  GroupEntry en;
+  int tile, rt, col0, ncols, n;  // tile of all, R tile, first column, columns, UMMA N
+  int u0, u1;                    // units of the tile taken by this CTA
+  bool first, last;              // the tile begins / ends here
+};
+
+struct VWalk {
+  const GroupGeom& g;
+  int32_t u, end, ebeg, eend, e;
+  GroupEntry en;
+  __device__ VWalk(const GroupGeom& g_, int32_t a, int32_t b, int32_t e0) : g(g_), u(a), end(b), ebeg(0), eend(0), e(e0) {
+    if (u < end) {
+      ebeg = g.vpre[e];
+      eend = g.vpre[e + 1];
+      en = g.ent[e];
+    }
+  }
+  __device__ bool next(VSeg* s) {
+    if (u >= end) return false;
+    while (u >= eend) { ++e; ebeg = eend; eend = g.vpre[e + 1]; if (u < eend) en = g.ent[e]; }
+    const uint32_t units = (en.len + kGVTok - 1) / kGVTok;
+    const uint32_t local = static_cast<uint32_t>(u - ebeg);
+    const uint32_t tile = local / units;
+    const uint32_t nt = tile / static_cast<uint32_t>(g.n_rt);
+    const int cols = en.nrows * g.H;
+    const int width = gv_width(cols, gv_tiles(cols));
+    s->en = en;
+    s->tile = en.tile0 + static_cast<int>(tile);
+    s->rt = static_cast<int>(tile - nt * g.n_rt);
+    s->col0 = static_cast<int>(nt) * width;
+    s->ncols = min(width, cols - s->col0);
+    s->n = (s->ncols + 15) / 16 * 16;
+    s->u0 = static_cast<int>(local - tile * units);
+    s->u1 = min(static_cast<int>(units), s->u0 + end - u);
+    s->first = s->u0 == 0;
+    s->last = s->u1 == static_cast<int>(units);
+    u += s->u1 - s->u0;
+    return true;
+  }
+};
+
+__global__ void __launch_bounds__(kGVThreads, 1)
+group_vpass_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap pmap0,
+                   const __grid_constant__ CUtensorMap pmap1, GroupVParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = align_smem_1024(smem_raw);
+  const GroupGeom& g = p.g;
+  const int S = p.stages;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(S) * p.stage_bytes);
+  uint64_t* empty = full + S;
+  uint64_t* zdone = empty + S;     // [2] a segment's products are complete
+  uint64_t* tfree = zdone + 2;     // [2] its accumulator has been stored
+  uint64_t* fixreq = tfree + 2;    // a partly filled page has landed
+  uint64_t* fixed = fixreq + 1;    // its rows past the end are zero
+  uint64_t* mmadone = fixed + 1;
+  __shared__ uint32_t taddr_s;
+  __shared__ int32_t s_e0;
+  __shared__ volatile int32_t abort_flag;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int a = 0; a < 2; ++a) { mbar_init(&zdone[a], 1); mbar_init(&tfree[a], kGVEpi / 32); }
+    mbar_init(fixreq, 1);
+    mbar_init(fixed, kGVEpi);
+    mbar_init(mmadone, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&vmap);
+    prefetch_tensormap(&pmap0);
+    prefetch_tensormap(&pmap1);
+  }
+  if (warp == 1) {
+    tmem_alloc(&taddr_s, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  Partition pt;
+  pt.P = g.vpre[g.E];
+  pt.G = static_cast<int32_t>(min(static_cast<int64_t>(gridDim.x), max(pt.P / kGVMinUnits, int64_t{1})));
+  const int cta = blockIdx.x;
+  const bool live = cta < pt.G;
+  const int32_t u0 = live ? static_cast<int32_t>(part_begin(cta, pt)) : 0;
+  const int32_t u1 = live ? static_cast<int32_t>(part_begin(cta + 1, pt)) : 0;
+  if (u0 < u1) find_entry(g.vpre, g.E, u0, &s_e0);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t taddr = taddr_s;
+  const int32_t e0 = u0 < u1 ? s_e0 : 0;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      const uint64_t pol_once = policy_evict_first(), pol_keep = policy_evict_last();
+      uint32_t k = 0;
+      bool ok = true;
+      VWalk walk(g, u0, u1, e0);
+      VSeg x;
+      while (ok && walk.next(&x)) {
+        const int32_t* trow = p.tables + static_cast<size_t>(x.en.tab) * g.MB + x.en.page0;
+        const int nbox = (x.n + kGVPBox - 1) / kGVPBox;
+        const int prow = x.en.row0 * g.H + x.col0;
+        const uint64_t pol = x.en.zsrc ? pol_once : pol_keep;
+        for (int u = x.u0; u < x.u1; ++u, ++k) {
+          const int s = static_cast<int>(k % S);
+          if (k >= static_cast<uint32_t>(S) && !mbar_wait(&empty[s], ((k / S) - 1) & 1)) { ok = false; break; }
+          const int t0 = u * kGVTok;
+          const int np = (min(kGVTok, x.en.len - t0) + kBlock - 1) / kBlock;
+          uint8_t* st = smem + static_cast<size_t>(s) * p.stage_bytes;
+          mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(np) * 8192u + static_cast<uint32_t>(nbox) * kGVPBox * 128u);
+          for (int c = 0; c < np; ++c) {
+            int32_t phys = trow[t0 / kBlock + c];
+            if (phys < 0 || phys >= g.NB) { set_flag(g.status, STARKV_FLAG_BAD_BLOCK_ID); phys = 0; }
+            tma_load_3d(st + c * 8192, &vmap, 0, phys * kBlock, x.rt * 4, &full[s], pol);
+          }
+          for (int b = 0; b < nbox; ++b) {
+            if (x.en.psrc) tma_load_2d(st + kGVABytes + b * kGVPBox * 128, &pmap1, t0, prow + b * kGVPBox, &full[s], pol);
+            else tma_load_2d(st + kGVABytes + b * kGVPBox * 128, &pmap0, t0, prow + b * kGVPBox, &full[s], pol);
+          }
+        }
+      }
+      if (!ok) {
+        set_timeout(g.status, kSiteVEmpty);
+        abort_flag = 1;
+      }
+      const uint32_t f0 = k >= static_cast<uint32_t>(S) ? k - S : 0u;
+      for (uint32_t kk = f0; kk < k; ++kk) mbar_wait(&full[kk % S], (kk / S) & 1);
+    }
+  } else if (warp == 1) {
+    // ----------------------------------------------------------------- MMA
+    // Segments of up to 128 columns alternate between two accumulators (256
+    // columns of tensor memory each, two 128-row tiles); a wider one takes both.
+    if (lane == 0) {
+      uint32_t k = 0, seg = 0, fix = 0;
+      bool ok = true, wide_before = false;
+      VWalk walk(g, u0, u1, e0);
+      VSeg x;
+      while (ok && walk.next(&x)) {
+        const uint32_t idesc = idesc_f16_f32(128, x.n, /*a_mn_major=*/true, /*b_mn_major=*/false);
+        const int mts = x.rt * kGVTile + 128 < g.R ? 2 : 1;
+        const bool wide = x.n > 128;
+        const uint32_t base = taddr + (wide ? 0u : (seg & 1) * 256u), mstep = wide ? 256u : 128u;
+        if (seg > 1 && !mbar_wait(&tfree[seg & 1], ((seg >> 1) - 1) & 1)) { ok = false; break; }
+        if (seg > 0 && (wide || wide_before) && !mbar_wait(&tfree[(seg - 1) & 1], ((seg - 1) >> 1) & 1)) { ok = false; break; }
+        wide_before = wide;
+        uint32_t acc = 0;
+        for (int u = x.u0; u < x.u1; ++u, ++k) {
+          const int s = static_cast<int>(k % S);
+          if (!mbar_wait(&full[s], (k / S) & 1) || abort_flag) { ok = false; break; }
+          const int nt = min(kGVTok, x.en.len - u * kGVTok);
+          if (nt & (kBlock - 1)) {   // a page that ends inside: its rows past the end are zeroed first
+            mbar_arrive(fixreq);
+            if (!mbar_wait(fixed, fix & 1)) { ok = false; break; }
+            ++fix;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + static_cast<size_t>(s) * p.stage_bytes);
+          const int np = (nt + kBlock - 1) / kBlock;
+          for (int c = 0; c < np; ++c) {
+            const uint64_t bd = smem_desc(sa + kGVABytes + c * 32u, 16u, 1024u, kSwizzle128B);
+            for (int m = 0; m < mts; ++m)
+              umma_f16_ss(base + m * mstep, smem_desc(sa + c * 8192u + m * 4096u, 2048u, 1024u, kSwizzle128B), bd, idesc,
+                          acc);
+            acc = 1;
+          }
+          umma_commit(&empty[s]);
+        }
+        if (!ok) break;
+        umma_commit(&zdone[seg & 1]);
+        ++seg;
+      }
+      if (!ok) { set_timeout(g.status, kSiteVFull); abort_flag = 1; }
+      umma_commit(mmadone);
+      if (!mbar_wait(mmadone, 0)) set_timeout(g.status, kSiteVMdone);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int et = tid - 64, q = warp & 3, hf = (warp - 2) >> 2, i4 = lane & 3;
+    uint32_t seg = 0, fix = 0, k = 0;
+    const uint64_t keep = policy_evict_last();   // partial sums: read back by the finish kernel
+    VWalk walk(g, u0, u1, e0);
+    VSeg x;
+    while (walk.next(&x)) {
+      k += static_cast<uint32_t>(x.u1 - x.u0);
+      const int ntl = x.en.len & (kBlock - 1);
+      if (x.last && ntl) {
+        if (!__all_sync(0xffffffffu, mbar_wait(fixreq, fix & 1))) { set_timeout(g.status, kSiteVPready); abort_flag = 1; break; }
+        ++fix;
+        const int c = ((x.en.len - 1) / kBlock) & 3;
+        uint8_t* pg = smem + static_cast<size_t>((k - 1) % S) * p.stage_bytes + c * 8192;
+        const int nz = kBlock - ntl;
+        for (int y = et; y < 4 * nz * 8; y += kGVEpi) {
+          const int ch = y / (nz * 8), rem = y % (nz * 8);
+          *reinterpret_cast<uint4*>(pg + ch * 2048 + (ntl + rem / 8) * 128 + (rem % 8) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(fixed);
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(&zdone[seg & 1], (seg >> 1) & 1) && !abort_flag)) {
+        set_timeout(g.status, kSiteVZdone);
+        abort_flag = 1;
+        break;
+      }
       tc_fence_after();
-      const size_t idx = static_cast<size_t>(x.en.row0) * g.H + x.col0;     // the tile's first column
-      const size_t rh = static_cast<size_t>(g.n_rows) * g.H;
-      const int code0 = (x.slab * C + c) * g.nch * 64;
-      float* dst = (x.first ? p.Z[x.en.src] + idx * g.R : p.zcarry + static_cast<size_t>(cl) * ncap * g.R) + code0;
-      const int codes = min(g.R - code0, g.nch * 64);
-      const int i4 = lane & 3;
-      const int npad = (x.ncols + 15) / 16 * 16;
+      if (et == 0) {
+        if (x.first) g.tfirst[x.tile] = cta;
+        if (x.last) g.tlast[x.tile] = cta;
+      }
+      const bool wide = x.n > 128;
+      const uint32_t base = taddr + (wide ? 0u : (seg & 1) * 256u), mstep = wide ? 256u : 128u;
+      float* dst;
+      size_t stride;
+      if (x.first) {
+        dst = p.Z[x.en.zsrc] + (static_cast<size_t>(x.en.row0) * g.H + x.col0) * g.R + x.rt * kGVTile;
+        stride = g.R;
+      } else {
+        dst = p.zcarry + static_cast<size_t>(cta) * kGVTile * kGVTile;
+        stride = kGVTile;
+      }
       for (int m = 0; m < 2; ++m) {
-        const int j0 = m * 128 + q * 32;
-        if (j0 >= codes) break;      // warp-uniform (codes is a multiple of 64)
+        const int j0 = m * 128 + q * 32;                  // the warp's first row of the R tile
+        if (x.rt * kGVTile + j0 >= g.R) break;            // warp-uniform (R is a multiple of 64)
         float* zq = dst + j0 + 4 * (lane >> 2);
-        for (int h0 = hf * 16; h0 < npad; h0 += 32) {
+        for (int h0 = hf * 16; h0 < x.n; h0 += 32) {
           __syncwarp();
           uint32_t v[32];
-          tmem_ld_32x32b_x16(tq + m * 128u + h0, v);
+          tmem_ld_32x32b_x16(base + (static_cast<uint32_t>(q * 32) << 16) + m * mstep + h0, v);
           tmem_ld_wait();
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float4 z = quad_transpose(__uint_as_float(v[4 * y]), __uint_as_float(v[4 * y + 1]),
-                                            __uint_as_float(v[4 * y + 2]), __uint_as_float(v[4 * y + 3]), i4);
-            const int col = h0 + 4 * y + i4;
-            if (col < x.ncols) st_global_hint_free(reinterpret_cast<float4*>(zq + static_cast<size_t>(col) * g.R), z, keep);
+          for (int c = 0; c < 4; ++c) {
+            const float4 f = quad_transpose(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1]),
+                                            __uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3]), i4);
+            const int col = h0 + 4 * c + i4;
+            if (col < x.ncols) st_global_hint_free(reinterpret_cast<float4*>(zq + col * stride), f, keep);
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(zfree);
-      if (et < x.ncols) {
-        const float sum = ((s_qsum[et] + s_qsum[ncap + et]) + s_qsum[2 * ncap + et]) + s_qsum[3 * ncap + et];
-        if (x.first) {
-          const size_t o = static_cast<size_t>(x.slab) * rh + idx + et;
-          p.l[x.en.src][o * C + c] = sum;
-          if (c == 0) p.m[x.en.src][o] = s_m[et];
-        } else {
-          const size_t o = static_cast<size_t>(cl) * ncap + et;
-          p.lcarry[o * C + c] = sum;
-          if (c == 0) p.mcarry[o] = s_m[et];
-        }
-      }
-      if (!group_sync(ebar, phase)) { ok = false; break; }   // the sums are read before the next segment clears them
+      if (lane == 0) mbar_arrive(&tfree[seg & 1]);
+      ++seg;
     }
-    if (!ok) { set_timeout(g.status, kSiteVPready); abort_flag = 1; }
   }
   __syncthreads();
-  if (C > 1) {
-    cluster_sync();   // nobody leaves while others may still copy to it or signal it
-    if (abort_flag) { // after a timeout copies may still be on their way here
-      const uint64_t t0 = globaltimer_ns();
-      for (uint32_t i = 0; i < (1u << 20) && globaltimer_ns() - t0 < 50000; ++i) {}
-    }
-    cluster_sync();
-  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(taddr, 512);
   }
 }
 
-// ================================================================= combine
-// Z / L of every (row, head): with M the largest of its segments' maxima, the
-// segments' sums scaled by exp2(m - M) and added in a fixed order, as fp16 hi +
-// lo halves (about 22 bits).  One warp per (row, head, 256 codes of R).  A row
-// without tokens gives zeros.
-struct GroupCombineParams {
-  GroupGeom g;
-  const float* Z[2];
-  const float* m[2];
-  const float* l[2];
-  const float* zcarry;
-  const float* mcarry;
-  const float* lcarry;
-  __half* zh;            // [n_rows * H][R]
-  __half* zl;
-  int clusters;
-};
-
-__global__ void __launch_bounds__(256) group_combine_kernel(GroupCombineParams p) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const GroupGeom& g = p.g;
-  const int lane = threadIdx.x & 31;
-  const int n_rt = (g.R + 255) / 256;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int64_t rh = static_cast<int64_t>(g.n_rows) * g.H;
-  if (w >= rh * n_rt) return;
-  const int code = static_cast<int>(w % n_rt) * 256 + lane * 8;
-  const int64_t rhi = w / n_rt;
-  const int row = static_cast<int>(rhi / g.H), h = static_cast<int>(rhi % g.H);
-  const int e = g.row_ent[row];
-  if (e < 0 || code >= g.R) return;
-  Partition pt;
-  pt.P = g.pre[g.E];
-  pt.G = p.clusters;
-  const int slab = code / (g.C * g.nch * 64);
-  const int j = h >> g.log2G;
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  float M = -INFINITY, L = 0.f;
-  for (int s = 0; s < (g.shared ? 2 : 1); ++s) {
-    if (s == 0 && !g.row_use[row]) continue;
-    const int es = s ? g.n_groups + row : e;
-    const GroupEntry en = g.ent[es];
-    if (en.len == 0) continue;
-    const TileShape ts = tile_shape(en.nrows, g);
-    const int within = ((row - en.row0) << g.log2G) + (h & ((1 << g.log2G) - 1));
-    int place;
-    const int ct = tile_of(ts, j, within, &place);
-    const size_t idx = static_cast<size_t>(en.row0) * g.H + static_cast<size_t>(j) * ts.m + within;
-    const int64_t blocks = entry_blocks(en), wt = g.weight[s];
-    const int64_t first = g.pre[es] + (static_cast<int64_t>(ct) * g.n_slab + slab) * blocks * wt;
-    const int32_t i0 = part_owner(first, pt), i1 = part_owner(first + (blocks - 1) * wt, pt);
-    for (int32_t i = i0; i <= i1; ++i) {
-      // clusters whose range holds no block's beginning have no segment
-      if (i > i0) {
-        const int64_t b = (part_begin(i, pt) - first + wt - 1) / wt;
-        if (first + b * wt >= part_begin(i + 1, pt)) continue;
-      }
-      const size_t o = i == i0 ? static_cast<size_t>(slab) * rh + idx : static_cast<size_t>(i) * (g.ncap) + place;
-      const float* zp = (i == i0 ? p.Z[s] + idx * g.R : p.zcarry + o * g.R) + code;
-      const float m = i == i0 ? p.m[s][o] : p.mcarry[o];
-      const float* lp = (i == i0 ? p.l[s] : p.lcarry) + o * g.C;
-      const float4 z0 = *reinterpret_cast<const float4*>(zp), z1 = *reinterpret_cast<const float4*>(zp + 4);
-      float l = 0.f;
-      for (int c = 0; c < g.C; ++c) l += lp[c];
-      // a segment whose logits are all NaN or -inf has m = -inf and l = NaN
-      const float Mn = fmaxf(M, m);
-      const float a = M > -INFINITY ? ex2_approx(M - Mn) : 1.f;
-      const float f = m > -INFINITY ? ex2_approx(m - Mn) : l;
-      L = L * a + l * f;
-      const float zz[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
-#pragma unroll
-      for (int u = 0; u < 8; ++u) acc[u] = acc[u] * a + zz[u] * f;
-      M = Mn;
-    }
-  }
-  const float il = L == 0.f ? 0.f : 1.f / L;   // no token at all: L = 0 and the result is 0
-  uint4 hv, lv;
-  uint32_t* hw = reinterpret_cast<uint32_t*>(&hv);
-  uint32_t* lw = reinterpret_cast<uint32_t*>(&lv);
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const float z0 = acc[2 * u] * il, z1 = acc[2 * u + 1] * il;
-    const __half2 hh = __floats2half2_rn(z0, z1);
-    const float2 f = __half22float2(hh);
-    const __half2 ll = __floats2half2_rn(z0 - f.x, z1 - f.y);
-    hw[u] = *reinterpret_cast<const uint32_t*>(&hh);
-    lw[u] = *reinterpret_cast<const uint32_t*>(&ll);
-  }
-  const size_t o = static_cast<size_t>(rhi) * g.R + code;
-  *reinterpret_cast<uint4*>(p.zh + o) = hv;
-  *reinterpret_cast<uint4*>(p.zl + o) = lv;
-}
-
-// ========================================================== up-projection
+// ================================================================== finish
 // out^T (128 rows of d x columns) = B_V^T . (Z / L)^T for the (row, query head)
-// columns of one KV head, K = R split over a cluster whose fp32 sums are added
-// in rank order.  A = 64 x 64 boxes of B_V (MN-major), B = the hi and lo halves.
-struct GroupUpParams {
+// columns of one KV head, with Z / L formed on the fly: eight converter warps add
+// a column's partial sums (its one or two entries, in a fixed order), scale by
+// 1 / L and split into fp16 hi + lo halves (about 22 bits) in the B operand.
+// K = R is split over a cluster whose fp32 sums are added in rank order.
+// A = 64 x 64 boxes of B_V (MN-major).  A row without tokens gives zeros.
+struct GroupFinishParams {
   GroupGeom g;
   __half* out;           // [n_rows][H][d]
+  const float* Z[2];
+  const float* zcarry;
   int n_mt;              // 128-row tiles of d
   int rows_tile;         // rows per column tile (rows_tile * G <= 256)
   int npad;              // UMMA N
@@ -1013,11 +1010,11 @@ struct GroupUpParams {
   uint32_t stage_bytes, tmem_cols;
 };
 
-constexpr int kGUThreads = 192;
+constexpr int kGFThreads = 320;
+constexpr int kGFConv = kGFThreads - 64;
 
-__global__ void __launch_bounds__(kGUThreads, 1)
-group_up_kernel(const __grid_constant__ CUtensorMap bvmap, const __grid_constant__ CUtensorMap zhmap,
-                const __grid_constant__ CUtensorMap zlmap, GroupUpParams p) {
+__global__ void __launch_bounds__(kGFThreads, 1)
+group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams p) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1026,10 +1023,14 @@ group_up_kernel(const __grid_constant__ CUtensorMap bvmap, const __grid_constant
   const int S = p.stages;
   const uint32_t a_bytes = 2u * 64u * 128u, b_bytes = static_cast<uint32_t>(p.npad) * 128u;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(S) * p.stage_bytes);
-  uint64_t* empty = full + S;
+  uint64_t* conv = full + S;
+  uint64_t* empty = conv + S;
   uint64_t* done = empty + S;
+  uint64_t* cbar = done + 1;                        // the converters' sync
   float* part = reinterpret_cast<float*>(smem);     // [npad][128], reuses the ring
   __shared__ uint32_t taddr_s;
+  __shared__ float s_il[256];
+  __shared__ int32_t s_i0[2][256], s_n[2][256], s_col[2][256];   // per source: first CTA, CTAs, column within the V tile
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int xi = blockIdx.x;
@@ -1039,11 +1040,14 @@ group_up_kernel(const __grid_constant__ CUtensorMap bvmap, const __grid_constant
   const int ks = blockIdx.y, KS = gridDim.y;
   const int k0 = ks * p.k_per_cta, k1 = min(g.R, k0 + p.k_per_cta);
   const int n_stages = k1 > k0 ? (k1 - k0 + 63) / 64 : 0;
+  const int ncols = p.rows_tile << g.log2G;
 
   if (tid == 0) {
-    for (int s = 0; s < S; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int s = 0; s < S; ++s) { mbar_init(&full[s], 1); mbar_init(&conv[s], kGFConv); mbar_init(&empty[s], 1); }
     mbar_init(done, 1);
+    mbar_init(cbar, kGFConv);
     fence_mbar_init();
+    prefetch_tensormap(&bvmap);
   }
   if (warp == 1) {
     tmem_alloc(&taddr_s, p.tmem_cols);
@@ -1054,13 +1058,9 @@ group_up_kernel(const __grid_constant__ CUtensorMap bvmap, const __grid_constant
   tc_fence_after();
   const uint32_t taddr = taddr_s;
   bool ok = true;
-  griddep_wait();
-  griddep_launch_dependents();
 
   if (warp == 0 && lane == 0) {
-    prefetch_tensormap(&bvmap);
-    prefetch_tensormap(&zhmap);
-    prefetch_tensormap(&zlmap);
+    // B_V is the caller's and no kernel before this one writes it: its copies need not wait
     const uint64_t pol = policy_evict_first();
     int i = 0;
     for (; i < n_stages; ++i) {
@@ -1068,20 +1068,17 @@ group_up_kernel(const __grid_constant__ CUtensorMap bvmap, const __grid_constant
       if (i >= S && !mbar_wait(&empty[s], ((i / S) - 1) & 1)) { ok = false; break; }
       uint8_t* st = smem + static_cast<size_t>(s) * p.stage_bytes;
       const int kr = k0 + i * 64, col = j * g.d + mt * 128;
-      const uint32_t zb = static_cast<uint32_t>(p.rows_tile << g.log2G) * 128u;
-      mbar_arrive_expect_tx(&full[s], a_bytes + 2u * zb);
+      mbar_arrive_expect_tx(&full[s], a_bytes);
       tma_load_2d(st, &bvmap, col, kr, &full[s], pol);
       tma_load_2d(st + 8192, &bvmap, col + 64, kr, &full[s], pol);
-      tma_load_3d(st + a_bytes, &zhmap, kr, j << g.log2G, row0, &full[s], pol);
-      tma_load_3d(st + a_bytes + b_bytes, &zlmap, kr, j << g.log2G, row0, &full[s], pol);
     }
-    // copies still in flight land before the ring is reused
     for (int kk = i > S ? i - S : 0; kk < i; ++kk) mbar_wait(&full[kk % S], (kk / S) & 1);
+    griddep_wait();
   } else if (warp == 1 && lane == 0) {
     const uint32_t idesc = idesc_f16_f32(128, p.npad, /*a_mn_major=*/true, /*b_mn_major=*/false);
     for (int i = 0; i < n_stages; ++i) {
       const int s = i % S;
-      if (!mbar_wait(&full[s], (i / S) & 1)) { ok = false; break; }
+      if (!mbar_wait(&full[s], (i / S) & 1) || !mbar_wait(&conv[s], (i / S) & 1)) { ok = false; break; }
       tc_fence_after();
       const uint32_t sa = smem_u32(smem + static_cast<size_t>(s) * p.stage_bytes);
       for (int kk = 0; kk < 4; ++kk) {
@@ -1092,13 +1089,126 @@ group_up_kernel(const __grid_constant__ CUtensorMap bvmap, const __grid_constant
       umma_commit(&empty[s]);
     }
     umma_commit(done);
+    griddep_wait();
+  } else if (warp >= 2) {
+    // ---------------------------------------------------------- converters
+    const int et = tid - 64;
+    griddep_wait();
+    const int n_src = g.shared ? 2 : 1;
+    // 1 / L of every column: a warp sums a column's chunks
+    for (int c = warp - 2; c < ncols; c += kGFConv / 32) {
+      const int row = row0 + (c >> g.log2G);
+      const int e = row < g.n_rows ? g.row_ent[row] : -1;
+      float L = 0.f;
+      if (e >= 0) {
+        const size_t rh = static_cast<size_t>(row) * g.H + (j << g.log2G) + (c & ((1 << g.log2G) - 1));
+        for (int s = 0; s < n_src; ++s) {
+          const GroupEntry en = g.ent[s ? g.n_groups + row : e];
+          if (en.len == 0 || (s == 0 && !g.row_use[row])) continue;
+          const int ch = gk_narrow(en.nrows, g) ? g.chunk_n : g.chunk_w;
+          const int nc = (en.len + ch - 1) / ch;
+          for (int i = lane; i < nc; i += 32) L += g.lpart[s][rh * g.n_ch[s] + i];
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+      if (lane == 0) s_il[c] = L == 0.f ? 0.f : 1.f / L;   // no token at all: L = 0 and the result is 0
+    }
+    int rt_at = -1;
+    uint32_t phase = 0;
+    for (int i = 0; i < n_stages && ok; ++i) {
+      const int s = i % S;
+      const int kr = k0 + i * 64, rt = kr / kGVTile;
+      if (rt != rt_at) {
+        // where the partial sums of each column stand for this tile of R
+        rt_at = rt;
+        if (!group_sync(cbar, phase)) { ok = false; break; }
+        for (int c = et; c < ncols; c += kGFConv) {
+          const int row = row0 + (c >> g.log2G), h = (j << g.log2G) + (c & ((1 << g.log2G) - 1));
+          const int e = row < g.n_rows ? g.row_ent[row] : -1;
+          for (int sr = 0; sr < 2; ++sr) {
+            int i0 = 0, n = 0, place = 0;
+            if (sr < n_src && e >= 0 && (sr || g.row_use[row])) {
+              const GroupEntry en = g.ent[sr ? g.n_groups + row : e];
+              if (en.len > 0) {
+                const int cols = en.nrows * g.H, width = gv_width(cols, gv_tiles(cols));
+                const int col = (row - en.row0) * g.H + h;
+                const int tile = en.tile0 + (col / width) * g.n_rt + rt;
+                i0 = g.tfirst[tile];
+                n = g.tlast[tile] - i0 + 1;
+                place = col % width;
+              }
+            }
+            s_i0[sr][c] = i0;
+            s_n[sr][c] = n;
+            s_col[sr][c] = place;
+          }
+        }
+        if (!group_sync(cbar, phase)) { ok = false; break; }
+      }
+      if (i >= S && !__all_sync(0xffffffffu, mbar_wait(&empty[s], ((i / S) - 1) & 1))) { ok = false; break; }
+      uint8_t* hi_t = smem + static_cast<size_t>(s) * p.stage_bytes + a_bytes;
+      // item = (column bl, 8-value chunk c of the stage's 64 rows of R)
+      for (int item = et; item < p.npad * 8; item += kGFConv) {
+        const int bl = item >> 3, c = item & 7;
+        float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (bl < ncols && row0 + (bl >> g.log2G) < g.n_rows) {
+          const int row = row0 + (bl >> g.log2G), h = (j << g.log2G) + (bl & ((1 << g.log2G) - 1));
+          const int code = kr + c * 8;
+          for (int sr = 0; sr < n_src; ++sr) {
+            const int n = s_n[sr][bl];
+            if (n == 0) continue;
+            const float* first = p.Z[sr] + (static_cast<size_t>(row) * g.H + h) * g.R + code;
+            const float* carry = p.zcarry + (static_cast<size_t>(s_i0[sr][bl]) * kGVTile + s_col[sr][bl]) * kGVTile +
+                                 (code - rt * kGVTile);
+            for (int u0 = 0; u0 < n; u0 += 4) {
+              float4 a[4], b[4];
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                if (u0 + u < n) {
+                  const float* src = u0 + u == 0 ? first : carry + static_cast<size_t>(u0 + u) * kGVTile * kGVTile;
+                  a[u] = *reinterpret_cast<const float4*>(src);
+                  b[u] = *reinterpret_cast<const float4*>(src + 4);
+                }
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                if (u0 + u < n) {
+                  z[0] += a[u].x; z[1] += a[u].y; z[2] += a[u].z; z[3] += a[u].w;
+                  z[4] += b[u].x; z[5] += b[u].y; z[6] += b[u].z; z[7] += b[u].w;
+                }
+            }
+          }
+          const float il = s_il[bl];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) z[u] *= il;
+        }
+        uint4 hv, lv;
+        uint32_t* hw = reinterpret_cast<uint32_t*>(&hv);
+        uint32_t* lw = reinterpret_cast<uint32_t*>(&lv);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const __half2 hh = __floats2half2_rn(z[2 * u], z[2 * u + 1]);
+          const float2 f = __half22float2(hh);
+          const __half2 ll = __floats2half2_rn(z[2 * u] - f.x, z[2 * u + 1] - f.y);
+          hw[u] = *reinterpret_cast<const uint32_t*>(&hh);
+          lw[u] = *reinterpret_cast<const uint32_t*>(&ll);
+        }
+        const uint32_t off = static_cast<uint32_t>(bl) * 128u + (static_cast<uint32_t>(c ^ (bl & 7)) << 4);
+        *reinterpret_cast<uint4*>(hi_t + off) = hv;
+        *reinterpret_cast<uint4*>(hi_t + b_bytes + off) = lv;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&conv[s]);
+    }
   }
+  griddep_launch_dependents();
   __syncthreads();
   if (!mbar_wait(done, 0)) ok = false;
   tc_fence_after();
-  if (warp >= 2) {
+  if (warp >= 2 && warp < 6) {
     const int q = warp & 3, row = q * 32 + lane;
     for (int c0 = 0; c0 < p.npad; c0 += 16) {
+      __syncwarp();
       uint32_t v[32];
       tmem_ld_32x32b_x16(taddr + (static_cast<uint32_t>(q * 32) << 16) + c0, v);
       tmem_ld_wait();
@@ -1112,10 +1222,10 @@ group_up_kernel(const __grid_constant__ CUtensorMap bvmap, const __grid_constant
   const int n_used = *g.n_used;
   const int per = (p.npad + KS - 1) / KS;
   const int n_lo = ks * per, n_hi = min(p.npad, n_lo + per);
-  for (int x = tid; x < (n_hi - n_lo) * 32; x += kGUThreads) {
+  for (int x = tid; x < (n_hi - n_lo) * 32; x += kGFThreads) {
     const int n = n_lo + x / 32, m = (x % 32) * 4, dm = mt * 128 + m;
     const int row = row0 + (n >> g.log2G);
-    if (n >= (p.rows_tile << g.log2G) || row >= n_used || dm >= g.d || g.row_ent[row] < 0) continue;
+    if (n >= ncols || row >= n_used || dm >= g.d || g.row_ent[row] < 0) continue;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < 8; ++c)

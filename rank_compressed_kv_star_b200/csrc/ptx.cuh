@@ -200,34 +200,6 @@ __device__ __forceinline__ void st_global_hint(float4* p, float4 v, uint64_t pol
                : "memory");
 }
 
-// ------------------------------------------------------------------ clusters
-__device__ __forceinline__ uint32_t cluster_ctarank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-// `bytes` of this CTA's shared memory to the same offset in CTA `rank` of the
-// cluster, counted on the barrier at `bar`'s offset there (16-byte multiples).
-__device__ __forceinline__ void bulk_s2cluster(const void* src, uint32_t rank, uint32_t bytes, uint64_t* bar) {
-  const uint32_t s = smem_u32(src), b = smem_u32(bar);
-  uint32_t rs, rb;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rs) : "r"(s), "r"(rank));
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rb) : "r"(b), "r"(rank));
-  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(rs),
-               "r"(s), "r"(bytes), "r"(rb)
-               : "memory");
-}
-
-// Arrival on the barrier at `bar`'s offset in CTA `rank` of the cluster (this CTA included).
-__device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank) {
-  uint32_t rb;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rb) : "r"(smem_u32(bar)), "r"(rank));
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(rb) : "memory");
-}
-
 // Generic-proxy writes to shared memory become visible to the async proxy
 // (TMA engine, tensor cores) after this fence.
 __device__ __forceinline__ void fence_proxy_async_smem() {

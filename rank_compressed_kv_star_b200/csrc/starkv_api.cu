@@ -1505,51 +1505,23 @@ bool encode_rows_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_
 
 struct GroupPlan {
   GroupGeom g;
-  // attend
-  int kb, ksteps, k_stages, v_stages, clusters;
-  uint32_t v_stage_bytes;
-  size_t at_smem;
-  // up-projection
-  int up_mt, up_rows, up_tiles, up_npad, up_ks, up_kpc, up_stages;
-  uint32_t up_stage_bytes, up_tmem;
-  size_t up_smem;
+  // K pass
+  int kb, ksteps, qbox, log2Hkv, nq, k_stages, k_ctas;
+  uint32_t a_bytes, q_bytes, k_tmem;
+  size_t k_smem;
+  // V pass
+  int v_stages, v_ctas;
+  size_t v_smem;
+  // finish
+  int f_mt, f_rows, f_tiles, f_npad, f_ks, f_kpc, f_stages;
+  uint32_t f_stage_bytes, f_tmem;
+  size_t f_smem;
   // absorption
   int abs_tile;
   // workspace
-  size_t ent_off, pre_off, row_ent_off, row_use_off, used_off, qh_off[2], ql_off[2], z_off[2], m_off[2], l_off[2],
-      zcarry_off, mcarry_off, lcarry_off, zh_off, zl_off, total;
+  size_t ent_off, kpre_off, vpre_off, row_ent_off, row_use_off, used_off, tfirst_off, tlast_off, mrow_off, lpart_off[2],
+      qh_off, ql_off, p_off[2], z_off[2], carry_off, total;
 };
-
-// Clusters of C CTAs of the attend kernel that the device holds at once.
-int max_attend_clusters(int C, size_t smem) {
-  static std::mutex mu;
-  static std::map<std::tuple<int, int, size_t>, int> known;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) { cudaGetLastError(); return device_sm_count() / C; }
-  std::lock_guard<std::mutex> lock(mu);
-  const auto key = std::make_tuple(dev, C, smem);
-  auto it = known.find(key);
-  if (it != known.end()) return it->second;
-  int n = 0;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(device_sm_count()), static_cast<unsigned>(C));
-  cfg.blockDim = dim3(kGAThreads);
-  cfg.dynamicSmemBytes = smem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = static_cast<unsigned>(C);
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (!set_smem(group_attend_kernel, smem) ||
-      cudaOccupancyMaxActiveClusters(&n, group_attend_kernel, &cfg) != cudaSuccess || n < 1) {
-    cudaGetLastError();
-    return device_sm_count() / C;   // no device: the host-side sizes only
-  }
-  known[key] = n;
-  return n;
-}
 
 starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n_groups, int32_t n_rows,
                               int32_t max0, int32_t max1, GroupPlan* gp) {
@@ -1564,47 +1536,86 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
   GroupGeom& g = p.g;
   g.H = d->num_heads; g.Hkv = kv_heads(d); g.d = d->head_dim; g.r = d->k_rank; g.R = d->v_rank;
   while ((g.Hkv << g.log2G) < g.H) ++g.log2G;
+  while ((1 << p.log2Hkv) < g.Hkv) ++p.log2Hkv;
   const int G = 1 << g.log2G;
   g.MB = d->max_blocks_per_seq; g.NB = d->num_blocks;
   g.n_rows = n_rows; g.n_groups = n_groups; g.shared = shared ? 1 : 0;
   g.E = n_groups + (shared ? n_rows : 0);
   g.max_len[0] = max0; g.max_len[1] = max1;
-  g.weight[0] = 2; g.weight[1] = 3;
+  g.t_pad[0] = max0 > 0 ? (max0 + 127) / 128 * 128 : 128;
+  g.t_pad[1] = max1 > 0 ? (max1 + 127) / 128 * 128 : 128;
+  g.n_rt = (g.R + kGVTile - 1) / kGVTile;
   const int sms = device_sm_count();
 
-  // attend: slabs of at most 2048 codes of R, each over a cluster of CTAs of at
-  // most 256 codes; as many columns as the query tile and the P blocks leave room for
-  g.n_slab = (g.R + 2047) / 2048;
-  g.C = (g.R + 256 * g.n_slab - 1) / (256 * g.n_slab);
-  g.nch = (g.R / 64 + g.n_slab * g.C - 1) / (g.n_slab * g.C);
+  // K pass: 128 columns per tile, 64 where the query tile of a large rank would
+  // leave no room for a ring; two query slots where three stages still fit
   p.kb = (g.r + 63) / 64;
   p.ksteps = (g.r + 15) / 16;
-  g.ncap = p.kb == 1 ? 128 : (p.kb == 2 ? 64 : 32);
-  p.k_stages = p.kb < 2 ? 2 : (p.kb == 3 ? 6 : 4);
-  p.v_stage_bytes = static_cast<uint32_t>(g.nch) * 4096u;
-  p.v_stages = 5;
-  p.at_smem = 1024 + attend_smem(g.ncap, p.kb, p.k_stages, p.v_stages, p.v_stage_bytes).total;
-  if (p.at_smem > 227u * 1024u) return STARKV_ERR_UNSUPPORTED;
-  p.clusters = max_attend_clusters(g.C, p.at_smem);
-
-  // up-projection
-  p.up_mt = (g.d + 127) / 128;
-  p.up_rows = 256 / G < n_rows ? 256 / G : (n_rows > 0 ? n_rows : 1);
-  p.up_tiles = n_rows > 0 ? (n_rows + p.up_rows - 1) / p.up_rows : 1;
-  p.up_npad = (p.up_rows * G + 15) / 16 * 16;
-  p.up_stage_bytes = 16384u + 2u * p.up_npad * 128u;
-  p.up_stages = static_cast<int>(200u * 1024u / p.up_stage_bytes);
-  if (p.up_stages > 6) p.up_stages = 6;
+  g.ncol = p.kb <= 2 ? 128 : 64;
+  p.qbox = G > 16 ? G : 16;
+  p.a_bytes = static_cast<uint32_t>(p.kb) * 16384u;
+  p.q_bytes = static_cast<uint32_t>(p.kb) * 2u * g.ncol * 128u;
+  const uint32_t staging = 4u * 32u * (g.ncol + 4) * 4u;
+  const uint32_t budget = 218u * 1024u - staging;
+  p.nq = budget >= 2u * p.q_bytes + 3u * p.a_bytes ? 2 : 1;
+  p.k_stages = static_cast<int>((budget - p.nq * p.q_bytes) / p.a_bytes);
+  if (p.k_stages > 8) p.k_stages = 8;
+  p.k_smem = 1024 + static_cast<size_t>(p.nq) * p.q_bytes + static_cast<size_t>(p.k_stages) * p.a_bytes +
+             (2 * p.k_stages + 4 + 2 * kGKAcc + 2) * sizeof(uint64_t) + staging;
+  p.k_tmem = static_cast<uint32_t>(kGKAcc * g.ncol);
+  p.k_ctas = sms;
+  const int64_t runs = n_groups < n_rows ? n_groups : n_rows;   // entries of several rows at most
+  const int own_max = max0 > max1 ? max0 : max1;                // a row's own pages: also those of a row shorter than its group's
+  const int64_t wide_tiles = runs + static_cast<int64_t>(n_rows) * G / g.ncol * 2 + 1;
   {
-    size_t ring = static_cast<size_t>(p.up_stages) * p.up_stage_bytes;
-    if (ring < static_cast<size_t>(p.up_npad) * 512) ring = static_cast<size_t>(p.up_npad) * 512;
-    p.up_smem = 1024 + ring + (2 * p.up_stages + 1) * sizeof(uint64_t);
+    // tokens per item: enough items for every CTA, each long enough to hide its start
+    const int64_t blocks = wide_tiles * g.Hkv * (g.t_pad[0] / 128);
+    int64_t n = blocks / (4 * static_cast<int64_t>(sms));
+    n = n < 1 ? 1 : (n > 8 ? 8 : n);
+    g.chunk_w = static_cast<int>(n) * 128;
+    const int unit = 128 / g.Hkv > 16 ? 128 / g.Hkv : 16;
+    const int64_t tokens = runs * max0 + (shared ? static_cast<int64_t>(n_rows) * max1 : 0);
+    n = tokens / (3 * static_cast<int64_t>(sms) * unit);
+    const int64_t least = (own_max + 64 * unit - 1) / (64 * unit);   // at most 64 sums of weights per column
+    if (n < least) n = least;
+    if (n < 1) n = 1;
+    g.chunk_n = static_cast<int>(n) * unit;
   }
-  p.up_ks = 1;
-  while (p.up_ks < 8 && static_cast<int64_t>(g.Hkv) * p.up_mt * p.up_tiles * p.up_ks * 2 <= sms && g.R / 64 >= p.up_ks * 2)
-    p.up_ks *= 2;
-  p.up_kpc = (g.R + p.up_ks * 64 - 1) / (p.up_ks * 64) * 64;
-  p.up_tmem = static_cast<uint32_t>(pow2_ceil(p.up_npad < 32 ? 32 : p.up_npad));
+  const int least_chunk = g.chunk_w < g.chunk_n ? g.chunk_w : g.chunk_n;
+  g.n_ch[0] = (g.t_pad[0] + least_chunk - 1) / least_chunk;
+  g.n_ch[1] = ((own_max > 0 ? own_max : 1) + least_chunk - 1) / least_chunk;
+
+  // V pass: one CTA per SM, three 64 KiB stages
+  p.v_stages = 3;
+  p.v_ctas = sms;
+  p.v_smem = 1024 + static_cast<size_t>(p.v_stages) * (kGVABytes + kGVBBytes) + (2 * p.v_stages + 8) * sizeof(uint64_t);
+  const int64_t v_tiles = g.n_rt * (runs + static_cast<int64_t>(n_rows) * g.H / kGVTile + 1 + (shared ? n_rows : 0));
+  // positions of K items and V units are 32-bit
+  const int64_t k_items = wide_tiles * g.Hkv * ((g.t_pad[0] + g.chunk_w - 1) / g.chunk_w) +
+                          (runs + (shared ? n_rows : 0)) * static_cast<int64_t>((own_max + g.chunk_n) / g.chunk_n + 1);
+  if (k_items > (1 << 30) || v_tiles * ((own_max + kGVTok) / kGVTok + 1) > (1 << 30)) return STARKV_ERR_UNSUPPORTED;
+
+  // finish: column tiles as wide as 256, halved while the grid would leave SMs idle
+  p.f_mt = (g.d + 127) / 128;
+  p.f_rows = 256 / G < n_rows ? 256 / G : (n_rows > 0 ? n_rows : 1);
+  while (p.f_rows > 1 && p.f_rows * G > 32 &&
+         static_cast<int64_t>(g.Hkv) * p.f_mt * ((n_rows + p.f_rows - 1) / p.f_rows) < sms)
+    p.f_rows = (p.f_rows + 1) / 2;
+  p.f_tiles = n_rows > 0 ? (n_rows + p.f_rows - 1) / p.f_rows : 1;
+  p.f_npad = (p.f_rows * G + 15) / 16 * 16;
+  p.f_stage_bytes = 16384u + 2u * p.f_npad * 128u;
+  p.f_stages = static_cast<int>(200u * 1024u / p.f_stage_bytes);
+  if (p.f_stages > 4) p.f_stages = 4;
+  {
+    size_t ring = static_cast<size_t>(p.f_stages) * p.f_stage_bytes;
+    if (ring < static_cast<size_t>(p.f_npad) * 512) ring = static_cast<size_t>(p.f_npad) * 512;
+    p.f_smem = 1024 + ring + (3 * p.f_stages + 2) * sizeof(uint64_t);
+  }
+  p.f_ks = 1;
+  while (p.f_ks < 8 && static_cast<int64_t>(g.Hkv) * p.f_mt * p.f_tiles * p.f_ks * 2 <= sms && g.R / 64 >= p.f_ks * 2)
+    p.f_ks *= 2;
+  p.f_kpc = (g.R + p.f_ks * 64 - 1) / (p.f_ks * 64) * 64;
+  p.f_tmem = static_cast<uint32_t>(pow2_ceil(p.f_npad < 32 ? 32 : p.f_npad));
 
   p.abs_tile = g.H * ((n_rows + 15) / 16) <= 2 * sms ? 16 : kAbsBT;
 
@@ -1612,25 +1623,32 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
   size_t off = 256;   // the status word
   auto take = [&](size_t bytes) { const size_t o = off; off = align_up(off + bytes, 256); return o; };
   p.ent_off = take(static_cast<size_t>(g.E) * sizeof(GroupEntry));
-  p.pre_off = take((static_cast<size_t>(g.E) + 1) * 8);
+  p.kpre_off = take((static_cast<size_t>(g.E) + 1) * 4);
+  p.vpre_off = take((static_cast<size_t>(g.E) + 1) * 4);
   p.row_ent_off = take(N * 4);
   p.row_use_off = take(N * 4);
   p.used_off = take(4);
+  p.tfirst_off = take(static_cast<size_t>(v_tiles) * 4);
+  p.tlast_off = take(static_cast<size_t>(v_tiles) * 4);
+  p.mrow_off = take(rh * 4);
+  p.qh_off = take(rh * g.r * 2);
+  p.ql_off = take(rh * g.r * 2);
   for (int s = 0; s < (shared ? 2 : 1); ++s) {
-    p.qh_off[s] = take(rh * g.r * 2);
-    p.ql_off[s] = take(rh * g.r * 2);
+    p.lpart_off[s] = take(rh * g.n_ch[s] * 4);
+    p.p_off[s] = take(rh * g.t_pad[s] * 2);
     p.z_off[s] = take(rh * g.R * 4);
-    p.m_off[s] = take(rh * g.n_slab * 4);
-    p.l_off[s] = take(rh * g.n_slab * g.C * 4);
   }
-  const size_t carry = static_cast<size_t>(p.clusters) * g.ncap;
-  p.zcarry_off = take(carry * g.R * 4);
-  p.mcarry_off = take(carry * 4);
-  p.lcarry_off = take(carry * g.C * 4);
-  p.zh_off = take(rh * g.R * 2);
-  p.zl_off = take(rh * g.R * 2);
+  p.carry_off = take(static_cast<size_t>(p.v_ctas) * kGVTile * kGVTile * 4);
   p.total = off;
   return STARKV_OK;
+}
+
+template <bool kWeights>
+cudaError_t launch_group_kpass(const GroupPlan& pl, const CUtensorMap (&km)[2], const CUtensorMap (&qm)[4],
+                               const GroupKParams& kp, cudaStream_t s) {
+  if (!set_smem(group_kpass_kernel<kWeights>, pl.k_smem)) return cudaErrorInvalidValue;
+  return launch(group_kpass_kernel<kWeights>, dim3(pl.k_ctas), dim3(kGKThreads), pl.k_smem, s, 1, km[0], km[1], qm[0],
+                qm[1], qm[2], qm[3], kp);
 }
 
 starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_groups, int32_t n_rows, int32_t max0,
@@ -1661,24 +1679,32 @@ starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_g
   GroupGeom& g = pl.g;
   g.status = i32(0);
   g.ent = reinterpret_cast<GroupEntry*>(ws + pl.ent_off);
-  g.pre = reinterpret_cast<int64_t*>(ws + pl.pre_off);
+  g.kpre = i32(pl.kpre_off);
+  g.vpre = i32(pl.vpre_off);
   g.row_ent = i32(pl.row_ent_off);
   g.row_use = i32(pl.row_use_off);
   g.n_used = i32(pl.used_off);
+  g.tfirst = i32(pl.tfirst_off);
+  g.tlast = i32(pl.tlast_off);
+  g.mrow = f32(pl.mrow_off);
   const int second = shared ? 1 : 0;   // an unused second source stands for the first
+  const int src[2] = {0, second};
+  for (int i = 0; i < 2; ++i) g.lpart[i] = f32(pl.lpart_off[src[i]]);
   const uint32_t G = 1u << g.log2G;
   const uint64_t rh = static_cast<uint64_t>(n_rows) * g.H;
+  const uint32_t tok_box = 128 / g.Hkv < 16 ? 128u / g.Hkv : 16u;
 
-  CUtensorMap kmap, vmap, qhmap[2], qlmap[2], bvmap, zhmap, zlmap;
-  if (!encode_kpool_map(&kmap, k_cache, g.r, g.Hkv, g.NB, 1, 16) ||
-      !encode_vpool_map(&vmap, v_cache, g.R, g.NB, static_cast<uint32_t>(g.nch)) ||
-      !encode_2d_map(&qhmap[0], ws + pl.qh_off[0], g.r, rh, 64, kGAQBox) ||
-      !encode_2d_map(&qlmap[0], ws + pl.ql_off[0], g.r, rh, 64, kGAQBox) ||
-      !encode_2d_map(&qhmap[1], ws + pl.qh_off[second], g.r, rh, 64, kGAQBox) ||
-      !encode_2d_map(&qlmap[1], ws + pl.ql_off[second], g.r, rh, 64, kGAQBox) ||
-      !encode_2d_map(&bvmap, B_V, static_cast<uint64_t>(g.Hkv) * g.d, g.R, 64, 64) ||
-      !encode_rows_map(&zhmap, ws + pl.zh_off, g.R, g.H, n_rows, G, static_cast<uint32_t>(pl.up_rows)) ||
-      !encode_rows_map(&zlmap, ws + pl.zl_off, g.R, g.H, n_rows, G, static_cast<uint32_t>(pl.up_rows)))
+  CUtensorMap km[2], qm[4], vmap, pmap[2], bvmap;
+  if (!encode_kpool_map(&km[0], k_cache, g.r, g.Hkv, g.NB, 1, 16) ||
+      !encode_kpool_map(&km[1], k_cache, g.r, g.Hkv, g.NB, static_cast<uint32_t>(g.Hkv), tok_box) ||
+      !encode_rows_map(&qm[0], ws + pl.qh_off, g.r, g.H, n_rows, G, static_cast<uint32_t>(pl.qbox) / G) ||
+      !encode_rows_map(&qm[1], ws + pl.ql_off, g.r, g.H, n_rows, G, static_cast<uint32_t>(pl.qbox) / G) ||
+      !encode_2d_map(&qm[2], ws + pl.qh_off, g.r, rh, 64, kGKQBox) ||
+      !encode_2d_map(&qm[3], ws + pl.ql_off, g.r, rh, 64, kGKQBox) ||
+      !encode_vpool_map(&vmap, v_cache, g.R, g.NB, 4) ||
+      !encode_2d_map(&pmap[0], ws + pl.p_off[0], g.t_pad[0], rh, 64, kGVPBox) ||
+      !encode_2d_map(&pmap[1], ws + pl.p_off[second], g.t_pad[second], rh, 64, kGVPBox) ||
+      !encode_2d_map(&bvmap, B_V, static_cast<uint64_t>(g.Hkv) * g.d, g.R, 64, 64))
     return STARKV_ERR_CUDA;
 
   GroupAbsorbParams ap{};
@@ -1688,10 +1714,8 @@ starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_g
   ap.su.shared_lens = shared_lens;
   ap.q = static_cast<const __half*>(q);
   ap.B_K = static_cast<const __half*>(B_K);
-  for (int i = 0; i < 2; ++i) {
-    ap.qh[i] = f16(pl.qh_off[i ? second : 0]);
-    ap.ql[i] = f16(pl.ql_off[i ? second : 0]);
-  }
+  ap.qh = f16(pl.qh_off);
+  ap.ql = f16(pl.ql_off);
   ap.coef = scale * kLog2e;
   ap.tile = pl.abs_tile;
   const size_t abs_smem = (static_cast<size_t>(g.d) * g.r + static_cast<size_t>(ap.tile) * g.d) * 2;
@@ -1700,45 +1724,37 @@ starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_g
   if (launch(group_absorb_kernel, dim3(abs_ctas), dim3(kPrepThreads), abs_smem, s, 1, ap) != cudaSuccess)
     return STARKV_ERR_CUDA;
 
-  // a launch of no more clusters than the call can have blocks
-  const int64_t tiles0 = (n_groups < n_rows ? n_groups : n_rows) + 2 * static_cast<int64_t>(rh) / g.ncap + 1;
-  const int64_t blocks = g.n_slab * (tiles0 * ((max0 + kGTok - 1) / kGTok) +
-                                     (shared ? n_rows * ((g.H + g.ncap - 1) / g.ncap) * static_cast<int64_t>((max1 + kGTok - 1) / kGTok + 1) : 0));
-  const int clusters = blocks < 1 ? 1 : (blocks < pl.clusters ? static_cast<int>(blocks) : pl.clusters);
-
-  GroupAttendParams tp{};
-  tp.g = g;
-  tp.tables = block_tables;
-  for (int i = 0; i < 2; ++i) {
-    const int x = i ? second : 0;
-    tp.Z[i] = f32(pl.z_off[x]); tp.m[i] = f32(pl.m_off[x]); tp.l[i] = f32(pl.l_off[x]);
-  }
-  tp.zcarry = f32(pl.zcarry_off); tp.mcarry = f32(pl.mcarry_off); tp.lcarry = f32(pl.lcarry_off);
-  tp.kb = pl.kb; tp.ksteps = pl.ksteps; tp.k_stages = pl.k_stages; tp.v_stages = pl.v_stages;
-  tp.v_stage_bytes = pl.v_stage_bytes;
-  if (!set_smem(group_attend_kernel, pl.at_smem)) return STARKV_ERR_CUDA;
-  if (launch(group_attend_kernel, dim3(clusters, g.C), dim3(kGAThreads), pl.at_smem, s, g.C, kmap, vmap, qhmap[0], qlmap[0],
-             qhmap[1], qlmap[1], tp) != cudaSuccess)
+  GroupKParams kp{};
+  kp.g = g;
+  kp.tables = block_tables;
+  for (int i = 0; i < 2; ++i) kp.P[i] = f16(pl.p_off[src[i]]);
+  kp.kb = pl.kb; kp.ksteps = pl.ksteps; kp.qbox = pl.qbox; kp.log2Hkv = pl.log2Hkv; kp.nq = pl.nq; kp.stages = pl.k_stages;
+  kp.a_bytes = pl.a_bytes; kp.q_bytes = pl.q_bytes; kp.tmem_cols = pl.k_tmem;
+  if (launch_group_kpass<false>(pl, km, qm, kp, s) != cudaSuccess || launch_group_kpass<true>(pl, km, qm, kp, s) != cudaSuccess)
     return STARKV_ERR_CUDA;
 
-  GroupCombineParams cp{};
-  cp.g = g;
-  for (int i = 0; i < 2; ++i) { cp.Z[i] = tp.Z[i]; cp.m[i] = tp.m[i]; cp.l[i] = tp.l[i]; }
-  cp.zcarry = tp.zcarry; cp.mcarry = tp.mcarry; cp.lcarry = tp.lcarry;
-  cp.zh = f16(pl.zh_off); cp.zl = f16(pl.zl_off);
-  cp.clusters = clusters;
-  const int64_t warps = static_cast<int64_t>(rh) * ((g.R + 255) / 256);
-  if (launch(group_combine_kernel, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, s, 1, cp) != cudaSuccess)
+  GroupVParams vp{};
+  vp.g = g;
+  vp.tables = block_tables;
+  for (int i = 0; i < 2; ++i) vp.Z[i] = f32(pl.z_off[src[i]]);
+  vp.zcarry = f32(pl.carry_off);
+  vp.stages = pl.v_stages;
+  vp.stage_bytes = kGVABytes + kGVBBytes;
+  if (!set_smem(group_vpass_kernel, pl.v_smem)) return STARKV_ERR_CUDA;
+  if (launch(group_vpass_kernel, dim3(pl.v_ctas), dim3(kGVThreads), pl.v_smem, s, 1, vmap, pmap[0], pmap[1], vp) !=
+      cudaSuccess)
     return STARKV_ERR_CUDA;
 
-  GroupUpParams up{};
-  up.g = g;
-  up.out = static_cast<__half*>(out);
-  up.n_mt = pl.up_mt; up.rows_tile = pl.up_rows; up.npad = pl.up_npad; up.k_per_cta = pl.up_kpc;
-  up.stages = pl.up_stages; up.stage_bytes = pl.up_stage_bytes; up.tmem_cols = pl.up_tmem;
-  if (!set_smem(group_up_kernel, pl.up_smem)) return STARKV_ERR_CUDA;
-  if (launch(group_up_kernel, dim3(g.Hkv * pl.up_mt * pl.up_tiles, pl.up_ks), dim3(kGUThreads), pl.up_smem, s, pl.up_ks,
-             bvmap, zhmap, zlmap, up) != cudaSuccess)
+  GroupFinishParams fp{};
+  fp.g = g;
+  fp.out = static_cast<__half*>(out);
+  fp.Z[0] = vp.Z[0]; fp.Z[1] = vp.Z[1];
+  fp.zcarry = vp.zcarry;
+  fp.n_mt = pl.f_mt; fp.rows_tile = pl.f_rows; fp.npad = pl.f_npad; fp.k_per_cta = pl.f_kpc;
+  fp.stages = pl.f_stages; fp.stage_bytes = pl.f_stage_bytes; fp.tmem_cols = pl.f_tmem;
+  if (!set_smem(group_finish_kernel, pl.f_smem)) return STARKV_ERR_CUDA;
+  if (launch(group_finish_kernel, dim3(g.Hkv * pl.f_mt * pl.f_tiles, pl.f_ks), dim3(kGFThreads), pl.f_smem, s, pl.f_ks, bvmap,
+             fp) != cudaSuccess)
     return STARKV_ERR_CUDA;
   return STARKV_OK;
 }
