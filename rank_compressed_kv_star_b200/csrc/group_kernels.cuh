@@ -40,7 +40,14 @@ struct alignas(16) GroupEntry {
   int32_t tab;
   int32_t psrc, zsrc;  // which P and Z matrices it uses: 0 a group's (or sequence's), 1 a row's own
   int32_t tile0;       // V tiles before it
+  // what the passes' walks would have to divide for
+  int32_t narrow;      // gk_narrow
+  int32_t k_nt, k_per; // wide: row tiles, rows per tile
+  int32_t v_units;     // 64-token units per V tile
+  int32_t v_width;     // columns per V tile
+  int32_t pad[3];
 };
+static_assert(sizeof(GroupEntry) == 64, "loaded as four 16-byte words");
 
 struct GroupGeom {
   int H, Hkv, log2G, d, r, R, MB, NB;
@@ -172,6 +179,14 @@ __device__ __forceinline__ void group_setup(const GroupSetupParams& p) {
       g.row_ent[b] = grp;
       g.row_use[b] = use;
     }
+    if (en.nrows > 0) {
+      const int cols = en.nrows * g.H;
+      en.narrow = gk_narrow(en.nrows, g);
+      en.k_nt = gk_tiles(en.nrows, g);
+      en.k_per = (en.nrows + en.k_nt - 1) / en.k_nt;
+      en.v_units = (en.len + kGVTok - 1) / kGVTok;
+      en.v_width = gv_width(cols, gv_tiles(cols));
+    }
     g.ent[e] = en;
     int32_t c[3];
     counts(en, c);
@@ -269,11 +284,35 @@ group_absorb_kernel(GroupAbsorbParams p) {
   });
 }
 
-// The entry that holds position x of a prefix array (pre[e] <= x < pre[e + 1]),
-// looked up by the whole CTA at once; s_e is shared.  Call before a __syncthreads.
-__device__ __forceinline__ void find_entry(const int32_t* pre, int32_t E, int32_t x, int32_t* s_e) {
-  for (int e = threadIdx.x; e < E; e += blockDim.x)
-    if (pre[e] <= x && x < pre[e + 1]) *s_e = e;
+// The entries and one of their prefix arrays as a CTA uses them: in shared memory
+// when they fit (one round of loads instead of a chain of them), else in place.
+constexpr int kGSmemE = 96;
+struct GroupTables {
+  const GroupEntry* ent;
+  const int32_t* pre;
+  int32_t E;
+};
+struct GroupTablesSmem {
+  GroupEntry ent[kGSmemE];
+  int32_t pre[kGSmemE + 1];
+};
+// Called by all threads after griddep_wait and before a __syncthreads.
+__device__ __forceinline__ GroupTables load_tables(const GroupGeom& g, const int32_t* pre, GroupTablesSmem* sm) {
+  if (g.E > kGSmemE) return GroupTables{g.ent, pre, g.E};
+  const uint4* src = reinterpret_cast<const uint4*>(g.ent);
+  uint4* dst = reinterpret_cast<uint4*>(sm->ent);
+  for (int i = threadIdx.x; i < g.E * 4; i += blockDim.x) dst[i] = src[i];
+  for (int i = threadIdx.x; i <= g.E; i += blockDim.x) sm->pre[i] = pre[i];
+  return GroupTables{sm->ent, sm->pre, g.E};
+}
+// Largest e with pre[e] <= x (0 <= x < pre[E]; empty entries are skipped).
+__device__ __forceinline__ int32_t entry_of(const GroupTables& t, int32_t x) {
+  int32_t lo = 0, hi = t.E - 1;
+  while (lo < hi) {
+    const int32_t mid = (lo + hi + 1) >> 1;
+    if (t.pre[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
 }
 
 // ================================================================== K pass
@@ -295,6 +334,7 @@ struct GroupKParams {
   __half* P[2];              // [n_rows * H][t_pad] by psrc
   int kb, ksteps;            // 64-code blocks and 16-code steps of r
   int qbox;                  // wide: columns per query box, max(16, G)
+  int nbox;                  // narrow: columns per query box
   int log2Hkv;
   int nq, stages;            // query slots, ring stages
   uint32_t a_bytes, q_bytes; // ring stage, query slot (hi then lo)
@@ -304,52 +344,55 @@ struct GroupKParams {
 constexpr int kGKThreads = 320;
 constexpr int kGKEpi = kGKThreads - 64;
 constexpr int kGKAcc = 4;
-constexpr int kGKQBox = 32;          // narrow: columns per query box
 
 struct KItem {
   GroupEntry en;
-  bool narrow;
   int j, row0, nrow, cols;        // KV head (wide), rows of the tile, columns
   int c, t0, t1, step;            // chunk, tokens [t0, t1), tokens per step
 };
 
-// Walks the items [it, end) of a CTA in order, from entry e0 on.
+// Walks the items [it, end) of a CTA in order.
 struct KWalk {
   const GroupGeom& g;
+  const GroupTables& tb;
+  int log2Hkv;
   int32_t it, end, ebeg, eend, e;
   GroupEntry en;
-  __device__ KWalk(const GroupGeom& g_, int32_t i0, int32_t i1, int32_t e0) : g(g_), it(i0), end(i1), ebeg(0), eend(0), e(e0) {
+  __device__ KWalk(const GroupGeom& g_, const GroupTables& tb_, int log2Hkv_, int32_t i0, int32_t i1)
+      : g(g_), tb(tb_), log2Hkv(log2Hkv_), it(i0), end(i1), ebeg(0), eend(0), e(0) {
     if (it < end) {
-      ebeg = g.kpre[e];
-      eend = g.kpre[e + 1];
-      en = g.ent[e];
+      e = entry_of(tb, it);
+      ebeg = tb.pre[e];
+      eend = tb.pre[e + 1];
+      en = tb.ent[e];
     }
   }
   __device__ bool next(KItem* x) {
     if (it >= end) return false;
-    while (it >= eend) { ++e; ebeg = eend; eend = g.kpre[e + 1]; if (it < eend) en = g.ent[e]; }
-    const uint32_t local = static_cast<uint32_t>(it - ebeg);
+    while (it >= eend) { ++e; ebeg = eend; eend = tb.pre[e + 1]; if (it < eend) en = tb.ent[e]; }
+    const int local = it - ebeg;
     x->en = en;
-    x->narrow = gk_narrow(en.nrows, g);
-    if (x->narrow) {
+    if (en.narrow) {
       x->j = 0;
       x->row0 = en.row0;
       x->nrow = en.nrows;
       x->cols = en.nrows * g.H;
       x->c = local;
-      x->t0 = x->c * g.chunk_n;
+      x->t0 = local * g.chunk_n;
       // whole pages: weights past the end are written as zeros
-      x->t1 = min((en.len + kBlock - 1) / kBlock * kBlock, x->t0 + g.chunk_n);
-      x->step = 128 / g.Hkv;
+      x->t1 = min((en.len + kBlock - 1) & ~(kBlock - 1), x->t0 + g.chunk_n);
+      x->step = 128 >> log2Hkv;
     } else {
-      const uint32_t nt = gk_tiles(en.nrows, g);
-      x->j = local % static_cast<uint32_t>(g.Hkv);
-      const uint32_t rest = local / static_cast<uint32_t>(g.Hkv);
-      const int rt = rest % nt;
-      x->c = rest / nt;
-      const int per = (en.nrows + nt - 1) / nt;
-      x->row0 = en.row0 + rt * per;
-      x->nrow = min(per, en.row0 + en.nrows - x->row0);
+      x->j = local & (g.Hkv - 1);
+      int rt = 0;
+      x->c = local >> log2Hkv;
+      if (en.k_nt > 1) {
+        const uint32_t rest = x->c, nt = en.k_nt;
+        x->c = rest / nt;
+        rt = rest - x->c * nt;
+      }
+      x->row0 = en.row0 + rt * en.k_per;
+      x->nrow = min(en.k_per, en.row0 + en.nrows - x->row0);
       x->cols = x->nrow << g.log2G;
       x->t0 = x->c * g.chunk_w;
       x->t1 = min(en.len, x->t0 + g.chunk_w);
@@ -357,6 +400,40 @@ struct KWalk {
     }
     ++it;
     return true;
+  }
+};
+
+// A position in a ring of n slots: slot s in its u-th use (parity u & 1).
+struct RingPos {
+  int s;
+  uint32_t u;
+  __device__ RingPos() : s(0), u(0) {}
+  __device__ void next(int n) { if (++s == n) { s = 0; ++u; } }
+};
+
+// The physical pages of a run of table entries, read 32 at a time by the lanes of
+// a warp and handed out in order: no dependent load per page.  Ids out of
+// range are flagged and read as page 0.
+struct PageReader {
+  const int32_t* row;   // entry of page 0 of the run
+  int n, base, NB;
+  int32_t cur, nxt;
+  int32_t* status;
+  int lane;
+  __device__ PageReader(const int32_t* row_, int n_, int NB_, int32_t* status_, int lane_)
+      : row(row_), n(n_), base(0), NB(NB_), status(status_), lane(lane_) {
+    cur = fetch(0);
+    nxt = fetch(32);
+  }
+  __device__ int32_t fetch(int b) {
+    int32_t x = b + lane < n ? row[b + lane] : 0;
+    if (x < 0 || x >= NB) { set_flag(status, STARKV_FLAG_BAD_BLOCK_ID); x = 0; }
+    return x;
+  }
+  // Called by the whole warp with i not falling below an earlier one minus 31.
+  __device__ int32_t page(int i) {
+    if (i - base >= 32) { cur = nxt; base += 32; nxt = fetch(base + 32); }
+    return __shfl_sync(0xffffffffu, cur, i - base);
   }
 };
 
@@ -395,7 +472,7 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
   float* stage = reinterpret_cast<float*>(ebar + 1);   // [4 warps][32 lanes][ncol + 4]
   __shared__ uint32_t taddr_s;
   __shared__ volatile int32_t abort_flag;
-  __shared__ int32_t s_e0;
+  __shared__ GroupTablesSmem s_tab;
   __shared__ int64_t s_off[128];   // P row of each column, or -1
   __shared__ int32_t s_rh[128];    // its (row, query head), or -1
   __shared__ float s_m[128];
@@ -424,110 +501,140 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
   }
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t total = g.kpre[g.E];
-  const int32_t i0 = static_cast<int32_t>(blockIdx.x * total / gridDim.x);
-  const int32_t i1 = static_cast<int32_t>((blockIdx.x + 1) * total / gridDim.x);
-  if (i0 < i1) find_entry(g.kpre, g.E, i0, &s_e0);
+  const GroupTables tab = load_tables(g, g.kpre, &s_tab);
   __syncthreads();
   tc_fence_after();
   const uint32_t taddr = taddr_s;
-  const int32_t e0 = i0 < i1 ? s_e0 : 0;
+  const int64_t total = tab.pre[g.E];
+  const int32_t i0 = static_cast<int32_t>(blockIdx.x * total / gridDim.x);
+  const int32_t i1 = static_cast<int32_t>((blockIdx.x + 1) * total / gridDim.x);
   const int G = 1 << g.log2G;
   const uint32_t half_q = p.q_bytes / 2;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      const uint64_t keep = policy_evict_last();
-      uint32_t k = 0, qi = 0;
-      bool ok = true;
-      KWalk walk(g, i0, i1, e0);
-      KItem x;
-      while (ok && walk.next(&x)) {
-        const int qs = static_cast<int>(qi % p.nq);
-        if (qi >= static_cast<uint32_t>(p.nq) && !mbar_wait(&qempty[qs], ((qi / p.nq) - 1) & 1)) { ok = false; break; }
-        uint8_t* qd = qslot + static_cast<size_t>(qs) * p.q_bytes;
-        if (x.narrow) {
-          const int nbox = (x.cols + kGKQBox - 1) / kGKQBox;
-          mbar_arrive_expect_tx(&qfull[qs], static_cast<uint32_t>(2 * p.kb * nbox * kGKQBox) * 128u);
-          for (int a = 0; a < p.kb; ++a)
-            for (int b = 0; b < nbox; ++b) {
-              const uint32_t o = static_cast<uint32_t>(a * g.ncol + b * kGKQBox) * 128u;
-              tma_load_2d(qd + o, &qhnmap, a * 64, x.row0 * g.H + b * kGKQBox, &qfull[qs], keep);
-              tma_load_2d(qd + half_q + o, &qlnmap, a * 64, x.row0 * g.H + b * kGKQBox, &qfull[qs], keep);
-            }
+    const uint64_t keep = policy_evict_last();
+    RingPos k;
+    uint32_t issued = 0, qi = 0;
+    bool ok = true;
+    KWalk walk(g, tab, p.log2Hkv, i0, i1);
+    KItem x;
+    while (ok && walk.next(&x)) {
+      PageReader pages(p.tables + static_cast<size_t>(x.en.tab) * g.MB + x.en.page0 + x.t0 / kBlock,
+                       (x.t1 - x.t0 + kBlock - 1) / kBlock, g.NB, g.status, lane);
+      const int qs = p.nq > 1 ? static_cast<int>(qi & 1) : 0;
+      const uint32_t qu = p.nq > 1 ? qi >> 1 : qi;
+      if (lane == 0) {
+        if (qu > 0 && !mbar_wait(&qempty[qs], (qu - 1) & 1)) {
+          ok = false;
         } else {
-          const int nbox = (x.cols + p.qbox - 1) / p.qbox;
-          const int rows_box = p.qbox >> g.log2G;
-          mbar_arrive_expect_tx(&qfull[qs], static_cast<uint32_t>(2 * p.kb * nbox * p.qbox) * 128u);
-          for (int a = 0; a < p.kb; ++a)
-            for (int b = 0; b < nbox; ++b) {
-              const uint32_t o = static_cast<uint32_t>(a * g.ncol + b * p.qbox) * 128u;
-              tma_load_3d(qd + o, &qhwmap, a * 64, x.j << g.log2G, x.row0 + b * rows_box, &qfull[qs], keep);
-              tma_load_3d(qd + half_q + o, &qlwmap, a * 64, x.j << g.log2G, x.row0 + b * rows_box, &qfull[qs], keep);
-            }
-        }
-        ++qi;
-        const int32_t* trow = p.tables + static_cast<size_t>(x.en.tab) * g.MB + x.en.page0;
-        const int tb = x.narrow ? min(kBlock, x.step) : kBlock;           // tokens per box
-        const uint32_t box = x.narrow ? static_cast<uint32_t>(tb * g.Hkv) * 128u : 2048u;
-        for (int t = x.t0; t < x.t1; t += x.step, ++k) {
-          const int s = static_cast<int>(k % S);
-          if (k >= static_cast<uint32_t>(S) && !mbar_wait(&empty[s], ((k / S) - 1) & 1)) { ok = false; break; }
-          const int nb = (min(x.step, x.t1 - t) + tb - 1) / tb;
-          uint8_t* st = smem + static_cast<size_t>(s) * p.a_bytes;
-          mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nb * p.kb) * box);
-          for (int c = 0; c < nb; ++c) {
-            const int tk = t + c * tb;
-            int32_t phys = trow[tk / kBlock];
-            if (phys < 0 || phys >= g.NB) { set_flag(g.status, STARKV_FLAG_BAD_BLOCK_ID); phys = 0; }
-            const int row = phys * kBlock + (tk & (kBlock - 1));
-            for (int a = 0; a < p.kb; ++a) {
-              if (x.narrow) tma_load_3d(st + a * 16384 + c * box, &knmap, a * 64, 0, row, &full[s], keep);
-              else tma_load_3d(st + a * 16384 + c * box, &kwmap, a * 64, x.j, row, &full[s], keep);
-            }
+          uint8_t* qd = qslot + static_cast<size_t>(qs) * p.q_bytes;
+          if (x.en.narrow) {
+            const int nbox = (x.cols + p.nbox - 1) / p.nbox;
+            mbar_arrive_expect_tx(&qfull[qs], static_cast<uint32_t>(2 * p.kb * nbox * p.nbox) * 128u);
+            for (int a = 0; a < p.kb; ++a)
+              for (int b = 0; b < nbox; ++b) {
+                const uint32_t o = static_cast<uint32_t>(a * g.ncol + b * p.nbox) * 128u;
+                tma_load_2d(qd + o, &qhnmap, a * 64, x.row0 * g.H + b * p.nbox, &qfull[qs], keep);
+                tma_load_2d(qd + half_q + o, &qlnmap, a * 64, x.row0 * g.H + b * p.nbox, &qfull[qs], keep);
+              }
+          } else {
+            const int nbox = (x.cols + p.qbox - 1) / p.qbox;
+            const int rows_box = p.qbox >> g.log2G;
+            mbar_arrive_expect_tx(&qfull[qs], static_cast<uint32_t>(2 * p.kb * nbox * p.qbox) * 128u);
+            for (int a = 0; a < p.kb; ++a)
+              for (int b = 0; b < nbox; ++b) {
+                const uint32_t o = static_cast<uint32_t>(a * g.ncol + b * p.qbox) * 128u;
+                tma_load_3d(qd + o, &qhwmap, a * 64, x.j << g.log2G, x.row0 + b * rows_box, &qfull[qs], keep);
+                tma_load_3d(qd + half_q + o, &qlwmap, a * 64, x.j << g.log2G, x.row0 + b * rows_box, &qfull[qs], keep);
+              }
           }
         }
       }
+      ++qi;
+      const int tb = x.en.narrow ? min(kBlock, x.step) : kBlock;           // tokens per box
+      const uint32_t box = x.en.narrow ? static_cast<uint32_t>(tb * g.Hkv) * 128u : 2048u;
+      const int boxes = x.step / tb;                                       // boxes of a whole step
+      for (int t = x.t0; t < x.t1; t += x.step) {
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        const int nb = t + x.step <= x.t1 ? boxes : (x.t1 - t + tb - 1) / tb;
+        uint8_t* st = smem + static_cast<size_t>(k.s) * p.a_bytes;
+        if (lane == 0) {
+          if (k.u > 0 && !mbar_wait(&empty[k.s], (k.u - 1) & 1)) ok = false;
+          else mbar_arrive_expect_tx(&full[k.s], static_cast<uint32_t>(nb * p.kb) * box);
+        }
+        for (int c = 0; c < nb; ++c) {
+          const int tk = t + c * tb;
+          const int row = pages.page((tk - x.t0) >> 4) * kBlock + (tk & (kBlock - 1));
+          if (lane == 0 && ok) {
+            if (x.en.narrow) {
+              for (int a = 0; a < p.kb; ++a) tma_load_3d(st + a * 16384 + c * box, &knmap, a * 64, 0, row, &full[k.s], keep);
+            } else {
+              for (int a = 0; a < p.kb; ++a) tma_load_3d(st + a * 16384 + c * box, &kwmap, a * 64, x.j, row, &full[k.s], keep);
+            }
+          }
+        }
+        if (ok) { ++issued; k.next(S); }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (lane == 0) {
       if (!ok) {
         set_timeout(g.status, kSiteKEmpty);
         abort_flag = 1;
       }
       // copies still in flight land before the CTA can exit
-      const uint32_t f0 = k >= static_cast<uint32_t>(S) ? k - S : 0u;
-      for (uint32_t kk = f0; kk < k; ++kk) mbar_wait(&full[kk % S], (kk / S) & 1);
-      const uint32_t q0 = qi >= static_cast<uint32_t>(p.nq) ? qi - p.nq : 0u;
-      for (uint32_t kk = q0; kk < qi; ++kk) mbar_wait(&qfull[kk % p.nq], (kk / p.nq) & 1);
+      for (uint32_t n = 0; n < issued && n < static_cast<uint32_t>(S); ++n) {
+        if (--k.s < 0) { k.s = S - 1; --k.u; }
+        mbar_wait(&full[k.s], k.u & 1);
+      }
+      for (uint32_t n = 0; n < qi && n < static_cast<uint32_t>(p.nq); ++n) {
+        const uint32_t z = qi - 1 - n;
+        mbar_wait(&qfull[p.nq > 1 ? z & 1 : 0], (p.nq > 1 ? z >> 1 : z) & 1);
+      }
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA
     if (lane == 0) {
-      uint32_t k = 0, qi = 0;
+      RingPos k, acc;
+      uint32_t qi = 0;
       bool ok = true;
-      KWalk walk(g, i0, i1, e0);
+      // descriptors of stage 0 and query slot 0; the start address field (bytes / 16)
+      // advances by plain addition: shared addresses stay below 256 KB
+      const uint64_t ad0 = smem_desc(smem_u32(smem), 16u, 1024u, kSwizzle128B);
+      const uint64_t bd0 = smem_desc(smem_u32(qslot), 16u, 1024u, kSwizzle128B);
+      const uint32_t half16 = half_q >> 4, blk16 = static_cast<uint32_t>(g.ncol) * 8u;
+      KWalk walk(g, tab, p.log2Hkv, i0, i1);
       KItem x;
       while (ok && walk.next(&x)) {
-        const int qs = static_cast<int>(qi % p.nq);
-        if (!mbar_wait(&qfull[qs], (qi / p.nq) & 1)) { ok = false; break; }
-        const int nmma = (x.cols + 15) / 16 * 16;
-        const uint32_t idesc = idesc_f16_f32(128, nmma, /*a_mn_major=*/false, /*b_mn_major=*/false);
-        const uint32_t sq = smem_u32(qslot + static_cast<size_t>(qs) * p.q_bytes);
-        for (int t = x.t0; t < x.t1; t += x.step, ++k) {
-          const int s = static_cast<int>(k % S), a = static_cast<int>(k % kGKAcc);
-          if (k >= kGKAcc && !mbar_wait(&tempty[a], ((k / kGKAcc) - 1) & 1)) { ok = false; break; }
-          if (!mbar_wait(&full[s], (k / S) & 1) || abort_flag) { ok = false; break; }
+        const int qs = p.nq > 1 ? static_cast<int>(qi & 1) : 0;
+        const uint32_t qu = p.nq > 1 ? qi >> 1 : qi;
+        const uint32_t idesc = idesc_f16_f32(128, (x.cols + 15) & ~15, /*a_mn_major=*/false, /*b_mn_major=*/false);
+        const uint64_t bq = bd0 + ((static_cast<uint32_t>(qs) * p.q_bytes) >> 4);
+        if (!mbar_wait(&qfull[qs], qu & 1)) { ok = false; break; }
+        for (int t = x.t0; t < x.t1; t += x.step) {
+          if (acc.u > 0 && !mbar_wait(&tempty[acc.s], (acc.u - 1) & 1)) { ok = false; break; }
+          const uint64_t as = ad0 + ((static_cast<uint32_t>(k.s) * p.a_bytes) >> 4);
+          const uint32_t dst = taddr + static_cast<uint32_t>(acc.s * g.ncol);
+          if (!mbar_wait(&full[k.s], k.u & 1) || abort_flag) { ok = false; break; }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + static_cast<size_t>(s) * p.a_bytes);
-          const uint32_t dst = taddr + static_cast<uint32_t>(a * g.ncol);
-          for (int ks = 0; ks < p.ksteps; ++ks) {
-            const uint32_t blk = ks >> 2, off = (ks & 3) * 32u;
-            const uint64_t ad = smem_desc(sa + blk * 16384u + off, 16u, 1024u, kSwizzle128B);
-            const uint32_t bo = sq + blk * static_cast<uint32_t>(g.ncol) * 128u + off;
-            umma_f16_ss(dst, ad, smem_desc(bo, 16u, 1024u, kSwizzle128B), idesc, ks > 0 ? 1u : 0u);
-            umma_f16_ss(dst, ad, smem_desc(bo + half_q, 16u, 1024u, kSwizzle128B), idesc, 1u);
+          int left = p.ksteps;
+          uint64_t a = as, b = bq;
+          uint32_t on = 0;
+          for (; left > 0; left -= 4, a += 1024u, b += blk16) {
+#pragma unroll
+            for (uint32_t kk = 0; kk < 4; ++kk)
+              if (static_cast<int>(kk) < left) {
+                umma_f16_ss(dst, a + kk * 2u, b + kk * 2u, idesc, on);
+                umma_f16_ss(dst, a + kk * 2u, b + kk * 2u + half16, idesc, 1u);
+                on = 1;
+              }
           }
-          umma_commit(&empty[s]);
-          umma_commit(&tfull[a]);
+          umma_commit(&empty[k.s]);
+          umma_commit(&tfull[acc.s]);
+          k.next(S);
+          acc.next(kGKAcc);
         }
         umma_commit(&qempty[qs]);
         ++qi;
@@ -543,7 +650,7 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
     const uint32_t tq = taddr + (static_cast<uint32_t>(q * 32) << 16);
     uint32_t k = 0, phase = 0;
     bool ok = true;
-    KWalk walk(g, i0, i1, e0);
+    KWalk walk(g, tab, p.log2Hkv, i0, i1);
     KItem x;
     while (ok && walk.next(&x)) {
       const int t_pad = g.t_pad[x.en.psrc];
@@ -554,21 +661,20 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
         int32_t rh = -1;
         float m = 0.f;
         if (et < x.cols) {
-          const int row = x.row0 + (x.narrow ? et / g.H : et >> g.log2G);
-          const int h = x.narrow ? et & (g.H - 1) : (x.j << g.log2G) + (et & (G - 1));
-          if (x.en.zsrc || g.row_use[row]) {
-            rh = row * g.H + h;
-            if (kWeights) m = g.mrow[rh];
-          }
+          const int row = x.row0 + (x.en.narrow ? et / g.H : et >> g.log2G);
+          const int h = x.en.narrow ? et & (g.H - 1) : (x.j << g.log2G) + (et & (G - 1));
+          rh = row * g.H + h;
+          const int use = x.en.zsrc ? 1 : g.row_use[row];
+          if (kWeights) m = g.mrow[rh];
+          if (!use) rh = -1;
         }
         s_rh[et] = rh;
         s_off[et] = rh < 0 ? -1 : static_cast<int64_t>(rh) * t_pad;
         s_m[et] = m;
-        if (kWeights)
-          for (int u = 0; u < 4; ++u) s_red[u][et] = 0.f;
+        for (int u = 0; u < 4; ++u) s_red[u][et] = kWeights ? 0.f : -INFINITY;
       }
       if (!group_sync(ebar, phase)) { ok = false; break; }
-      if (x.narrow) {
+      if (x.en.narrow) {
         // lane: code row rho = q * 32 + lane of the step, i.e. token rho / Hkv, KV head
         // rho % Hkv; value i is (row i / G of the entry, query head i % G of the head)
         const int rho = q * 32 + lane, j = rho & (g.Hkv - 1), tl = rho >> p.log2Hkv;
@@ -627,10 +733,7 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
                 run[i] = kWeights ? run[i] + y : fmaxf(run[i], y);
               }
               const int col = (i >> g.log2G) * g.H + (j << g.log2G) + (i & (G - 1));
-              if (lane < g.Hkv) {
-                if constexpr (kWeights) s_red[q][col] = run[i];
-                else if (s_rh[col] >= 0 && run[i] > -INFINITY) atomic_max_f32(&g.mrow[s_rh[col]], run[i]);
-              }
+              if (lane < g.Hkv) s_red[q][col] = run[i];
             }
         }
       } else {
@@ -689,14 +792,18 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
                 const float m = warp_max_f32(run[i][u]);
                 if (lane == u) mine = m;
               }
-              const int c = cb * 16 + (lane & 15);
-              if (lane < 16 && s_rh[c] >= 0 && mine > -INFINITY) atomic_max_f32(&g.mrow[s_rh[c]], mine);
+              if (lane < 16) s_red[q][cb * 16 + lane] = mine;
             }
           }
         }
       }
-      if constexpr (kWeights) {
-        if (!group_sync(ebar, phase)) { ok = false; break; }
+      if (!group_sync(ebar, phase)) { ok = false; break; }
+      if constexpr (!kWeights) {
+        if (et < x.cols && s_rh[et] >= 0) {
+          const float m = fmaxf(fmaxf(s_red[0][et], s_red[1][et]), fmaxf(s_red[2][et], s_red[3][et]));
+          if (m > -INFINITY) atomic_max_f32(&g.mrow[s_rh[et]], m);
+        }
+      } else {
         if (et < x.cols && s_rh[et] >= 0) {
           const float L = ((s_red[0][et] + s_red[1][et]) + s_red[2][et]) + s_red[3][et];
           g.lpart[x.en.zsrc][static_cast<size_t>(s_rh[et]) * g.n_ch[x.en.zsrc] + x.c] = L;
@@ -734,7 +841,6 @@ constexpr int kGVThreads = 320;                    // warp 0 TMA, warp 1 MMA, wa
 constexpr int kGVEpi = kGVThreads - 64;
 constexpr uint32_t kGVABytes = 4u * 8192u;         // 4 pages x 16 tokens x 256 codes
 constexpr uint32_t kGVBBytes = kGVTile * 128u;     // 256 columns x 64 tokens
-constexpr int kGVPBox = 32;                        // P rows per TMA box
 constexpr int kGVMinUnits = 3;                     // units per CTA at least, in a call with few
 
 struct VSeg {
@@ -746,30 +852,31 @@ struct VSeg {
 
 struct VWalk {
   const GroupGeom& g;
+  const GroupTables& tb;
   int32_t u, end, ebeg, eend, e;
   GroupEntry en;
-  __device__ VWalk(const GroupGeom& g_, int32_t a, int32_t b, int32_t e0) : g(g_), u(a), end(b), ebeg(0), eend(0), e(e0) {
+  __device__ VWalk(const GroupGeom& g_, const GroupTables& tb_, int32_t a, int32_t b)
+      : g(g_), tb(tb_), u(a), end(b), ebeg(0), eend(0), e(0) {
     if (u < end) {
-      ebeg = g.vpre[e];
-      eend = g.vpre[e + 1];
-      en = g.ent[e];
+      e = entry_of(tb, u);
+      ebeg = tb.pre[e];
+      eend = tb.pre[e + 1];
+      en = tb.ent[e];
     }
   }
   __device__ bool next(VSeg* s) {
     if (u >= end) return false;
-    while (u >= eend) { ++e; ebeg = eend; eend = g.vpre[e + 1]; if (u < eend) en = g.ent[e]; }
-    const uint32_t units = (en.len + kGVTok - 1) / kGVTok;
+    while (u >= eend) { ++e; ebeg = eend; eend = tb.pre[e + 1]; if (u < eend) en = tb.ent[e]; }
+    const uint32_t units = en.v_units;
     const uint32_t local = static_cast<uint32_t>(u - ebeg);
     const uint32_t tile = local / units;
     const uint32_t nt = tile / static_cast<uint32_t>(g.n_rt);
-    const int cols = en.nrows * g.H;
-    const int width = gv_width(cols, gv_tiles(cols));
     s->en = en;
     s->tile = en.tile0 + static_cast<int>(tile);
     s->rt = static_cast<int>(tile - nt * g.n_rt);
-    s->col0 = static_cast<int>(nt) * width;
-    s->ncols = min(width, cols - s->col0);
-    s->n = (s->ncols + 15) / 16 * 16;
+    s->col0 = static_cast<int>(nt) * en.v_width;
+    s->ncols = min(en.v_width, en.nrows * g.H - s->col0);
+    s->n = (s->ncols + 15) & ~15;
     s->u0 = static_cast<int>(local - tile * units);
     s->u1 = min(static_cast<int>(units), s->u0 + end - u);
     s->first = s->u0 == 0;
@@ -781,7 +888,8 @@ struct VWalk {
 
 __global__ void __launch_bounds__(kGVThreads, 1)
 group_vpass_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap pmap0,
-                   const __grid_constant__ CUtensorMap pmap1, GroupVParams p) {
+                   const __grid_constant__ CUtensorMap pmap1, const __grid_constant__ CUtensorMap pmap0b,
+                   const __grid_constant__ CUtensorMap pmap1b, GroupVParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
   const GroupGeom& g = p.g;
@@ -794,7 +902,7 @@ group_vpass_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_consta
   uint64_t* fixed = fixreq + 1;    // its rows past the end are zero
   uint64_t* mmadone = fixed + 1;
   __shared__ uint32_t taddr_s;
-  __shared__ int32_t s_e0;
+  __shared__ GroupTablesSmem s_tab;
   __shared__ volatile int32_t abort_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -809,6 +917,8 @@ group_vpass_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_consta
     prefetch_tensormap(&vmap);
     prefetch_tensormap(&pmap0);
     prefetch_tensormap(&pmap1);
+    prefetch_tensormap(&pmap0b);
+    prefetch_tensormap(&pmap1b);
   }
   if (warp == 1) {
     tmem_alloc(&taddr_s, 512);
@@ -817,95 +927,112 @@ group_vpass_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_consta
   }
   griddep_wait();
   griddep_launch_dependents();
+  const GroupTables tab = load_tables(g, g.vpre, &s_tab);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t taddr = taddr_s;
   Partition pt;
-  pt.P = g.vpre[g.E];
+  pt.P = tab.pre[g.E];
   pt.G = static_cast<int32_t>(min(static_cast<int64_t>(gridDim.x), max(pt.P / kGVMinUnits, int64_t{1})));
   const int cta = blockIdx.x;
   const bool live = cta < pt.G;
   const int32_t u0 = live ? static_cast<int32_t>(part_begin(cta, pt)) : 0;
   const int32_t u1 = live ? static_cast<int32_t>(part_begin(cta + 1, pt)) : 0;
-  if (u0 < u1) find_entry(g.vpre, g.E, u0, &s_e0);
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t taddr = taddr_s;
-  const int32_t e0 = u0 < u1 ? s_e0 : 0;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      const uint64_t pol_once = policy_evict_first(), pol_keep = policy_evict_last();
-      uint32_t k = 0;
-      bool ok = true;
-      VWalk walk(g, u0, u1, e0);
-      VSeg x;
-      while (ok && walk.next(&x)) {
-        const int32_t* trow = p.tables + static_cast<size_t>(x.en.tab) * g.MB + x.en.page0;
-        const int nbox = (x.n + kGVPBox - 1) / kGVPBox;
-        const int prow = x.en.row0 * g.H + x.col0;
-        const uint64_t pol = x.en.zsrc ? pol_once : pol_keep;
-        for (int u = x.u0; u < x.u1; ++u, ++k) {
-          const int s = static_cast<int>(k % S);
-          if (k >= static_cast<uint32_t>(S) && !mbar_wait(&empty[s], ((k / S) - 1) & 1)) { ok = false; break; }
-          const int t0 = u * kGVTok;
-          const int np = (min(kGVTok, x.en.len - t0) + kBlock - 1) / kBlock;
-          uint8_t* st = smem + static_cast<size_t>(s) * p.stage_bytes;
-          mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(np) * 8192u + static_cast<uint32_t>(nbox) * kGVPBox * 128u);
-          for (int c = 0; c < np; ++c) {
-            int32_t phys = trow[t0 / kBlock + c];
-            if (phys < 0 || phys >= g.NB) { set_flag(g.status, STARKV_FLAG_BAD_BLOCK_ID); phys = 0; }
-            tma_load_3d(st + c * 8192, &vmap, 0, phys * kBlock, x.rt * 4, &full[s], pol);
-          }
-          for (int b = 0; b < nbox; ++b) {
-            if (x.en.psrc) tma_load_2d(st + kGVABytes + b * kGVPBox * 128, &pmap1, t0, prow + b * kGVPBox, &full[s], pol);
-            else tma_load_2d(st + kGVABytes + b * kGVPBox * 128, &pmap0, t0, prow + b * kGVPBox, &full[s], pol);
+    const uint64_t pol_once = policy_evict_first(), pol_keep = policy_evict_last();
+    RingPos k;
+    uint32_t issued = 0;
+    bool ok = true;
+    VWalk walk(g, tab, u0, u1);
+    VSeg x;
+    while (ok && walk.next(&x)) {
+      PageReader pages(p.tables + static_cast<size_t>(x.en.tab) * g.MB + x.en.page0 + x.u0 * (kGVTok / kBlock),
+                       (min(x.en.len, x.u1 * kGVTok) - x.u0 * kGVTok + kBlock - 1) / kBlock, g.NB, g.status, lane);
+      // P boxes of 128 columns for wide tiles, of 32 for narrow ones
+      const bool big = x.n > 64;
+      const int pbox = big ? 128 : 32, nbox = (x.n + pbox - 1) / pbox;
+      const CUtensorMap* pm = x.en.psrc ? (big ? &pmap1b : &pmap1) : (big ? &pmap0b : &pmap0);
+      const int prow = x.en.row0 * g.H + x.col0;
+      const uint64_t pol = x.en.zsrc ? pol_once : pol_keep;
+      int pi = 0;
+      for (int u = x.u0; u < x.u1; ++u, pi += 4) {
+        const int t0 = u * kGVTok;
+        const int np = t0 + kGVTok <= x.en.len ? 4 : (x.en.len - t0 + kBlock - 1) / kBlock;
+        const int32_t p0 = pages.page(pi), p1 = pages.page(pi + 1), p2 = pages.page(pi + 2), p3 = pages.page(pi + 3);
+        uint8_t* st = smem + static_cast<size_t>(k.s) * p.stage_bytes;
+        if (lane == 0) {
+          if (k.u > 0 && !mbar_wait(&empty[k.s], (k.u - 1) & 1)) {
+            ok = false;
+          } else {
+            mbar_arrive_expect_tx(&full[k.s], static_cast<uint32_t>(np) * 8192u + static_cast<uint32_t>(nbox * pbox) * 128u);
+            tma_load_3d(st, &vmap, 0, p0 * kBlock, x.rt * 4, &full[k.s], pol);
+            if (np > 1) tma_load_3d(st + 8192, &vmap, 0, p1 * kBlock, x.rt * 4, &full[k.s], pol);
+            if (np > 2) tma_load_3d(st + 16384, &vmap, 0, p2 * kBlock, x.rt * 4, &full[k.s], pol);
+            if (np > 3) tma_load_3d(st + 24576, &vmap, 0, p3 * kBlock, x.rt * 4, &full[k.s], pol);
+            for (int b = 0; b < nbox; ++b)
+              tma_load_2d(st + kGVABytes + b * pbox * 128, pm, t0, prow + b * pbox, &full[k.s], pol);
           }
         }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        ++issued;
+        k.next(S);
       }
+    }
+    if (lane == 0) {
       if (!ok) {
         set_timeout(g.status, kSiteVEmpty);
         abort_flag = 1;
       }
-      const uint32_t f0 = k >= static_cast<uint32_t>(S) ? k - S : 0u;
-      for (uint32_t kk = f0; kk < k; ++kk) mbar_wait(&full[kk % S], (kk / S) & 1);
+      // copies still in flight land before the CTA can exit
+      for (uint32_t n = 0; n < issued && n < static_cast<uint32_t>(S); ++n) {
+        if (--k.s < 0) { k.s = S - 1; --k.u; }
+        mbar_wait(&full[k.s], k.u & 1);
+      }
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA
     // Segments of up to 128 columns alternate between two accumulators (256
     // columns of tensor memory each, two 128-row tiles); a wider one takes both.
     if (lane == 0) {
-      uint32_t k = 0, seg = 0, fix = 0;
+      RingPos k;
+      uint32_t seg = 0, fix = 0;
       bool ok = true, wide_before = false;
-      VWalk walk(g, u0, u1, e0);
+      const uint64_t ad0 = smem_desc(smem_u32(smem), 2048u, 1024u, kSwizzle128B);
+      const uint64_t bd0 = smem_desc(smem_u32(smem) + kGVABytes, 16u, 1024u, kSwizzle128B);
+      VWalk walk(g, tab, u0, u1);
       VSeg x;
       while (ok && walk.next(&x)) {
         const uint32_t idesc = idesc_f16_f32(128, x.n, /*a_mn_major=*/true, /*b_mn_major=*/false);
-        const int mts = x.rt * kGVTile + 128 < g.R ? 2 : 1;
+        const bool two = x.rt * kGVTile + 128 < g.R;
         const bool wide = x.n > 128;
         const uint32_t base = taddr + (wide ? 0u : (seg & 1) * 256u), mstep = wide ? 256u : 128u;
         if (seg > 1 && !mbar_wait(&tfree[seg & 1], ((seg >> 1) - 1) & 1)) { ok = false; break; }
         if (seg > 0 && (wide || wide_before) && !mbar_wait(&tfree[(seg - 1) & 1], ((seg - 1) >> 1) & 1)) { ok = false; break; }
         wide_before = wide;
         uint32_t acc = 0;
-        for (int u = x.u0; u < x.u1; ++u, ++k) {
-          const int s = static_cast<int>(k % S);
-          if (!mbar_wait(&full[s], (k / S) & 1) || abort_flag) { ok = false; break; }
+        for (int u = x.u0; u < x.u1; ++u) {
+          const uint32_t so = (static_cast<uint32_t>(k.s) * p.stage_bytes) >> 4;
           const int nt = min(kGVTok, x.en.len - u * kGVTok);
+          if (!mbar_wait(&full[k.s], k.u & 1) || abort_flag) { ok = false; break; }
           if (nt & (kBlock - 1)) {   // a page that ends inside: its rows past the end are zeroed first
             mbar_arrive(fixreq);
             if (!mbar_wait(fixed, fix & 1)) { ok = false; break; }
             ++fix;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + static_cast<size_t>(s) * p.stage_bytes);
-          const int np = (nt + kBlock - 1) / kBlock;
-          for (int c = 0; c < np; ++c) {
-            const uint64_t bd = smem_desc(sa + kGVABytes + c * 32u, 16u, 1024u, kSwizzle128B);
-            for (int m = 0; m < mts; ++m)
-              umma_f16_ss(base + m * mstep, smem_desc(sa + c * 8192u + m * 4096u, 2048u, 1024u, kSwizzle128B), bd, idesc,
-                          acc);
-            acc = 1;
-          }
-          umma_commit(&empty[s]);
+          const uint64_t a = ad0 + so, b = bd0 + so;
+#pragma unroll
+          for (uint32_t c = 0; c < 4; ++c)
+            if (static_cast<int>(c) * kBlock < nt) {
+              umma_f16_ss(base, a + c * 512u, b + c * 2u, idesc, acc);
+              if (two) umma_f16_ss(base + mstep, a + c * 512u + 256u, b + c * 2u, idesc, acc);
+              acc = 1;
+            }
+          umma_commit(&empty[k.s]);
+          k.next(S);
         }
         if (!ok) break;
         umma_commit(&zdone[seg & 1]);
@@ -917,10 +1044,10 @@ group_vpass_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_consta
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int et = tid - 64, q = warp & 3, hf = (warp - 2) >> 2, i4 = lane & 3;
+    const int et = tid - 64, q = warp & 3, hf = (warp - 2) >> 2;
     uint32_t seg = 0, fix = 0, k = 0;
     const uint64_t keep = policy_evict_last();   // partial sums: read back by the finish kernel
-    VWalk walk(g, u0, u1, e0);
+    VWalk walk(g, tab, u0, u1);
     VSeg x;
     while (walk.next(&x)) {
       k += static_cast<uint32_t>(x.u1 - x.u0);
@@ -962,19 +1089,16 @@ group_vpass_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_consta
       for (int m = 0; m < 2; ++m) {
         const int j0 = m * 128 + q * 32;                  // the warp's first row of the R tile
         if (x.rt * kGVTile + j0 >= g.R) break;            // warp-uniform (R is a multiple of 64)
-        float* zq = dst + j0 + 4 * (lane >> 2);
+        // a warp stores 128 contiguous bytes of a column per instruction
+        float* zq = dst + j0 + lane;
         for (int h0 = hf * 16; h0 < x.n; h0 += 32) {
           __syncwarp();
           uint32_t v[32];
           tmem_ld_32x32b_x16(base + (static_cast<uint32_t>(q * 32) << 16) + m * mstep + h0, v);
           tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float4 f = quad_transpose(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1]),
-                                            __uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3]), i4);
-            const int col = h0 + 4 * c + i4;
-            if (col < x.ncols) st_global_hint_free(reinterpret_cast<float4*>(zq + col * stride), f, keep);
-          }
+          for (int c = 0; c < 16; ++c)
+            if (h0 + c < x.ncols) st_global_hint_free(zq + (h0 + c) * stride, __uint_as_float(v[c]), keep);
         }
       }
       tc_fence_before();
@@ -1007,13 +1131,14 @@ struct GroupFinishParams {
   int npad;              // UMMA N
   int k_per_cta;         // rows of R per CTA, a multiple of 64
   int stages;
+  int log2cg;            // converter groups: the warps split into 1 << log2cg groups that take stages in turn
   uint32_t stage_bytes, tmem_cols;
 };
 
 constexpr int kGFThreads = 320;
 constexpr int kGFConv = kGFThreads - 64;
 
-__global__ void __launch_bounds__(kGFThreads, 1)
+__global__ void __launch_bounds__(kGFThreads, 2)
 group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams p) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
@@ -1030,6 +1155,7 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
   float* part = reinterpret_cast<float*>(smem);     // [npad][128], reuses the ring
   __shared__ uint32_t taddr_s;
   __shared__ float s_il[256];
+  __shared__ GroupTablesSmem s_tab;
   __shared__ int32_t s_i0[2][256], s_n[2][256], s_col[2][256];   // per source: first CTA, CTAs, column within the V tile
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1043,7 +1169,7 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
   const int ncols = p.rows_tile << g.log2G;
 
   if (tid == 0) {
-    for (int s = 0; s < S; ++s) { mbar_init(&full[s], 1); mbar_init(&conv[s], kGFConv); mbar_init(&empty[s], 1); }
+    for (int s = 0; s < S; ++s) { mbar_init(&full[s], 1); mbar_init(&conv[s], kGFConv >> p.log2cg); mbar_init(&empty[s], 1); }
     mbar_init(done, 1);
     mbar_init(cbar, kGFConv);
     fence_mbar_init();
@@ -1095,17 +1221,25 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
     const int et = tid - 64;
     griddep_wait();
     const int n_src = g.shared ? 2 : 1;
+    uint32_t phase = 0;
+    const GroupEntry* ent = g.ent;
+    if (g.E <= kGSmemE) {
+      for (int i = et; i < g.E * 4; i += kGFConv)
+        reinterpret_cast<uint4*>(s_tab.ent)[i] = reinterpret_cast<const uint4*>(g.ent)[i];
+      ent = s_tab.ent;
+      if (!group_sync(cbar, phase)) ok = false;
+    }
     // 1 / L of every column: a warp sums a column's chunks
     for (int c = warp - 2; c < ncols; c += kGFConv / 32) {
       const int row = row0 + (c >> g.log2G);
-      const int e = row < g.n_rows ? g.row_ent[row] : -1;
+      const int e = row < g.n_rows ? g.row_ent[row] : -1, use = row < g.n_rows ? g.row_use[row] : 0;
       float L = 0.f;
       if (e >= 0) {
         const size_t rh = static_cast<size_t>(row) * g.H + (j << g.log2G) + (c & ((1 << g.log2G) - 1));
         for (int s = 0; s < n_src; ++s) {
-          const GroupEntry en = g.ent[s ? g.n_groups + row : e];
-          if (en.len == 0 || (s == 0 && !g.row_use[row])) continue;
-          const int ch = gk_narrow(en.nrows, g) ? g.chunk_n : g.chunk_w;
+          const GroupEntry en = ent[s ? g.n_groups + row : e];
+          if (en.len == 0 || (s == 0 && !use)) continue;
+          const int ch = en.narrow ? g.chunk_n : g.chunk_w;
           const int nc = (en.len + ch - 1) / ch;
           for (int i = lane; i < nc; i += 32) L += g.lpart[s][rh * g.n_ch[s] + i];
         }
@@ -1114,8 +1248,8 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
       for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
       if (lane == 0) s_il[c] = L == 0.f ? 0.f : 1.f / L;   // no token at all: L = 0 and the result is 0
     }
+    const int cthr = kGFConv >> p.log2cg, cgrp = et / cthr;   // threads of a group, this thread's group
     int rt_at = -1;
-    uint32_t phase = 0;
     for (int i = 0; i < n_stages && ok; ++i) {
       const int s = i % S;
       const int kr = k0 + i * 64, rt = kr / kGVTile;
@@ -1125,18 +1259,17 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
         if (!group_sync(cbar, phase)) { ok = false; break; }
         for (int c = et; c < ncols; c += kGFConv) {
           const int row = row0 + (c >> g.log2G), h = (j << g.log2G) + (c & ((1 << g.log2G) - 1));
-          const int e = row < g.n_rows ? g.row_ent[row] : -1;
+          const int e = row < g.n_rows ? g.row_ent[row] : -1, use = row < g.n_rows ? g.row_use[row] : 0;
           for (int sr = 0; sr < 2; ++sr) {
             int i0 = 0, n = 0, place = 0;
-            if (sr < n_src && e >= 0 && (sr || g.row_use[row])) {
-              const GroupEntry en = g.ent[sr ? g.n_groups + row : e];
+            if (sr < n_src && e >= 0 && (sr || use)) {
+              const GroupEntry en = ent[sr ? g.n_groups + row : e];
               if (en.len > 0) {
-                const int cols = en.nrows * g.H, width = gv_width(cols, gv_tiles(cols));
-                const int col = (row - en.row0) * g.H + h;
-                const int tile = en.tile0 + (col / width) * g.n_rt + rt;
+                const int col = (row - en.row0) * g.H + h, nt = col / en.v_width;
+                const int tile = en.tile0 + nt * g.n_rt + rt;
                 i0 = g.tfirst[tile];
                 n = g.tlast[tile] - i0 + 1;
-                place = col % width;
+                place = col - nt * en.v_width;
               }
             }
             s_i0[sr][c] = i0;
@@ -1146,10 +1279,11 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
         }
         if (!group_sync(cbar, phase)) { ok = false; break; }
       }
+      if ((i & ((1 << p.log2cg) - 1)) != cgrp) continue;   // another group's stage
       if (i >= S && !__all_sync(0xffffffffu, mbar_wait(&empty[s], ((i / S) - 1) & 1))) { ok = false; break; }
       uint8_t* hi_t = smem + static_cast<size_t>(s) * p.stage_bytes + a_bytes;
       // item = (column bl, 8-value chunk c of the stage's 64 rows of R)
-      for (int item = et; item < p.npad * 8; item += kGFConv) {
+      for (int item = et & (cthr - 1); item < p.npad * 8; item += cthr) {
         const int bl = item >> 3, c = item & 7;
         float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (bl < ncols && row0 + (bl >> g.log2G) < g.n_rows) {

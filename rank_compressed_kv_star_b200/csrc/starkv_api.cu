@@ -1506,14 +1506,14 @@ bool encode_rows_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_
 struct GroupPlan {
   GroupGeom g;
   // K pass
-  int kb, ksteps, qbox, log2Hkv, nq, k_stages, k_ctas;
+  int kb, ksteps, qbox, nbox, log2Hkv, nq, k_stages, k_ctas;
   uint32_t a_bytes, q_bytes, k_tmem;
   size_t k_smem;
   // V pass
   int v_stages, v_ctas;
   size_t v_smem;
   // finish
-  int f_mt, f_rows, f_tiles, f_npad, f_ks, f_kpc, f_stages;
+  int f_mt, f_rows, f_tiles, f_npad, f_ks, f_kpc, f_stages, f_log2cg;
   uint32_t f_stage_bytes, f_tmem;
   size_t f_smem;
   // absorption
@@ -1552,11 +1552,15 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
   p.kb = (g.r + 63) / 64;
   p.ksteps = (g.r + 15) / 16;
   g.ncol = p.kb <= 2 ? 128 : 64;
+  // query boxes: all columns a tile of this call can have, so that a tile takes few copies
   p.qbox = G > 16 ? G : 16;
+  while (p.qbox < g.ncol && p.qbox < n_rows * G) p.qbox *= 2;
+  p.nbox = 32;
+  while (p.nbox < g.ncol && p.nbox < (n_groups > 0 && n_rows > n_groups ? n_rows * g.H : g.H)) p.nbox *= 2;
   p.a_bytes = static_cast<uint32_t>(p.kb) * 16384u;
   p.q_bytes = static_cast<uint32_t>(p.kb) * 2u * g.ncol * 128u;
   const uint32_t staging = 4u * 32u * (g.ncol + 4) * 4u;
-  const uint32_t budget = 218u * 1024u - staging;
+  const uint32_t budget = 214u * 1024u - staging;
   p.nq = budget >= 2u * p.q_bytes + 3u * p.a_bytes ? 2 : 1;
   p.k_stages = static_cast<int>((budget - p.nq * p.q_bytes) / p.a_bytes);
   if (p.k_stages > 8) p.k_stages = 8;
@@ -1611,9 +1615,14 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
     if (ring < static_cast<size_t>(p.f_npad) * 512) ring = static_cast<size_t>(p.f_npad) * 512;
     p.f_smem = 1024 + ring + (3 * p.f_stages + 2) * sizeof(uint64_t);
   }
+  // split R over clusters while the grid stays within one wave (two CTAs per SM where they fit)
+  const int f_per_sm = p.f_smem + 12 * 1024 <= 113u * 1024u ? 2 : 1;
   p.f_ks = 1;
-  while (p.f_ks < 8 && static_cast<int64_t>(g.Hkv) * p.f_mt * p.f_tiles * p.f_ks * 2 <= sms && g.R / 64 >= p.f_ks * 2)
+  while (p.f_ks < 8 && static_cast<int64_t>(g.Hkv) * p.f_mt * p.f_tiles * p.f_ks * 2 <= f_per_sm * sms &&
+         g.R / 64 >= p.f_ks * 2)
     p.f_ks *= 2;
+  // few columns: groups of converter warps take the stages in turn
+  p.f_log2cg = p.f_npad <= 16 ? 1 : 0;
   p.f_kpc = (g.R + p.f_ks * 64 - 1) / (p.f_ks * 64) * 64;
   p.f_tmem = static_cast<uint32_t>(pow2_ceil(p.f_npad < 32 ? 32 : p.f_npad));
 
@@ -1694,16 +1703,18 @@ starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_g
   const uint64_t rh = static_cast<uint64_t>(n_rows) * g.H;
   const uint32_t tok_box = 128 / g.Hkv < 16 ? 128u / g.Hkv : 16u;
 
-  CUtensorMap km[2], qm[4], vmap, pmap[2], bvmap;
+  CUtensorMap km[2], qm[4], vmap, pmap[4], bvmap;
   if (!encode_kpool_map(&km[0], k_cache, g.r, g.Hkv, g.NB, 1, 16) ||
       !encode_kpool_map(&km[1], k_cache, g.r, g.Hkv, g.NB, static_cast<uint32_t>(g.Hkv), tok_box) ||
       !encode_rows_map(&qm[0], ws + pl.qh_off, g.r, g.H, n_rows, G, static_cast<uint32_t>(pl.qbox) / G) ||
       !encode_rows_map(&qm[1], ws + pl.ql_off, g.r, g.H, n_rows, G, static_cast<uint32_t>(pl.qbox) / G) ||
-      !encode_2d_map(&qm[2], ws + pl.qh_off, g.r, rh, 64, kGKQBox) ||
-      !encode_2d_map(&qm[3], ws + pl.ql_off, g.r, rh, 64, kGKQBox) ||
+      !encode_2d_map(&qm[2], ws + pl.qh_off, g.r, rh, 64, static_cast<uint32_t>(pl.nbox)) ||
+      !encode_2d_map(&qm[3], ws + pl.ql_off, g.r, rh, 64, static_cast<uint32_t>(pl.nbox)) ||
       !encode_vpool_map(&vmap, v_cache, g.R, g.NB, 4) ||
-      !encode_2d_map(&pmap[0], ws + pl.p_off[0], g.t_pad[0], rh, 64, kGVPBox) ||
-      !encode_2d_map(&pmap[1], ws + pl.p_off[second], g.t_pad[second], rh, 64, kGVPBox) ||
+      !encode_2d_map(&pmap[0], ws + pl.p_off[0], g.t_pad[0], rh, 64, 32) ||
+      !encode_2d_map(&pmap[1], ws + pl.p_off[second], g.t_pad[second], rh, 64, 32) ||
+      !encode_2d_map(&pmap[2], ws + pl.p_off[0], g.t_pad[0], rh, 64, 128) ||
+      !encode_2d_map(&pmap[3], ws + pl.p_off[second], g.t_pad[second], rh, 64, 128) ||
       !encode_2d_map(&bvmap, B_V, static_cast<uint64_t>(g.Hkv) * g.d, g.R, 64, 64))
     return STARKV_ERR_CUDA;
 
@@ -1728,7 +1739,7 @@ starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_g
   kp.g = g;
   kp.tables = block_tables;
   for (int i = 0; i < 2; ++i) kp.P[i] = f16(pl.p_off[src[i]]);
-  kp.kb = pl.kb; kp.ksteps = pl.ksteps; kp.qbox = pl.qbox; kp.log2Hkv = pl.log2Hkv; kp.nq = pl.nq; kp.stages = pl.k_stages;
+  kp.kb = pl.kb; kp.ksteps = pl.ksteps; kp.qbox = pl.qbox; kp.nbox = pl.nbox; kp.log2Hkv = pl.log2Hkv; kp.nq = pl.nq; kp.stages = pl.k_stages;
   kp.a_bytes = pl.a_bytes; kp.q_bytes = pl.q_bytes; kp.tmem_cols = pl.k_tmem;
   if (launch_group_kpass<false>(pl, km, qm, kp, s) != cudaSuccess || launch_group_kpass<true>(pl, km, qm, kp, s) != cudaSuccess)
     return STARKV_ERR_CUDA;
@@ -1741,8 +1752,8 @@ starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_g
   vp.stages = pl.v_stages;
   vp.stage_bytes = kGVABytes + kGVBBytes;
   if (!set_smem(group_vpass_kernel, pl.v_smem)) return STARKV_ERR_CUDA;
-  if (launch(group_vpass_kernel, dim3(pl.v_ctas), dim3(kGVThreads), pl.v_smem, s, 1, vmap, pmap[0], pmap[1], vp) !=
-      cudaSuccess)
+  if (launch(group_vpass_kernel, dim3(pl.v_ctas), dim3(kGVThreads), pl.v_smem, s, 1, vmap, pmap[0], pmap[1], pmap[2],
+             pmap[3], vp) != cudaSuccess)
     return STARKV_ERR_CUDA;
 
   GroupFinishParams fp{};
@@ -1751,7 +1762,7 @@ starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_g
   fp.Z[0] = vp.Z[0]; fp.Z[1] = vp.Z[1];
   fp.zcarry = vp.zcarry;
   fp.n_mt = pl.f_mt; fp.rows_tile = pl.f_rows; fp.npad = pl.f_npad; fp.k_per_cta = pl.f_kpc;
-  fp.stages = pl.f_stages; fp.stage_bytes = pl.f_stage_bytes; fp.tmem_cols = pl.f_tmem;
+  fp.stages = pl.f_stages; fp.log2cg = pl.f_log2cg; fp.stage_bytes = pl.f_stage_bytes; fp.tmem_cols = pl.f_tmem;
   if (!set_smem(group_finish_kernel, pl.f_smem)) return STARKV_ERR_CUDA;
   if (launch(group_finish_kernel, dim3(g.Hkv * pl.f_mt * pl.f_tiles, pl.f_ks), dim3(kGFThreads), pl.f_smem, s, pl.f_ks, bvmap,
              fp) != cudaSuccess)
