@@ -45,7 +45,8 @@ struct alignas(16) GroupEntry {
   int32_t k_nt, k_per; // wide: row tiles, rows per tile
   int32_t v_units;     // 64-token units per V tile
   int32_t v_width;     // columns per V tile
-  int32_t pad[3];
+  int32_t a_nt, a_per; // attend: row tiles, rows per tile
+  int32_t a_tile0;     // attend tiles before it
 };
 static_assert(sizeof(GroupEntry) == 64, "loaded as four 16-byte words");
 
@@ -62,6 +63,9 @@ struct GroupGeom {
   GroupEntry* ent;             // [E]
   int32_t* kpre;               // [E + 1] K items before each entry
   int32_t* vpre;               // [E + 1] V units before each entry
+  int32_t* apre;               // [E + 1] attend blocks before each entry
+  int a_rows;                  // attend: rows per tile at most (0: the call does not use it)
+  int C, nch;                  // attend: CTAs per cluster, 64-code blocks of R per CTA
   int32_t* row_ent;            // [n_rows] the row's group, or -1
   int32_t* row_use;            // [n_rows] 1: the row attends over its group's pages
   int32_t* n_used;             // rows that belong to groups (row_offsets[n_groups])
@@ -125,7 +129,7 @@ __device__ __forceinline__ int group_of_row(const GroupSetupParams& p, int b) {
 __device__ __forceinline__ void group_setup(const GroupSetupParams& p) {
   const GroupGeom& g = p.g;
   __shared__ int32_t bad;
-  __shared__ int32_t warp_sum[3][8];
+  __shared__ int32_t warp_sum[5][8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) bad = 0;
   __syncthreads();
@@ -133,15 +137,17 @@ __device__ __forceinline__ void group_setup(const GroupSetupParams& p) {
   // thread t makes the entries [t per, (t + 1) per)
   const int per = (g.E + 255) / 256;
   const int e0 = tid * per, e1 = min(g.E, e0 + per);
-  int32_t mine[3] = {0, 0, 0};   // K items, V units, V tiles
-  auto counts = [&](const GroupEntry& en, int32_t (&c)[3]) {
-    c[0] = c[1] = c[2] = 0;
+  int32_t mine[5] = {0, 0, 0, 0, 0};   // K items, V units, V tiles, attend blocks, attend tiles
+  auto counts = [&](const GroupEntry& en, int32_t (&c)[5]) {
+    c[0] = c[1] = c[2] = c[3] = c[4] = 0;
     if (en.nrows == 0 || en.len == 0) return;
     const int nt = gv_tiles(en.nrows * g.H) * g.n_rt;
     c[0] = gk_narrow(en.nrows, g) ? (en.len + g.chunk_n - 1) / g.chunk_n
                                   : gk_tiles(en.nrows, g) * g.Hkv * ((en.len + g.chunk_w - 1) / g.chunk_w);
     c[1] = nt * ((en.len + kGVTok - 1) / kGVTok);
     c[2] = nt;
+    c[3] = en.a_nt * en.v_units;
+    c[4] = en.a_nt;
   };
   for (int e = e0; e < e1; ++e) {
     GroupEntry en{};
@@ -186,11 +192,15 @@ __device__ __forceinline__ void group_setup(const GroupSetupParams& p) {
       en.k_per = (en.nrows + en.k_nt - 1) / en.k_nt;
       en.v_units = (en.len + kGVTok - 1) / kGVTok;
       en.v_width = gv_width(cols, gv_tiles(cols));
+      if (g.a_rows > 0) {
+        en.a_nt = (en.nrows + g.a_rows - 1) / g.a_rows;
+        en.a_per = (en.nrows + en.a_nt - 1) / en.a_nt;
+      }
     }
     g.ent[e] = en;
-    int32_t c[3];
+    int32_t c[5];
     counts(en, c);
-    for (int i = 0; i < 3; ++i) mine[i] += c[i];
+    for (int i = 0; i < 5; ++i) mine[i] += c[i];
   }
   if (!g.shared)
     for (int b = tid; b < g.n_rows; b += 256) {
@@ -199,33 +209,36 @@ __device__ __forceinline__ void group_setup(const GroupSetupParams& p) {
       g.row_use[b] = grp >= 0 ? 1 : 0;
     }
   // exclusive prefix sums
-  int32_t v[3] = {mine[0], mine[1], mine[2]};
+  int32_t v[5] = {mine[0], mine[1], mine[2], mine[3], mine[4]};
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 5; ++i) {
       const int32_t y = __shfl_up_sync(0xffffffffu, v[i], o);
       if (lane >= o) v[i] += y;
     }
   if (lane == 31)
-    for (int i = 0; i < 3; ++i) warp_sum[i][warp] = v[i];
+    for (int i = 0; i < 5; ++i) warp_sum[i][warp] = v[i];
   __syncthreads();
-  int32_t at[3];
-  for (int i = 0; i < 3; ++i) {
+  int32_t at[5];
+  for (int i = 0; i < 5; ++i) {
     at[i] = v[i] - mine[i];
     for (int w = 0; w < warp; ++w) at[i] += warp_sum[i][w];
   }
   for (int e = e0; e < e1; ++e) {
-    int32_t c[3];
+    int32_t c[5];
     counts(g.ent[e], c);
     g.kpre[e] = at[0];
     g.vpre[e] = at[1];
     g.ent[e].tile0 = at[2];
-    for (int i = 0; i < 3; ++i) at[i] += c[i];
+    g.apre[e] = at[3];
+    g.ent[e].a_tile0 = at[4];
+    for (int i = 0; i < 5; ++i) at[i] += c[i];
   }
   if (tid == 255) {
     g.kpre[g.E] = at[0];
     g.vpre[g.E] = at[1];
+    g.apre[g.E] = at[3];
     *g.status = bad;
   }
 }
@@ -1114,6 +1127,673 @@ group_vpass_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_consta
   }
 }
 
+// ================================================================== attend
+// The small calls' form of the K and V passes, one launch: latency instead of
+// throughput.  A tile is up to 64 (row, query head) columns of an entry, all
+// heads of its rows; a segment is a run of 64-token blocks of a tile.  One
+// cluster of C CTAs works on a segment: CTA c accumulates Z for its own 64 nch
+// codes of R in tensor memory, and the 16-token parts of the blocks go round the
+// CTAs: a part's logits, maxima and weights are formed by one CTA and sent to
+// the others through distributed shared memory.  So no logit or weight leaves
+// the SMs and nothing waits for a grid.
+//   S      = c_K . (q~ hi + q~ lo) for 128 code rows in page order at a time (see
+//            gk_narrow); each row keeps its own head's columns
+//   m      = max of the first block's logits, per column; raised, with Z and l
+//            rescaled, when a later block exceeds it by more than 15 (weights
+//            then stay below 2^15 and keep fp16's relative precision)
+//   w      = fp16(exp2(s - m)),  l = sum w,  Z += w . c_V
+// A segment leaves (m, l, Z); the finish joins a column's segments.
+// Warps: 0 loads q~ and K codes, 1 issues the S products, 2 loads V codes, 3
+// issues the Z products, 4..7 gather logits and store Z, 8..11 take maxima and form
+// weights (a thread per column, two teams on alternate parts), 12 tells the
+// other CTAs that a block of weights has been consumed here.
+struct GroupAttendParams {
+  GroupGeom g;
+  const int32_t* tables;
+  float* Z[2];               // by zsrc, [n_rows * H][R]
+  float* m[2];               // by zsrc, [n_rows * H]
+  float* l[2];               // by zsrc, [n_rows * H][C]
+  float* zcarry;             // [clusters][64][R]
+  float* mcarry;             // [clusters][64]
+  float* lcarry;             // [clusters][64][C]
+  int kb, ksteps;            // 64-code blocks and 16-code steps of r
+  int log2Hkv;
+  int utok, part;            // tokens per unit (128 code rows) and per part
+  int lstride, lslots;       // floats per token of a logit slot, logit slots
+  int k_stages, v_stages;
+  uint32_t v_stage_bytes;    // 2 pages x 16 tokens x 64 nch codes
+  uint32_t q_bytes;          // q~ tile: kb x (hi 64 columns, lo 64 columns) x 128 B
+};
+
+constexpr int kGAThreads = 416;
+constexpr int kGACols = 64;
+constexpr int kGATok = 64;         // tokens per block
+constexpr int kGAVTok = 32;        // tokens per V stage
+constexpr int kGAMaxC = 8;
+constexpr int kGAPSlots = 4;       // blocks of weights
+constexpr int kGAMSlots = 8;       // blocks of maxima: a CTA may be up to kGAPSlots + 2 blocks ahead of another
+constexpr int kGAAcc = 4;          // S accumulators
+constexpr float kGARaise = 15.f;
+
+struct ASeg {
+  GroupEntry en;
+  int tile, row0, nr, ncols;     // tile of all, first row, rows, columns
+  int b0, b1;                    // blocks
+  bool first, last;
+};
+
+struct AWalk {
+  const GroupGeom& g;
+  const GroupTables& tb;
+  int32_t x, end, ebeg, eend, e;
+  GroupEntry en;
+  __device__ AWalk(const GroupGeom& g_, const GroupTables& tb_, int32_t a, int32_t b)
+      : g(g_), tb(tb_), x(a), end(b), ebeg(0), eend(0), e(0) {
+    if (x < end) {
+      e = entry_of(tb, x);
+      ebeg = tb.pre[e];
+      eend = tb.pre[e + 1];
+      en = tb.ent[e];
+    }
+  }
+  __device__ bool next(ASeg* s) {
+    if (x >= end) return false;
+    while (x >= eend) { ++e; ebeg = eend; eend = tb.pre[e + 1]; if (x < eend) en = tb.ent[e]; }
+    int b = x - ebeg, t = 0;
+    if (en.a_nt > 1) {
+      t = static_cast<uint32_t>(b) / static_cast<uint32_t>(en.v_units);
+      b -= t * en.v_units;
+    }
+    s->en = en;
+    s->tile = en.a_tile0 + t;
+    s->row0 = en.row0 + t * en.a_per;
+    s->nr = min(en.a_per, en.row0 + en.nrows - s->row0);
+    s->ncols = s->nr * g.H;
+    s->b0 = b;
+    s->b1 = min(en.v_units, b + end - x);
+    s->first = b == 0;
+    s->last = s->b1 == en.v_units;
+    x += s->b1 - s->b0;
+    return true;
+  }
+};
+
+// Shared-memory layout (bytes from the 1024-aligned base).
+struct AttendSmem {
+  uint32_t v, q, k, p, ls, stage, mx, bars, total;
+};
+__host__ __device__ __forceinline__ AttendSmem attend_smem(uint32_t q_bytes, int k_stages, int v_stages,
+                                                           uint32_t v_stage_bytes, int lslots, uint32_t lslot_bytes) {
+  AttendSmem s;
+  s.v = 0;
+  s.q = s.v + ((v_stages * v_stage_bytes + 1023u) & ~1023u);
+  s.k = s.q + q_bytes;
+  s.p = s.k + static_cast<uint32_t>(k_stages) * 16384u;
+  s.ls = s.p + kGAPSlots * kGACols * 128u;
+  s.stage = s.ls + lslots * lslot_bytes;
+  s.mx = s.stage + 128u * 36u * 4u;                               // a gathering lane's 32 columns (+ 4)
+  s.bars = s.mx + kGAMSlots * 4u * kGACols * 4u;                  // maxima: [slot][part of the block][column]
+  s.total = s.bars + 8u * static_cast<uint32_t>(2 * k_stages + 3 * v_stages + 2 * lslots + 3 * kGAPSlots + kGAMSlots + 2 * kGAAcc + 16);
+  return s;
+}
+
+__global__ void __launch_bounds__(kGAThreads, 1)
+group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                    const __grid_constant__ CUtensorMap qhmap, const __grid_constant__ CUtensorMap qlmap,
+                    GroupAttendParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = align_smem_1024(smem_raw);
+  const GroupGeom& g = p.g;
+  const int KS = p.k_stages, VS = p.v_stages, LS = p.lslots, C = g.C;
+  const uint32_t lslot = static_cast<uint32_t>(p.part * p.lstride);      // floats
+  const AttendSmem lay = attend_smem(p.q_bytes, KS, VS, p.v_stage_bytes, LS, lslot * 4u);
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + lay.bars);
+  uint64_t* kempty = kfull + KS;
+  uint64_t* vfull = kempty + KS;
+  uint64_t* vempty = vfull + VS;
+  uint64_t* vfix = vempty + VS;            // [VS] the stage's partly filled page is zero behind its end
+  uint64_t* lfull = vfix + VS;             // [LS] a part's logits gathered
+  uint64_t* lempty = lfull + LS;           // [LS] read
+  uint64_t* pfull = lempty + LS;           // [P slots] weights of a block complete, from all CTAs
+  uint64_t* pdone = pfull + kGAPSlots;     // [P slots] consumed by this CTA's products
+  uint64_t* pempty = pdone + kGAPSlots;    // [P slots] consumed by all CTAs
+  uint64_t* mfull = pempty + kGAPSlots;    // [M slots] maxima of a block, from all CTAs
+  uint64_t* tfull = mfull + kGAMSlots;     // [acc] logits ready
+  uint64_t* tempty = tfull + kGAAcc;       // [acc] logits read
+  uint64_t* qfull = tempty + kGAAcc;
+  uint64_t* qempty = qfull + 1;
+  uint64_t* zdone = qempty + 1;
+  uint64_t* zfree = zdone + 1;
+  uint64_t* sdone = zfree + 1;
+  uint64_t* mdone = sdone + 1;
+  uint64_t* bbar = mdone + 1;              // warps 8..11
+  float* s_ls = reinterpret_cast<float*>(smem + lay.ls);
+  float* s_mx = reinterpret_cast<float*>(smem + lay.mx);
+  __shared__ uint32_t taddr_s;
+  __shared__ volatile int32_t abort_flag;
+  __shared__ GroupTablesSmem s_tab;
+  __shared__ float s_f[kGACols];           // rescaling factors; sums of one team
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int c = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int ppb = kGATok / p.part;         // parts per block
+  if (tid == 0) {
+    for (int s = 0; s < KS; ++s) { mbar_init(&kfull[s], 1); mbar_init(&kempty[s], 1); }
+    for (int s = 0; s < VS; ++s) { mbar_init(&vfull[s], 1); mbar_init(&vempty[s], 1); mbar_init(&vfix[s], 1); }
+    for (int s = 0; s < LS; ++s) { mbar_init(&lfull[s], 4); mbar_init(&lempty[s], 2); }
+    for (int s = 0; s < kGAPSlots; ++s) {
+      mbar_init(&pfull[s], 2 * ppb + 1);   // two warps per part, and this CTA's own go-ahead
+      mbar_init(&pdone[s], 1);
+      mbar_init(&pempty[s], C);
+    }
+    for (int s = 0; s < kGAMSlots; ++s) mbar_init(&mfull[s], 2 * ppb);
+    for (int s = 0; s < kGAAcc; ++s) { mbar_init(&tfull[s], 1); mbar_init(&tempty[s], 4); }
+    mbar_init(qfull, 1);
+    mbar_init(qempty, 1);
+    mbar_init(zdone, 1);
+    mbar_init(zfree, 4);
+    mbar_init(sdone, 1);
+    mbar_init(mdone, 1);
+    mbar_init(bbar, 128);
+    abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
+    prefetch_tensormap(&qhmap);
+    prefetch_tensormap(&qlmap);
+  }
+  if (warp == 1) {
+    tmem_alloc(&taddr_s, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  if (C > 1) cluster_sync();     // every CTA's barriers exist before anyone signals them
+  griddep_wait();
+  griddep_launch_dependents();
+  const GroupTables tab = load_tables(g, g.apre, &s_tab);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t taddr = taddr_s;
+  const uint32_t tS = taddr + 128u;        // S accumulators: 64 columns each, behind Z's two 128-row tiles
+  const int cl = blockIdx.x;               // clusters lie along y
+  // every cluster below `live` has a block: the carries between first and last are all written
+  const int64_t total = tab.pre[g.E], live = total < gridDim.x ? total : gridDim.x;
+  const int32_t x0 = cl < live ? static_cast<int32_t>(cl * total / live) : 0;
+  const int32_t x1 = cl < live ? static_cast<int32_t>((cl + 1) * total / live) : 0;
+
+  if (warp == 0) {
+    // ------------------------------------------------------- q~ and K codes
+    const uint64_t keep = policy_evict_last();
+    RingPos k;
+    uint32_t issued = 0, seg = 0;
+    bool ok = true;
+    AWalk walk(g, tab, x0, x1);
+    ASeg x;
+    const int tb = min(kBlock, p.utok), boxes = p.utok / tb;
+    const uint32_t box = static_cast<uint32_t>(tb * g.Hkv) * 128u;
+    while (ok && walk.next(&x)) {
+      const int tbeg = x.b0 * kGATok, tend = min(x.en.len, x.b1 * kGATok);
+      PageReader pages(p.tables + static_cast<size_t>(x.en.tab) * g.MB + x.en.page0 + tbeg / kBlock,
+                       (tend - tbeg + kBlock - 1) / kBlock, g.NB, g.status, lane);
+      if (lane == 0) {
+        if (seg > 0 && !mbar_wait(qempty, (seg - 1) & 1)) {
+          ok = false;
+        } else {
+          mbar_arrive_expect_tx(qfull, p.q_bytes);
+          for (int a = 0; a < p.kb; ++a) {
+            uint8_t* d = smem + lay.q + static_cast<uint32_t>(a) * kGACols * 128u;
+            tma_load_2d(d, &qhmap, a * 64, x.row0 * g.H, qfull, keep);
+            tma_load_2d(d + p.q_bytes / 2, &qlmap, a * 64, x.row0 * g.H, qfull, keep);
+          }
+        }
+      }
+      ++seg;
+      const int plast = (tend + p.part - 1) / p.part;
+      for (int gp = x.b0 * ppb; gp < plast; ++gp) {
+        if (gp % C != c) continue;
+        for (int t = gp * p.part; t < gp * p.part + p.part; t += p.utok) {
+          const int nb = t + p.utok <= tend ? boxes : max(0, ((tend + kBlock - 1) / kBlock * kBlock - t + tb - 1) / tb);
+          for (int a = 0; a < p.kb; ++a) {
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            uint8_t* st = smem + lay.k + k.s * 16384u;
+            if (lane == 0) {
+              if (k.u > 0 && !mbar_wait(&kempty[k.s], (k.u - 1) & 1)) ok = false;
+              else mbar_arrive_expect_tx(&kfull[k.s], static_cast<uint32_t>(min(nb, boxes)) * box);
+            }
+            for (int b = 0; b < min(nb, boxes); ++b) {
+              const int tk = t + b * tb;
+              const int row = pages.page((tk - tbeg) >> 4) * kBlock + (tk & (kBlock - 1));
+              if (lane == 0 && ok) tma_load_3d(st + b * box, &kmap, a * 64, 0, row, &kfull[k.s], keep);
+            }
+            if (ok) { ++issued; k.next(KS); }
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (lane == 0) {
+      if (!ok) {
+        set_timeout(g.status, kSiteKEmpty);
+        abort_flag = 1;
+      }
+      for (uint32_t n = 0; n < issued && n < static_cast<uint32_t>(KS); ++n) {
+        if (--k.s < 0) { k.s = KS - 1; --k.u; }
+        mbar_wait(&kfull[k.s], k.u & 1);
+      }
+      if (seg > 0) mbar_wait(qfull, (seg - 1) & 1);
+    }
+  } else if (warp == 1) {
+    // ----------------------------------------------------------- S products
+    if (lane == 0) {
+      RingPos k, acc;
+      uint32_t seg = 0;
+      bool ok = true;
+      const uint64_t ad0 = smem_desc(smem_u32(smem + lay.k), 16u, 1024u, kSwizzle128B);
+      const uint64_t bd0 = smem_desc(smem_u32(smem + lay.q), 16u, 1024u, kSwizzle128B);
+      const uint32_t half16 = p.q_bytes >> 5;
+      AWalk walk(g, tab, x0, x1);
+      ASeg x;
+      while (ok && walk.next(&x)) {
+        const uint32_t idesc = idesc_f16_f32(128, (x.ncols + 15) & ~15, /*a_mn_major=*/false, /*b_mn_major=*/false);
+        const int tend = min(x.en.len, x.b1 * kGATok), plast = (tend + p.part - 1) / p.part;
+        if (!mbar_wait(qfull, seg & 1)) { ok = false; break; }
+        ++seg;
+        for (int gp = x.b0 * ppb; gp < plast && ok; ++gp) {
+          if (gp % C != c) continue;
+          for (int t = 0; t < p.part && ok; t += p.utok) {
+            if (acc.u > 0 && !mbar_wait(&tempty[acc.s], (acc.u - 1) & 1)) { ok = false; break; }
+            const uint32_t dst = tS + static_cast<uint32_t>(acc.s) * kGACols;
+            uint32_t on = 0;
+            int left = p.ksteps;
+            uint64_t b = bd0;
+            for (int a = 0; a < p.kb; ++a, left -= 4, b += kGACols * 8u) {
+              if (!mbar_wait(&kfull[k.s], k.u & 1) || abort_flag) { ok = false; break; }
+              tc_fence_after();
+              const uint64_t ad = ad0 + static_cast<uint32_t>(k.s) * 1024u;
+#pragma unroll
+              for (uint32_t kk = 0; kk < 4; ++kk)
+                if (static_cast<int>(kk) < left) {
+                  umma_f16_ss(dst, ad + kk * 2u, b + kk * 2u, idesc, on);
+                  umma_f16_ss(dst, ad + kk * 2u, b + kk * 2u + half16, idesc, 1u);
+                  on = 1;
+                }
+              umma_commit(&kempty[k.s]);
+              k.next(KS);
+            }
+            if (!ok) break;
+            umma_commit(&tfull[acc.s]);
+            acc.next(kGAAcc);
+          }
+        }
+        umma_commit(qempty);
+      }
+      if (!ok) { set_timeout(g.status, kSiteKFull); abort_flag = 1; }
+      umma_commit(sdone);
+      if (!mbar_wait(sdone, 0)) set_timeout(g.status, kSiteVMdone);
+    }
+  } else if (warp == 2) {
+    // -------------------------------------------------------------- V codes
+    // A page that the entry's end leaves partly filled is zeroed behind it, so that
+    // whatever its unused slots hold contributes exactly 0.
+    const uint64_t pol_once = policy_evict_first(), pol_keep = policy_evict_last();
+    RingPos k;
+    uint32_t issued = 0;
+    bool ok = true;
+    AWalk walk(g, tab, x0, x1);
+    ASeg x;
+    const int chunk0 = c * g.nch;
+    while (ok && walk.next(&x)) {
+      const int tbeg = x.b0 * kGATok, tend = min(x.en.len, x.b1 * kGATok);
+      PageReader pages(p.tables + static_cast<size_t>(x.en.tab) * g.MB + x.en.page0 + tbeg / kBlock,
+                       (tend - tbeg + kBlock - 1) / kBlock, g.NB, g.status, lane);
+      const uint64_t pol = x.en.a_nt > 1 ? pol_keep : pol_once;
+      int pi = 0;
+      for (int t0 = tbeg; t0 < tend; t0 += kGAVTok, pi += 2) {
+        const int nt = min(kGAVTok, tend - t0), np = (nt + kBlock - 1) / kBlock;
+        const int32_t p0 = pages.page(pi), p1 = pages.page(pi + 1);
+        uint8_t* st = smem + lay.v + static_cast<size_t>(k.s) * p.v_stage_bytes;
+        if (lane == 0) {
+          if (k.u > 0 && !mbar_wait(&vempty[k.s], (k.u - 1) & 1)) {
+            ok = false;
+          } else {
+            mbar_arrive_expect_tx(&vfull[k.s], static_cast<uint32_t>(np * g.nch) * 2048u);
+            tma_load_3d(st, &vmap, 0, p0 * kBlock, chunk0, &vfull[k.s], pol);
+            if (np > 1) tma_load_3d(st + g.nch * 2048, &vmap, 0, p1 * kBlock, chunk0, &vfull[k.s], pol);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        const int ntl = nt & (kBlock - 1);
+        if (ntl) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&vfull[k.s], k.u & 1))) { ok = false; break; }
+          uint8_t* pg = st + (np - 1) * g.nch * 2048;
+          const int nz = kBlock - ntl;
+          for (int y = lane; y < g.nch * nz * 8; y += 32) {
+            const int ch = y / (nz * 8), rem = y % (nz * 8);
+            *reinterpret_cast<uint4*>(pg + ch * 2048 + (ntl + rem / 8) * 128 + (rem % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(&vfix[k.s]);
+        ++issued;
+        k.next(VS);
+      }
+    }
+    if (lane == 0) {
+      if (!ok) {
+        set_timeout(g.status, kSiteVEmpty);
+        abort_flag = 1;
+      }
+      for (uint32_t n = 0; n < issued && n < static_cast<uint32_t>(VS); ++n) {
+        if (--k.s < 0) { k.s = VS - 1; --k.u; }
+        mbar_wait(&vfull[k.s], k.u & 1);
+      }
+    }
+  } else if (warp == 3) {
+    // ----------------------------------------------------------- Z products
+    if (lane == 0) {
+      RingPos k, pb;
+      uint32_t seg = 0;
+      bool ok = true;
+      const uint64_t ad0 = smem_desc(smem_u32(smem + lay.v), 2048u, 1024u, kSwizzle128B);
+      const uint64_t bd0 = smem_desc(smem_u32(smem + lay.p), 16u, 1024u, kSwizzle128B);
+      const int codes = min(g.R - c * g.nch * 64, g.nch * 64);      // codes of R of this CTA
+      AWalk walk(g, tab, x0, x1);
+      ASeg x;
+      while (ok && walk.next(&x)) {
+        const uint32_t idesc = idesc_f16_f32(128, (x.ncols + 15) & ~15, /*a_mn_major=*/true, /*b_mn_major=*/false);
+        if (seg > 0 && !mbar_wait(zfree, (seg - 1) & 1)) { ok = false; break; }
+        ++seg;
+        uint32_t on = 0;
+        for (int b = x.b0; b < x.b1 && ok; ++b) {
+          const int nt = min(kGATok, x.en.len - b * kGATok);
+          if (!mbar_wait_cluster(&pfull[pb.s], pb.u & 1) || abort_flag) { ok = false; break; }
+          fence_proxy_async_all();
+          const uint64_t bp = bd0 + static_cast<uint32_t>(pb.s) * (kGACols * 8u);
+          for (int t = 0; t < nt; t += kGAVTok) {
+            if (!mbar_wait(&vfull[k.s], k.u & 1) || !mbar_wait(&vfix[k.s], k.u & 1) || abort_flag) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t av = ad0 + ((static_cast<uint32_t>(k.s) * p.v_stage_bytes) >> 4);
+#pragma unroll
+            for (int pg = 0; pg < 2; ++pg)
+              if (t + pg * kBlock < nt) {
+                const uint64_t a = av + static_cast<uint32_t>(pg * g.nch) * 128u, bb = bp + (t >> 3) + pg * 2;
+                umma_f16_ss(taddr, a, bb, idesc, on);
+                if (codes > 128) umma_f16_ss(taddr + 64u, a + 256u, bb, idesc, on);
+                on = 1;
+              }
+            umma_commit(&vempty[k.s]);
+            k.next(VS);
+          }
+          if (!ok) break;
+          umma_commit(&pdone[pb.s]);
+          pb.next(kGAPSlots);
+        }
+        if (ok) umma_commit(zdone);
+      }
+      if (!ok) { set_timeout(g.status, kSiteVFull); abort_flag = 1; }
+      umma_commit(mdone);
+      if (!mbar_wait(mdone, 0)) set_timeout(g.status, kSiteVMdone);
+    }
+  } else if (warp == 12) {
+    // ------------------------------------- consumed weight blocks, to all CTAs
+    RingPos pb;
+    bool ok = true;
+    AWalk walk(g, tab, x0, x1);
+    ASeg x;
+    while (ok && walk.next(&x))
+      for (int b = x.b0; b < x.b1; ++b, pb.next(kGAPSlots)) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&pdone[pb.s], pb.u & 1) && !abort_flag)) { ok = false; break; }
+        if (lane < C) mbar_arrive_cluster(&pempty[pb.s], static_cast<uint32_t>(lane));
+        __syncwarp();
+      }
+    if (!ok && lane == 0) { set_timeout(g.status, kSiteVTfree); abort_flag = 1; }
+  } else if (warp < 8) {
+    // ------------------------------------------------ gather logits, store Z
+    const int q = warp & 3;
+    const uint32_t lq = static_cast<uint32_t>(q * 32) << 16;
+    const int rho = q * 32 + lane, j = rho & (g.Hkv - 1), tl = rho >> p.log2Hkv, G = 1 << g.log2G;
+    const int log2H = p.log2Hkv + g.log2G;
+    float* st = reinterpret_cast<float*>(smem + lay.stage) + rho * 36;
+    const uint64_t keep = policy_evict_last();
+    RingPos acc, ls;
+    uint32_t seg = 0;
+    bool ok = true;
+    AWalk walk(g, tab, x0, x1);
+    ASeg x;
+    const int code0 = c * g.nch * 64, codes = min(g.R - code0, g.nch * 64);
+    while (ok && walk.next(&x)) {
+      const int tend = min(x.en.len, x.b1 * kGATok), plast = (tend + p.part - 1) / p.part;
+      for (int gp = x.b0 * ppb; gp < plast && ok; ++gp) {
+        if (gp % C != c) continue;
+        if (!__all_sync(0xffffffffu, ls.u == 0 || mbar_wait(&lempty[ls.s], (ls.u - 1) & 1))) { ok = false; break; }
+        float* out = s_ls + static_cast<uint32_t>(ls.s) * lslot;
+        for (int t = 0; t < p.part; t += p.utok) {
+          const bool ready = mbar_wait(&tfull[acc.s], acc.u & 1);
+          if (!__all_sync(0xffffffffu, ready && !abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          for (int c0 = 0; c0 < x.ncols; c0 += 32) {
+            __syncwarp();
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(tS + lq + static_cast<uint32_t>(acc.s) * kGACols + c0, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              *reinterpret_cast<uint4*>(st + 4 * u) = make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+            // the row's own head's columns among these 32
+            if (tl < p.utok)
+              for (int i = c0 >> log2H; (i << log2H) < min(x.ncols, c0 + 32); ++i)
+                for (int gg = 0; gg < G; ++gg) {
+                  const int col = (i << log2H) + (j << g.log2G) + gg, o = col - c0;
+                  if (o >= 0 && o < 32) out[(t + tl) * p.lstride + col] = st[o];
+                }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[acc.s]);
+          acc.next(kGAAcc);
+        }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&lfull[ls.s]);
+        ls.next(LS);
+      }
+      if (!ok) break;
+      const bool done = mbar_wait(zdone, seg & 1);
+      if (!__all_sync(0xffffffffu, done && !abort_flag)) { ok = false; break; }
+      ++seg;
+      tc_fence_after();
+      if (tid == 128 && c == 0) {
+        if (x.first) g.tfirst[x.tile] = cl;
+        if (x.last) g.tlast[x.tile] = cl;
+      }
+      float* dst = (x.first ? p.Z[x.en.zsrc] + static_cast<size_t>(x.row0) * g.H * g.R
+                            : p.zcarry + static_cast<size_t>(cl) * kGACols * g.R) + code0;
+      for (int m = 0; m < 2; ++m) {
+        const int j0 = m * 128 + q * 32;
+        if (j0 >= codes) break;              // warp-uniform (codes is a multiple of 64)
+        float* zq = dst + j0 + lane;         // a warp stores 128 contiguous bytes of a column per instruction
+        for (int h0 = 0; h0 < x.ncols; h0 += 16) {
+          __syncwarp();
+          uint32_t v[32];
+          tmem_ld_32x32b_x16(taddr + lq + m * 64u + h0, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int u = 0; u < 16; ++u)
+            if (h0 + u < x.ncols) st_global_hint_free(zq + static_cast<size_t>(h0 + u) * g.R, __uint_as_float(v[u]), keep);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(zfree);
+    }
+    if (!ok) { set_timeout(g.status, kSiteKFull); abort_flag = 1; }
+  } else {
+    // ----------------------------------------------- maxima and weights
+    const int et = tid - 256, team = et >> 6, col = et & 63, oth = col ^ 32;
+    const int q = warp & 3;
+    RingPos pb, mb, ms, lr, lw;      // blocks of weights; of maxima read, sent; logit slots read for maxima, for weights
+    uint32_t phase = 0;
+    bool ok = true;
+    AWalk walk(g, tab, x0, x1);
+    ASeg x;
+    // own part number n (counted over the whole walk) is team n & 1's
+    uint32_t nr = 0, nw = 0;
+    while (ok && walk.next(&x)) {
+      const int len = x.en.len;
+      float ref = 0.f, ref_o = 0.f, l = 0.f;
+      // the maxima of the CTA's own parts of block b, to every CTA
+      auto send = [&](int b) {
+        for (int pi = 0; pi < ppb; ++pi) {
+          const int gp = b * ppb + pi;
+          if (gp % C != c) continue;
+          const int t0 = gp * p.part;
+          const bool live = t0 < len;
+          const bool mine = live ? static_cast<int>(nr & 1) == team : team == 0;
+          if (mine) {
+            float m = -INFINITY;
+            if (live) {
+              if (!__all_sync(0xffffffffu, mbar_wait(&lfull[lr.s], lr.u & 1) && !abort_flag)) return false;
+              const float* src = s_ls + static_cast<uint32_t>(lr.s) * lslot + col;
+              const int n = min(p.part, len - t0);
+              if (col < x.ncols) {
+                if (n == kBlock) {
+#pragma unroll
+                  for (int t = 0; t < kBlock; ++t) m = fmaxf(m, src[t * p.lstride]);
+                } else {
+                  for (int t = 0; t < n; ++t) m = fmaxf(m, src[t * p.lstride]);
+                }
+              }
+            }
+            float* at = s_mx + (ms.s * 4 + pi) * kGACols + col;
+            if (C == 1) *at = m;
+            else
+              for (int o = 0; o < C; ++o) st_cluster(map_cluster(at, static_cast<uint32_t>(o)), m);
+            __syncwarp();
+            if (lane < C) mbar_arrive_cluster(&mfull[ms.s], static_cast<uint32_t>(lane));
+          }
+          if (live) { ++nr; lr.next(LS); }
+        }
+        ms.next(kGAMSlots);
+        return true;
+      };
+      if (!send(x.b0)) { ok = false; break; }
+      for (int b = x.b0; b < x.b1; ++b) {
+        if (b + 1 < x.b1 && !send(b + 1)) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&mfull[mb.s], mb.u & 1) && !abort_flag)) { ok = false; break; }
+        float bm = -INFINITY, bo = -INFINITY;
+        for (int pi = 0; pi < ppb; ++pi) {
+          bm = fmaxf(bm, s_mx[(mb.s * 4 + pi) * kGACols + col]);
+          bo = fmaxf(bo, s_mx[(mb.s * 4 + pi) * kGACols + oth]);
+        }
+        mb.next(kGAMSlots);
+        // the slot's earlier weights have been consumed by every CTA
+        if (pb.u > 0 && !__all_sync(0xffffffffu, mbar_wait_cluster(&pempty[pb.s], (pb.u - 1) & 1) && !abort_flag)) { ok = false; break; }
+        if (b == x.b0) {
+          ref = bm;
+          ref_o = bo;
+        } else {
+          // every warp sees all 64 columns, so all warps of all CTAs decide alike
+          const bool up = bm > ref + kGARaise || (bm > -INFINITY && ref == -INFINITY);
+          const bool up_o = bo > ref_o + kGARaise || (bo > -INFINITY && ref_o == -INFINITY);
+          if (__any_sync(0xffffffffu, up || up_o)) {
+            const float f = up ? (ref > -INFINITY ? ex2_approx(ref - bm) : 1.f) : 1.f;
+            if (up) ref = bm;
+            if (up_o) ref_o = bo;
+            l *= f;
+            if (team == 0) s_f[col] = f;
+            // the products of the block before have completed; nothing follows until this CTA's go-ahead
+            const int ps = pb.s == 0 ? kGAPSlots - 1 : pb.s - 1;
+            const uint32_t pu = pb.s == 0 ? pb.u - 1 : pb.u;
+            if (!__all_sync(0xffffffffu, mbar_wait(&pdone[ps], pu & 1) && !abort_flag) || !group_sync(bbar, phase)) { ok = false; break; }
+            tc_fence_after();
+            for (int m = 0; m < 2; ++m)
+              for (int h0 = 0; h0 < kGACols; h0 += 16) {
+                __syncwarp();
+                const uint32_t at = taddr + (static_cast<uint32_t>(q * 32) << 16) + m * 64u + h0;
+                uint32_t v[32];
+                tmem_ld_32x32b_x16(at, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int u = 0; u < 16; ++u) v[u] = __float_as_uint(__uint_as_float(v[u]) * s_f[h0 + u]);
+                tmem_st_32x32b_x16(at, v);
+              }
+            tmem_st_wait();
+            tc_fence_before();
+            if (!group_sync(bbar, phase)) { ok = false; break; }
+          }
+        }
+        if (et == 0) mbar_arrive(&pfull[pb.s]);
+        uint8_t* pbase = smem + lay.p + static_cast<uint32_t>(pb.s) * (kGACols * 128u) + col * 128;
+        for (int pi = 0; pi < ppb; ++pi) {
+          const int gp = b * ppb + pi;
+          if (gp % C != c) continue;
+          const int t0 = gp * p.part;
+          const bool live = t0 < len;
+          const bool mine = live ? static_cast<int>(nw & 1) == team : team == 0;
+          if (mine) {
+            if (live) {
+              const float* src = s_ls + static_cast<uint32_t>(lw.s) * lslot + col;
+              const float base = ref > -INFINITY ? ref : 0.f;   // a column whose logits are all -inf so far
+              for (int t8 = 0; t8 < p.part; t8 += 8) {
+                // weights of eight tokens, rounded to fp16 for the products; the sum takes the rounded weights
+                uint4 w4;
+                uint32_t* w = reinterpret_cast<uint32_t*>(&w4);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  const int t = t8 + 2 * u;
+                  const float a = t0 + t < len ? ex2_approx(src[t * p.lstride] - base) : 0.f;
+                  const float b2 = t0 + t + 1 < len ? ex2_approx(src[(t + 1) * p.lstride] - base) : 0.f;
+                  const __half2 h = __floats2half2_rn(a, b2);
+                  const float2 hf = __half22float2(h);
+                  l += hf.x;
+                  l += hf.y;
+                  w[u] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                uint8_t* at = pbase + ((static_cast<uint32_t>((pi * p.part + t8) >> 3) ^ (static_cast<uint32_t>(col) & 7u)) << 4);
+                if (col < x.ncols) {
+                  if (C == 1) *reinterpret_cast<uint4*>(at) = w4;
+                  else
+                    for (int o = 0; o < C; ++o) st_cluster(map_cluster(at, static_cast<uint32_t>(o)), w4);
+                }
+              }
+            }
+            fence_proxy_async_all();
+            __syncwarp();
+            if (lane == 0 && live) mbar_arrive(&lempty[lw.s]);
+            if (lane < C) mbar_arrive_cluster(&pfull[pb.s], static_cast<uint32_t>(lane));
+          }
+          if (live) { ++nw; lw.next(LS); }
+        }
+        pb.next(kGAPSlots);
+      }
+      if (!ok) break;
+      // m and l of the segment: both teams' sums
+      if (team == 1) s_f[col] = l;
+      if (!group_sync(bbar, phase)) { ok = false; break; }
+      if (team == 0 && col < x.ncols) {
+        const float sum = l + s_f[col];
+        const size_t o = x.first ? static_cast<size_t>(x.row0) * g.H + col : static_cast<size_t>(cl) * kGACols + col;
+        (x.first ? p.l[x.en.zsrc] : p.lcarry)[o * C + c] = sum;
+        if (c == 0) (x.first ? p.m[x.en.zsrc] : p.mcarry)[o] = ref;
+      }
+      if (!group_sync(bbar, phase)) { ok = false; break; }
+    }
+    if (!ok) { set_timeout(g.status, kSiteVPready); abort_flag = 1; }
+  }
+  __syncthreads();
+  if (C > 1) {
+    cluster_sync();   // nobody leaves while others may still write to it or signal it
+    cluster_sync();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(taddr, 512);
+  }
+}
+
 // ================================================================== finish
 // out^T (128 rows of d x columns) = B_V^T . (Z / L)^T for the (row, query head)
 // columns of one KV head, with Z / L formed on the fly: eight converter warps add
@@ -1126,6 +1806,11 @@ struct GroupFinishParams {
   __half* out;           // [n_rows][H][d]
   const float* Z[2];
   const float* zcarry;
+  // sums of the attend kernel (null m[0]: of the V pass, all relative to one maximum):
+  const float* m[2];     // by zsrc, [n_rows * H] the first segment's maximum
+  const float* l[2];     // [n_rows * H][C] its sums of weights
+  const float* mcarry;   // [clusters][64]
+  const float* lcarry;   // [clusters][64][C]
   int n_mt;              // 128-row tiles of d
   int rows_tile;         // rows per column tile (rows_tile * G <= 256)
   int npad;              // UMMA N
@@ -1154,7 +1839,7 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
   uint64_t* cbar = done + 1;                        // the converters' sync
   float* part = reinterpret_cast<float*>(smem);     // [npad][128], reuses the ring
   __shared__ uint32_t taddr_s;
-  __shared__ float s_il[256];
+  __shared__ float s_il[256], s_M[256];
   __shared__ GroupTablesSmem s_tab;
   __shared__ int32_t s_i0[2][256], s_n[2][256], s_col[2][256];   // per source: first CTA, CTAs, column within the V tile
 
@@ -1229,8 +1914,49 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
       ent = s_tab.ent;
       if (!group_sync(cbar, phase)) ok = false;
     }
+    const bool attend = p.m[0] != nullptr;
+    if (attend) {
+      // M and 1 / L of every column over its segments: a warp per column, a lane per segment
+      for (int c = warp - 2; c < ncols; c += kGFConv / 32) {
+        const int row = row0 + (c >> g.log2G), h = (j << g.log2G) + (c & ((1 << g.log2G) - 1));
+        const int e = row < g.n_rows ? g.row_ent[row] : -1, use = row < g.n_rows ? g.row_use[row] : 0;
+        float M = -INFINITY, L = 0.f;
+        for (int pass = 0; pass < 2; ++pass) {
+          for (int sr = 0; sr < n_src; ++sr) {
+            if (e < 0 || (sr == 0 && !use)) continue;
+            const GroupEntry en = ent[sr ? g.n_groups + row : e];
+            if (en.len == 0) continue;
+            const int t = (row - en.row0) / en.a_per, place = (row - en.row0 - t * en.a_per) * g.H + h;
+            const int i0 = g.tfirst[en.a_tile0 + t], n = g.tlast[en.a_tile0 + t] - i0 + 1;
+            const size_t o = static_cast<size_t>(row) * g.H + h;
+            for (int i = lane; i < n; i += 32) {
+              const size_t oc = static_cast<size_t>(i0 + i) * kGACols + place;
+              const float m = i == 0 ? p.m[sr][o] : p.mcarry[oc];
+              if (pass == 0) {
+                M = fmaxf(M, m);
+              } else {
+                const float* lp = i == 0 ? p.l[sr] + o * g.C : p.lcarry + oc * g.C;
+                float l = 0.f;
+                for (int u = 0; u < g.C; ++u) l += lp[u];
+                // a segment whose logits are all NaN or -inf has m = -inf and l = NaN
+                L += m > -INFINITY ? l * ex2_approx(m - M) : l;
+              }
+            }
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            if (pass == 0) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            else L += __shfl_xor_sync(0xffffffffu, L, o);
+          }
+        }
+        if (lane == 0) {
+          s_il[c] = L == 0.f ? 0.f : 1.f / L;
+          s_M[c] = M;
+        }
+      }
+    }
     // 1 / L of every column: a warp sums a column's chunks
-    for (int c = warp - 2; c < ncols; c += kGFConv / 32) {
+    for (int c = attend ? ncols : warp - 2; c < ncols; c += kGFConv / 32) {
       const int row = row0 + (c >> g.log2G);
       const int e = row < g.n_rows ? g.row_ent[row] : -1, use = row < g.n_rows ? g.row_use[row] : 0;
       float L = 0.f;
@@ -1265,11 +1991,12 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
             if (sr < n_src && e >= 0 && (sr || use)) {
               const GroupEntry en = ent[sr ? g.n_groups + row : e];
               if (en.len > 0) {
-                const int col = (row - en.row0) * g.H + h, nt = col / en.v_width;
-                const int tile = en.tile0 + nt * g.n_rt + rt;
+                const int per = attend ? en.a_per * g.H : en.v_width;
+                const int col = (row - en.row0) * g.H + h, nt = col / per;
+                const int tile = attend ? en.a_tile0 + nt : en.tile0 + nt * g.n_rt + rt;
                 i0 = g.tfirst[tile];
                 n = g.tlast[tile] - i0 + 1;
-                place = col - nt * en.v_width;
+                place = col - nt * per;
               }
             }
             s_i0[sr][c] = i0;
@@ -1293,22 +2020,30 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
             const int n = s_n[sr][bl];
             if (n == 0) continue;
             const float* first = p.Z[sr] + (static_cast<size_t>(row) * g.H + h) * g.R + code;
-            const float* carry = p.zcarry + (static_cast<size_t>(s_i0[sr][bl]) * kGVTile + s_col[sr][bl]) * kGVTile +
-                                 (code - rt * kGVTile);
+            const size_t place = static_cast<size_t>(s_i0[sr][bl]) * (attend ? kGACols : kGVTile) + s_col[sr][bl];
+            const float* carry = attend ? p.zcarry + place * g.R + code : p.zcarry + place * kGVTile + (code - rt * kGVTile);
+            const size_t cstep = attend ? static_cast<size_t>(kGACols) * g.R : static_cast<size_t>(kGVTile) * kGVTile;
             for (int u0 = 0; u0 < n; u0 += 4) {
               float4 a[4], b[4];
+              float f[4];
 #pragma unroll
               for (int u = 0; u < 4; ++u)
                 if (u0 + u < n) {
-                  const float* src = u0 + u == 0 ? first : carry + static_cast<size_t>(u0 + u) * kGVTile * kGVTile;
+                  const float* src = u0 + u == 0 ? first : carry + static_cast<size_t>(u0 + u) * cstep;
                   a[u] = *reinterpret_cast<const float4*>(src);
                   b[u] = *reinterpret_cast<const float4*>(src + 4);
+                  f[u] = 1.f;
+                  if (attend) {
+                    const float m = u0 + u == 0 ? p.m[sr][static_cast<size_t>(row) * g.H + h]
+                                                : p.mcarry[place + static_cast<size_t>(u0 + u) * kGACols];
+                    f[u] = m > -INFINITY ? ex2_approx(m - s_M[bl]) : 1.f;
+                  }
                 }
 #pragma unroll
               for (int u = 0; u < 4; ++u)
                 if (u0 + u < n) {
-                  z[0] += a[u].x; z[1] += a[u].y; z[2] += a[u].z; z[3] += a[u].w;
-                  z[4] += b[u].x; z[5] += b[u].y; z[6] += b[u].z; z[7] += b[u].w;
+                  z[0] += a[u].x * f[u]; z[1] += a[u].y * f[u]; z[2] += a[u].z * f[u]; z[3] += a[u].w * f[u];
+                  z[4] += b[u].x * f[u]; z[5] += b[u].y * f[u]; z[6] += b[u].z * f[u]; z[7] += b[u].w * f[u];
                 }
             }
           }

@@ -58,6 +58,9 @@
 #ifndef STARKV_APP_KS_MAX
 #define STARKV_APP_KS_MAX 4     // largest cluster splitting the V-code GEMM's K range
 #endif
+#ifndef STARKV_ATTEND_BLOCKS
+#define STARKV_ATTEND_BLOCKS 24   // attend form of the group calls: at most so many blocks per cluster
+#endif
 #ifndef STARKV_V_RING_BYTES
 #define STARKV_V_RING_BYTES (105 * 1024)
 #endif
@@ -1516,12 +1519,47 @@ struct GroupPlan {
   int f_mt, f_rows, f_tiles, f_npad, f_ks, f_kpc, f_stages, f_log2cg;
   uint32_t f_stage_bytes, f_tmem;
   size_t f_smem;
+  // attend (g.a_rows > 0)
+  int at_utok, at_part, at_lstride, at_lslots, at_k_stages, at_v_stages, at_clusters;
+  uint32_t at_v_stage, at_q_bytes;
+  size_t at_smem;
   // absorption
   int abs_tile;
   // workspace
-  size_t ent_off, kpre_off, vpre_off, row_ent_off, row_use_off, used_off, tfirst_off, tlast_off, mrow_off, lpart_off[2],
+  size_t apre_off, m_off[2], l_off[2], mcarry_off, lcarry_off, ent_off, kpre_off, vpre_off, row_ent_off, row_use_off, used_off, tfirst_off, tlast_off, mrow_off, lpart_off[2],
       qh_off, ql_off, p_off[2], z_off[2], carry_off, total;
 };
+
+// Clusters of C CTAs of the attend kernel that the device holds at once.
+int max_attend_clusters(int C, size_t smem) {
+  static std::mutex mu;
+  static std::map<std::tuple<int, int, size_t>, int> known;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) { cudaGetLastError(); return device_sm_count() / C; }
+  std::lock_guard<std::mutex> lock(mu);
+  const auto key = std::make_tuple(dev, C, smem);
+  const auto it = known.find(key);
+  if (it != known.end()) return it->second;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(device_sm_count()), static_cast<unsigned>(C));
+  cfg.blockDim = dim3(kGAThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = static_cast<unsigned>(C);
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (!set_smem(group_attend_kernel, smem) ||
+      cudaOccupancyMaxActiveClusters(&n, group_attend_kernel, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return device_sm_count() / C;   // no device: the host-side sizes only
+  }
+  known[key] = n;
+  return n;
+}
 
 starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n_groups, int32_t n_rows,
                               int32_t max0, int32_t max1, GroupPlan* gp) {
@@ -1628,26 +1666,70 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
 
   p.abs_tile = g.H * ((n_rows + 15) / 16) <= 2 * sms ? 16 : kAbsBT;
 
+  // the attend form: one cluster covers R (<= 2048 codes), a row's head uses at
+  // most 16 columns of a tile, the query tile leaves room for the rings
+  if (g.R <= 2048 && G <= 16 && p.kb <= 2) {
+    g.C = (g.R + 255) / 256;
+    g.nch = (g.R / 64 + g.C - 1) / g.C;
+    int rows = kGACols / g.H;
+    if (rows > 16 / G) rows = 16 / G;
+    p.at_utok = 128 / g.Hkv < 64 ? 128 / g.Hkv : 64;
+    p.at_part = p.at_utok > 16 ? p.at_utok : 16;
+    const int ppb = kGATok / p.at_part, own = (ppb + g.C - 1) / g.C;
+    p.at_lslots = 2 * own > 4 ? 2 * own : 4;       // two blocks of a CTA's parts
+    p.at_lstride = rows * g.H + 4;
+    p.at_q_bytes = static_cast<uint32_t>(p.kb) * 2u * kGACols * 128u;
+    p.at_k_stages = 3;
+    p.at_v_stage = static_cast<uint32_t>(g.nch) * 4096u;
+    const uint32_t lslot = static_cast<uint32_t>(p.at_part * p.at_lstride) * 4u;
+    const size_t room = 217u * 1024u, rest = 2048 + attend_smem(p.at_q_bytes, p.at_k_stages, 0, p.at_v_stage, p.at_lslots, lslot).total;
+    p.at_v_stages = rest < room ? static_cast<int>((room - rest) / (p.at_v_stage + 24u)) : 0;
+    if (p.at_v_stages > 8) p.at_v_stages = 8;
+    p.at_smem = 1024 + attend_smem(p.at_q_bytes, p.at_k_stages, p.at_v_stages, p.at_v_stage, p.at_lslots, lslot).total;
+    const int64_t tiles = runs + (n_rows + rows - 1) / rows;
+    const int64_t blocks = tiles * ((max0 + kGATok - 1) / kGATok) +
+                           (shared ? static_cast<int64_t>(n_rows) * ((max1 + kGATok - 1) / kGATok) : 0);
+    const int most = p.at_v_stages >= 3 ? max_attend_clusters(g.C, p.at_smem) : 0;
+    if (p.at_v_stages >= 3 && blocks <= static_cast<int64_t>(STARKV_ATTEND_BLOCKS) * most) {
+      g.a_rows = rows;
+      p.at_clusters = blocks < 1 ? 1 : (blocks < most ? static_cast<int>(blocks) : most);
+    }
+  }
+
   const size_t N = static_cast<size_t>(n_rows), rh = N * g.H;
   size_t off = 256;   // the status word
   auto take = [&](size_t bytes) { const size_t o = off; off = align_up(off + bytes, 256); return o; };
   p.ent_off = take(static_cast<size_t>(g.E) * sizeof(GroupEntry));
   p.kpre_off = take((static_cast<size_t>(g.E) + 1) * 4);
   p.vpre_off = take((static_cast<size_t>(g.E) + 1) * 4);
+  p.apre_off = take((static_cast<size_t>(g.E) + 1) * 4);
   p.row_ent_off = take(N * 4);
   p.row_use_off = take(N * 4);
   p.used_off = take(4);
-  p.tfirst_off = take(static_cast<size_t>(v_tiles) * 4);
-  p.tlast_off = take(static_cast<size_t>(v_tiles) * 4);
+  const int64_t tiles = g.a_rows > 0 ? runs + n_rows / g.a_rows + 1 + (shared ? n_rows : 0) : v_tiles;
+  p.tfirst_off = take(static_cast<size_t>(tiles) * 4);
+  p.tlast_off = take(static_cast<size_t>(tiles) * 4);
   p.mrow_off = take(rh * 4);
   p.qh_off = take(rh * g.r * 2);
   p.ql_off = take(rh * g.r * 2);
   for (int s = 0; s < (shared ? 2 : 1); ++s) {
-    p.lpart_off[s] = take(rh * g.n_ch[s] * 4);
-    p.p_off[s] = take(rh * g.t_pad[s] * 2);
     p.z_off[s] = take(rh * g.R * 4);
+    if (g.a_rows > 0) {
+      p.m_off[s] = take(rh * 4);
+      p.l_off[s] = take(rh * g.C * 4);
+    } else {
+      p.lpart_off[s] = take(rh * g.n_ch[s] * 4);
+      p.p_off[s] = take(rh * g.t_pad[s] * 2);
+    }
   }
-  p.carry_off = take(static_cast<size_t>(p.v_ctas) * kGVTile * kGVTile * 4);
+  if (g.a_rows > 0) {
+    const size_t cols = static_cast<size_t>(p.at_clusters) * kGACols;
+    p.carry_off = take(cols * g.R * 4);
+    p.mcarry_off = take(cols * 4);
+    p.lcarry_off = take(cols * g.C * 4);
+  } else {
+    p.carry_off = take(static_cast<size_t>(p.v_ctas) * kGVTile * kGVTile * 4);
+  }
   p.total = off;
   return STARKV_OK;
 }
@@ -1690,6 +1772,7 @@ starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_g
   g.ent = reinterpret_cast<GroupEntry*>(ws + pl.ent_off);
   g.kpre = i32(pl.kpre_off);
   g.vpre = i32(pl.vpre_off);
+  g.apre = i32(pl.apre_off);
   g.row_ent = i32(pl.row_ent_off);
   g.row_use = i32(pl.row_use_off);
   g.n_used = i32(pl.used_off);
@@ -1703,20 +1786,8 @@ starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_g
   const uint64_t rh = static_cast<uint64_t>(n_rows) * g.H;
   const uint32_t tok_box = 128 / g.Hkv < 16 ? 128u / g.Hkv : 16u;
 
-  CUtensorMap km[2], qm[4], vmap, pmap[4], bvmap;
-  if (!encode_kpool_map(&km[0], k_cache, g.r, g.Hkv, g.NB, 1, 16) ||
-      !encode_kpool_map(&km[1], k_cache, g.r, g.Hkv, g.NB, static_cast<uint32_t>(g.Hkv), tok_box) ||
-      !encode_rows_map(&qm[0], ws + pl.qh_off, g.r, g.H, n_rows, G, static_cast<uint32_t>(pl.qbox) / G) ||
-      !encode_rows_map(&qm[1], ws + pl.ql_off, g.r, g.H, n_rows, G, static_cast<uint32_t>(pl.qbox) / G) ||
-      !encode_2d_map(&qm[2], ws + pl.qh_off, g.r, rh, 64, static_cast<uint32_t>(pl.nbox)) ||
-      !encode_2d_map(&qm[3], ws + pl.ql_off, g.r, rh, 64, static_cast<uint32_t>(pl.nbox)) ||
-      !encode_vpool_map(&vmap, v_cache, g.R, g.NB, 4) ||
-      !encode_2d_map(&pmap[0], ws + pl.p_off[0], g.t_pad[0], rh, 64, 32) ||
-      !encode_2d_map(&pmap[1], ws + pl.p_off[second], g.t_pad[second], rh, 64, 32) ||
-      !encode_2d_map(&pmap[2], ws + pl.p_off[0], g.t_pad[0], rh, 64, 128) ||
-      !encode_2d_map(&pmap[3], ws + pl.p_off[second], g.t_pad[second], rh, 64, 128) ||
-      !encode_2d_map(&bvmap, B_V, static_cast<uint64_t>(g.Hkv) * g.d, g.R, 64, 64))
-    return STARKV_ERR_CUDA;
+  CUtensorMap bvmap;
+  if (!encode_2d_map(&bvmap, B_V, static_cast<uint64_t>(g.Hkv) * g.d, g.R, 64, 64)) return STARKV_ERR_CUDA;
 
   GroupAbsorbParams ap{};
   ap.su.g = g;
@@ -1735,32 +1806,75 @@ starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_g
   if (launch(group_absorb_kernel, dim3(abs_ctas), dim3(kPrepThreads), abs_smem, s, 1, ap) != cudaSuccess)
     return STARKV_ERR_CUDA;
 
-  GroupKParams kp{};
-  kp.g = g;
-  kp.tables = block_tables;
-  for (int i = 0; i < 2; ++i) kp.P[i] = f16(pl.p_off[src[i]]);
-  kp.kb = pl.kb; kp.ksteps = pl.ksteps; kp.qbox = pl.qbox; kp.nbox = pl.nbox; kp.log2Hkv = pl.log2Hkv; kp.nq = pl.nq; kp.stages = pl.k_stages;
-  kp.a_bytes = pl.a_bytes; kp.q_bytes = pl.q_bytes; kp.tmem_cols = pl.k_tmem;
-  if (launch_group_kpass<false>(pl, km, qm, kp, s) != cudaSuccess || launch_group_kpass<true>(pl, km, qm, kp, s) != cudaSuccess)
-    return STARKV_ERR_CUDA;
-
-  GroupVParams vp{};
-  vp.g = g;
-  vp.tables = block_tables;
-  for (int i = 0; i < 2; ++i) vp.Z[i] = f32(pl.z_off[src[i]]);
-  vp.zcarry = f32(pl.carry_off);
-  vp.stages = pl.v_stages;
-  vp.stage_bytes = kGVABytes + kGVBBytes;
-  if (!set_smem(group_vpass_kernel, pl.v_smem)) return STARKV_ERR_CUDA;
-  if (launch(group_vpass_kernel, dim3(pl.v_ctas), dim3(kGVThreads), pl.v_smem, s, 1, vmap, pmap[0], pmap[1], pmap[2],
-             pmap[3], vp) != cudaSuccess)
-    return STARKV_ERR_CUDA;
-
   GroupFinishParams fp{};
+  for (int i = 0; i < 2; ++i) fp.Z[i] = f32(pl.z_off[src[i]]);
+  fp.zcarry = f32(pl.carry_off);
+  if (g.a_rows > 0) {
+    CUtensorMap kmap, vmap, qh, ql;
+    if (!encode_kpool_map(&kmap, k_cache, g.r, g.Hkv, g.NB, static_cast<uint32_t>(g.Hkv), tok_box) ||
+        !encode_vpool_map(&vmap, v_cache, g.R, g.NB, static_cast<uint32_t>(g.nch)) ||
+        !encode_2d_map(&qh, ws + pl.qh_off, g.r, rh, 64, kGACols) || !encode_2d_map(&ql, ws + pl.ql_off, g.r, rh, 64, kGACols))
+      return STARKV_ERR_CUDA;
+    GroupAttendParams tp{};
+    tp.g = g;
+    tp.tables = block_tables;
+    for (int i = 0; i < 2; ++i) {
+      tp.Z[i] = f32(pl.z_off[src[i]]);
+      tp.m[i] = f32(pl.m_off[src[i]]);
+      tp.l[i] = f32(pl.l_off[src[i]]);
+      fp.m[i] = tp.m[i];
+      fp.l[i] = tp.l[i];
+    }
+    tp.zcarry = f32(pl.carry_off);
+    tp.mcarry = f32(pl.mcarry_off);
+    tp.lcarry = f32(pl.lcarry_off);
+    fp.mcarry = tp.mcarry;
+    fp.lcarry = tp.lcarry;
+    tp.kb = pl.kb; tp.ksteps = pl.ksteps; tp.log2Hkv = pl.log2Hkv;
+    tp.utok = pl.at_utok; tp.part = pl.at_part; tp.lstride = pl.at_lstride; tp.lslots = pl.at_lslots;
+    tp.k_stages = pl.at_k_stages; tp.v_stages = pl.at_v_stages; tp.v_stage_bytes = pl.at_v_stage; tp.q_bytes = pl.at_q_bytes;
+    if (!set_smem(group_attend_kernel, pl.at_smem)) return STARKV_ERR_CUDA;
+    if (launch(group_attend_kernel, dim3(pl.at_clusters, g.C), dim3(kGAThreads), pl.at_smem, s, g.C, kmap, vmap, qh, ql, tp) !=
+        cudaSuccess)
+      return STARKV_ERR_CUDA;
+  } else {
+    CUtensorMap km[2], qm[4], vmap, pmap[4];
+    if (!encode_kpool_map(&km[0], k_cache, g.r, g.Hkv, g.NB, 1, 16) ||
+        !encode_kpool_map(&km[1], k_cache, g.r, g.Hkv, g.NB, static_cast<uint32_t>(g.Hkv), tok_box) ||
+        !encode_rows_map(&qm[0], ws + pl.qh_off, g.r, g.H, n_rows, G, static_cast<uint32_t>(pl.qbox) / G) ||
+        !encode_rows_map(&qm[1], ws + pl.ql_off, g.r, g.H, n_rows, G, static_cast<uint32_t>(pl.qbox) / G) ||
+        !encode_2d_map(&qm[2], ws + pl.qh_off, g.r, rh, 64, static_cast<uint32_t>(pl.nbox)) ||
+        !encode_2d_map(&qm[3], ws + pl.ql_off, g.r, rh, 64, static_cast<uint32_t>(pl.nbox)) ||
+        !encode_vpool_map(&vmap, v_cache, g.R, g.NB, 4) ||
+        !encode_2d_map(&pmap[0], ws + pl.p_off[0], g.t_pad[0], rh, 64, 32) ||
+        !encode_2d_map(&pmap[1], ws + pl.p_off[second], g.t_pad[second], rh, 64, 32) ||
+        !encode_2d_map(&pmap[2], ws + pl.p_off[0], g.t_pad[0], rh, 64, 128) ||
+        !encode_2d_map(&pmap[3], ws + pl.p_off[second], g.t_pad[second], rh, 64, 128))
+      return STARKV_ERR_CUDA;
+    GroupKParams kp{};
+    kp.g = g;
+    kp.tables = block_tables;
+    for (int i = 0; i < 2; ++i) kp.P[i] = f16(pl.p_off[src[i]]);
+    kp.kb = pl.kb; kp.ksteps = pl.ksteps; kp.qbox = pl.qbox; kp.nbox = pl.nbox; kp.log2Hkv = pl.log2Hkv; kp.nq = pl.nq; kp.stages = pl.k_stages;
+    kp.a_bytes = pl.a_bytes; kp.q_bytes = pl.q_bytes; kp.tmem_cols = pl.k_tmem;
+    if (launch_group_kpass<false>(pl, km, qm, kp, s) != cudaSuccess || launch_group_kpass<true>(pl, km, qm, kp, s) != cudaSuccess)
+      return STARKV_ERR_CUDA;
+
+    GroupVParams vp{};
+    vp.g = g;
+    vp.tables = block_tables;
+    for (int i = 0; i < 2; ++i) vp.Z[i] = f32(pl.z_off[src[i]]);
+    vp.zcarry = f32(pl.carry_off);
+    vp.stages = pl.v_stages;
+    vp.stage_bytes = kGVABytes + kGVBBytes;
+    if (!set_smem(group_vpass_kernel, pl.v_smem)) return STARKV_ERR_CUDA;
+    if (launch(group_vpass_kernel, dim3(pl.v_ctas), dim3(kGVThreads), pl.v_smem, s, 1, vmap, pmap[0], pmap[1], pmap[2],
+               pmap[3], vp) != cudaSuccess)
+      return STARKV_ERR_CUDA;
+  }
+
   fp.g = g;
   fp.out = static_cast<__half*>(out);
-  fp.Z[0] = vp.Z[0]; fp.Z[1] = vp.Z[1];
-  fp.zcarry = vp.zcarry;
   fp.n_mt = pl.f_mt; fp.rows_tile = pl.f_rows; fp.npad = pl.f_npad; fp.k_per_cta = pl.f_kpc;
   fp.stages = pl.f_stages; fp.log2cg = pl.f_log2cg; fp.stage_bytes = pl.f_stage_bytes; fp.tmem_cols = pl.f_tmem;
   if (!set_smem(group_finish_kernel, pl.f_smem)) return STARKV_ERR_CUDA;
