@@ -254,6 +254,64 @@ struct GroupAbsorbParams {
   int tile;            // rows per item
 };
 
+// A few rows (<= kGAbsRows): a warp per rank index, the lanes along d, eight rank
+// indices at a time.  B_K is read in its own order, one round of loads per eight
+// indices, where the staged product of more rows transposes it first.
+constexpr int kGAbsRows = 4;
+template <int EPL>   // d = 32 EPL
+__device__ __forceinline__ void absorb_few(const GroupAbsorbParams& p, int h, int b0, int nb) {
+  const GroupGeom& g = p.su.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = g.r, D = 32 * EPL;
+  float q[kGAbsRows][EPL];
+#pragma unroll
+  for (int b = 0; b < kGAbsRows; ++b)
+#pragma unroll
+    for (int u = 0; u < EPL; ++u)
+      q[b][u] = b < nb ? __half2float(p.q[(static_cast<size_t>(b0 + b) * g.H + h) * D + lane * EPL + u]) : 0.f;
+  const __half* bk = p.B_K + static_cast<size_t>(h >> g.log2G) * r * D + lane * EPL;
+  for (int i0 = warp * 8; i0 < r; i0 += kPrepThreads / 32 * 8) {
+    __half w[8][EPL];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {   // r is a multiple of 16
+      const __half* src = bk + static_cast<size_t>(i0 + x) * D;
+      if constexpr (EPL == 8) *reinterpret_cast<uint4*>(w[x]) = *reinterpret_cast<const uint4*>(src);
+      else if constexpr (EPL == 4) *reinterpret_cast<uint2*>(w[x]) = *reinterpret_cast<const uint2*>(src);
+      else if constexpr (EPL == 2) *reinterpret_cast<uint32_t*>(w[x]) = *reinterpret_cast<const uint32_t*>(src);
+      else w[x][0] = *src;
+    }
+#pragma unroll
+    for (int b = 0; b < kGAbsRows; ++b) {
+      if (b >= nb) break;
+      float a[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        a[x] = 0.f;
+#pragma unroll
+        for (int u = 0; u < EPL; ++u) a[x] += q[b][u] * __half2float(w[x][u]);
+      }
+      // eight sums over the lanes: lane l ends with index l >> 2
+#pragma unroll
+      for (int o = 16, n = 4; o >= 4; o >>= 1, n >>= 1) {
+        const bool up = (lane & o) != 0;
+#pragma unroll
+        for (int x = 0; x < n; ++x) {
+          const float give = up ? a[x] : a[x + n], keep = up ? a[x + n] : a[x];
+          a[x] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+      }
+      a[0] += __shfl_xor_sync(0xffffffffu, a[0], 2);
+      a[0] += __shfl_xor_sync(0xffffffffu, a[0], 1);
+      if ((lane & 3) == 0) {
+        const float v = a[0] * p.coef;
+        const size_t o = (static_cast<size_t>(b0 + b) * g.H + h) * r + i0 + (lane >> 2);
+        const __half hi = __float2half_rn(v);
+        p.qh[o] = hi;
+        p.ql[o] = __float2half_rn(v - __half2float(hi));
+      }
+    }
+  }
+}
+
 // CTA 0: the tables; CTA 1 + i: query head i % H, rows [tile * (i / H), + tile).
 __global__ void __launch_bounds__(kPrepThreads)
 group_absorb_kernel(GroupAbsorbParams p) {
@@ -272,6 +330,13 @@ group_absorb_kernel(GroupAbsorbParams p) {
   __half* Ws = reinterpret_cast<__half*>(smem_raw);   // [d][r]: B_K[g(h)] transposed
   __half* qs = Ws + static_cast<size_t>(D) * r;       // [tile][d]
   for (int b = tid; b < nb; b += kPrepThreads) g.mrow[static_cast<size_t>(b0 + b) * g.H + h] = -INFINITY;
+  if (nb <= kGAbsRows) {
+    if (D == 128) absorb_few<4>(p, h, b0, nb);
+    else if (D == 64) absorb_few<2>(p, h, b0, nb);
+    else if (D == 256) absorb_few<8>(p, h, b0, nb);
+    else absorb_few<1>(p, h, b0, nb);
+    return;
+  }
   const __half* bk = p.B_K + static_cast<size_t>(h >> g.log2G) * r * D;
   for (int x = tid; x < r * (D / 8); x += kPrepThreads) {
     const int i = x % r, jb = x / r;
@@ -1059,7 +1124,6 @@ group_vpass_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_consta
     // ------------------------------------------------------------ epilogue
     const int et = tid - 64, q = warp & 3, hf = (warp - 2) >> 2;
     uint32_t seg = 0, fix = 0, k = 0;
-    const uint64_t keep = policy_evict_last();   // partial sums: read back by the finish kernel
     VWalk walk(g, tab, u0, u1);
     VSeg x;
     while (walk.next(&x)) {
@@ -1103,15 +1167,20 @@ group_vpass_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_consta
         const int j0 = m * 128 + q * 32;                  // the warp's first row of the R tile
         if (x.rt * kGVTile + j0 >= g.R) break;            // warp-uniform (R is a multiple of 64)
         // a warp stores 128 contiguous bytes of a column per instruction
-        float* zq = dst + j0 + lane;
         for (int h0 = hf * 16; h0 < x.n; h0 += 32) {
           __syncwarp();
           uint32_t v[32];
           tmem_ld_32x32b_x16(base + (static_cast<uint32_t>(q * 32) << 16) + m * mstep + h0, v);
           tmem_ld_wait();
+          float* zq = dst + j0 + lane + static_cast<size_t>(h0) * stride;
+          if (h0 + 16 <= x.ncols) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
-            if (h0 + c < x.ncols) st_global_hint_free(zq + (h0 + c) * stride, __uint_as_float(v[c]), keep);
+            for (int c = 0; c < 16; ++c, zq += stride) *zq = __uint_as_float(v[c]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 16; ++c, zq += stride)
+              if (h0 + c < x.ncols) *zq = __uint_as_float(v[c]);
+          }
         }
       }
       tc_fence_before();
@@ -1555,9 +1624,7 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     const int q = warp & 3;
     const uint32_t lq = static_cast<uint32_t>(q * 32) << 16;
     const int rho = q * 32 + lane, j = rho & (g.Hkv - 1), tl = rho >> p.log2Hkv, G = 1 << g.log2G;
-    const int log2H = p.log2Hkv + g.log2G;
     float* st = reinterpret_cast<float*>(smem + lay.stage) + rho * 36;
-    const uint64_t keep = policy_evict_last();
     RingPos acc, ls;
     uint32_t seg = 0;
     bool ok = true;
@@ -1582,13 +1649,21 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 #pragma unroll
             for (int u = 0; u < 8; ++u)
               *reinterpret_cast<uint4*>(st + 4 * u) = make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
-            // the row's own head's columns among these 32
-            if (tl < p.utok)
-              for (int i = c0 >> log2H; (i << log2H) < min(x.ncols, c0 + 32); ++i)
-                for (int gg = 0; gg < G; ++gg) {
-                  const int col = (i << log2H) + (j << g.log2G) + gg, o = col - c0;
-                  if (o >= 0 && o < 32) out[(t + tl) * p.lstride + col] = st[o];
+            // the row's own head's columns among these 32, row by row of the tile
+            if (tl < p.utok) {
+              float* dst = out + (t + tl) * p.lstride + c0;
+              int o = (j << g.log2G) - (c0 & (g.H - 1));
+              for (int left = c0 + 32 < x.ncols ? 32 : x.ncols - c0; left > 0; left -= g.H, o += g.H) {
+                if (o < 0 || o >= 32) continue;
+                if (G >= 4) {
+                  for (int gg = 0; gg < G; gg += 4)
+                    *reinterpret_cast<float4*>(dst + o + gg) = *reinterpret_cast<const float4*>(st + o + gg);
+                } else {
+                  dst[o] = st[o];
+                  if (G == 2) dst[o + 1] = st[o + 1];
                 }
+              }
+            }
           }
           tc_fence_before();
           __syncwarp();
@@ -1615,14 +1690,19 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         const int j0 = m * 128 + q * 32;
         if (j0 >= codes) break;              // warp-uniform (codes is a multiple of 64)
         float* zq = dst + j0 + lane;         // a warp stores 128 contiguous bytes of a column per instruction
-        for (int h0 = 0; h0 < x.ncols; h0 += 16) {
+        for (int h0 = 0; h0 < x.ncols; h0 += 32) {
           __syncwarp();
           uint32_t v[32];
-          tmem_ld_32x32b_x16(taddr + lq + m * 64u + h0, v);
+          tmem_ld_32x32b_x32(taddr + lq + m * 64u + h0, v);
           tmem_ld_wait();
+          if (h0 + 32 <= x.ncols) {
 #pragma unroll
-          for (int u = 0; u < 16; ++u)
-            if (h0 + u < x.ncols) st_global_hint_free(zq + static_cast<size_t>(h0 + u) * g.R, __uint_as_float(v[u]), keep);
+            for (int u = 0; u < 32; ++u, zq += g.R) *zq = __uint_as_float(v[u]);
+          } else {
+#pragma unroll
+            for (int u = 0; u < 32; ++u, zq += g.R)
+              if (h0 + u < x.ncols) *zq = __uint_as_float(v[u]);
+          }
         }
       }
       tc_fence_before();
@@ -1679,9 +1759,28 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         ms.next(kGAMSlots);
         return true;
       };
+      // whether send(b) would not wait, for the whole warp
+      auto ready = [&](int b) {
+        RingPos r = lr;
+        uint32_t n = nr;
+        bool yes = true;
+        for (int pi = 0; pi < ppb; ++pi) {
+          const int gp = b * ppb + pi;
+          if (gp % C != c || gp * p.part >= len) continue;
+          if (static_cast<int>(n & 1) == team) yes = yes && mbar_try_wait(&lfull[r.s], r.u & 1);
+          ++n;
+          r.next(LS);
+        }
+        return __all_sync(0xffffffffu, yes) != 0;
+      };
       if (!send(x.b0)) { ok = false; break; }
       for (int b = x.b0; b < x.b1; ++b) {
-        if (b + 1 < x.b1 && !send(b + 1)) { ok = false; break; }
+        // the next block's maxima early when its logits are there already
+        bool sent = b + 1 >= x.b1;
+        if (!sent && ready(b + 1)) {
+          sent = true;
+          if (!send(b + 1)) { ok = false; break; }
+        }
         if (!__all_sync(0xffffffffu, mbar_wait_cluster(&mfull[mb.s], mb.u & 1) && !abort_flag)) { ok = false; break; }
         float bm = -INFINITY, bo = -INFINITY;
         for (int pi = 0; pi < ppb; ++pi) {
@@ -1768,6 +1867,7 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           if (live) { ++nw; lw.next(LS); }
         }
         pb.next(kGAPSlots);
+        if (!sent && !send(b + 1)) { ok = false; break; }
       }
       if (!ok) break;
       // m and l of the segment: both teams' sums
@@ -1804,8 +1904,9 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 struct GroupFinishParams {
   GroupGeom g;
   __half* out;           // [n_rows][H][d]
-  const float* Z[2];
-  const float* zcarry;
+  const float* base;     // the workspace, as floats
+  int64_t z_at[2], carry_at;   // offsets of the Z matrices (by zsrc) and of the carries
+  int log2cap;           // segments listed per column
   // sums of the attend kernel (null m[0]: of the V pass, all relative to one maximum):
   const float* m[2];     // by zsrc, [n_rows * H] the first segment's maximum
   const float* l[2];     // [n_rows * H][C] its sums of weights
@@ -1837,11 +1938,13 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
   uint64_t* empty = conv + S;
   uint64_t* done = empty + S;
   uint64_t* cbar = done + 1;                        // the converters' sync
+  int64_t* s_off = reinterpret_cast<int64_t*>(cbar + 1);   // [columns][1 << log2cap] where the segments stand
+  float* s_fac = reinterpret_cast<float*>(s_off + (static_cast<size_t>(p.npad) << p.log2cap));   // attend: their exp2(m - M)
   float* part = reinterpret_cast<float*>(smem);     // [npad][128], reuses the ring
   __shared__ uint32_t taddr_s;
   __shared__ float s_il[256], s_M[256];
   __shared__ GroupTablesSmem s_tab;
-  __shared__ int32_t s_i0[2][256], s_n[2][256], s_col[2][256];   // per source: first CTA, CTAs, column within the V tile
+  __shared__ int32_t s_ent[2][256], s_i0[2][256], s_n[2][256], s_col[2][256];   // per source: first CTA, CTAs, column within the V tile
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int xi = blockIdx.x;
@@ -1906,165 +2009,191 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
     const int et = tid - 64;
     griddep_wait();
     const int n_src = g.shared ? 2 : 1;
+    const bool attend = p.m[0] != nullptr;
     uint32_t phase = 0;
     const GroupEntry* ent = g.ent;
     if (g.E <= kGSmemE) {
       for (int i = et; i < g.E * 4; i += kGFConv)
         reinterpret_cast<uint4*>(s_tab.ent)[i] = reinterpret_cast<const uint4*>(g.ent)[i];
       ent = s_tab.ent;
-      if (!group_sync(cbar, phase)) ok = false;
     }
-    const bool attend = p.m[0] != nullptr;
+    int rt_at = attend ? 0 : -1;
+    // exp2(m - M) of segment u of a column, for calls whose list of factors is too short
+    auto seg_factor = [&](int u, int bl, int n0) {
+      const int sr = u >= n0 ? 1 : 0, k = u - (sr ? n0 : 0);
+      const int row = row0 + (bl >> g.log2G), h = (j << g.log2G) + (bl & ((1 << g.log2G) - 1));
+      const float m = k == 0 ? p.m[sr][static_cast<size_t>(row) * g.H + h]
+                             : p.mcarry[static_cast<size_t>(s_i0[sr][bl] + k) * kGACols + s_col[sr][bl]];
+      return m > -INFINITY ? ex2_approx(m - s_M[bl]) : 1.f;
+    };
+    // the entries of each column: -1 where it has none, or none of their tokens
+    for (int x = et; x < 2 * ncols; x += kGFConv) {
+      const int sr = x >= ncols ? 1 : 0, c = x - sr * ncols, row = row0 + (c >> g.log2G);
+      int e = -1;
+      if (sr < n_src && row < g.n_rows) {
+        const int grp = g.row_ent[row], use = g.row_use[row];
+        if (grp >= 0) e = sr ? g.n_groups + row : (use ? grp : -1);
+      }
+      s_ent[sr][c] = e;
+    }
+    if (!group_sync(cbar, phase)) ok = false;
+    // where the partial sums of each column stand (for the V pass: for one tile of R): the
+    // offset, in floats from the workspace's start, of code 0 of each of its segments
+    auto seg_off = [&](int sr, int c, int k) -> int64_t {   // segment k of source sr
+      const int row = row0 + (c >> g.log2G), h = (j << g.log2G) + (c & ((1 << g.log2G) - 1));
+      if (k == 0) return p.z_at[sr] + (static_cast<int64_t>(row) * g.H + h) * g.R;
+      const int64_t place = static_cast<int64_t>(s_i0[sr][c] + k) * (attend ? kGACols : kGVTile) + s_col[sr][c];
+      return p.carry_at + (attend ? place * g.R : (place - rt_at) * kGVTile);
+    };
+    auto places = [&]() {
+      for (int x = et; x < 2 * ncols; x += kGFConv) {
+        const int sr = x >= ncols ? 1 : 0, c = x - sr * ncols;
+        const int row = row0 + (c >> g.log2G), h = (j << g.log2G) + (c & ((1 << g.log2G) - 1));
+        int i0 = 0, n = 0, place = 0;
+        const int e = s_ent[sr][c];
+        if (e >= 0 && ent[e].len > 0) {
+          const GroupEntry& en = ent[e];
+          const int per = attend ? en.a_per * g.H : en.v_width;
+          const int col = (row - en.row0) * g.H + h, nt = col / per;
+          const int tile = attend ? en.a_tile0 + nt : en.tile0 + nt * g.n_rt + rt_at;
+          i0 = g.tfirst[tile];
+          n = g.tlast[tile] - i0 + 1;
+          place = col - nt * per;
+        }
+        s_i0[sr][c] = i0;
+        s_n[sr][c] = n;
+        s_col[sr][c] = place;
+      }
+      if (!group_sync(cbar, phase)) ok = false;
+      for (int x = et; x < ncols << p.log2cap; x += kGFConv) {
+        const int c = x >> p.log2cap, k = x & ((1 << p.log2cap) - 1), n0 = s_n[0][c];
+        if (k < n0 + s_n[1][c]) s_off[x] = k < n0 ? seg_off(0, c, k) : seg_off(1, c, k - n0);
+      }
+    };
     if (attend) {
-      // M and 1 / L of every column over its segments: a warp per column, a lane per segment
+      places();
+      if (!group_sync(cbar, phase)) ok = false;
+      // M, 1 / L and each segment's exp2(m - M): a warp per column, a lane per segment
       for (int c = warp - 2; c < ncols; c += kGFConv / 32) {
         const int row = row0 + (c >> g.log2G), h = (j << g.log2G) + (c & ((1 << g.log2G) - 1));
-        const int e = row < g.n_rows ? g.row_ent[row] : -1, use = row < g.n_rows ? g.row_use[row] : 0;
+        const size_t o = static_cast<size_t>(row) * g.H + h;
+        const int n0 = s_n[0][c], n = n0 + s_n[1][c];
         float M = -INFINITY, L = 0.f;
-        for (int pass = 0; pass < 2; ++pass) {
-          for (int sr = 0; sr < n_src; ++sr) {
-            if (e < 0 || (sr == 0 && !use)) continue;
-            const GroupEntry en = ent[sr ? g.n_groups + row : e];
-            if (en.len == 0) continue;
-            const int t = (row - en.row0) / en.a_per, place = (row - en.row0 - t * en.a_per) * g.H + h;
-            const int i0 = g.tfirst[en.a_tile0 + t], n = g.tlast[en.a_tile0 + t] - i0 + 1;
-            const size_t o = static_cast<size_t>(row) * g.H + h;
-            for (int i = lane; i < n; i += 32) {
-              const size_t oc = static_cast<size_t>(i0 + i) * kGACols + place;
-              const float m = i == 0 ? p.m[sr][o] : p.mcarry[oc];
-              if (pass == 0) {
-                M = fmaxf(M, m);
-              } else {
-                const float* lp = i == 0 ? p.l[sr] + o * g.C : p.lcarry + oc * g.C;
-                float l = 0.f;
-                for (int u = 0; u < g.C; ++u) l += lp[u];
-                // a segment whose logits are all NaN or -inf has m = -inf and l = NaN
-                L += m > -INFINITY ? l * ex2_approx(m - M) : l;
-              }
-            }
-          }
+        for (int b = 0; b < n; b += 32) {   // a further round only for more than 32 segments
+          const int i = b + lane;
+          float m = -INFINITY, l = 0.f;
+          if (i < n) {
+            const int sr = i >= n0 ? 1 : 0, k = i - (sr ? n0 : 0);
+            const size_t oc = static_cast<size_t>(s_i0[sr][c] + k) * kGACols + s_col[sr][c];
+            m = k == 0 ? p.m[sr][o] : p.mcarry[oc];
+            const float* lp = k == 0 ? p.l[sr] + o * g.C : p.lcarry + oc * g.C;
+            float l8[8];
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) {
-            if (pass == 0) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            else L += __shfl_xor_sync(0xffffffffu, L, o);
+            for (int u = 0; u < 8; ++u) l8[u] = u < g.C ? lp[u] : 0.f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) l += l8[u];
           }
+          float Mb = m;
+#pragma unroll
+          for (int q = 16; q > 0; q >>= 1) Mb = fmaxf(Mb, __shfl_xor_sync(0xffffffffu, Mb, q));
+          const float Mn = fmaxf(M, Mb);
+          // a segment whose logits are all NaN or -inf has m = -inf and l = NaN
+          float Lb = i < n ? (m > -INFINITY ? l * ex2_approx(m - Mn) : l) : 0.f;
+#pragma unroll
+          for (int q = 16; q > 0; q >>= 1) Lb += __shfl_xor_sync(0xffffffffu, Lb, q);
+          L = (M > -INFINITY ? L * ex2_approx(M - Mn) : L) + Lb;
+          M = Mn;
+          if (n <= 32 && i < n && i < 1 << p.log2cap) s_fac[(c << p.log2cap) + i] = m > -INFINITY ? ex2_approx(m - M) : 1.f;
         }
         if (lane == 0) {
-          s_il[c] = L == 0.f ? 0.f : 1.f / L;
+          s_il[c] = L == 0.f ? 0.f : 1.f / L;   // no token at all: L = 0 and the result is 0
           s_M[c] = M;
         }
       }
-    }
-    // 1 / L of every column: a warp sums a column's chunks
-    for (int c = attend ? ncols : warp - 2; c < ncols; c += kGFConv / 32) {
-      const int row = row0 + (c >> g.log2G);
-      const int e = row < g.n_rows ? g.row_ent[row] : -1, use = row < g.n_rows ? g.row_use[row] : 0;
-      float L = 0.f;
-      if (e >= 0) {
+    } else {
+      // 1 / L of every column: a warp sums a column's chunks
+      for (int c = warp - 2; c < ncols; c += kGFConv / 32) {
+        const int row = row0 + (c >> g.log2G);
         const size_t rh = static_cast<size_t>(row) * g.H + (j << g.log2G) + (c & ((1 << g.log2G) - 1));
-        for (int s = 0; s < n_src; ++s) {
-          const GroupEntry en = ent[s ? g.n_groups + row : e];
-          if (en.len == 0 || (s == 0 && !use)) continue;
-          const int ch = en.narrow ? g.chunk_n : g.chunk_w;
-          const int nc = (en.len + ch - 1) / ch;
-          for (int i = lane; i < nc; i += 32) L += g.lpart[s][rh * g.n_ch[s] + i];
+        float L = 0.f;
+        for (int sr = 0; sr < n_src; ++sr) {
+          const int e = s_ent[sr][c];
+          if (e < 0 || ent[e].len == 0) continue;
+          const int ch = ent[e].narrow ? g.chunk_n : g.chunk_w;
+          const int nc = (ent[e].len + ch - 1) / ch;
+          for (int i = lane; i < nc; i += 32) L += g.lpart[sr][rh * g.n_ch[sr] + i];
         }
-      }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-      if (lane == 0) s_il[c] = L == 0.f ? 0.f : 1.f / L;   // no token at all: L = 0 and the result is 0
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        if (lane == 0) s_il[c] = L == 0.f ? 0.f : 1.f / L;
+      }
     }
+    if (!group_sync(cbar, phase)) ok = false;
     const int cthr = kGFConv >> p.log2cg, cgrp = et / cthr;   // threads of a group, this thread's group
-    int rt_at = -1;
     for (int i = 0; i < n_stages && ok; ++i) {
       const int s = i % S;
-      const int kr = k0 + i * 64, rt = kr / kGVTile;
-      if (rt != rt_at) {
-        // where the partial sums of each column stand for this tile of R
-        rt_at = rt;
+      const int kr = k0 + i * 64;
+      if (!attend && kr / kGVTile != rt_at) {
         if (!group_sync(cbar, phase)) { ok = false; break; }
-        for (int c = et; c < ncols; c += kGFConv) {
-          const int row = row0 + (c >> g.log2G), h = (j << g.log2G) + (c & ((1 << g.log2G) - 1));
-          const int e = row < g.n_rows ? g.row_ent[row] : -1, use = row < g.n_rows ? g.row_use[row] : 0;
-          for (int sr = 0; sr < 2; ++sr) {
-            int i0 = 0, n = 0, place = 0;
-            if (sr < n_src && e >= 0 && (sr || use)) {
-              const GroupEntry en = ent[sr ? g.n_groups + row : e];
-              if (en.len > 0) {
-                const int per = attend ? en.a_per * g.H : en.v_width;
-                const int col = (row - en.row0) * g.H + h, nt = col / per;
-                const int tile = attend ? en.a_tile0 + nt : en.tile0 + nt * g.n_rt + rt;
-                i0 = g.tfirst[tile];
-                n = g.tlast[tile] - i0 + 1;
-                place = col - nt * per;
-              }
-            }
-            s_i0[sr][c] = i0;
-            s_n[sr][c] = n;
-            s_col[sr][c] = place;
-          }
-        }
+        rt_at = kr / kGVTile;
+        places();
         if (!group_sync(cbar, phase)) { ok = false; break; }
       }
       if ((i & ((1 << p.log2cg) - 1)) != cgrp) continue;   // another group's stage
       if (i >= S && !__all_sync(0xffffffffu, mbar_wait(&empty[s], ((i / S) - 1) & 1))) { ok = false; break; }
       uint8_t* hi_t = smem + static_cast<size_t>(s) * p.stage_bytes + a_bytes;
-      // item = (column bl, 8-value chunk c of the stage's 64 rows of R)
+      // item = (column bl, 8-value chunk c of the stage's 64 rows of R), four segments at a
+      // time: eight 16-byte loads in flight per thread
       for (int item = et & (cthr - 1); item < p.npad * 8; item += cthr) {
         const int bl = item >> 3, c = item & 7;
         float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (bl < ncols && row0 + (bl >> g.log2G) < g.n_rows) {
-          const int row = row0 + (bl >> g.log2G), h = (j << g.log2G) + (bl & ((1 << g.log2G) - 1));
-          const int code = kr + c * 8;
-          for (int sr = 0; sr < n_src; ++sr) {
-            const int n = s_n[sr][bl];
-            if (n == 0) continue;
-            const float* first = p.Z[sr] + (static_cast<size_t>(row) * g.H + h) * g.R + code;
-            const size_t place = static_cast<size_t>(s_i0[sr][bl]) * (attend ? kGACols : kGVTile) + s_col[sr][bl];
-            const float* carry = attend ? p.zcarry + place * g.R + code : p.zcarry + place * kGVTile + (code - rt * kGVTile);
-            const size_t cstep = attend ? static_cast<size_t>(kGACols) * g.R : static_cast<size_t>(kGVTile) * kGVTile;
-            for (int u0 = 0; u0 < n; u0 += 4) {
-              float4 a[4], b[4];
-              float f[4];
+        const int n0 = bl < ncols ? s_n[0][bl] : 0, n = bl < ncols ? n0 + s_n[1][bl] : 0;
+        const float* at = p.base + kr + c * 8;
+        const int cap = min(n, 1 << p.log2cap);
+        const int64_t* off = s_off + (bl << p.log2cap);
+        const float* fac = s_fac + (bl << p.log2cap);
+        for (int u0 = 0; u0 < cap; u0 += 4) {
+          float4 a[4], b[4];
 #pragma unroll
-              for (int u = 0; u < 4; ++u)
-                if (u0 + u < n) {
-                  const float* src = u0 + u == 0 ? first : carry + static_cast<size_t>(u0 + u) * cstep;
-                  a[u] = *reinterpret_cast<const float4*>(src);
-                  b[u] = *reinterpret_cast<const float4*>(src + 4);
-                  f[u] = 1.f;
-                  if (attend) {
-                    const float m = u0 + u == 0 ? p.m[sr][static_cast<size_t>(row) * g.H + h]
-                                                : p.mcarry[place + static_cast<size_t>(u0 + u) * kGACols];
-                    f[u] = m > -INFINITY ? ex2_approx(m - s_M[bl]) : 1.f;
-                  }
-                }
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                if (u0 + u < n) {
-                  z[0] += a[u].x * f[u]; z[1] += a[u].y * f[u]; z[2] += a[u].z * f[u]; z[3] += a[u].w * f[u];
-                  z[4] += b[u].x * f[u]; z[5] += b[u].y * f[u]; z[6] += b[u].z * f[u]; z[7] += b[u].w * f[u];
-                }
+          for (int u = 0; u < 4; ++u) {
+            a[u] = b[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (u0 + u < cap) {
+              const float4* src = reinterpret_cast<const float4*>(at + off[u0 + u]);
+              a[u] = src[0];
+              b[u] = src[1];
             }
           }
-          const float il = s_il[bl];
 #pragma unroll
-          for (int u = 0; u < 8; ++u) z[u] *= il;
+          for (int u = 0; u < 4; ++u)
+            if (u0 + u < cap) {
+              const float f = attend ? (n <= 32 ? fac[u0 + u] : seg_factor(u0 + u, bl, n0)) : 1.f;
+              z[0] += a[u].x * f; z[1] += a[u].y * f; z[2] += a[u].z * f; z[3] += a[u].w * f;
+              z[4] += b[u].x * f; z[5] += b[u].y * f; z[6] += b[u].z * f; z[7] += b[u].w * f;
+            }
         }
+        for (int u = cap; u < n; ++u) {   // more segments than the list holds
+          const float4* src = reinterpret_cast<const float4*>(at + (u < n0 ? seg_off(0, bl, u) : seg_off(1, bl, u - n0)));
+          const float4 a = src[0], b = src[1];
+          const float f = attend ? seg_factor(u, bl, n0) : 1.f;
+          z[0] += a.x * f; z[1] += a.y * f; z[2] += a.z * f; z[3] += a.w * f;
+          z[4] += b.x * f; z[5] += b.y * f; z[6] += b.z * f; z[7] += b.w * f;
+        }
+        const float il = n > 0 ? s_il[bl] : 0.f;
         uint4 hv, lv;
         uint32_t* hw = reinterpret_cast<uint32_t*>(&hv);
         uint32_t* lw = reinterpret_cast<uint32_t*>(&lv);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const __half2 hh = __floats2half2_rn(z[2 * u], z[2 * u + 1]);
+          const float z0 = z[2 * u] * il, z1 = z[2 * u + 1] * il;
+          const __half2 hh = __floats2half2_rn(z0, z1);
           const float2 f = __half22float2(hh);
-          const __half2 ll = __floats2half2_rn(z[2 * u] - f.x, z[2 * u + 1] - f.y);
+          const __half2 ll = __floats2half2_rn(z0 - f.x, z1 - f.y);
           hw[u] = *reinterpret_cast<const uint32_t*>(&hh);
           lw[u] = *reinterpret_cast<const uint32_t*>(&ll);
         }
-        const uint32_t off = static_cast<uint32_t>(bl) * 128u + (static_cast<uint32_t>(c ^ (bl & 7)) << 4);
-        *reinterpret_cast<uint4*>(hi_t + off) = hv;
-        *reinterpret_cast<uint4*>(hi_t + b_bytes + off) = lv;
+        const uint32_t off16 = static_cast<uint32_t>(bl) * 128u + (static_cast<uint32_t>(c ^ (bl & 7)) << 4);
+        *reinterpret_cast<uint4*>(hi_t + off16) = hv;
+        *reinterpret_cast<uint4*>(hi_t + b_bytes + off16) = lv;
       }
       fence_proxy_async_smem();
       mbar_arrive(&conv[s]);

@@ -1516,7 +1516,7 @@ struct GroupPlan {
   int v_stages, v_ctas;
   size_t v_smem;
   // finish
-  int f_mt, f_rows, f_tiles, f_npad, f_ks, f_kpc, f_stages, f_log2cg;
+  int f_mt, f_rows, f_tiles, f_npad, f_ks, f_kpc, f_stages, f_log2cg, f_log2cap;
   uint32_t f_stage_bytes, f_tmem;
   size_t f_smem;
   // attend (g.a_rows > 0)
@@ -1645,16 +1645,19 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
     p.f_rows = (p.f_rows + 1) / 2;
   p.f_tiles = n_rows > 0 ? (n_rows + p.f_rows - 1) / p.f_rows : 1;
   p.f_npad = (p.f_rows * G + 15) / 16 * 16;
+  p.f_log2cap = p.f_npad <= 64 ? 5 : 3;   // segments listed per column: 32, or 8 of many columns
   p.f_stage_bytes = 16384u + 2u * p.f_npad * 128u;
-  p.f_stages = static_cast<int>(200u * 1024u / p.f_stage_bytes);
+  // as many stages (up to four) as let two CTAs share an SM, else what one CTA holds
+  p.f_stages = static_cast<int>(84u * 1024u / p.f_stage_bytes);
+  if (p.f_stages < 3) p.f_stages = static_cast<int>(190u * 1024u / p.f_stage_bytes);
   if (p.f_stages > 4) p.f_stages = 4;
   {
     size_t ring = static_cast<size_t>(p.f_stages) * p.f_stage_bytes;
     if (ring < static_cast<size_t>(p.f_npad) * 512) ring = static_cast<size_t>(p.f_npad) * 512;
-    p.f_smem = 1024 + ring + (3 * p.f_stages + 2) * sizeof(uint64_t);
+    p.f_smem = 1024 + ring + (3 * p.f_stages + 2) * sizeof(uint64_t) + (static_cast<size_t>(p.f_npad) << p.f_log2cap) * 12;
   }
   // split R over clusters while the grid stays within one wave (two CTAs per SM where they fit)
-  const int f_per_sm = p.f_smem + 12 * 1024 <= 113u * 1024u ? 2 : 1;
+  const int f_per_sm = p.f_smem + 19 * 1024 <= 114u * 1024u ? 2 : 1;   // 18 KB static, 1 KB reserved
   p.f_ks = 1;
   while (p.f_ks < 8 && static_cast<int64_t>(g.Hkv) * p.f_mt * p.f_tiles * p.f_ks * 2 <= f_per_sm * sms &&
          g.R / 64 >= p.f_ks * 2)
@@ -1807,8 +1810,9 @@ starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_g
     return STARKV_ERR_CUDA;
 
   GroupFinishParams fp{};
-  for (int i = 0; i < 2; ++i) fp.Z[i] = f32(pl.z_off[src[i]]);
-  fp.zcarry = f32(pl.carry_off);
+  fp.base = f32(0);
+  for (int i = 0; i < 2; ++i) fp.z_at[i] = static_cast<int64_t>(pl.z_off[src[i]] / 4);
+  fp.carry_at = static_cast<int64_t>(pl.carry_off / 4);
   if (g.a_rows > 0) {
     CUtensorMap kmap, vmap, qh, ql;
     if (!encode_kpool_map(&kmap, k_cache, g.r, g.Hkv, g.NB, static_cast<uint32_t>(g.Hkv), tok_box) ||
@@ -1876,7 +1880,7 @@ starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_g
   fp.g = g;
   fp.out = static_cast<__half*>(out);
   fp.n_mt = pl.f_mt; fp.rows_tile = pl.f_rows; fp.npad = pl.f_npad; fp.k_per_cta = pl.f_kpc;
-  fp.stages = pl.f_stages; fp.log2cg = pl.f_log2cg; fp.stage_bytes = pl.f_stage_bytes; fp.tmem_cols = pl.f_tmem;
+  fp.stages = pl.f_stages; fp.log2cg = pl.f_log2cg; fp.log2cap = pl.f_log2cap; fp.stage_bytes = pl.f_stage_bytes; fp.tmem_cols = pl.f_tmem;
   if (!set_smem(group_finish_kernel, pl.f_smem)) return STARKV_ERR_CUDA;
   if (launch(group_finish_kernel, dim3(g.Hkv * pl.f_mt * pl.f_tiles, pl.f_ks), dim3(kGFThreads), pl.f_smem, s, pl.f_ks, bvmap,
              fp) != cudaSuccess)
