@@ -1204,7 +1204,7 @@ group_vpass_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_consta
 // codes of R in tensor memory, and the 16-token parts of the blocks go round the
 // CTAs: a part's logits, maxima and weights are formed by one CTA and sent to
 // the others through distributed shared memory.  So no logit or weight leaves
-// the SMs and nothing waits for a grid.
+// the SMs and no phase waits for a grid.
 //   S      = c_K . (q~ hi + q~ lo) for 128 code rows in page order at a time (see
 //            gk_narrow); each row keeps its own head's columns
 //   m      = max of the first block's logits, per column; raised, with Z and l
@@ -1227,7 +1227,7 @@ struct GroupAttendParams {
   float* lcarry;             // [clusters][64][C]
   int kb, ksteps;            // 64-code blocks and 16-code steps of r
   int log2Hkv;
-  int utok, part;            // tokens per unit (128 code rows) and per part
+  int utok, part, log2part;  // tokens per unit (128 code rows) and per part
   int lstride, lslots;       // floats per token of a logit slot, logit slots
   int k_stages, v_stages;
   uint32_t v_stage_bytes;    // 2 pages x 16 tokens x 64 nch codes
@@ -1287,6 +1287,12 @@ struct AWalk {
   }
 };
 
+// First part at or after gp that is CTA c's of C (parts go round the CTAs).
+__device__ __forceinline__ int first_own(int gp, int c, int C) {
+  const int r = static_cast<int>(static_cast<uint32_t>(gp) % static_cast<uint32_t>(C));
+  return gp + (c >= r ? c - r : c - r + C);
+}
+
 // Shared-memory layout (bytes from the 1024-aligned base).
 struct AttendSmem {
   uint32_t v, q, k, p, ls, stage, mx, bars, total;
@@ -1345,17 +1351,17 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int ppb = kGATok / p.part;         // parts per block
+  const int ppb = kGATok >> p.log2part;    // parts per block
   if (tid == 0) {
     for (int s = 0; s < KS; ++s) { mbar_init(&kfull[s], 1); mbar_init(&kempty[s], 1); }
     for (int s = 0; s < VS; ++s) { mbar_init(&vfull[s], 1); mbar_init(&vempty[s], 1); mbar_init(&vfix[s], 1); }
     for (int s = 0; s < LS; ++s) { mbar_init(&lfull[s], 4); mbar_init(&lempty[s], 2); }
     for (int s = 0; s < kGAPSlots; ++s) {
-      mbar_init(&pfull[s], 2 * ppb + 1);   // two warps per part, and this CTA's own go-ahead
+      mbar_init(&pfull[s], 4);             // this CTA's weight warps; the others' weights count as bytes
       mbar_init(&pdone[s], 1);
       mbar_init(&pempty[s], C);
     }
-    for (int s = 0; s < kGAMSlots; ++s) mbar_init(&mfull[s], 2 * ppb);
+    for (int s = 0; s < kGAMSlots; ++s) mbar_init(&mfull[s], 4);
     for (int s = 0; s < kGAAcc; ++s) { mbar_init(&tfull[s], 1); mbar_init(&tempty[s], 4); }
     mbar_init(qfull, 1);
     mbar_init(qempty, 1);
@@ -1398,8 +1404,7 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     bool ok = true;
     AWalk walk(g, tab, x0, x1);
     ASeg x;
-    const int tb = min(kBlock, p.utok), boxes = p.utok / tb;
-    const uint32_t box = static_cast<uint32_t>(tb * g.Hkv) * 128u;
+    const uint32_t box = static_cast<uint32_t>(min(kBlock, p.utok) * g.Hkv) * 128u;
     while (ok && walk.next(&x)) {
       const int tbeg = x.b0 * kGATok, tend = min(x.en.len, x.b1 * kGATok);
       PageReader pages(p.tables + static_cast<size_t>(x.en.tab) * g.MB + x.en.page0 + tbeg / kBlock,
@@ -1417,26 +1422,38 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         }
       }
       ++seg;
-      const int plast = (tend + p.part - 1) / p.part;
-      for (int gp = x.b0 * ppb; gp < plast; ++gp) {
-        if (gp % C != c) continue;
-        for (int t = gp * p.part; t < gp * p.part + p.part; t += p.utok) {
-          const int nb = t + p.utok <= tend ? boxes : max(0, ((tend + kBlock - 1) / kBlock * kBlock - t + tb - 1) / tb);
+      // the CTA's own parts are every C-th
+      for (int gp = first_own(x.b0 * ppb, c, C); gp * p.part < tend; gp += C) {
+        const int pi = (gp * p.part - tbeg) >> 4;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (p.utok >= kBlock) {
+          // one unit of whole pages
+          const int np = min(p.part, tend - gp * p.part + kBlock - 1) >> 4;
           for (int a = 0; a < p.kb; ++a) {
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) break;
             uint8_t* st = smem + lay.k + k.s * 16384u;
             if (lane == 0) {
               if (k.u > 0 && !mbar_wait(&kempty[k.s], (k.u - 1) & 1)) ok = false;
-              else mbar_arrive_expect_tx(&kfull[k.s], static_cast<uint32_t>(min(nb, boxes)) * box);
+              else mbar_arrive_expect_tx(&kfull[k.s], static_cast<uint32_t>(np) * box);
             }
-            for (int b = 0; b < min(nb, boxes); ++b) {
-              const int tk = t + b * tb;
-              const int row = pages.page((tk - tbeg) >> 4) * kBlock + (tk & (kBlock - 1));
+            for (int b = 0; b < np; ++b) {
+              const int row = pages.page(pi + b) * kBlock;
               if (lane == 0 && ok) tma_load_3d(st + b * box, &kmap, a * 64, 0, row, &kfull[k.s], keep);
             }
             if (ok) { ++issued; k.next(KS); }
           }
+        } else {
+          // one page in units of utok tokens
+          const int row = pages.page(pi) * kBlock;
+          if (lane == 0)
+            for (int u = 0; u < kBlock && ok; u += p.utok)
+              for (int a = 0; a < p.kb; ++a) {
+                if (k.u > 0 && !mbar_wait(&kempty[k.s], (k.u - 1) & 1)) { ok = false; break; }
+                mbar_arrive_expect_tx(&kfull[k.s], box);
+                tma_load_3d(smem + lay.k + k.s * 16384u, &kmap, a * 64, 0, row + u, &kfull[k.s], keep);
+                ++issued;
+                k.next(KS);
+              }
         }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -1465,11 +1482,10 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       ASeg x;
       while (ok && walk.next(&x)) {
         const uint32_t idesc = idesc_f16_f32(128, (x.ncols + 15) & ~15, /*a_mn_major=*/false, /*b_mn_major=*/false);
-        const int tend = min(x.en.len, x.b1 * kGATok), plast = (tend + p.part - 1) / p.part;
+        const int tend = min(x.en.len, x.b1 * kGATok);
         if (!mbar_wait(qfull, seg & 1)) { ok = false; break; }
         ++seg;
-        for (int gp = x.b0 * ppb; gp < plast && ok; ++gp) {
-          if (gp % C != c) continue;
+        for (int gp = first_own(x.b0 * ppb, c, C); gp * p.part < tend && ok; gp += C) {
           for (int t = 0; t < p.part && ok; t += p.utok) {
             if (acc.u > 0 && !mbar_wait(&tempty[acc.s], (acc.u - 1) & 1)) { ok = false; break; }
             const uint32_t dst = tS + static_cast<uint32_t>(acc.s) * kGACols;
@@ -1567,7 +1583,8 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       uint32_t seg = 0;
       bool ok = true;
       const uint64_t ad0 = smem_desc(smem_u32(smem + lay.v), 2048u, 1024u, kSwizzle128B);
-      const uint64_t bd0 = smem_desc(smem_u32(smem + lay.p), 16u, 1024u, kSwizzle128B);
+      // weights: 8 tokens x 64 columns (16 bytes each) are 1 KB, no swizzle
+      const uint64_t bd0 = smem_desc(smem_u32(smem + lay.p), 1024u, 128u, kSwizzleNone);
       const int codes = min(g.R - c * g.nch * 64, g.nch * 64);      // codes of R of this CTA
       AWalk walk(g, tab, x0, x1);
       ASeg x;
@@ -1578,8 +1595,7 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         uint32_t on = 0;
         for (int b = x.b0; b < x.b1 && ok; ++b) {
           const int nt = min(kGATok, x.en.len - b * kGATok);
-          if (!mbar_wait_cluster(&pfull[pb.s], pb.u & 1) || abort_flag) { ok = false; break; }
-          fence_proxy_async_all();
+          if (!mbar_wait(&pfull[pb.s], pb.u & 1) || abort_flag) { ok = false; break; }
           const uint64_t bp = bd0 + static_cast<uint32_t>(pb.s) * (kGACols * 8u);
           for (int t = 0; t < nt; t += kGAVTok) {
             if (!mbar_wait(&vfull[k.s], k.u & 1) || !mbar_wait(&vfix[k.s], k.u & 1) || abort_flag) { ok = false; break; }
@@ -1588,7 +1604,7 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 #pragma unroll
             for (int pg = 0; pg < 2; ++pg)
               if (t + pg * kBlock < nt) {
-                const uint64_t a = av + static_cast<uint32_t>(pg * g.nch) * 128u, bb = bp + (t >> 3) + pg * 2;
+                const uint64_t a = av + static_cast<uint32_t>(pg * g.nch) * 128u, bb = bp + static_cast<uint32_t>(t + pg * kBlock) * 8u;
                 umma_f16_ss(taddr, a, bb, idesc, on);
                 if (codes > 128) umma_f16_ss(taddr + 64u, a + 256u, bb, idesc, on);
                 on = 1;
@@ -1632,9 +1648,8 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     ASeg x;
     const int code0 = c * g.nch * 64, codes = min(g.R - code0, g.nch * 64);
     while (ok && walk.next(&x)) {
-      const int tend = min(x.en.len, x.b1 * kGATok), plast = (tend + p.part - 1) / p.part;
-      for (int gp = x.b0 * ppb; gp < plast && ok; ++gp) {
-        if (gp % C != c) continue;
+      const int tend = min(x.en.len, x.b1 * kGATok);
+      for (int gp = first_own(x.b0 * ppb, c, C); gp * p.part < tend && ok; gp += C) {
         if (!__all_sync(0xffffffffu, ls.u == 0 || mbar_wait(&lempty[ls.s], (ls.u - 1) & 1))) { ok = false; break; }
         float* out = s_ls + static_cast<uint32_t>(ls.s) * lslot;
         for (int t = 0; t < p.part; t += p.utok) {
@@ -1724,37 +1739,44 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     while (ok && walk.next(&x)) {
       const int len = x.en.len;
       float ref = 0.f, ref_o = 0.f, l = 0.f;
+      int os = first_own(x.b0 * ppb, c, C), ow = os;   // next own part to take maxima, weights of
       // the maxima of the CTA's own parts of block b, to every CTA
       auto send = [&](int b) {
-        for (int pi = 0; pi < ppb; ++pi) {
-          const int gp = b * ppb + pi;
-          if (gp % C != c) continue;
-          const int t0 = gp * p.part;
-          const bool live = t0 < len;
-          const bool mine = live ? static_cast<int>(nr & 1) == team : team == 0;
-          if (mine) {
+        const int g0 = b * ppb, live = min(ppb, (len - g0 * p.part + p.part - 1) >> p.log2part);
+        uint32_t others = live;   // live parts of other CTAs
+        for (; os < g0 + live; os += C) {
+          const int pi = os - g0, t0 = os * p.part;
+          --others;
+          if (static_cast<int>(nr & 1) == team) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&lfull[lr.s], lr.u & 1) && !abort_flag)) return false;
+            const float* src = s_ls + static_cast<uint32_t>(lr.s) * lslot + col;
+            const int n = min(p.part, len - t0);
             float m = -INFINITY;
-            if (live) {
-              if (!__all_sync(0xffffffffu, mbar_wait(&lfull[lr.s], lr.u & 1) && !abort_flag)) return false;
-              const float* src = s_ls + static_cast<uint32_t>(lr.s) * lslot + col;
-              const int n = min(p.part, len - t0);
-              if (col < x.ncols) {
-                if (n == kBlock) {
+            if (col < x.ncols) {
+              if (n == kBlock) {
 #pragma unroll
-                  for (int t = 0; t < kBlock; ++t) m = fmaxf(m, src[t * p.lstride]);
-                } else {
-                  for (int t = 0; t < n; ++t) m = fmaxf(m, src[t * p.lstride]);
-                }
+                for (int t = 0; t < kBlock; ++t) m = fmaxf(m, src[t * p.lstride]);
+              } else {
+                for (int t = 0; t < n; ++t) m = fmaxf(m, src[t * p.lstride]);
               }
             }
             float* at = s_mx + (ms.s * 4 + pi) * kGACols + col;
-            if (C == 1) *at = m;
-            else
-              for (int o = 0; o < C; ++o) st_cluster(map_cluster(at, static_cast<uint32_t>(o)), m);
-            __syncwarp();
-            if (lane < C) mbar_arrive_cluster(&mfull[ms.s], static_cast<uint32_t>(lane));
+            *at = m;
+            if (C > 1) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0)
+                for (int o = 1; o < C; ++o)
+                  bulk_s2cluster(at, static_cast<uint32_t>(c + o < C ? c + o : c + o - C), 128u, &mfull[ms.s]);
+            }
           }
-          if (live) { ++nr; lr.next(LS); }
+          ++nr;
+          lr.next(LS);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          if (warp == 8) mbar_arrive_expect_tx(&mfull[ms.s], others * 256u);
+          else mbar_arrive(&mfull[ms.s]);
         }
         ms.next(kGAMSlots);
         return true;
@@ -1764,9 +1786,7 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         RingPos r = lr;
         uint32_t n = nr;
         bool yes = true;
-        for (int pi = 0; pi < ppb; ++pi) {
-          const int gp = b * ppb + pi;
-          if (gp % C != c || gp * p.part >= len) continue;
+        for (int gp = os; gp < (b + 1) * ppb && gp * p.part < len; gp += C) {
           if (static_cast<int>(n & 1) == team) yes = yes && mbar_try_wait(&lfull[r.s], r.u & 1);
           ++n;
           r.next(LS);
@@ -1781,15 +1801,16 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           sent = true;
           if (!send(b + 1)) { ok = false; break; }
         }
-        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&mfull[mb.s], mb.u & 1) && !abort_flag)) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, mbar_wait(&mfull[mb.s], mb.u & 1) && !abort_flag)) { ok = false; break; }
         float bm = -INFINITY, bo = -INFINITY;
-        for (int pi = 0; pi < ppb; ++pi) {
+        const int nlive = min(ppb, (len - b * kGATok + p.part - 1) >> p.log2part);
+        for (int pi = 0; pi < nlive; ++pi) {
           bm = fmaxf(bm, s_mx[(mb.s * 4 + pi) * kGACols + col]);
           bo = fmaxf(bo, s_mx[(mb.s * 4 + pi) * kGACols + oth]);
         }
         mb.next(kGAMSlots);
         // the slot's earlier weights have been consumed by every CTA
-        if (pb.u > 0 && !__all_sync(0xffffffffu, mbar_wait_cluster(&pempty[pb.s], (pb.u - 1) & 1) && !abort_flag)) { ok = false; break; }
+        if (pb.u > 0 && !__all_sync(0xffffffffu, mbar_wait(&pempty[pb.s], (pb.u - 1) & 1) && !abort_flag)) { ok = false; break; }
         if (b == x.b0) {
           ref = bm;
           ref_o = bo;
@@ -1824,47 +1845,55 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             if (!group_sync(bbar, phase)) { ok = false; break; }
           }
         }
-        if (et == 0) mbar_arrive(&pfull[pb.s]);
-        uint8_t* pbase = smem + lay.p + static_cast<uint32_t>(pb.s) * (kGACols * 128u) + col * 128;
-        for (int pi = 0; pi < ppb; ++pi) {
-          const int gp = b * ppb + pi;
-          if (gp % C != c) continue;
-          const int t0 = gp * p.part;
-          const bool live = t0 < len;
-          const bool mine = live ? static_cast<int>(nw & 1) == team : team == 0;
-          if (mine) {
-            if (live) {
-              const float* src = s_ls + static_cast<uint32_t>(lw.s) * lslot + col;
-              const float base = ref > -INFINITY ? ref : 0.f;   // a column whose logits are all -inf so far
-              for (int t8 = 0; t8 < p.part; t8 += 8) {
-                // weights of eight tokens, rounded to fp16 for the products; the sum takes the rounded weights
-                uint4 w4;
-                uint32_t* w = reinterpret_cast<uint32_t*>(&w4);
+        uint8_t* pbase = smem + lay.p + static_cast<uint32_t>(pb.s) * (kGACols * 128u) + col * 16;
+        const float base = ref > -INFINITY ? ref : 0.f;   // a column whose logits are all -inf so far
+        const int g0 = b * ppb, live = min(ppb, (len - g0 * p.part + p.part - 1) >> p.log2part);
+        uint32_t others = live;
+        for (; ow < g0 + live; ow += C) {
+          const int pi = ow - g0, t0 = ow * p.part;
+          --others;
+          if (static_cast<int>(nw & 1) == team) {
+            const float* src = s_ls + static_cast<uint32_t>(lw.s) * lslot + col;
+            for (int t8 = 0; t8 < p.part; t8 += 8, src += 8 * p.lstride) {
+              // weights of eight tokens, rounded to fp16 for the products; the sum takes the rounded weights
+              float e[8];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                  const int t = t8 + 2 * u;
-                  const float a = t0 + t < len ? ex2_approx(src[t * p.lstride] - base) : 0.f;
-                  const float b2 = t0 + t + 1 < len ? ex2_approx(src[(t + 1) * p.lstride] - base) : 0.f;
-                  const __half2 h = __floats2half2_rn(a, b2);
-                  const float2 hf = __half22float2(h);
-                  l += hf.x;
-                  l += hf.y;
-                  w[u] = *reinterpret_cast<const uint32_t*>(&h);
-                }
-                uint8_t* at = pbase + ((static_cast<uint32_t>((pi * p.part + t8) >> 3) ^ (static_cast<uint32_t>(col) & 7u)) << 4);
-                if (col < x.ncols) {
-                  if (C == 1) *reinterpret_cast<uint4*>(at) = w4;
-                  else
-                    for (int o = 0; o < C; ++o) st_cluster(map_cluster(at, static_cast<uint32_t>(o)), w4);
-                }
+              for (int u = 0; u < 8; ++u) e[u] = ex2_approx(src[u * p.lstride] - base);
+              if (t0 + t8 + 8 > len) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                  if (t0 + t8 + u >= len) e[u] = 0.f;
+              }
+              uint4 w4;
+              uint32_t* w = reinterpret_cast<uint32_t*>(&w4);
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const __half2 h = __floats2half2_rn(e[2 * u], e[2 * u + 1]);
+                const float2 hf = __half22float2(h);
+                l += hf.x;
+                l += hf.y;
+                w[u] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              *reinterpret_cast<uint4*>(pbase + ((pi * p.part + t8) >> 3) * 1024) = w4;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&lempty[lw.s]);
+              for (int o = 1; o < C; ++o) {
+                const uint32_t to = static_cast<uint32_t>(c + o < C ? c + o : c + o - C);
+                for (int t8 = 0; t8 < p.part; t8 += 8)
+                  bulk_s2cluster(pbase + ((pi * p.part + t8) >> 3) * 1024, to, 512u, &pfull[pb.s]);
               }
             }
-            fence_proxy_async_all();
-            __syncwarp();
-            if (lane == 0 && live) mbar_arrive(&lempty[lw.s]);
-            if (lane < C) mbar_arrive_cluster(&pfull[pb.s], static_cast<uint32_t>(lane));
           }
-          if (live) { ++nw; lw.next(LS); }
+          ++nw;
+          lw.next(LS);
+        }
+        __syncwarp();
+        if (lane == 0) {   // also this CTA's go-ahead: its accumulator holds the scale of these weights
+          if (warp == 8) mbar_arrive_expect_tx(&pfull[pb.s], others * static_cast<uint32_t>(p.part) * 128u);
+          else mbar_arrive(&pfull[pb.s]);
         }
         pb.next(kGAPSlots);
         if (!sent && !send(b + 1)) { ok = false; break; }

@@ -209,48 +209,24 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
-// Shared-memory address of CTA `rank` of the cluster that corresponds to `p` here.
-__device__ __forceinline__ uint32_t map_cluster(const void* p, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-__device__ __forceinline__ void st_cluster(uint32_t addr, uint4 v) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+// `bytes` of this CTA's shared memory to the same offset in CTA `rank` of the
+// cluster, counted on the barrier at `bar`'s offset there (16-byte multiples).
+// One lane of a warp at a time: the operands are warp-uniform in hardware.
+__device__ __forceinline__ void bulk_s2cluster(const void* src, uint32_t rank, uint32_t bytes, uint64_t* bar) {
+  const uint32_t s = smem_u32(src), b = smem_u32(bar);
+  uint32_t rs, rb;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rs) : "r"(s), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rb) : "r"(b), "r"(rank));
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(rs),
+               "r"(s), "r"(bytes), "r"(rb)
                : "memory");
 }
-// Arrival on the barrier at `bar`'s offset in CTA `rank` of the cluster (this CTA
-// included); releases the thread's earlier writes to the cluster.
+// Arrival on the barrier at `bar`'s offset in CTA `rank` of the cluster (this CTA included).
 __device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_cluster(bar, rank)) : "memory");
+  uint32_t rb;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rb) : "r"(smem_u32(bar)), "r"(rank));
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(rb) : "memory");
 }
-// mbar_wait that acquires what other CTAs of the cluster released.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(kWaitSleepNs)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  const uint64_t limit = *const_cast<const volatile uint64_t*>(&g_wait_limit_ns);
-  for (uint32_t i = 0; i < kWaitLimitPolls; ++i) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((i & 7u) == 7u && globaltimer_ns() - t0 > limit) return false;
-  }
-  return false;
-}
-// Generic-proxy writes to any shared memory of the cluster become visible to the async proxy.
-__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // Generic-proxy writes to shared memory become visible to the async proxy
 // (TMA engine, tensor cores) after this fence.

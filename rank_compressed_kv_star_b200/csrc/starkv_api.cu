@@ -1835,7 +1835,9 @@ starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_g
     fp.mcarry = tp.mcarry;
     fp.lcarry = tp.lcarry;
     tp.kb = pl.kb; tp.ksteps = pl.ksteps; tp.log2Hkv = pl.log2Hkv;
-    tp.utok = pl.at_utok; tp.part = pl.at_part; tp.lstride = pl.at_lstride; tp.lslots = pl.at_lslots;
+    tp.utok = pl.at_utok; tp.part = pl.at_part;
+    while ((1 << tp.log2part) < tp.part) ++tp.log2part;
+    tp.lstride = pl.at_lstride; tp.lslots = pl.at_lslots;
     tp.k_stages = pl.at_k_stages; tp.v_stages = pl.at_v_stages; tp.v_stage_bytes = pl.at_v_stage; tp.q_bytes = pl.at_q_bytes;
     if (!set_smem(group_attend_kernel, pl.at_smem)) return STARKV_ERR_CUDA;
     if (launch(group_attend_kernel, dim3(pl.at_clusters, g.C), dim3(kGAThreads), pl.at_smem, s, g.C, kmap, vmap, qh, ql, tp) !=
