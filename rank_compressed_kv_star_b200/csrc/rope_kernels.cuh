@@ -198,4 +198,178 @@ rope_append_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
   if (it < p.q_items) rope_q_item(p, it);
 }
 
+// ------------------------------------------------------------ many rows
+// A prompt's rows: the V-code tiles and the rotated keys' codes are two launches,
+// the second beside the first (it waits for the first only at its end).  A block
+// of the second is one KV head's 128 rows, on tcgen05:
+//   D (128 rows x r) = k' (128 x d) . A_K[h] (d x r),
+// the rotated rows written to shared memory as fp16 hi + lo halves (22 bits, so the
+// code still rounds once) in the K-major operand layout, A_K[h] by TMA boxes of 64
+// ranks x 64 rows (MN-major); or it rotates a run of query units.
+struct RopeRowsParams {
+  RopeTable rope;
+  AppendKParams k;
+  const __half* q;         // [n][H][d] or null
+  __half* q_out;
+  int n, H, d;
+  int k_tiles;             // row tiles of 128
+  int kc, nc;              // 64-element chunks of d, 64-rank chunks of r
+  int b_slots;             // chunks of A_K[h] in shared memory at a time
+  uint32_t tmem_cols;
+};
+
+__global__ void __launch_bounds__(kPrepThreads)
+rope_rows_kernel(const __grid_constant__ CUtensorMap akmap, RopeRowsParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int k_blocks = p.k_tiles * p.k.H;
+  if (static_cast<int>(blockIdx.x) >= k_blocks) {
+    RopeParams rp{};
+    rp.rope = p.rope;
+    rp.q = p.q;
+    rp.q_out = p.q_out;
+    rp.n = p.n; rp.H = p.H; rp.d = p.d;
+    rope_q_item(rp, blockIdx.x - k_blocks);
+    griddep_wait();
+    return;
+  }
+  uint8_t* smem = align_smem_1024(smem_raw);
+  const uint32_t a_chunk = 128u * 128u, b_chunk = static_cast<uint32_t>(p.nc) * 8192u;
+  uint8_t* a_hi = smem;
+  uint8_t* a_lo = a_hi + p.kc * a_chunk;
+  uint8_t* bsm = a_lo + p.kc * a_chunk;
+  __shared__ uint64_t bfull[4], bfree[4], done;
+  __shared__ uint32_t taddr_s, failed;
+  const AppendKParams& kp = p.k;
+  const int h = blockIdx.x % kp.H, b0 = (blockIdx.x / kp.H) * 128;
+  const int nb = min(128, kp.B - b0), d = kp.d, r = kp.r;
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) { mbar_init(&bfull[i], 1); mbar_init(&bfree[i], 1); }
+    mbar_init(&done, 1);
+    failed = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&akmap);
+  }
+  if (warp == 0) {
+    tmem_alloc(&taddr_s, p.tmem_cols);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t taddr = taddr_s;
+  auto load_b = [&](int c) {
+    const int s = c % p.b_slots;
+    mbar_arrive_expect_tx(&bfull[s], b_chunk);
+    for (int x = 0; x < p.nc; ++x)
+      tma_load_2d(bsm + s * b_chunk + x * 8192, &akmap, x * 64, h * d + c * 64, &bfull[s], policy_evict_last());
+  };
+  if (tid == 0)
+    for (int c = 0; c < p.kc && c < p.b_slots; ++c) load_b(c);
+  // the rotated rows; rows past the end and rows that will be skipped are zeros
+  const int upr = rope_units(d, p.rope.rot, p.rope.interleaved);
+  for (int x = tid; x < 128 * upr; x += kPrepThreads) {
+    const int b = x / upr;
+    const float* cs = b < nb ? rope_row(p.rope, p.rope.positions[b0 + b]) : nullptr;
+    auto put = [&](int o, const float (&y)[8]) {
+      float lo[8];
+      uint4 hv;
+      uint32_t* hw = reinterpret_cast<uint32_t*>(&hv);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float e = 0.5f * y[2 * u], o2 = 0.5f * y[2 * u + 1];   // a rotation grows a value by up to sqrt(2)
+        const __half2 hh = __floats2half2_rn(e, o2);
+        const float2 f = __half22float2(hh);
+        lo[2 * u] = isinf(f.x) ? 0.f : e - f.x;
+        lo[2 * u + 1] = isinf(f.y) ? 0.f : o2 - f.y;
+        hw[u] = *reinterpret_cast<const uint32_t*>(&hh);
+      }
+      const uint32_t at = static_cast<uint32_t>(o >> 6) * a_chunk + b * 128u + ((((o & 63) >> 3) ^ (b & 7)) << 4);
+      *reinterpret_cast<uint4*>(a_hi + at) = hv;
+      *reinterpret_cast<uint4*>(a_lo + at) = pack8(lo);
+    };
+    if (cs) {
+      rope_unit(kp.k + (static_cast<size_t>(b0 + b) * kp.H + h) * d, cs, p.rope.rot, p.rope.interleaved, x % upr, put);
+    } else {
+      const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      const int u = x % upr, pairs = p.rope.interleaved ? 0 : p.rope.rot / 16;
+      if (u < pairs) { put(8 * u, zero); put(p.rope.rot / 2 + 8 * u, zero); }
+      else put(p.rope.interleaved ? 8 * u : p.rope.rot + 8 * (u - pairs), zero);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncthreads();
+  if (tid == 0) {
+    const uint32_t idesc = idesc_f16_f32(128, r, /*a_mn_major=*/false, /*b_mn_major=*/true);
+    uint32_t on = 0;
+    for (int c = 0; c < p.kc; ++c) {
+      const int s = c % p.b_slots;
+      if (!mbar_wait(&bfull[s], (c / p.b_slots) & 1)) {
+        failed = 1;   // this chunk's copies, and those of the chunks after it, may still land
+        for (int e = c; e < p.kc && e < c + p.b_slots; ++e) mbar_wait(&bfull[e % p.b_slots], (e / p.b_slots) & 1);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t sh = smem_u32(a_hi + c * a_chunk), sl = smem_u32(a_lo + c * a_chunk), sb = smem_u32(bsm + s * b_chunk);
+      for (int kk = 0; kk < min(64, d - c * 64) / 16; ++kk) {
+        const uint64_t bd = smem_desc(sb + kk * 2048u, 8192u, 1024u, kSwizzle128B);
+        umma_f16_ss(taddr, smem_desc(sh + kk * 32u, 16u, 1024u, kSwizzle128B), bd, idesc, on);
+        umma_f16_ss(taddr, smem_desc(sl + kk * 32u, 16u, 1024u, kSwizzle128B), bd, idesc, 1u);
+        on = 1;
+      }
+      umma_commit(&bfree[s]);
+      if (c + p.b_slots < p.kc) {
+        if (!mbar_wait(&bfree[s], (c / p.b_slots) & 1)) {
+          failed = 1;
+          for (int e = c + 1; e < c + p.b_slots; ++e) mbar_wait(&bfull[e % p.b_slots], (e / p.b_slots) & 1);
+          break;
+        }
+        load_b(c + p.b_slots);
+      }
+    }
+    umma_commit(&done);
+  }
+  // codes of row 32 (warp % 4) + lane; warps 4..7 take the upper half of the ranks
+  __syncwarp();
+  const bool landed = mbar_wait(&done, 0) && !*static_cast<volatile uint32_t*>(&failed);
+  if (__all_sync(0xffffffffu, landed)) {
+    tc_fence_after();
+    const int b = (warp & 3) * 32 + lane;
+    const int64_t row = b < nb ? append_row(kp.tgt, b0 + b) : -1;
+    if (b < nb && row < 0 && h == 0 && warp < 4) append_skipped(kp.tgt, row);
+    __half* out = kp.k_cache + (row < 0 ? 0 : (row * kp.H + h) * r);
+    for (int c0 = (warp >> 2) * 16; c0 < r; c0 += 32) {
+      __syncwarp();
+      uint32_t v[32];
+      tmem_ld_32x32b_x16(taddr + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0, v);
+      tmem_ld_wait();
+      if (row >= 0) {
+        float y[8];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) y[u] = 2.f * __uint_as_float(v[8 * g + u]);
+          *reinterpret_cast<uint4*>(out + c0 + 8 * g) = pack8(y);
+        }
+      }
+    }
+    tc_fence_before();
+  } else if (lane == 0) {
+    append_skipped(kp.tgt, -STARKV_FLAG_TIMEOUT);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(taddr, p.tmem_cols);
+  }
+  griddep_wait();   // this grid ends after the V-code tiles launched before it
+}
+
+// The V-code tiles of a prompt's rows (see append_v_tile).
+__global__ void __launch_bounds__(kPrepThreads, 1)
+rope_vrows_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap vmap, AppendVParams p, int v_mt) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  append_v_tile(&amap, &vmap, p, blockIdx.x % v_mt, blockIdx.y, gridDim.y, blockIdx.x / v_mt, align_smem_1024(smem_raw));
+}
+
 }  // namespace starkv

@@ -61,6 +61,9 @@
 #ifndef STARKV_ATTEND_BLOCKS
 #define STARKV_ATTEND_BLOCKS 24   // attend form of the group calls: at most so many blocks per cluster
 #endif
+#ifndef STARKV_ROPE_ROWS
+#define STARKV_ROPE_ROWS 128     // rotary append: from so many rows on, the keys' codes on tensor cores
+#endif
 #ifndef STARKV_V_RING_BYTES
 #define STARKV_V_RING_BYTES (105 * 1024)
 #endif
@@ -1452,6 +1455,35 @@ starkv_status rope_impl(const starkv_layer_desc* desc, const starkv_rope* rope, 
   rp.n = n;
   rp.H = desc->num_heads;
   rp.d = desc->head_dim;
+  if (n >= STARKV_ROPE_ROWS) {
+    // many rows: V-code tiles, and beside them the rotated keys' codes and the queries
+    const size_t v_smem = ap.v_smem + 1024;
+    if (!set_smem(rope_vrows_kernel, v_smem)) return STARKV_ERR_CUDA;
+    if (launch(rope_vrows_kernel, dim3(ap.v_cols, ap.KS), dim3(kPrepThreads), v_smem, static_cast<cudaStream_t>(stream), ap.KS,
+               ap.amap, ap.vmap, ap.vp, ap.v_mt) != cudaSuccess)
+      return STARKV_ERR_CUDA;
+    RopeRowsParams pr{};
+    pr.rope = rp.rope;
+    pr.k = ap.kp;
+    pr.q = rp.q; pr.q_out = rp.q_out;
+    pr.n = n; pr.H = rp.H; pr.d = rp.d;
+    pr.k_tiles = (n + 127) / 128;
+    pr.kc = (rp.d + 63) / 64;
+    pr.nc = (ap.kp.r + 63) / 64;
+    const size_t a_bytes = static_cast<size_t>(pr.kc) * 2 * 16384, b_chunk = static_cast<size_t>(pr.nc) * 8192;
+    pr.b_slots = pr.kc;
+    while (pr.b_slots > 1 && a_bytes + pr.b_slots * b_chunk > 200 * 1024) --pr.b_slots;
+    pr.tmem_cols = static_cast<uint32_t>(pow2_ceil(ap.kp.r < 32 ? 32 : ap.kp.r));
+    CUtensorMap akmap;
+    if (!encode_2d_map(&akmap, A_K, static_cast<uint64_t>(ap.kp.r), static_cast<uint64_t>(ap.kp.H) * rp.d, 64, 64))
+      return STARKV_ERR_CUDA;
+    const int64_t units = static_cast<int64_t>(n) * rp.H * rope_units(rp.d, rp.rope.rot, rp.rope.interleaved);
+    const int q_blocks = q ? static_cast<int>((units + kRopeQUnits - 1) / kRopeQUnits) : 0;
+    const size_t smem = 1024 + a_bytes + pr.b_slots * b_chunk;
+    if (!set_smem(rope_rows_kernel, smem)) return STARKV_ERR_CUDA;
+    return launch(rope_rows_kernel, dim3(pr.k_tiles * pr.k.H + q_blocks), dim3(kPrepThreads), smem,
+                  static_cast<cudaStream_t>(stream), 1, akmap, pr) == cudaSuccess ? STARKV_OK : STARKV_ERR_CUDA;
+  }
   const int KS = ap.KS;
   rp.k.tile = kRopeKB;
   rp.v_mt = ap.v_mt;
