@@ -29,8 +29,7 @@ __device__ __forceinline__ const float* rope_row(const RopeTable& t, int32_t p) 
   return p < 0 || p >= t.max_position ? nullptr : t.cos_sin + static_cast<size_t>(p) * t.rot;
 }
 
-__device__ __forceinline__ void load8(const __half* p, float (&x)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void widen8(const uint4& v, float (&x)[8]) {
   const __half2* h = reinterpret_cast<const __half2*>(&v);
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
@@ -46,48 +45,72 @@ __host__ __device__ __forceinline__ int rope_units(int d, int rot, int interleav
   return interleaved ? d / 8 : rot / 16 + (d - rot) / 8;
 }
 
-// Unit u of the head at `x`: emit(first element, eight rotated values) per run.
-template <typename Emit>
-__device__ __forceinline__ void rope_unit(const __half* x, const float* cs, int rot, int interleaved, int u, Emit&& emit) {
-  float a[8], b[8];
-  if (interleaved) {
-    load8(x + 8 * u, a);
-    if (8 * u < rot) {
-      const float4 c = *reinterpret_cast<const float4*>(cs + 4 * u);
-      const float4 s = *reinterpret_cast<const float4*>(cs + rot / 2 + 4 * u);
-      const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+// Unit u of the head at `x`, in two parts, so that a thread has the loads of several
+// units in flight: load, then finish, which calls emit(first element, eight rotated
+// values) per run.
+struct RopeUnit {
+  int a, b;           // first elements of the runs; b = -1: one run
+  bool turned;
+  uint4 xa, xb;
+  float c[8], s[8];
+
+  __device__ __forceinline__ void load(const __half* x, const float* cs, int rot, int interleaved, int u) {
+    const int pairs = interleaved ? 0 : rot / 16;
+    a = interleaved || u < pairs ? 8 * u : rot + 8 * (u - pairs);
+    b = u < pairs ? rot / 2 + 8 * u : -1;
+    turned = a < rot;
+    xa = *reinterpret_cast<const uint4*>(x + a);
+    if (b >= 0) xb = *reinterpret_cast<const uint4*>(x + b);
+    if (turned) {
+      const float* ct = cs + (interleaved ? 4 * u : 8 * u);
+      *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(ct);
+      *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(ct + rot / 2);
+      if (!interleaved) {
+        *reinterpret_cast<float4*>(c + 4) = *reinterpret_cast<const float4*>(ct + 4);
+        *reinterpret_cast<float4*>(s + 4) = *reinterpret_cast<const float4*>(ct + rot / 2 + 4);
+      }
+    }
+  }
+
+  // a unit of a row that is skipped: zeros
+  __device__ __forceinline__ void zero(int rot, int interleaved, int u) {
+    const int pairs = interleaved ? 0 : rot / 16;
+    a = interleaved || u < pairs ? 8 * u : rot + 8 * (u - pairs);
+    b = u < pairs ? rot / 2 + 8 * u : -1;
+    turned = false;
+    xa = xb = make_uint4(0, 0, 0, 0);
+  }
+
+  template <typename Emit>
+  __device__ __forceinline__ void finish(Emit&& emit) const {
+    float va[8], y[8];
+    widen8(xa, va);
+    if (b >= 0) {
+      float vb[8];
+      widen8(xb, vb);
+      if (!turned) {
+        emit(a, va);
+        emit(b, vb);
+        return;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = va[i] * c[i] - vb[i] * s[i];
+      emit(a, y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = vb[i] * c[i] + va[i] * s[i];
+      emit(b, y);
+    } else if (turned) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        b[2 * i] = a[2 * i] * cc[i] - a[2 * i + 1] * ss[i];
-        b[2 * i + 1] = a[2 * i + 1] * cc[i] + a[2 * i] * ss[i];
+        y[2 * i] = va[2 * i] * c[i] - va[2 * i + 1] * s[i];
+        y[2 * i + 1] = va[2 * i + 1] * c[i] + va[2 * i] * s[i];
       }
-      emit(8 * u, b);
+      emit(a, y);
     } else {
-      emit(8 * u, a);
+      emit(a, va);
     }
-    return;
   }
-  const int pairs = rot / 16;
-  if (u >= pairs) {
-    const int o = rot + 8 * (u - pairs);
-    load8(x + o, a);
-    emit(o, a);
-    return;
-  }
-  load8(x + 8 * u, a);
-  load8(x + rot / 2 + 8 * u, b);
-  float c[8], s[8], y[8];
-  *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(cs + 8 * u);
-  *reinterpret_cast<float4*>(c + 4) = *reinterpret_cast<const float4*>(cs + 8 * u + 4);
-  *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(cs + rot / 2 + 8 * u);
-  *reinterpret_cast<float4*>(s + 4) = *reinterpret_cast<const float4*>(cs + rot / 2 + 8 * u + 4);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = a[i] * c[i] - b[i] * s[i];
-  emit(8 * u, y);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = b[i] * c[i] + a[i] * s[i];
-  emit(rot / 2 + 8 * u, y);
-}
+};
 
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   uint4 v;
@@ -98,6 +121,36 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
     w[u] = *reinterpret_cast<const uint32_t*>(&h);
   }
   return v;
+}
+
+#ifndef STARKV_ROPE_QB
+#define STARKV_ROPE_QB 2
+#endif
+constexpr int kRopeBatch = STARKV_ROPE_QB;   // query units of a thread in flight
+
+// Rotation units x0, x0 + step, ... (kRopeBatch of them) of the queries: all loads
+// before the stores, which may be to the same rows.
+__device__ __forceinline__ void rope_q_units(const RopeTable& t, const __half* q, __half* q_out, int H, int d, int upr,
+                                             int64_t total, int64_t x0, int64_t step) {
+  RopeUnit w[kRopeBatch];
+  int32_t pos[kRopeBatch];
+  const __half* at[kRopeBatch];
+#pragma unroll
+  for (int i = 0; i < kRopeBatch; ++i) {
+    const int64_t x = x0 + i * step;
+    pos[i] = x < total ? t.positions[x / upr / H] : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < kRopeBatch; ++i) {
+    const int64_t x = x0 + i * step, hd = x / upr;
+    const float* cs = rope_row(t, pos[i]);
+    at[i] = cs ? q + hd * d : nullptr;
+    if (cs) w[i].load(at[i], cs, t.rot, t.interleaved, static_cast<int>(x - hd * upr));
+  }
+#pragma unroll
+  for (int i = 0; i < kRopeBatch; ++i)
+    if (at[i])
+      w[i].finish([&](int o, const float (&v)[8]) { *reinterpret_cast<uint4*>(q_out + (at[i] - q) + o) = pack8(v); });
 }
 
 struct RopeParams {
@@ -113,7 +166,8 @@ struct RopeParams {
 };
 
 constexpr int kRopeKB = 32;                       // rows per K-code item
-constexpr int kRopeQUnits = kPrepThreads * 4;     // rotation units per query item
+constexpr int kRopeQUnits = kPrepThreads * kRopeBatch;
+constexpr int kRopeKBatch = 4;                    // key units of a thread in flight     // rotation units per query item
 
 // One K-code item: KV head h, rows [b0, b0 + tile).  The rotated rows stand in
 // shared memory as fp32 beside A_K[h].
@@ -130,31 +184,47 @@ __device__ __forceinline__ void rope_k_item(const RopeParams& p, int h, int b0, 
     const int b = x / upr;
     const float* cs = rope_row(p.rope, p.rope.positions[b0 + b]);
     if (!cs) continue;   // the row is skipped when its code is stored
-    rope_unit(kp.k + (static_cast<size_t>(b0 + b) * kp.H + h) * d, cs, p.rope.rot, p.rope.interleaved, x % upr,
-              [&](int o, const float (&y)[8]) {
-                float4* dst = reinterpret_cast<float4*>(xs + static_cast<size_t>(b) * d + o);
-                dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-                dst[1] = make_float4(y[4], y[5], y[6], y[7]);
-              });
+    RopeUnit w;
+    w.load(kp.k + (static_cast<size_t>(b0 + b) * kp.H + h) * d, cs, p.rope.rot, p.rope.interleaved, x % upr);
+    w.finish([&](int o, const float (&y)[8]) {
+      float4* dst = reinterpret_cast<float4*>(xs + static_cast<size_t>(b) * d + o);
+      dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+      dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+    });
   }
   __syncthreads();
   const int np = r >> 1, nbl = kPrepThreads / np;
   const int c = tid % np, bl = tid / np;
   if (bl >= nbl) return;
-  for (int b = bl; b < nb; b += nbl) {
-    float2 acc = make_float2(0.f, 0.f);
-    for (int j = 0; j < d; j += 4) {
-      const float4 xv = *reinterpret_cast<const float4*>(xs + static_cast<size_t>(b) * d + j);
-      const float x4[4] = {xv.x, xv.y, xv.z, xv.w};
+  // four rows per thread and pass: a weight is read and widened once for them
+  for (int b0t = bl; b0t < nb; b0t += 4 * nbl) {
+    float2 acc[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        acc = ffma2(make_float2(x4[u], x4[u]),
-                    __half22float2(*reinterpret_cast<const __half2*>(As + static_cast<size_t>(j + u) * r + 2 * c)), acc);
+    for (int s = 0; s < 4; ++s) acc[s] = make_float2(0.f, 0.f);
+    for (int j = 0; j < d; j += 4) {
+      float2 w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) w[u] = __half22float2(*reinterpret_cast<const __half2*>(As + static_cast<size_t>(j + u) * r + 2 * c));
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (b0t + s * nbl < nb) {
+          const float4 xv = *reinterpret_cast<const float4*>(xs + static_cast<size_t>(b0t + s * nbl) * d + j);
+          acc[s] = ffma2(make_float2(xv.x, xv.x), w[0], acc[s]);
+          acc[s] = ffma2(make_float2(xv.y, xv.y), w[1], acc[s]);
+          acc[s] = ffma2(make_float2(xv.z, xv.z), w[2], acc[s]);
+          acc[s] = ffma2(make_float2(xv.w, xv.w), w[3], acc[s]);
+        }
+      }
     }
-    const int64_t row = append_row(kp.tgt, b0 + b);
-    if (row >= 0)
-      *reinterpret_cast<__half2*>(kp.k_cache + (row * kp.H + h) * r + 2 * c) = __floats2half2_rn(acc.x, acc.y);
-    else if (h == 0 && c == 0) append_skipped(kp.tgt, row);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int b = b0t + s * nbl;
+      if (b >= nb) break;
+      const int64_t row = append_row(kp.tgt, b0 + b);
+      if (row >= 0)
+        *reinterpret_cast<__half2*>(kp.k_cache + (row * kp.H + h) * r + 2 * c) = __floats2half2_rn(acc[s].x, acc[s].y);
+      else if (h == 0 && c == 0) append_skipped(kp.tgt, row);
+    }
   }
 }
 
@@ -162,16 +232,8 @@ __device__ __forceinline__ void rope_k_item(const RopeParams& p, int h, int b0, 
 __device__ __forceinline__ void rope_q_item(const RopeParams& p, int item) {
   const int upr = rope_units(p.d, p.rope.rot, p.rope.interleaved);
   const int64_t total = static_cast<int64_t>(p.n) * p.H * upr;
-#pragma unroll
-  for (int i = 0; i < kRopeQUnits / kPrepThreads; ++i) {
-    const int64_t x = static_cast<int64_t>(item) * kRopeQUnits + i * kPrepThreads + threadIdx.x;
-    if (x >= total) return;
-    const int64_t hd = x / upr;
-    const float* cs = rope_row(p.rope, p.rope.positions[hd / p.H]);
-    if (!cs) continue;
-    rope_unit(p.q + hd * p.d, cs, p.rope.rot, p.rope.interleaved, static_cast<int>(x - hd * upr),
-              [&](int o, const float (&y)[8]) { *reinterpret_cast<uint4*>(p.q_out + hd * p.d + o) = pack8(y); });
-  }
+  rope_q_units(p.rope, p.q, p.q_out, p.H, p.d, upr, total, static_cast<int64_t>(item) * kRopeQUnits + threadIdx.x,
+               kPrepThreads);
 }
 
 // Grid columns: V-code tiles, K-code items, query items (clusters of KS along y).
@@ -199,40 +261,34 @@ rope_append_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
 }
 
 // ------------------------------------------------------------ many rows
-// A prompt's rows: the V-code tiles and the rotated keys' codes are two launches,
-// the second beside the first (it waits for the first only at its end).  A block
-// of the second is one KV head's 128 rows, on tcgen05:
+// A prompt's rows take three launches, the second and third beside the first (they
+// read nothing that it writes, start when its blocks have seen the work before it
+// end, and wait for it only at their end): V-code tiles, query units, key codes.
+#ifndef STARKV_ROPE_QO
+#define STARKV_ROPE_QO 3
+#endif
+__global__ void __launch_bounds__(kPrepThreads, STARKV_ROPE_QO) rope_q_kernel(RopeParams p) {
+  rope_q_item(p, blockIdx.x);
+  griddep_wait();
+}
+
+// Key codes: a block is one KV head's 128 rows, on tcgen05,
 //   D (128 rows x r) = k' (128 x d) . A_K[h] (d x r),
 // the rotated rows written to shared memory as fp16 hi + lo halves (22 bits, so the
 // code still rounds once) in the K-major operand layout, A_K[h] by TMA boxes of 64
-// ranks x 64 rows (MN-major); or it rotates a run of query units.
+// ranks x 64 rows (MN-major).
 struct RopeRowsParams {
   RopeTable rope;
   AppendKParams k;
-  const __half* q;         // [n][H][d] or null
-  __half* q_out;
-  int n, H, d;
-  int k_tiles;             // row tiles of 128
   int kc, nc;              // 64-element chunks of d, 64-rank chunks of r
   int b_slots;             // chunks of A_K[h] in shared memory at a time
   uint32_t tmem_cols;
 };
 
-__global__ void __launch_bounds__(kPrepThreads)
+__global__ void __launch_bounds__(kPrepThreads, 2)
 rope_rows_kernel(const __grid_constant__ CUtensorMap akmap, RopeRowsParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int k_blocks = p.k_tiles * p.k.H;
-  if (static_cast<int>(blockIdx.x) >= k_blocks) {
-    RopeParams rp{};
-    rp.rope = p.rope;
-    rp.q = p.q;
-    rp.q_out = p.q_out;
-    rp.n = p.n; rp.H = p.H; rp.d = p.d;
-    rope_q_item(rp, blockIdx.x - k_blocks);
-    griddep_wait();
-    return;
-  }
   uint8_t* smem = align_smem_1024(smem_raw);
   const uint32_t a_chunk = 128u * 128u, b_chunk = static_cast<uint32_t>(p.nc) * 8192u;
   uint8_t* a_hi = smem;
@@ -258,6 +314,7 @@ rope_rows_kernel(const __grid_constant__ CUtensorMap akmap, RopeRowsParams p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t taddr = taddr_s;
+  griddep_launch_dependents();
   auto load_b = [&](int c) {
     const int s = c % p.b_slots;
     mbar_arrive_expect_tx(&bfull[s], b_chunk);
@@ -266,35 +323,47 @@ rope_rows_kernel(const __grid_constant__ CUtensorMap akmap, RopeRowsParams p) {
   };
   if (tid == 0)
     for (int c = 0; c < p.kc && c < p.b_slots; ++c) load_b(c);
+  // the target of the row that this thread writes in the end, read early
+  const int wb = (warp & 3) * 32 + lane;
+  const int64_t row = wb < nb ? append_row(kp.tgt, b0 + wb) : -1;
   // the rotated rows; rows past the end and rows that will be skipped are zeros
   const int upr = rope_units(d, p.rope.rot, p.rope.interleaved);
-  for (int x = tid; x < 128 * upr; x += kPrepThreads) {
-    const int b = x / upr;
-    const float* cs = b < nb ? rope_row(p.rope, p.rope.positions[b0 + b]) : nullptr;
-    auto put = [&](int o, const float (&y)[8]) {
-      float lo[8];
-      uint4 hv;
-      uint32_t* hw = reinterpret_cast<uint32_t*>(&hv);
+  auto put = [&](int b, int o, const float (&y)[8]) {
+    float lo[8];
+    uint4 hv;
+    uint32_t* hw = reinterpret_cast<uint32_t*>(&hv);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float e = 0.5f * y[2 * u], o2 = 0.5f * y[2 * u + 1];   // a rotation grows a value by up to sqrt(2)
-        const __half2 hh = __floats2half2_rn(e, o2);
-        const float2 f = __half22float2(hh);
-        lo[2 * u] = isinf(f.x) ? 0.f : e - f.x;
-        lo[2 * u + 1] = isinf(f.y) ? 0.f : o2 - f.y;
-        hw[u] = *reinterpret_cast<const uint32_t*>(&hh);
-      }
-      const uint32_t at = static_cast<uint32_t>(o >> 6) * a_chunk + b * 128u + ((((o & 63) >> 3) ^ (b & 7)) << 4);
-      *reinterpret_cast<uint4*>(a_hi + at) = hv;
-      *reinterpret_cast<uint4*>(a_lo + at) = pack8(lo);
-    };
-    if (cs) {
-      rope_unit(kp.k + (static_cast<size_t>(b0 + b) * kp.H + h) * d, cs, p.rope.rot, p.rope.interleaved, x % upr, put);
-    } else {
-      const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      const int u = x % upr, pairs = p.rope.interleaved ? 0 : p.rope.rot / 16;
-      if (u < pairs) { put(8 * u, zero); put(p.rope.rot / 2 + 8 * u, zero); }
-      else put(p.rope.interleaved ? 8 * u : p.rope.rot + 8 * (u - pairs), zero);
+    for (int u = 0; u < 4; ++u) {
+      const float e = 0.5f * y[2 * u], o2 = 0.5f * y[2 * u + 1];   // a rotation grows a value by up to sqrt(2)
+      const __half2 hh = __floats2half2_rn(e, o2);
+      const float2 f = __half22float2(hh);
+      lo[2 * u] = isinf(f.x) ? 0.f : e - f.x;
+      lo[2 * u + 1] = isinf(f.y) ? 0.f : o2 - f.y;
+      hw[u] = *reinterpret_cast<const uint32_t*>(&hh);
+    }
+    const uint32_t at = static_cast<uint32_t>(o >> 6) * a_chunk + b * 128u + ((((o & 63) >> 3) ^ (b & 7)) << 4);
+    *reinterpret_cast<uint4*>(a_hi + at) = hv;
+    *reinterpret_cast<uint4*>(a_lo + at) = pack8(lo);
+  };
+  for (int x0 = tid; x0 < 128 * upr; x0 += kPrepThreads * kRopeKBatch) {
+    RopeUnit w[kRopeKBatch];
+    int32_t pos[kRopeKBatch];
+#pragma unroll
+    for (int i = 0; i < kRopeKBatch; ++i) {
+      const int b = (x0 + i * kPrepThreads) / upr;
+      pos[i] = b < nb ? p.rope.positions[b0 + b] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kRopeKBatch; ++i) {
+      const int x = x0 + i * kPrepThreads, b = x / upr, u = x - b * upr;
+      const float* cs = rope_row(p.rope, pos[i]);
+      if (cs) w[i].load(kp.k + (static_cast<size_t>(b0 + b) * kp.H + h) * d, cs, p.rope.rot, p.rope.interleaved, u);
+      else w[i].zero(p.rope.rot, p.rope.interleaved, u);
+    }
+#pragma unroll
+    for (int i = 0; i < kRopeKBatch; ++i) {
+      const int x = x0 + i * kPrepThreads;
+      if (x < 128 * upr) w[i].finish([&](int o, const float (&y)[8]) { put(x / upr, o, y); });
     }
   }
   fence_proxy_async_smem();
@@ -334,9 +403,7 @@ rope_rows_kernel(const __grid_constant__ CUtensorMap akmap, RopeRowsParams p) {
   const bool landed = mbar_wait(&done, 0) && !*static_cast<volatile uint32_t*>(&failed);
   if (__all_sync(0xffffffffu, landed)) {
     tc_fence_after();
-    const int b = (warp & 3) * 32 + lane;
-    const int64_t row = b < nb ? append_row(kp.tgt, b0 + b) : -1;
-    if (b < nb && row < 0 && h == 0 && warp < 4) append_skipped(kp.tgt, row);
+    if (wb < nb && row < 0 && h == 0 && warp < 4) append_skipped(kp.tgt, row);
     __half* out = kp.k_cache + (row < 0 ? 0 : (row * kp.H + h) * r);
     for (int c0 = (warp >> 2) * 16; c0 < r; c0 += 32) {
       __syncwarp();
@@ -370,6 +437,137 @@ __global__ void __launch_bounds__(kPrepThreads, 1)
 rope_vrows_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap vmap, AppendVParams p, int v_mt) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   append_v_tile(&amap, &vmap, p, blockIdx.x % v_mt, blockIdx.y, gridDim.y, blockIdx.x / v_mt, align_smem_1024(smem_raw));
+}
+
+// The V codes of a long prompt, C (n x R) = v (n x HD) . A_V (HD x R): persistent
+// CTAs over tiles of 256 rows x `nt` ranks, rows in the TMEM lanes (two M = 128
+// products side by side), so that a thread of the epilogue writes runs of one row's
+// codes.
+//   warp 0: TMA (v K-major, A_V MN-major boxes of 64 x 64); warp 1: MMAs;
+//   warps 4..11: epilogue.
+constexpr int kRVThreads = 384;
+struct RopeVParams {
+  AppendTarget tgt;
+  __half* v_cache;
+  int n, HD, R;
+  int nt, n_nt, tiles;     // ranks per tile (128 or 256), rank tiles, all tiles
+  int stages;
+};
+
+__global__ void __launch_bounds__(kRVThreads, 1)
+rope_vgemm_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap amap, RopeVParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = align_smem_1024(smem_raw);
+  __shared__ uint64_t full[4], empty[4], done, drained;
+  __shared__ uint32_t taddr_s, failed;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t a_bytes = 2u * 128u * 128u, stage_bytes = a_bytes + static_cast<uint32_t>(p.nt) * 128u;
+  const int S = p.stages, steps = (p.HD + 63) / 64;
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+    mbar_init(&done, 1);
+    mbar_init(&drained, 8);
+    failed = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&vmap);
+    prefetch_tensormap(&amap);
+  }
+  if (warp == 1) {
+    tmem_alloc(&taddr_s, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t taddr = taddr_s;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_last();
+      int i = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
+        const int n0 = (t % p.n_nt) * p.nt, b0 = t / p.n_nt * 256;
+        for (int c = 0; c < steps; ++c, ++i) {
+          const int s = i % S;
+          if (i >= S && !mbar_wait(&empty[s], ((i / S) - 1) & 1)) { ok = false; break; }
+          uint8_t* st = smem + static_cast<size_t>(s) * stage_bytes;
+          mbar_arrive_expect_tx(&full[s], stage_bytes);
+          tma_load_2d(st, &vmap, c * 64, b0, &full[s], pol);
+          for (int x = 0; x < p.nt / 64; ++x)
+            tma_load_2d(st + a_bytes + x * 8192, &amap, n0 + x * 64, c * 64, &full[s], pol);
+        }
+      }
+      // the copies in flight end before the block does
+      for (int e = i > S ? i - S : 0; e < i; ++e) mbar_wait(&full[e % S], (e / S) & 1);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_f16_f32(128, p.nt, /*a_mn_major=*/false, /*b_mn_major=*/true);
+      int i = 0, j = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x, ++j) {
+        if (j > 0 && !mbar_wait(&drained, (j - 1) & 1)) { ok = false; break; }
+        tc_fence_after();
+        for (int c = 0; c < steps; ++c, ++i) {
+          const int s = i % S;
+          if (!mbar_wait(&full[s], (i / S) & 1)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + static_cast<size_t>(s) * stage_bytes), sb = sa + a_bytes;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t bd = smem_desc(sb + kk * 2048u, 8192u, 1024u, kSwizzle128B);
+            umma_f16_ss(taddr, smem_desc(sa + kk * 32u, 16u, 1024u, kSwizzle128B), bd, idesc, c + kk > 0 ? 1u : 0u);
+            umma_f16_ss(taddr + 256, smem_desc(sa + 16384u + kk * 32u, 16u, 1024u, kSwizzle128B), bd, idesc, c + kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&empty[s]);
+        }
+        if (!ok) *static_cast<volatile uint32_t*>(&failed) = 1;
+        umma_commit(&done);
+      }
+    }
+  } else if (warp >= 4) {
+    // warps 4..7 the first 128 rows of the tile, 8..11 the others
+    const int half = (warp - 4) >> 2, quarter = warp & 3;
+    const uint32_t tq = taddr + half * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
+    int j = 0;
+    for (int t = blockIdx.x; t < p.tiles; t += gridDim.x, ++j) {
+      const int n0 = (t % p.n_nt) * p.nt, b = t / p.n_nt * 256 + half * 128 + quarter * 32 + lane;
+      const int64_t row = b < p.n ? append_row(p.tgt, b) : -1;
+      if (b < p.n && row < 0 && n0 == 0) append_skipped(p.tgt, row);
+      const bool landed = mbar_wait(&done, j & 1) && !*static_cast<volatile uint32_t*>(&failed);
+      if (!__all_sync(0xffffffffu, landed)) {
+        if (lane == 0) append_skipped(p.tgt, -STARKV_FLAG_TIMEOUT);
+        break;
+      }
+      tc_fence_after();
+      __half* out = p.v_cache + (row < 0 ? 0 : row * p.R) + n0;
+      const int width = min(p.nt, p.R - n0);
+      for (int c0 = 0; c0 < width; c0 += 16) {
+        __syncwarp();
+        uint32_t v[32];
+        tmem_ld_32x32b_x16(tq + c0, v);
+        tmem_ld_wait();
+        if (row < 0) continue;
+        float y[8];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) y[u] = __uint_as_float(v[8 * g + u]);
+          if (c0 + 8 * g < width) *reinterpret_cast<uint4*>(out + c0 + 8 * g) = pack8(y);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&drained);
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(taddr, 512);
+  }
 }
 
 }  // namespace starkv

@@ -64,6 +64,9 @@
 #ifndef STARKV_ROPE_ROWS
 #define STARKV_ROPE_ROWS 128     // rotary append: from so many rows on, the keys' codes on tensor cores
 #endif
+#ifndef STARKV_ROPE_SPLIT
+#define STARKV_ROPE_SPLIT 12     // rotary append of many rows: V codes split over a cluster when that saves a block so many steps
+#endif
 #ifndef STARKV_V_RING_BYTES
 #define STARKV_V_RING_BYTES (105 * 1024)
 #endif
@@ -1456,18 +1459,43 @@ starkv_status rope_impl(const starkv_layer_desc* desc, const starkv_rope* rope, 
   rp.H = desc->num_heads;
   rp.d = desc->head_dim;
   if (n >= STARKV_ROPE_ROWS) {
-    // many rows: V-code tiles, and beside them the rotated keys' codes and the queries
-    const size_t v_smem = ap.v_smem + 1024;
-    if (!set_smem(rope_vrows_kernel, v_smem)) return STARKV_ERR_CUDA;
-    if (launch(rope_vrows_kernel, dim3(ap.v_cols, ap.KS), dim3(kPrepThreads), v_smem, static_cast<cudaStream_t>(stream), ap.KS,
-               ap.amap, ap.vmap, ap.vp, ap.v_mt) != cudaSuccess)
-      return STARKV_ERR_CUDA;
+    // many rows: V-code tiles, and beside them the queries and the rotated keys' codes
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const int sms = device_sm_count(), rows256 = (n + 255) / 256;
+    // rank tiles of 256 or 128: the one whose waves move fewer bytes into an SM
+    const int t256 = rows256 * ((ap.vp.R + 255) / 256), t128 = rows256 * ((ap.vp.R + 127) / 128);
+    // K ranges of a cluster: one block per SM, and clusters of four fill three quarters of the SMs at best
+    ap.KS = 1;
+    while (ap.KS < STARKV_APP_KS_MAX && ap.v_cols * ap.KS * 2 <= (ap.KS == 1 ? sms : sms * 3 / 4) &&
+           ap.vp.HD / kAppKC >= ap.KS * 2)
+      ap.KS *= 2;
+    if (ap.vp.HD / kAppKC * (ap.KS - 1) / ap.KS < STARKV_ROPE_SPLIT) {
+      RopeVParams pv{};
+      pv.tgt = ap.vp.tgt;
+      pv.v_cache = ap.vp.v_cache;
+      pv.n = n; pv.HD = ap.vp.HD; pv.R = ap.vp.R;
+      pv.nt = (t256 + sms - 1) / sms * 4 <= (t128 + sms - 1) / sms * 3 ? 256 : 128;
+      pv.n_nt = (pv.R + pv.nt - 1) / pv.nt;
+      pv.tiles = rows256 * pv.n_nt;
+      pv.stages = pv.nt == 256 ? 3 : 4;
+      const size_t v_smem = 1024 + static_cast<size_t>(pv.stages) * (32768 + pv.nt * 128);
+      CUtensorMap vmap;
+      if (!encode_2d_map(&vmap, v, static_cast<uint64_t>(pv.HD), static_cast<uint64_t>(n), 64, 256) ||
+          !set_smem(rope_vgemm_kernel, v_smem) ||
+          launch(rope_vgemm_kernel, dim3(pv.tiles < sms ? pv.tiles : sms), dim3(kRVThreads), v_smem, cs, 1, vmap, ap.amap,
+                 pv) != cudaSuccess)
+        return STARKV_ERR_CUDA;
+    } else {
+      const size_t v_smem = ap.v_smem + 1024;
+      ap.vp.k_per_cta = (ap.vp.HD + ap.KS * kAppKC - 1) / (ap.KS * kAppKC) * kAppKC;
+      if (!set_smem(rope_vrows_kernel, v_smem) ||
+          launch(rope_vrows_kernel, dim3(ap.v_cols, ap.KS), dim3(kPrepThreads), v_smem, cs, ap.KS, ap.amap, ap.vmap, ap.vp,
+                 ap.v_mt) != cudaSuccess)
+        return STARKV_ERR_CUDA;
+    }
     RopeRowsParams pr{};
     pr.rope = rp.rope;
     pr.k = ap.kp;
-    pr.q = rp.q; pr.q_out = rp.q_out;
-    pr.n = n; pr.H = rp.H; pr.d = rp.d;
-    pr.k_tiles = (n + 127) / 128;
     pr.kc = (rp.d + 63) / 64;
     pr.nc = (ap.kp.r + 63) / 64;
     const size_t a_bytes = static_cast<size_t>(pr.kc) * 2 * 16384, b_chunk = static_cast<size_t>(pr.nc) * 8192;
@@ -1475,14 +1503,18 @@ starkv_status rope_impl(const starkv_layer_desc* desc, const starkv_rope* rope, 
     while (pr.b_slots > 1 && a_bytes + pr.b_slots * b_chunk > 200 * 1024) --pr.b_slots;
     pr.tmem_cols = static_cast<uint32_t>(pow2_ceil(ap.kp.r < 32 ? 32 : ap.kp.r));
     CUtensorMap akmap;
-    if (!encode_2d_map(&akmap, A_K, static_cast<uint64_t>(ap.kp.r), static_cast<uint64_t>(ap.kp.H) * rp.d, 64, 64))
-      return STARKV_ERR_CUDA;
-    const int64_t units = static_cast<int64_t>(n) * rp.H * rope_units(rp.d, rp.rope.rot, rp.rope.interleaved);
-    const int q_blocks = q ? static_cast<int>((units + kRopeQUnits - 1) / kRopeQUnits) : 0;
     const size_t smem = 1024 + a_bytes + pr.b_slots * b_chunk;
-    if (!set_smem(rope_rows_kernel, smem)) return STARKV_ERR_CUDA;
-    return launch(rope_rows_kernel, dim3(pr.k_tiles * pr.k.H + q_blocks), dim3(kPrepThreads), smem,
-                  static_cast<cudaStream_t>(stream), 1, akmap, pr) == cudaSuccess ? STARKV_OK : STARKV_ERR_CUDA;
+    if (!encode_2d_map(&akmap, A_K, static_cast<uint64_t>(ap.kp.r), static_cast<uint64_t>(ap.kp.H) * rp.d, 64, 64) ||
+        !set_smem(rope_rows_kernel, smem) ||
+        launch(rope_rows_kernel, dim3((n + 127) / 128 * pr.k.H), dim3(kPrepThreads), smem, cs, 1, akmap, pr) != cudaSuccess)
+      return STARKV_ERR_CUDA;
+    if (q) {
+      const int64_t units = static_cast<int64_t>(n) * rp.H * rope_units(rp.d, rp.rope.rot, rp.rope.interleaved);
+      if (launch(rope_q_kernel, dim3(static_cast<unsigned>((units + kRopeQUnits - 1) / kRopeQUnits)), dim3(kPrepThreads), 0,
+                 cs, 1, rp) != cudaSuccess)
+        return STARKV_ERR_CUDA;
+    }
+    return STARKV_OK;
   }
   const int KS = ap.KS;
   rp.k.tile = kRopeKB;

@@ -145,6 +145,53 @@ def test_rope_large_prompt():
     c.verify(g)
 
 
+@pytest.mark.parametrize("H,Hkv,d,r,R,n,inter", [
+    (4, 4, 32, 16, 2048, 2561, False), (2, 1, 32, 48, 1088, 2500, True), (8, 2, 64, 80, 1984, 5000, False),
+    (2, 2, 256, 256, 2048, 1300, True), (32, 32, 128, 64, 2048, 1281, False)])
+def test_rope_many_rows_and_ranks(H, Hkv, d, r, R, n, inter):
+    """Enough 256-row tiles of V codes to fill the device: one and several per block, odd edges, no queries."""
+    L = Layer(29, H, Hkv, d, r, R)
+    c = Case(L, n, 32, inter, max_position=8192, form="store")
+    g = c.device()
+    c.call(g)
+    c.verify(g)
+    g = c.device()
+    c.call(g, q="none", q_out="none")
+    c.verify(g, q_rows=np.zeros(n, bool))
+
+
+def test_rope_many_rows_skipped():
+    L = Layer(31, 2, 2, 32, 16, 2048)
+    c = Case(L, 2561, 32, False, max_position=4096, form="store")
+    keep = np.ones(c.n, bool)
+    g = c.device()
+    slots = c.slots.astype(np.int32)
+    slots[[0, 255, 256, 2560]] = [-1, c.nb * PAGE, 1 << 30, -(1 << 31)]
+    keep[[0, 255, 256, 2560]] = False
+    g["where"].copy_(dev(slots))
+    c.call(g)
+    c.verify(g, keep, None, S.FLAG_BAD_BLOCK_ID)
+
+
+@pytest.mark.parametrize("n,R", [(150, 64), (2561, 2048)])
+def test_rope_large_values(n, R):
+    """Keys next to the type's largest value, whose rotation is past it; a row with infinities stays to itself."""
+    L = Layer(32, 2, 2, 32, 16, R)
+    L.A_K = (L.A_K.astype(np.float64) * 2.0 ** -10).astype(np.float16)
+    c = Case(L, n, 32, False, max_position=4096, form="store")
+    c.k = np.where(c.k >= 0, np.float16(65504), np.float16(-65504)).astype(np.float16)
+    g = c.device()
+    g["k"][3, 1, 5] = float("inf")
+    keep = np.ones(n, bool)
+    c.call(g)
+    kc = g["k_cache"].view(-1, 2, 16)
+    bad = kc[int(c.slots[3])].clone()
+    assert not torch.isfinite(bad[1]).any() and torch.isfinite(bad[0]).all()
+    g["k"][3, 1, 5] = float(c.k[3, 1, 5])
+    c.call(g)
+    c.verify(g, keep)
+
+
 @pytest.mark.parametrize("inter", [False, True])
 def test_rope_in_place_and_without_queries(inter):
     L = Layer(24, 8, 2, 128, 64, 256)
