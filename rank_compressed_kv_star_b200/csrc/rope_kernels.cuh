@@ -123,10 +123,7 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return v;
 }
 
-#ifndef STARKV_ROPE_QB
-#define STARKV_ROPE_QB 2
-#endif
-constexpr int kRopeBatch = STARKV_ROPE_QB;   // query units of a thread in flight
+constexpr int kRopeBatch = 2;   // query units of a thread in flight
 
 // Rotation units x0, x0 + step, ... (kRopeBatch of them) of the queries: all loads
 // before the stores, which may be to the same rows.
@@ -166,8 +163,10 @@ struct RopeParams {
 };
 
 constexpr int kRopeKB = 32;                       // rows per K-code item
+// Blocks of a cluster that share a V-code tile's depth: eight beat four (one row, 32
+// heads of 128, R = 2048: 6.7 against 9.0 us; 64 rows: 8.9 against 11.2).
+constexpr int kRopeKS = 8;
 constexpr int kRopeQUnits = kPrepThreads * kRopeBatch;
-constexpr int kRopeKBatch = 4;                    // key units of a thread in flight     // rotation units per query item
 
 // One K-code item: KV head h, rows [b0, b0 + tile).  The rotated rows stand in
 // shared memory as fp32 beside A_K[h].
@@ -262,14 +261,12 @@ rope_append_kernel(const __grid_constant__ CUtensorMap amap, const __grid_consta
 
 // ------------------------------------------------------------ many rows
 // A prompt's rows take three launches, the second and third beside the first (they
-// read nothing that it writes, start when its blocks have seen the work before it
-// end, and wait for it only at their end): V-code tiles, query units, key codes.
-#ifndef STARKV_ROPE_QO
-#define STARKV_ROPE_QO 3
-#endif
-__global__ void __launch_bounds__(kPrepThreads, STARKV_ROPE_QO) rope_q_kernel(RopeParams p) {
+// read nothing that it writes and start when its blocks have seen the work before
+// it end; their last blocks wait for the launch before, so that none of them ends
+// ahead of it): V-code tiles, key codes, query units.
+__global__ void __launch_bounds__(kPrepThreads, 3) rope_q_kernel(RopeParams p) {
   rope_q_item(p, blockIdx.x);
-  griddep_wait();
+  if (blockIdx.x == gridDim.x - 1) griddep_wait();
 }
 
 // Key codes: a block is one KV head's 128 rows, on tcgen05,
@@ -277,6 +274,7 @@ __global__ void __launch_bounds__(kPrepThreads, STARKV_ROPE_QO) rope_q_kernel(Ro
 // the rotated rows written to shared memory as fp16 hi + lo halves (22 bits, so the
 // code still rounds once) in the K-major operand layout, A_K[h] by TMA boxes of 64
 // ranks x 64 rows (MN-major).
+constexpr int kRRThreads = 512;
 struct RopeRowsParams {
   RopeTable rope;
   AppendKParams k;
@@ -285,7 +283,7 @@ struct RopeRowsParams {
   uint32_t tmem_cols;
 };
 
-__global__ void __launch_bounds__(kPrepThreads, 2)
+__global__ void __launch_bounds__(kRRThreads, 2)
 rope_rows_kernel(const __grid_constant__ CUtensorMap akmap, RopeRowsParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -337,34 +335,22 @@ rope_rows_kernel(const __grid_constant__ CUtensorMap akmap, RopeRowsParams p) {
       const float e = 0.5f * y[2 * u], o2 = 0.5f * y[2 * u + 1];   // a rotation grows a value by up to sqrt(2)
       const __half2 hh = __floats2half2_rn(e, o2);
       const float2 f = __half22float2(hh);
-      lo[2 * u] = isinf(f.x) ? 0.f : e - f.x;
-      lo[2 * u + 1] = isinf(f.y) ? 0.f : o2 - f.y;
+      // at most half a step of 2^15; an infinity less itself is no number, and -64 keeps it an infinity
+      lo[2 * u] = fmaxf(e - f.x, -64.f);
+      lo[2 * u + 1] = fmaxf(o2 - f.y, -64.f);
       hw[u] = *reinterpret_cast<const uint32_t*>(&hh);
     }
     const uint32_t at = static_cast<uint32_t>(o >> 6) * a_chunk + b * 128u + ((((o & 63) >> 3) ^ (b & 7)) << 4);
     *reinterpret_cast<uint4*>(a_hi + at) = hv;
     *reinterpret_cast<uint4*>(a_lo + at) = pack8(lo);
   };
-  for (int x0 = tid; x0 < 128 * upr; x0 += kPrepThreads * kRopeKBatch) {
-    RopeUnit w[kRopeKBatch];
-    int32_t pos[kRopeKBatch];
-#pragma unroll
-    for (int i = 0; i < kRopeKBatch; ++i) {
-      const int b = (x0 + i * kPrepThreads) / upr;
-      pos[i] = b < nb ? p.rope.positions[b0 + b] : -1;
-    }
-#pragma unroll
-    for (int i = 0; i < kRopeKBatch; ++i) {
-      const int x = x0 + i * kPrepThreads, b = x / upr, u = x - b * upr;
-      const float* cs = rope_row(p.rope, pos[i]);
-      if (cs) w[i].load(kp.k + (static_cast<size_t>(b0 + b) * kp.H + h) * d, cs, p.rope.rot, p.rope.interleaved, u);
-      else w[i].zero(p.rope.rot, p.rope.interleaved, u);
-    }
-#pragma unroll
-    for (int i = 0; i < kRopeKBatch; ++i) {
-      const int x = x0 + i * kPrepThreads;
-      if (x < 128 * upr) w[i].finish([&](int o, const float (&y)[8]) { put(x / upr, o, y); });
-    }
+  for (int x = tid; x < 128 * upr; x += kRRThreads) {
+    const int b = x / upr, u = x - b * upr;
+    const float* cs = b < nb ? rope_row(p.rope, p.rope.positions[b0 + b]) : nullptr;
+    RopeUnit w;
+    if (cs) w.load(kp.k + (static_cast<size_t>(b0 + b) * kp.H + h) * d, cs, p.rope.rot, p.rope.interleaved, u);
+    else w.zero(p.rope.rot, p.rope.interleaved, u);
+    w.finish([&](int o, const float (&y)[8]) { put(b, o, y); });
   }
   fence_proxy_async_smem();
   __syncthreads();
@@ -398,14 +384,14 @@ rope_rows_kernel(const __grid_constant__ CUtensorMap akmap, RopeRowsParams p) {
     }
     umma_commit(&done);
   }
-  // codes of row 32 (warp % 4) + lane; warps 4..7 take the upper half of the ranks
+  // codes of row 32 (warp % 4) + lane; the warps of a row group take turns of 16 ranks
   __syncwarp();
   const bool landed = mbar_wait(&done, 0) && !*static_cast<volatile uint32_t*>(&failed);
   if (__all_sync(0xffffffffu, landed)) {
     tc_fence_after();
     if (wb < nb && row < 0 && h == 0 && warp < 4) append_skipped(kp.tgt, row);
     __half* out = kp.k_cache + (row < 0 ? 0 : (row * kp.H + h) * r);
-    for (int c0 = (warp >> 2) * 16; c0 < r; c0 += 32) {
+    for (int c0 = (warp >> 2) * 16; c0 < r; c0 += kRRThreads / 8) {
       __syncwarp();
       uint32_t v[32];
       tmem_ld_32x32b_x16(taddr + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0, v);
@@ -429,7 +415,7 @@ rope_rows_kernel(const __grid_constant__ CUtensorMap akmap, RopeRowsParams p) {
     tc_fence_after();
     tmem_dealloc(taddr, p.tmem_cols);
   }
-  griddep_wait();   // this grid ends after the V-code tiles launched before it
+  if (blockIdx.x == gridDim.x - 1) griddep_wait();
 }
 
 // The V-code tiles of a prompt's rows (see append_v_tile).

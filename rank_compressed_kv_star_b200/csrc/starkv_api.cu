@@ -61,8 +61,8 @@
 #ifndef STARKV_ATTEND_BLOCKS
 #define STARKV_ATTEND_BLOCKS 24   // attend form of the group calls: at most so many blocks per cluster
 #endif
-#ifndef STARKV_ROPE_ROWS
-#define STARKV_ROPE_ROWS 128     // rotary append: from so many rows on, the keys' codes on tensor cores
+#ifndef STARKV_ROPE_MACS
+#define STARKV_ROPE_MACS (24 << 20)   // rotary append: from so many key-code products on, tensor cores and three launches
 #endif
 #ifndef STARKV_ROPE_SPLIT
 #define STARKV_ROPE_SPLIT 12     // rotary append of many rows: V codes split over a cluster when that saves a block so many steps
@@ -616,7 +616,7 @@ struct AppendPlan {
 
 starkv_status plan_append(const starkv_layer_desc* desc, int32_t batch, const void* k, const void* v,
                           const void* A_K, const void* A_V, AppendTarget tgt, void* k_cache, void* v_cache,
-                          AppendPlan* ap) {
+                          AppendPlan* ap, int ks_max = STARKV_APP_KS_MAX) {
   if (!k || !v || !A_K || !A_V || !k_cache || !v_cache) return STARKV_ERR_INVALID_ARG;
   if (!tgt.slots && (!tgt.tables || !tgt.positions)) return STARKV_ERR_INVALID_ARG;
   if (!aligned16(k) || !aligned16(v) || !aligned16(A_K) || !aligned16(A_V) || !aligned16(k_cache) ||
@@ -640,7 +640,7 @@ starkv_status plan_append(const starkv_layer_desc* desc, int32_t batch, const vo
   // <= one wave at 2 CTAs/SM, and clusters of at most 4: the whole prep grid
   // (K-code and absorption items too) is launched in clusters of KS, and with
   // 8 some of them found no free GPC slots until the V tiles had ended
-  while (KS < STARKV_APP_KS_MAX && ap->v_cols * KS * 2 <= 2 * sms && (HD / kAppKC) >= KS * 2) KS *= 2;
+  while (KS < ks_max && ap->v_cols * KS * 2 <= 2 * sms && (HD / kAppKC) >= KS * 2) KS *= 2;
   ap->KS = KS;
   AppendVParams& vp = ap->vp;
   vp.tgt = tgt;
@@ -1443,7 +1443,7 @@ starkv_status rope_impl(const starkv_layer_desc* desc, const starkv_rope* rope, 
   tgt.rope_positions = positions;
   tgt.rope_max = rope->max_position;
   AppendPlan ap{};
-  st = plan_append(desc, n, k, v, A_K, A_V, tgt, k_cache, v_cache, &ap);
+  st = plan_append(desc, n, k, v, A_K, A_V, tgt, k_cache, v_cache, &ap, kRopeKS);
   if (st != STARKV_OK) return st;
   RopeParams rp{};
   rp.rope.cos_sin = rope->cos_sin;
@@ -1458,7 +1458,7 @@ starkv_status rope_impl(const starkv_layer_desc* desc, const starkv_rope* rope, 
   rp.n = n;
   rp.H = desc->num_heads;
   rp.d = desc->head_dim;
-  if (n >= STARKV_ROPE_ROWS) {
+  if (static_cast<int64_t>(n) * ap.kp.H * rp.d * ap.kp.r >= STARKV_ROPE_MACS) {
     // many rows: V-code tiles, and beside them the queries and the rotated keys' codes
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const int sms = device_sm_count(), rows256 = (n + 255) / 256;
@@ -1466,7 +1466,7 @@ starkv_status rope_impl(const starkv_layer_desc* desc, const starkv_rope* rope, 
     const int t256 = rows256 * ((ap.vp.R + 255) / 256), t128 = rows256 * ((ap.vp.R + 127) / 128);
     // K ranges of a cluster: one block per SM, and clusters of four fill three quarters of the SMs at best
     ap.KS = 1;
-    while (ap.KS < STARKV_APP_KS_MAX && ap.v_cols * ap.KS * 2 <= (ap.KS == 1 ? sms : sms * 3 / 4) &&
+    while (ap.KS < kRopeKS && ap.v_cols * ap.KS * 2 <= (ap.KS == 1 ? sms : sms * 3 / 4) &&
            ap.vp.HD / kAppKC >= ap.KS * 2)
       ap.KS *= 2;
     if (ap.vp.HD / kAppKC * (ap.KS - 1) / ap.KS < STARKV_ROPE_SPLIT) {
@@ -1506,7 +1506,7 @@ starkv_status rope_impl(const starkv_layer_desc* desc, const starkv_rope* rope, 
     const size_t smem = 1024 + a_bytes + pr.b_slots * b_chunk;
     if (!encode_2d_map(&akmap, A_K, static_cast<uint64_t>(ap.kp.r), static_cast<uint64_t>(ap.kp.H) * rp.d, 64, 64) ||
         !set_smem(rope_rows_kernel, smem) ||
-        launch(rope_rows_kernel, dim3((n + 127) / 128 * pr.k.H), dim3(kPrepThreads), smem, cs, 1, akmap, pr) != cudaSuccess)
+        launch(rope_rows_kernel, dim3((n + 127) / 128 * pr.k.H), dim3(kRRThreads), smem, cs, 1, akmap, pr) != cudaSuccess)
       return STARKV_ERR_CUDA;
     if (q) {
       const int64_t units = static_cast<int64_t>(n) * rp.H * rope_units(rp.d, rp.rope.rot, rp.rope.interleaved);
