@@ -23,6 +23,7 @@
 #pragma once
 #include <cooperative_groups.h>
 #include <cstdint>
+#include <type_traits>
 #include <cuda_fp16.h>
 
 #include "ptx.cuh"
@@ -2140,21 +2141,34 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
         }
       }
     } else {
-      // 1 / L of every column: a warp sums a column's chunks
-      for (int c = warp - 2; c < ncols; c += kGFConv / 32) {
-        const int row = row0 + (c >> g.log2G);
-        const size_t rh = static_cast<size_t>(row) * g.H + (j << g.log2G) + (c & ((1 << g.log2G) - 1));
+      // 1 / L of every column: its chunks' sums by as many lanes as there are threads for, four
+      // loads in flight each
+      int log2t = 0;
+      while (log2t < 5 && (ncols << (log2t + 1)) <= kGFConv) ++log2t;
+      const int t = 1 << log2t;
+      for (int c0 = 0; c0 < ncols; c0 += kGFConv >> log2t) {
+        const int c = c0 + (et >> log2t), i0 = et & (t - 1);
         float L = 0.f;
-        for (int sr = 0; sr < n_src; ++sr) {
-          const int e = s_ent[sr][c];
-          if (e < 0 || ent[e].len == 0) continue;
-          const int ch = ent[e].narrow ? g.chunk_n : g.chunk_w;
-          const int nc = (ent[e].len + ch - 1) / ch;
-          for (int i = lane; i < nc; i += 32) L += g.lpart[sr][rh * g.n_ch[sr] + i];
-        }
+        if (c < ncols) {
+          const int row = row0 + (c >> g.log2G);
+          const size_t rh = static_cast<size_t>(row) * g.H + (j << g.log2G) + (c & ((1 << g.log2G) - 1));
+          for (int sr = 0; sr < n_src; ++sr) {
+            const int e = s_ent[sr][c];
+            if (e < 0 || ent[e].len == 0) continue;
+            const int ch = ent[e].narrow ? g.chunk_n : g.chunk_w;
+            const int nc = (ent[e].len + ch - 1) / ch;
+            const float* lp = g.lpart[sr] + rh * g.n_ch[sr];
+            for (int i = i0; i < nc; i += 4 * t) {
+              float l4[4];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-        if (lane == 0) s_il[c] = L == 0.f ? 0.f : 1.f / L;
+              for (int u = 0; u < 4; ++u) l4[u] = i + u * t < nc ? lp[i + u * t] : 0.f;
+#pragma unroll
+              for (int u = 0; u < 4; ++u) L += l4[u];
+            }
+          }
+        }
+        for (int o = t >> 1; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        if (c < ncols && i0 == 0) s_il[c] = L == 0.f ? 0.f : 1.f / L;
       }
     }
     if (!group_sync(cbar, phase)) ok = false;
@@ -2171,59 +2185,83 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
       if ((i & ((1 << p.log2cg) - 1)) != cgrp) continue;   // another group's stage
       if (i >= S && !__all_sync(0xffffffffu, mbar_wait(&empty[s], ((i / S) - 1) & 1))) { ok = false; break; }
       uint8_t* hi_t = smem + static_cast<size_t>(s) * p.stage_bytes + a_bytes;
-      // item = (column bl, 8-value chunk c of the stage's 64 rows of R), four segments at a
-      // time: eight 16-byte loads in flight per thread
-      for (int item = et & (cthr - 1); item < p.npad * 8; item += cthr) {
-        const int bl = item >> 3, c = item & 7;
-        float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        const int n0 = bl < ncols ? s_n[0][bl] : 0, n = bl < ncols ? n0 + s_n[1][bl] : 0;
-        const float* at = p.base + kr + c * 8;
-        const int cap = min(n, 1 << p.log2cap);
-        const int64_t* off = s_off + (bl << p.log2cap);
-        const float* fac = s_fac + (bl << p.log2cap);
-        for (int u0 = 0; u0 < cap; u0 += 4) {
-          float4 a[4], b[4];
+      // item = (column bl, 8-value chunk c of the stage's 64 rows of R); eight 16-byte loads in
+      // flight per thread: NI items by 4 / NI of their segments at a time, more items at once
+      // where a thread has them (a call of 1024 rows, 256 columns a block: 120 us with NI = 1)
+      auto convert = [&](auto ni) {
+        constexpr int NI = decltype(ni)::value, NS = 4 / NI;
+        for (int it0 = et & (cthr - 1); it0 < p.npad * 8; it0 += cthr * NI) {
+          float z[NI][8];
+          int n[NI], most = 0;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            a[u] = b[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (u0 + u < cap) {
-              const float4* src = reinterpret_cast<const float4*>(at + off[u0 + u]);
-              a[u] = src[0];
-              b[u] = src[1];
-            }
+          for (int v = 0; v < NI; ++v) {
+            const int bl = (it0 + v * cthr) >> 3;
+            n[v] = bl < ncols ? s_n[0][bl] + s_n[1][bl] : 0;
+            most = max(most, n[v]);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) z[v][u] = 0.f;
+          }
+          most = min(most, 1 << p.log2cap);
+          for (int u0 = 0; u0 < most; u0 += NS) {
+            float4 a[NI][NS], b[NI][NS];
+#pragma unroll
+            for (int v = 0; v < NI; ++v)
+#pragma unroll
+              for (int u = 0; u < NS; ++u) {
+                a[v][u] = b[v][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (u0 + u < min(n[v], most)) {
+                  const int it = it0 + v * cthr;
+                  const float4* src = reinterpret_cast<const float4*>(p.base + kr + (it & 7) * 8 + s_off[((it >> 3) << p.log2cap) + u0 + u]);
+                  a[v][u] = src[0];
+                  b[v][u] = src[1];
+                }
+              }
+#pragma unroll
+            for (int v = 0; v < NI; ++v)
+#pragma unroll
+              for (int u = 0; u < NS; ++u)
+                if (u0 + u < min(n[v], most)) {
+                  const int bl = (it0 + v * cthr) >> 3;
+                  const float f = attend ? (n[v] <= 32 ? s_fac[(bl << p.log2cap) + u0 + u] : seg_factor(u0 + u, bl, s_n[0][bl])) : 1.f;
+                  const float4 x = a[v][u], y = b[v][u];
+                  z[v][0] += x.x * f; z[v][1] += x.y * f; z[v][2] += x.z * f; z[v][3] += x.w * f;
+                  z[v][4] += y.x * f; z[v][5] += y.y * f; z[v][6] += y.z * f; z[v][7] += y.w * f;
+                }
           }
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (u0 + u < cap) {
-              const float f = attend ? (n <= 32 ? fac[u0 + u] : seg_factor(u0 + u, bl, n0)) : 1.f;
-              z[0] += a[u].x * f; z[1] += a[u].y * f; z[2] += a[u].z * f; z[3] += a[u].w * f;
-              z[4] += b[u].x * f; z[5] += b[u].y * f; z[6] += b[u].z * f; z[7] += b[u].w * f;
+          for (int v = 0; v < NI; ++v) {
+            const int it = it0 + v * cthr, bl = it >> 3, c = it & 7;
+            if (it >= p.npad * 8) break;
+            for (int u = most; u < n[v]; ++u) {   // more segments than the list holds
+              const int n0 = s_n[0][bl];
+              const float4* src = reinterpret_cast<const float4*>(p.base + kr + c * 8 + (u < n0 ? seg_off(0, bl, u) : seg_off(1, bl, u - n0)));
+              const float4 x = src[0], y = src[1];
+              const float f = attend ? seg_factor(u, bl, n0) : 1.f;
+              z[v][0] += x.x * f; z[v][1] += x.y * f; z[v][2] += x.z * f; z[v][3] += x.w * f;
+              z[v][4] += y.x * f; z[v][5] += y.y * f; z[v][6] += y.z * f; z[v][7] += y.w * f;
             }
-        }
-        for (int u = cap; u < n; ++u) {   // more segments than the list holds
-          const float4* src = reinterpret_cast<const float4*>(at + (u < n0 ? seg_off(0, bl, u) : seg_off(1, bl, u - n0)));
-          const float4 a = src[0], b = src[1];
-          const float f = attend ? seg_factor(u, bl, n0) : 1.f;
-          z[0] += a.x * f; z[1] += a.y * f; z[2] += a.z * f; z[3] += a.w * f;
-          z[4] += b.x * f; z[5] += b.y * f; z[6] += b.z * f; z[7] += b.w * f;
-        }
-        const float il = n > 0 ? s_il[bl] : 0.f;
-        uint4 hv, lv;
-        uint32_t* hw = reinterpret_cast<uint32_t*>(&hv);
-        uint32_t* lw = reinterpret_cast<uint32_t*>(&lv);
+            const float il = n[v] > 0 ? s_il[bl] : 0.f;
+            uint4 hv, lv;
+            uint32_t* hw = reinterpret_cast<uint32_t*>(&hv);
+            uint32_t* lw = reinterpret_cast<uint32_t*>(&lv);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float z0 = z[2 * u] * il, z1 = z[2 * u + 1] * il;
-          const __half2 hh = __floats2half2_rn(z0, z1);
-          const float2 f = __half22float2(hh);
-          const __half2 ll = __floats2half2_rn(z0 - f.x, z1 - f.y);
-          hw[u] = *reinterpret_cast<const uint32_t*>(&hh);
-          lw[u] = *reinterpret_cast<const uint32_t*>(&ll);
+            for (int u = 0; u < 4; ++u) {
+              const float z0 = z[v][2 * u] * il, z1 = z[v][2 * u + 1] * il;
+              const __half2 hh = __floats2half2_rn(z0, z1);
+              const float2 f = __half22float2(hh);
+              const __half2 ll = __floats2half2_rn(z0 - f.x, z1 - f.y);
+              hw[u] = *reinterpret_cast<const uint32_t*>(&hh);
+              lw[u] = *reinterpret_cast<const uint32_t*>(&ll);
+            }
+            const uint32_t off16 = static_cast<uint32_t>(bl) * 128u + (static_cast<uint32_t>(c ^ (bl & 7)) << 4);
+            *reinterpret_cast<uint4*>(hi_t + off16) = hv;
+            *reinterpret_cast<uint4*>(hi_t + b_bytes + off16) = lv;
+          }
         }
-        const uint32_t off16 = static_cast<uint32_t>(bl) * 128u + (static_cast<uint32_t>(c ^ (bl & 7)) << 4);
-        *reinterpret_cast<uint4*>(hi_t + off16) = hv;
-        *reinterpret_cast<uint4*>(hi_t + b_bytes + off16) = lv;
-      }
+      };
+      if (p.npad * 8 >= 4 * cthr) convert(std::integral_constant<int, 4>{});
+      else if (p.npad * 8 >= 2 * cthr) convert(std::integral_constant<int, 2>{});
+      else convert(std::integral_constant<int, 1>{});
       fence_proxy_async_smem();
       mbar_arrive(&conv[s]);
     }
