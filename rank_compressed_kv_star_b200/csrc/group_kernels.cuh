@@ -62,7 +62,7 @@ struct GroupGeom {
   int n_ch[2];                 // chunks per row of the sums of weights
   int max_len[2];              // host bounds of the entries' lengths
   GroupEntry* ent;             // [E]
-  int32_t* kpre;               // [E + 1] K items before each entry
+  int32_t* kpre;               // [E + 1] cost of the K items before each entry
   int32_t* vpre;               // [E + 1] V units before each entry
   int32_t* apre;               // [E + 1] attend blocks before each entry
   int a_rows;                  // attend: rows per tile at most (0: the call does not use it)
@@ -101,6 +101,19 @@ __device__ __forceinline__ int gk_tiles(int nrows, const GroupGeom& g) {
 }
 
 // ================================================================= tables
+// What an item of the K pass costs, for the partition of the items over the CTAs: its
+// steps, a wide one by its columns (128 tokens by 16 columns are one accumulator block of
+// a warp), plus its start.  By number instead of cost, a call of 64 rows over 8192 shared
+// and up to 256 own tokens (32 heads) took 274 us, its last CTAs twice the median.
+#ifndef STARKV_GK_START
+#define STARKV_GK_START 8
+#endif
+constexpr int kGKStart = STARKV_GK_START;
+__device__ __forceinline__ int gk_cost(const GroupEntry& en, const GroupGeom& g, int log2Hkv) {
+  if (en.narrow) return (g.chunk_n >> (7 - log2Hkv)) * (2 + ((en.nrows * g.H) >> 4)) + kGKStart;
+  return (g.chunk_w >> 7) * (4 + ((en.k_per << g.log2G) >> 4)) + kGKStart;
+}
+
 struct GroupSetupParams {
   GroupGeom g;
   const int32_t* row_offsets;  // [n_groups + 1]
@@ -138,13 +151,14 @@ __device__ __forceinline__ void group_setup(const GroupSetupParams& p) {
   // thread t makes the entries [t per, (t + 1) per)
   const int per = (g.E + 255) / 256;
   const int e0 = tid * per, e1 = min(g.E, e0 + per);
-  int32_t mine[5] = {0, 0, 0, 0, 0};   // K items, V units, V tiles, attend blocks, attend tiles
+  int32_t mine[5] = {0, 0, 0, 0, 0};   // cost of the K items, V units, V tiles, attend blocks, attend tiles
   auto counts = [&](const GroupEntry& en, int32_t (&c)[5]) {
     c[0] = c[1] = c[2] = c[3] = c[4] = 0;
     if (en.nrows == 0 || en.len == 0) return;
     const int nt = gv_tiles(en.nrows * g.H) * g.n_rt;
-    c[0] = gk_narrow(en.nrows, g) ? (en.len + g.chunk_n - 1) / g.chunk_n
-                                  : gk_tiles(en.nrows, g) * g.Hkv * ((en.len + g.chunk_w - 1) / g.chunk_w);
+    c[0] = en.narrow ? (en.len + g.chunk_n - 1) / g.chunk_n
+                     : en.k_nt * g.Hkv * ((en.len + g.chunk_w - 1) / g.chunk_w);
+    c[0] *= gk_cost(en, g, 31 - __clz(g.Hkv));
     c[1] = nt * ((en.len + kGVTok - 1) / kGVTok);
     c[2] = nt;
     c[3] = en.a_nt * en.v_units;
@@ -403,8 +417,8 @@ __device__ __forceinline__ int32_t entry_of(const GroupTables& t, int32_t x) {
 // narrow entry is one chunk of tokens of all heads (see gk_narrow).  Warp 0
 // issues the copies, warp 1 the MMAs into a ring of accumulators, warps 2..9
 // drain them: wide, each takes one lane quarter and every other block of 16
-// columns; narrow, four of them stage their quarter in shared memory and each
-// lane reads its own head's columns.  The weights pass forms S a second time
+// columns; narrow, four of them (the two fours take turns) stage their quarter in
+// shared memory and each lane reads its own head's columns.  The weights pass forms S a second time
 // rather than keeping it: r / R of the V pass's products against 8 bytes of
 // traffic per logit.
 struct GroupKParams {
@@ -420,8 +434,9 @@ struct GroupKParams {
   uint32_t tmem_cols;
 };
 
-constexpr int kGKThreads = 320;
-constexpr int kGKEpi = kGKThreads - 64;
+constexpr int kGKProd = 3;                        // producer warps: 0, 10, 11
+constexpr int kGKEpi = 256;
+constexpr int kGKThreads = kGKEpi + 32 * (1 + kGKProd);
 constexpr int kGKAcc = 4;
 
 struct KItem {
@@ -430,26 +445,35 @@ struct KItem {
   int c, t0, t1, step;            // chunk, tokens [t0, t1), tokens per step
 };
 
-// Walks the items [it, end) of a CTA in order.
+// Walks a CTA's items in order: those that begin in the costs [it, end).
 struct KWalk {
   const GroupGeom& g;
   const GroupTables& tb;
   int log2Hkv;
-  int32_t it, end, ebeg, eend, e;
+  int32_t it, end, eend, e, at, cost;
   GroupEntry en;
   __device__ KWalk(const GroupGeom& g_, const GroupTables& tb_, int log2Hkv_, int32_t i0, int32_t i1)
-      : g(g_), tb(tb_), log2Hkv(log2Hkv_), it(i0), end(i1), ebeg(0), eend(0), e(0) {
+      : g(g_), tb(tb_), log2Hkv(log2Hkv_), it(i0), end(i1), eend(0), e(0), at(0), cost(1) {
     if (it < end) {
       e = entry_of(tb, it);
-      ebeg = tb.pre[e];
+      const int32_t ebeg = tb.pre[e];
       eend = tb.pre[e + 1];
       en = tb.ent[e];
+      cost = gk_cost(en, g, log2Hkv);
+      at = (it - ebeg + cost - 1) / cost;
+      it = ebeg + at * cost;
     }
   }
   __device__ bool next(KItem* x) {
     if (it >= end) return false;
-    while (it >= eend) { ++e; ebeg = eend; eend = tb.pre[e + 1]; if (it < eend) en = tb.ent[e]; }
-    const int local = it - ebeg;
+    while (it >= eend) {
+      ++e;
+      eend = tb.pre[e + 1];
+      at = 0;
+      if (it < eend) { en = tb.ent[e]; cost = gk_cost(en, g, log2Hkv); }
+    }
+    const int local = at++;
+    it += cost;
     x->en = en;
     if (en.narrow) {
       x->j = 0;
@@ -477,7 +501,6 @@ struct KWalk {
       x->t1 = min(en.len, x->t0 + g.chunk_w);
       x->step = 128;
     }
-    ++it;
     return true;
   }
 };
@@ -548,14 +571,14 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
   uint64_t* tempty = tfull + kGKAcc;
   uint64_t* mmadone = tempty + kGKAcc;
   uint64_t* ebar = mmadone + 1;
-  float* stage = reinterpret_cast<float*>(ebar + 1);   // [4 warps][32 lanes][ncol + 4]
+  float* stage = reinterpret_cast<float*>(ebar + 1);   // [8 warps][32 lanes][ncol / 2 + 4]
   __shared__ uint32_t taddr_s;
   __shared__ volatile int32_t abort_flag;
   __shared__ GroupTablesSmem s_tab;
   __shared__ int64_t s_off[128];   // P row of each column, or -1
   __shared__ int32_t s_rh[128];    // its (row, query head), or -1
   __shared__ float s_m[128];
-  __shared__ float s_red[4][128];
+  __shared__ float s_red[8][128];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -590,8 +613,12 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
   const int G = 1 << g.log2G;
   const uint32_t half_q = p.q_bytes / 2;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
+  if (warp == 0 || warp >= 2 + kGKEpi / 32) {
+    // ----------------------------------------------------------- producers
+    // A step's boxes are dealt out to the producer warps (one lane's issue of eight boxes takes
+    // 2 us, as long as everything else of a step together); the first also brings the queries
+    // and arrives for all: a box that lands before the arrival is counted all the same.
+    const int pid = warp == 0 ? 0 : warp - (1 + kGKEpi / 32);
     const uint64_t keep = policy_evict_last();
     RingPos k;
     uint32_t issued = 0, qi = 0;
@@ -603,7 +630,7 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
                        (x.t1 - x.t0 + kBlock - 1) / kBlock, g.NB, g.status, lane);
       const int qs = p.nq > 1 ? static_cast<int>(qi & 1) : 0;
       const uint32_t qu = p.nq > 1 ? qi >> 1 : qi;
-      if (lane == 0) {
+      if (lane == 0 && pid == 0) {
         if (qu > 0 && !mbar_wait(&qempty[qs], (qu - 1) & 1)) {
           ok = false;
         } else {
@@ -641,9 +668,9 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
         uint8_t* st = smem + static_cast<size_t>(k.s) * p.a_bytes;
         if (lane == 0) {
           if (k.u > 0 && !mbar_wait(&empty[k.s], (k.u - 1) & 1)) ok = false;
-          else mbar_arrive_expect_tx(&full[k.s], static_cast<uint32_t>(nb * p.kb) * box);
+          else if (pid == 0) mbar_arrive_expect_tx(&full[k.s], static_cast<uint32_t>(nb * p.kb) * box);
         }
-        for (int c = 0; c < nb; ++c) {
+        for (int c = pid; c < nb; c += kGKProd) {
           const int tk = t + c * tb;
           const int row = pages.page((tk - x.t0) >> 4) * kBlock + (tk & (kBlock - 1));
           if (lane == 0 && ok) {
@@ -668,7 +695,7 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
         if (--k.s < 0) { k.s = S - 1; --k.u; }
         mbar_wait(&full[k.s], k.u & 1);
       }
-      for (uint32_t n = 0; n < qi && n < static_cast<uint32_t>(p.nq); ++n) {
+      for (uint32_t n = 0; pid == 0 && n < qi && n < static_cast<uint32_t>(p.nq); ++n) {
         const uint32_t z = qi - 1 - n;
         mbar_wait(&qfull[p.nq > 1 ? z & 1 : 0], (p.nq > 1 ? z >> 1 : z) & 1);
       }
@@ -750,7 +777,7 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
         s_rh[et] = rh;
         s_off[et] = rh < 0 ? -1 : static_cast<int64_t>(rh) * t_pad;
         s_m[et] = m;
-        for (int u = 0; u < 4; ++u) s_red[u][et] = kWeights ? 0.f : -INFINITY;
+        for (int u = 0; u < 8; ++u) s_red[u][et] = kWeights ? 0.f : -INFINITY;
       }
       if (!group_sync(ebar, phase)) { ok = false; break; }
       if (x.en.narrow) {
@@ -758,7 +785,8 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
         // rho % Hkv; value i is (row i / G of the entry, query head i % G of the head)
         const int rho = q * 32 + lane, j = rho & (g.Hkv - 1), tl = rho >> p.log2Hkv;
         const int ng = x.nrow << g.log2G;
-        float* st = stage + static_cast<size_t>(q * 32 + lane) * (g.ncol + 4);
+        const int sc = g.ncol >> 1;   // columns staged at a time
+        float* st = stage + static_cast<size_t>((warp - 2) * 32 + lane) * (sc + 4);
         float run[kGNarrowPer];
 #pragma unroll
         for (int i = 0; i < kGNarrowPer; ++i) run[i] = kWeights ? 0.f : -INFINITY;
@@ -766,55 +794,60 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
           const int a = static_cast<int>(k % kGKAcc);
           const bool ready = mbar_wait(&tfull[a], (k / kGKAcc) & 1);
           if (!__all_sync(0xffffffffu, ready && !abort_flag)) { ok = false; break; }
-          if (hf == 0) {
+          if (hf == static_cast<int>(k & 1)) {   // the two teams of four warps take turns
             tc_fence_after();
-            for (int cb = 0; cb < x.cols; cb += 16) {
-              __syncwarp();
-              uint32_t v[32];
-              tmem_ld_32x32b_x16(tq + static_cast<uint32_t>(a * g.ncol + cb), v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                *reinterpret_cast<uint4*>(st + cb + 4 * u) = make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
-            }
-            tc_fence_before();
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&tempty[a]);
-          if (hf == 0) {
             const int t = tb + tl;
             const bool in = t < x.en.len;
             const bool page = t < x.t1;
+            for (int cg = 0; cg < x.cols; cg += sc) {
+              const int ce = min(x.cols, cg + sc);
+              for (int cb = cg; cb < ce; cb += 16) {
+                __syncwarp();
+                uint32_t v[32];
+                tmem_ld_32x32b_x16(tq + static_cast<uint32_t>(a * g.ncol + cb), v);
+                tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < kGNarrowPer; ++i) {
-              if (i < ng) {
+                for (int u = 0; u < 4; ++u)
+                  *reinterpret_cast<uint4*>(st + (cb - cg) + 4 * u) = make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+              }
+              if (ce == x.cols) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tempty[a]);
+              }
+              // a lane reads what it wrote itself
+#pragma unroll
+              for (int i = 0; i < kGNarrowPer; ++i) {
                 const int col = (i >> g.log2G) * g.H + (j << g.log2G) + (i & (G - 1));
-                const float s = st[col];
-                if constexpr (kWeights) {
-                  const __half w = __float2half_rn(in ? ex2_approx(s - s_m[col]) : 0.f);
-                  run[i] += __half2float(w);
-                  if (page && s_off[col] >= 0) P[s_off[col] + t] = w;
-                } else {
-                  run[i] = fmaxf(run[i], in ? s : -INFINITY);
+                if (i < ng && col >= cg && col < ce) {
+                  const float s = st[col - cg];
+                  if constexpr (kWeights) {
+                    const __half w = __float2half_rn(in ? ex2_approx(s - s_m[col]) : 0.f);
+                    run[i] += __half2float(w);
+                    if (page && s_off[col] >= 0) P[s_off[col] + t] = w;
+                  } else {
+                    run[i] = fmaxf(run[i], in ? s : -INFINITY);
+                  }
                 }
               }
             }
+          } else {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[a]);
           }
         }
         if (!ok) break;
-        if (hf == 0) {
-          // lanes of the same KV head join: lane l < Hkv (or every lane) speaks for its head
+        // lanes of the same KV head join: lane l < Hkv (or every lane) speaks for its head
 #pragma unroll
-          for (int i = 0; i < kGNarrowPer; ++i)
-            if (i < ng) {
-              for (int o = 16; o >= g.Hkv; o >>= 1) {
-                const float y = __shfl_xor_sync(0xffffffffu, run[i], o);
-                run[i] = kWeights ? run[i] + y : fmaxf(run[i], y);
-              }
-              const int col = (i >> g.log2G) * g.H + (j << g.log2G) + (i & (G - 1));
-              if (lane < g.Hkv) s_red[q][col] = run[i];
+        for (int i = 0; i < kGNarrowPer; ++i)
+          if (i < ng) {
+            for (int o = 16; o >= g.Hkv; o >>= 1) {
+              const float y = __shfl_xor_sync(0xffffffffu, run[i], o);
+              run[i] = kWeights ? run[i] + y : fmaxf(run[i], y);
             }
-        }
+            const int col = (i >> g.log2G) * g.H + (j << g.log2G) + (i & (G - 1));
+            if (lane < g.Hkv) s_red[hf * 4 + q][col] = run[i];
+          }
       } else {
         const int ncb = (x.cols + 15) / 16;
         float run[4][16];
@@ -879,12 +912,16 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
       if (!group_sync(ebar, phase)) { ok = false; break; }
       if constexpr (!kWeights) {
         if (et < x.cols && s_rh[et] >= 0) {
-          const float m = fmaxf(fmaxf(s_red[0][et], s_red[1][et]), fmaxf(s_red[2][et], s_red[3][et]));
+          float m = s_red[0][et];
+#pragma unroll
+          for (int u = 1; u < 8; ++u) m = fmaxf(m, s_red[u][et]);
           if (m > -INFINITY) atomic_max_f32(&g.mrow[s_rh[et]], m);
         }
       } else {
         if (et < x.cols && s_rh[et] >= 0) {
-          const float L = ((s_red[0][et] + s_red[1][et]) + s_red[2][et]) + s_red[3][et];
+          float L = s_red[0][et];
+#pragma unroll
+          for (int u = 1; u < 8; ++u) L += s_red[u][et];
           g.lpart[x.en.zsrc][static_cast<size_t>(s_rh[et]) * g.n_ch[x.en.zsrc] + x.c] = L;
         }
       }

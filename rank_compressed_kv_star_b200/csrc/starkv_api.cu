@@ -61,6 +61,12 @@
 #ifndef STARKV_ATTEND_BLOCKS
 #define STARKV_ATTEND_BLOCKS 24   // attend form of the group calls: at most so many blocks per cluster
 #endif
+#ifndef STARKV_GK_W
+#define STARKV_GK_W 4
+#endif
+#ifndef STARKV_GK_N
+#define STARKV_GK_N 3
+#endif
 #ifndef STARKV_ROPE_MACS
 #define STARKV_ROPE_MACS (24 << 20)   // rotary append: from so many key-code products on, tensor cores and three launches
 #endif
@@ -1661,8 +1667,8 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
   while (p.nbox < g.ncol && p.nbox < (n_groups > 0 && n_rows > n_groups ? n_rows * g.H : g.H)) p.nbox *= 2;
   p.a_bytes = static_cast<uint32_t>(p.kb) * 16384u;
   p.q_bytes = static_cast<uint32_t>(p.kb) * 2u * g.ncol * 128u;
-  const uint32_t staging = 4u * 32u * (g.ncol + 4) * 4u;
-  const uint32_t budget = 214u * 1024u - staging;
+  const uint32_t staging = 8u * 32u * (g.ncol / 2 + 4) * 4u;
+  const uint32_t budget = 212u * 1024u - staging;
   p.nq = budget >= 2u * p.q_bytes + 3u * p.a_bytes ? 2 : 1;
   p.k_stages = static_cast<int>((budget - p.nq * p.q_bytes) / p.a_bytes);
   if (p.k_stages > 8) p.k_stages = 8;
@@ -1676,20 +1682,26 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
   {
     // tokens per item: enough items for every CTA, each long enough to hide its start
     const int64_t blocks = wide_tiles * g.Hkv * (g.t_pad[0] / 128);
-    int64_t n = blocks / (4 * static_cast<int64_t>(sms));
+    int64_t n = blocks / (STARKV_GK_W * static_cast<int64_t>(sms));
     n = n < 1 ? 1 : (n > 8 ? 8 : n);
     g.chunk_w = static_cast<int>(n) * 128;
     const int unit = 128 / g.Hkv > 16 ? 128 / g.Hkv : 16;
     const int64_t tokens = runs * max0 + (shared ? static_cast<int64_t>(n_rows) * max1 : 0);
-    n = tokens / (3 * static_cast<int64_t>(sms) * unit);
-    const int64_t least = (own_max + 64 * unit - 1) / (64 * unit);   // at most 64 sums of weights per column
+    n = tokens / (STARKV_GK_N * static_cast<int64_t>(sms) * unit);
+    const int64_t least = (own_max + 256 * unit - 1) / (256 * unit);   // at most 256 sums of weights per column
     if (n < least) n = least;
     if (n < 1) n = 1;
     g.chunk_n = static_cast<int>(n) * unit;
   }
-  const int least_chunk = g.chunk_w < g.chunk_n ? g.chunk_w : g.chunk_n;
-  g.n_ch[0] = (g.t_pad[0] + least_chunk - 1) / least_chunk;
-  g.n_ch[1] = ((own_max > 0 ? own_max : 1) + least_chunk - 1) / least_chunk;
+  // sums of weights per column, whichever kind reads its tokens; grows with the bounds, as the
+  // chunks' lengths do not always
+  auto sums = [&](int tokens) {
+    const int unit = 128 / g.Hkv > 16 ? 128 / g.Hkv : 16;
+    const int wide = (tokens + 127) / 128 + 1, narrow = (tokens + unit - 1) / unit + 1;
+    return narrow < 257 ? (narrow > wide ? narrow : wide) : (wide > 257 ? wide : 257);
+  };
+  g.n_ch[0] = sums(g.t_pad[0]);
+  g.n_ch[1] = sums(own_max > 0 ? own_max : 1);
 
   // V pass: one CTA per SM, three 64 KiB stages
   p.v_stages = 3;
@@ -1699,7 +1711,7 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
   // positions of K items and V units are 32-bit
   const int64_t k_items = wide_tiles * g.Hkv * ((g.t_pad[0] + g.chunk_w - 1) / g.chunk_w) +
                           (runs + (shared ? n_rows : 0)) * static_cast<int64_t>((own_max + g.chunk_n) / g.chunk_n + 1);
-  if (k_items > (1 << 30) || v_tiles * ((own_max + kGVTok) / kGVTok + 1) > (1 << 30)) return STARKV_ERR_UNSUPPORTED;
+  if (k_items > (1 << 30) / (((g.chunk_w >> 7) + g.chunk_n) * (4 + (g.ncol >> 4)) + kGKStart) || v_tiles * ((own_max + kGVTok) / kGVTok + 1) > (1 << 30)) return STARKV_ERR_UNSUPPORTED;
 
   // finish: column tiles as wide as 256, halved while the grid would leave SMs idle
   p.f_mt = (g.d + 127) / 128;
