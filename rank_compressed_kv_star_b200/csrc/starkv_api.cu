@@ -61,12 +61,6 @@
 #ifndef STARKV_ATTEND_BLOCKS
 #define STARKV_ATTEND_BLOCKS 24   // attend form of the group calls: at most so many blocks per cluster
 #endif
-#ifndef STARKV_GK_W
-#define STARKV_GK_W 4
-#endif
-#ifndef STARKV_GK_N
-#define STARKV_GK_N 3
-#endif
 #ifndef STARKV_ROPE_MACS
 #define STARKV_ROPE_MACS (24 << 20)   // rotary append: from so many key-code products on, tensor cores and three launches
 #endif
@@ -1680,14 +1674,27 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
   const int own_max = max0 > max1 ? max0 : max1;                // a row's own pages: also those of a row shorter than its group's
   const int64_t wide_tiles = runs + static_cast<int64_t>(n_rows) * G / g.ncol * 2 + 1;
   {
-    // tokens per item: enough items for every CTA, each long enough to hide its start
-    const int64_t blocks = wide_tiles * g.Hkv * (g.t_pad[0] / 128);
-    int64_t n = blocks / (STARKV_GK_W * static_cast<int64_t>(sms));
-    n = n < 1 ? 1 : (n > 8 ? 8 : n);
-    g.chunk_w = static_cast<int>(n) * 128;
+    // steps of 128 tokens per wide item: an item costs about two steps beside its own
+    const int64_t steps = g.t_pad[0] / 128;
+    int n_w = 1;
+    if (shared) {
+      // enough items for every CTA; the rows' own (narrow) items fill up the last wave
+      const int64_t n = wide_tiles * g.Hkv * steps / (4 * static_cast<int64_t>(sms));
+      n_w = static_cast<int>(n < 1 ? 1 : (n > 8 ? 8 : n));
+    } else {
+      // whole waves of items: the count whose waves take the fewest steps
+      const int64_t tiles = runs + static_cast<int64_t>(n_rows) * G / g.ncol;
+      int64_t best = 0;
+      for (int n = 8; n > 0; --n) {
+        const int64_t chunks = (steps + n - 1) / n, len = (steps + chunks - 1) / chunks;
+        const int64_t cost = (tiles * g.Hkv * chunks + sms - 1) / sms * (len + 2);
+        if (n == 8 || cost < best) { best = cost; n_w = static_cast<int>(len); }
+      }
+    }
+    g.chunk_w = n_w * 128;
     const int unit = 128 / g.Hkv > 16 ? 128 / g.Hkv : 16;
     const int64_t tokens = runs * max0 + (shared ? static_cast<int64_t>(n_rows) * max1 : 0);
-    n = tokens / (STARKV_GK_N * static_cast<int64_t>(sms) * unit);
+    int64_t n = tokens / (3 * static_cast<int64_t>(sms) * unit);
     const int64_t least = (own_max + 256 * unit - 1) / (256 * unit);   // at most 256 sums of weights per column
     if (n < least) n = least;
     if (n < 1) n = 1;
@@ -1713,27 +1720,46 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
                           (runs + (shared ? n_rows : 0)) * static_cast<int64_t>((own_max + g.chunk_n) / g.chunk_n + 1);
   if (k_items > (1 << 30) / (((g.chunk_w >> 7) + g.chunk_n) * (4 + (g.ncol >> 4)) + kGKStart) || v_tiles * ((own_max + kGVTok) / kGVTok + 1) > (1 << 30)) return STARKV_ERR_UNSUPPORTED;
 
-  // finish: column tiles as wide as 256, halved while the grid would leave SMs idle
+  // finish
   p.f_mt = (g.d + 127) / 128;
-  p.f_rows = 256 / G < n_rows ? 256 / G : (n_rows > 0 ? n_rows : 1);
-  while (p.f_rows > 1 && p.f_rows * G > 32 &&
-         static_cast<int64_t>(g.Hkv) * p.f_mt * ((n_rows + p.f_rows - 1) / p.f_rows) < sms)
-    p.f_rows = (p.f_rows + 1) / 2;
+  // ring stages (up to four), segments listed per column (32, or 8 of many columns) and
+  // dynamic shared memory for `cols` columns; returns the CTAs per SM, two where two stages fit
+  auto f_fit = [&](int cols, int* stages, int* log2cap, size_t* smem) {
+    const size_t stage = 16384u + 2u * cols * 128u;
+    *log2cap = cols <= 64 ? 5 : 3;
+    const size_t lists = (static_cast<size_t>(cols) << *log2cap) * 12;
+    const size_t two = 114 * 1024 - 19 * 1024 - 1200 - lists;   // 18 KB static, 1 KB reserved
+    const int per_sm = two / stage >= 2 && two >= static_cast<size_t>(cols) * 512 ? 2 : 1;
+    const int n = static_cast<int>((per_sm == 2 ? two : 190u * 1024u) / stage);
+    *stages = n > 4 ? 4 : n;
+    size_t ring = *stages * stage;
+    if (ring < static_cast<size_t>(cols) * 512) ring = static_cast<size_t>(cols) * 512;
+    *smem = 1024 + ring + (3 * *stages + 2) * sizeof(uint64_t) + lists;
+    return per_sm;
+  };
+  {
+    // rows per column tile (as many as 256 columns, as few as 32): the SM with the most tiles
+    // works off their columns one after the other, and each of its waves costs as much as
+    // 64 columns more (1024 rows of 8 KV heads: 160 tiles of 256 columns took 78 us)
+    const int most = 256 / G < n_rows ? 256 / G : (n_rows > 0 ? n_rows : 1);
+    const int64_t per_row = static_cast<int64_t>(g.Hkv) * p.f_mt;
+    int64_t best = 0;
+    for (int f = most; f > 0; --f) {
+      const int cols = (f * G + 15) / 16 * 16;
+      if (f < most && (cols < 32 || f * G % 16 != 0)) continue;
+      const int64_t tiles = per_row * ((n_rows + f - 1) / f);
+      int stages, log2cap;
+      size_t smem;
+      const int per_sm = f_fit(cols, &stages, &log2cap, &smem);
+      const int64_t cost = (tiles + sms - 1) / sms * cols + (tiles + per_sm * sms - 1) / (per_sm * sms) * 64;
+      if (f == most || cost < best) { best = cost; p.f_rows = f; }
+    }
+  }
   p.f_tiles = n_rows > 0 ? (n_rows + p.f_rows - 1) / p.f_rows : 1;
   p.f_npad = (p.f_rows * G + 15) / 16 * 16;
-  p.f_log2cap = p.f_npad <= 64 ? 5 : 3;   // segments listed per column: 32, or 8 of many columns
   p.f_stage_bytes = 16384u + 2u * p.f_npad * 128u;
-  // as many stages (up to four) as let two CTAs share an SM, else what one CTA holds
-  p.f_stages = static_cast<int>(84u * 1024u / p.f_stage_bytes);
-  if (p.f_stages < 3) p.f_stages = static_cast<int>(190u * 1024u / p.f_stage_bytes);
-  if (p.f_stages > 4) p.f_stages = 4;
-  {
-    size_t ring = static_cast<size_t>(p.f_stages) * p.f_stage_bytes;
-    if (ring < static_cast<size_t>(p.f_npad) * 512) ring = static_cast<size_t>(p.f_npad) * 512;
-    p.f_smem = 1024 + ring + (3 * p.f_stages + 2) * sizeof(uint64_t) + (static_cast<size_t>(p.f_npad) << p.f_log2cap) * 12;
-  }
-  // split R over clusters while the grid stays within one wave (two CTAs per SM where they fit)
-  const int f_per_sm = p.f_smem + 19 * 1024 <= 114u * 1024u ? 2 : 1;   // 18 KB static, 1 KB reserved
+  const int f_per_sm = f_fit(p.f_npad, &p.f_stages, &p.f_log2cap, &p.f_smem);
+  // split R over clusters while the grid stays within one wave
   p.f_ks = 1;
   while (p.f_ks < 8 && static_cast<int64_t>(g.Hkv) * p.f_mt * p.f_tiles * p.f_ks * 2 <= f_per_sm * sms &&
          g.R / 64 >= p.f_ks * 2)
