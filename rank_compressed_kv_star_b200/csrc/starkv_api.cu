@@ -58,9 +58,6 @@
 #ifndef STARKV_APP_KS_MAX
 #define STARKV_APP_KS_MAX 4     // largest cluster splitting the V-code GEMM's K range
 #endif
-#ifndef STARKV_ATTEND_BLOCKS
-#define STARKV_ATTEND_BLOCKS 24   // attend form of the group calls: at most so many blocks per cluster
-#endif
 #ifndef STARKV_ROPE_MACS
 #define STARKV_ROPE_MACS (24 << 20)   // rotary append: from so many key-code products on, tensor cores and three launches
 #endif
@@ -1795,47 +1792,64 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
     const int64_t blocks = tiles * ((max0 + kGATok - 1) / kGATok) +
                            (shared ? static_cast<int64_t>(n_rows) * ((max1 + kGATok - 1) / kGATok) : 0);
     const int most = p.at_v_stages >= 3 ? max_attend_clusters(g.C, p.at_smem) : 0;
-    if (p.at_v_stages >= 3 && blocks <= static_cast<int64_t>(STARKV_ATTEND_BLOCKS) * most) {
+    // The cluster kernel reads an entry's pages once per row tile, the separate passes once; it
+    // saves their launches.  So: while the blocks read again stay below some per cluster (a block
+    // takes it as long as one and a half of the passes').  Measured, cluster kernel : passes, in us:
+    // 32 KV heads, R = 2048: 1 row x 16000 tokens 75 : 103, 16 x 1000 65 : 66, 16 x 4000 127 : 89,
+    // 64 x 500 100 : 72, 16 x (4 x 1500) 139 : 167; 8 KV heads, R = 512: 1 x 500 27 : 39,
+    // 16 x 1000 44 : 55, 64 x 500 53 : 59, 16 x 4000 62 : 55, 64 x 2000 97 : 67.
+    const int64_t b0 = (max0 + kGATok - 1) / kGATok;
+    const int64_t own_b = shared ? static_cast<int64_t>(n_rows) * ((max1 + kGATok - 1) / kGATok) : 0;
+    const int64_t about = n_rows / rows + runs / 2, once = runs * b0 + own_b,
+                  read = (about > runs ? about : runs) * b0 + own_b;
+    if (p.at_v_stages >= 3 && 2 * read - 3 * once <= 11 * static_cast<int64_t>(most)) {
       g.a_rows = rows;
       p.at_clusters = blocks < 1 ? 1 : (blocks < most ? static_cast<int>(blocks) : most);
     }
   }
 
   const size_t N = static_cast<size_t>(n_rows), rh = N * g.H;
-  size_t off = 256;   // the status word
-  auto take = [&](size_t bytes) { const size_t o = off; off = align_up(off + bytes, 256); return o; };
-  p.ent_off = take(static_cast<size_t>(g.E) * sizeof(GroupEntry));
-  p.kpre_off = take((static_cast<size_t>(g.E) + 1) * 4);
-  p.vpre_off = take((static_cast<size_t>(g.E) + 1) * 4);
-  p.apre_off = take((static_cast<size_t>(g.E) + 1) * 4);
-  p.row_ent_off = take(N * 4);
-  p.row_use_off = take(N * 4);
-  p.used_off = take(4);
-  const int64_t tiles = g.a_rows > 0 ? runs + n_rows / g.a_rows + 1 + (shared ? n_rows : 0) : v_tiles;
-  p.tfirst_off = take(static_cast<size_t>(tiles) * 4);
-  p.tlast_off = take(static_cast<size_t>(tiles) * 4);
-  p.mrow_off = take(rh * 4);
-  p.qh_off = take(rh * g.r * 2);
-  p.ql_off = take(rh * g.r * 2);
-  for (int s = 0; s < (shared ? 2 : 1); ++s) {
-    p.z_off[s] = take(rh * g.R * 4);
-    if (g.a_rows > 0) {
-      p.m_off[s] = take(rh * 4);
-      p.l_off[s] = take(rh * g.C * 4);
-    } else {
-      p.lpart_off[s] = take(rh * g.n_ch[s] * 4);
-      p.p_off[s] = take(rh * g.t_pad[s] * 2);
+  // the larger of both forms' sizes, so that a workspace for the largest bounds serves all calls
+  size_t off = 0;
+  auto layout = [&](bool attend) {
+    off = 256;   // the status word
+    auto take = [&](size_t bytes) { const size_t o = off; off = align_up(off + bytes, 256); return o; };
+    p.ent_off = take(static_cast<size_t>(g.E) * sizeof(GroupEntry));
+    p.kpre_off = take((static_cast<size_t>(g.E) + 1) * 4);
+    p.vpre_off = take((static_cast<size_t>(g.E) + 1) * 4);
+    p.apre_off = take((static_cast<size_t>(g.E) + 1) * 4);
+    p.row_ent_off = take(N * 4);
+    p.row_use_off = take(N * 4);
+    p.used_off = take(4);
+    const int64_t tiles = attend ? runs + n_rows / g.a_rows + 1 + (shared ? n_rows : 0) : v_tiles;
+    p.tfirst_off = take(static_cast<size_t>(tiles) * 4);
+    p.tlast_off = take(static_cast<size_t>(tiles) * 4);
+    p.mrow_off = take(rh * 4);
+    p.qh_off = take(rh * g.r * 2);
+    p.ql_off = take(rh * g.r * 2);
+    for (int s = 0; s < (shared ? 2 : 1); ++s) {
+      p.z_off[s] = take(rh * g.R * 4);
+      if (attend) {
+        p.m_off[s] = take(rh * 4);
+        p.l_off[s] = take(rh * g.C * 4);
+      } else {
+        p.lpart_off[s] = take(rh * g.n_ch[s] * 4);
+        p.p_off[s] = take(rh * g.t_pad[s] * 2);
+      }
     }
-  }
-  if (g.a_rows > 0) {
-    const size_t cols = static_cast<size_t>(p.at_clusters) * kGACols;
-    p.carry_off = take(cols * g.R * 4);
-    p.mcarry_off = take(cols * 4);
-    p.lcarry_off = take(cols * g.C * 4);
-  } else {
-    p.carry_off = take(static_cast<size_t>(p.v_ctas) * kGVTile * kGVTile * 4);
-  }
-  p.total = off;
+    if (attend) {
+      const size_t cols = static_cast<size_t>(p.at_clusters) * kGACols;
+      p.carry_off = take(cols * g.R * 4);
+      p.mcarry_off = take(cols * 4);
+      p.lcarry_off = take(cols * g.C * 4);
+    } else {
+      p.carry_off = take(static_cast<size_t>(p.v_ctas) * kGVTile * kGVTile * 4);
+    }
+    return off;
+  };
+  p.total = g.a_rows > 0 ? layout(false) : 0;
+  const size_t used = layout(g.a_rows > 0);
+  if (used > p.total) p.total = used;
   return STARKV_OK;
 }
 
