@@ -1693,6 +1693,7 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
     const int64_t tokens = runs * max0 + (shared ? static_cast<int64_t>(n_rows) * max1 : 0);
     int64_t n = tokens / (3 * static_cast<int64_t>(sms) * unit);
     const int64_t least = (own_max + 256 * unit - 1) / (256 * unit);   // at most 256 sums of weights per column
+    if (n > 64) n = 64;   // bounds far above the real lengths
     if (n < least) n = least;
     if (n < 1) n = 1;
     g.chunk_n = static_cast<int>(n) * unit;
@@ -1712,10 +1713,12 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
   p.v_ctas = sms;
   p.v_smem = 1024 + static_cast<size_t>(p.v_stages) * (kGVABytes + kGVBBytes) + (2 * p.v_stages + 8) * sizeof(uint64_t);
   const int64_t v_tiles = g.n_rt * (runs + static_cast<int64_t>(n_rows) * g.H / kGVTile + 1 + (shared ? n_rows : 0));
-  // positions of K items and V units are 32-bit
-  const int64_t k_items = wide_tiles * g.Hkv * ((g.t_pad[0] + g.chunk_w - 1) / g.chunk_w) +
-                          (runs + (shared ? n_rows : 0)) * static_cast<int64_t>((own_max + g.chunk_n) / g.chunk_n + 1);
-  if (k_items > (1 << 30) / (((g.chunk_w >> 7) + g.chunk_n) * (4 + (g.ncol >> 4)) + kGKStart) || v_tiles * ((own_max + kGVTok) / kGVTok + 1) > (1 << 30)) return STARKV_ERR_UNSUPPORTED;
+  // positions in the K items' costs and in the V units are 32-bit
+  const int64_t k_cost =
+      wide_tiles * g.Hkv * ((g.t_pad[0] + g.chunk_w - 1) / g.chunk_w) * ((g.chunk_w >> 7) * (4 + g.ncol / 16) + kGKStart) +
+      (runs + (shared ? n_rows : 0)) * static_cast<int64_t>((own_max + g.chunk_n) / g.chunk_n + 1) *
+          (static_cast<int64_t>(g.chunk_n) * g.Hkv / 128 * (2 + g.ncol / 16) + kGKStart);
+  if (k_cost > (1 << 30) || v_tiles * ((own_max + kGVTok) / kGVTok + 1) > (1 << 30)) return STARKV_ERR_UNSUPPORTED;
 
   // finish
   p.f_mt = (g.d + 127) / 128;
