@@ -1988,10 +1988,13 @@ struct GroupFinishParams {
   uint32_t stage_bytes, tmem_cols;
 };
 
-constexpr int kGFThreads = 320;
-constexpr int kGFConv = kGFThreads - 64;
+// Beside the copying and the multiplying warp: the converters, whose arithmetic bounds the
+// kernel (some 300 instructions per eight values of a column); 16 warps where a CTA has its SM
+// to itself, else 8 in each of two.  96 registers for either.
+constexpr int kGFConvOne = 512, kGFConvTwo = 256;
 
-__global__ void __launch_bounds__(kGFThreads, 2)
+template <bool kAttend>
+__global__ void __maxnreg__(96)
 group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams p) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
@@ -2014,6 +2017,7 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
   __shared__ int32_t s_ent[2][256], s_i0[2][256], s_n[2][256], s_col[2][256];   // per source: first CTA, CTAs, column within the V tile
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int conv_threads = blockDim.x - 64;
   int xi = blockIdx.x;
   const int j = xi % g.Hkv; xi /= g.Hkv;
   const int mt = xi % p.n_mt;
@@ -2024,9 +2028,9 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
   const int ncols = p.rows_tile << g.log2G;
 
   if (tid == 0) {
-    for (int s = 0; s < S; ++s) { mbar_init(&full[s], 1); mbar_init(&conv[s], kGFConv >> p.log2cg); mbar_init(&empty[s], 1); }
+    for (int s = 0; s < S; ++s) { mbar_init(&full[s], 1); mbar_init(&conv[s], conv_threads >> p.log2cg); mbar_init(&empty[s], 1); }
     mbar_init(done, 1);
-    mbar_init(cbar, kGFConv);
+    mbar_init(cbar, conv_threads);
     fence_mbar_init();
     prefetch_tensormap(&bvmap);
   }
@@ -2076,11 +2080,11 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
     const int et = tid - 64;
     griddep_wait();
     const int n_src = g.shared ? 2 : 1;
-    const bool attend = p.m[0] != nullptr;
+    constexpr bool attend = kAttend;
     uint32_t phase = 0;
     const GroupEntry* ent = g.ent;
     if (g.E <= kGSmemE) {
-      for (int i = et; i < g.E * 4; i += kGFConv)
+      for (int i = et; i < g.E * 4; i += conv_threads)
         reinterpret_cast<uint4*>(s_tab.ent)[i] = reinterpret_cast<const uint4*>(g.ent)[i];
       ent = s_tab.ent;
     }
@@ -2094,7 +2098,7 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
       return m > -INFINITY ? ex2_approx(m - s_M[bl]) : 1.f;
     };
     // the entries of each column: -1 where it has none, or none of their tokens
-    for (int x = et; x < 2 * ncols; x += kGFConv) {
+    for (int x = et; x < 2 * ncols; x += conv_threads) {
       const int sr = x >= ncols ? 1 : 0, c = x - sr * ncols, row = row0 + (c >> g.log2G);
       int e = -1;
       if (sr < n_src && row < g.n_rows) {
@@ -2113,7 +2117,7 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
       return p.carry_at + (attend ? place * g.R : (place - rt_at) * kGVTile);
     };
     auto places = [&]() {
-      for (int x = et; x < 2 * ncols; x += kGFConv) {
+      for (int x = et; x < 2 * ncols; x += conv_threads) {
         const int sr = x >= ncols ? 1 : 0, c = x - sr * ncols;
         const int row = row0 + (c >> g.log2G), h = (j << g.log2G) + (c & ((1 << g.log2G) - 1));
         int i0 = 0, n = 0, place = 0;
@@ -2132,7 +2136,7 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
         s_col[sr][c] = place;
       }
       if (!group_sync(cbar, phase)) ok = false;
-      for (int x = et; x < ncols << p.log2cap; x += kGFConv) {
+      for (int x = et; x < ncols << p.log2cap; x += conv_threads) {
         const int c = x >> p.log2cap, k = x & ((1 << p.log2cap) - 1), n0 = s_n[0][c];
         if (k < n0 + s_n[1][c]) s_off[x] = k < n0 ? seg_off(0, c, k) : seg_off(1, c, k - n0);
       }
@@ -2141,7 +2145,7 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
       places();
       if (!group_sync(cbar, phase)) ok = false;
       // M, 1 / L and each segment's exp2(m - M): a warp per column, a lane per segment
-      for (int c = warp - 2; c < ncols; c += kGFConv / 32) {
+      for (int c = warp - 2; c < ncols; c += (conv_threads >> 5)) {
         const int row = row0 + (c >> g.log2G), h = (j << g.log2G) + (c & ((1 << g.log2G) - 1));
         const size_t o = static_cast<size_t>(row) * g.H + h;
         const int n0 = s_n[0][c], n = n0 + s_n[1][c];
@@ -2181,9 +2185,9 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
       // 1 / L of every column: its chunks' sums by as many lanes as there are threads for, four
       // loads in flight each
       int log2t = 0;
-      while (log2t < 5 && (ncols << (log2t + 1)) <= kGFConv) ++log2t;
+      while (log2t < 5 && (ncols << (log2t + 1)) <= conv_threads) ++log2t;
       const int t = 1 << log2t;
-      for (int c0 = 0; c0 < ncols; c0 += kGFConv >> log2t) {
+      for (int c0 = 0; c0 < ncols; c0 += conv_threads >> log2t) {
         const int c = c0 + (et >> log2t), i0 = et & (t - 1);
         float L = 0.f;
         if (c < ncols) {
@@ -2209,7 +2213,7 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
       }
     }
     if (!group_sync(cbar, phase)) ok = false;
-    const int cthr = kGFConv >> p.log2cg, cgrp = et / cthr;   // threads of a group, this thread's group
+    const int cthr = conv_threads >> p.log2cg, cgrp = et / cthr;   // threads of a group, this thread's group
     for (int i = 0; i < n_stages && ok; ++i) {
       const int s = i % S;
       const int kr = k0 + i * 64;
@@ -2324,7 +2328,7 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
   const int n_used = *g.n_used;
   const int per = (p.npad + KS - 1) / KS;
   const int n_lo = ks * per, n_hi = min(p.npad, n_lo + per);
-  for (int x = tid; x < (n_hi - n_lo) * 32; x += kGFThreads) {
+  for (int x = tid; x < (n_hi - n_lo) * 32; x += blockDim.x) {
     const int n = n_lo + x / 32, m = (x % 32) * 4, dm = mt * 128 + m;
     const int row = row0 + (n >> g.log2G);
     if (n >= ncols || row >= n_used || dm >= g.d || g.row_ent[row] < 0) continue;
