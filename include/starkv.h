@@ -166,19 +166,20 @@ typedef struct {
 /*
  * starkv_rope_compress_append -- starkv_compress_append with the rotary
  * position embedding applied on the way, and the new tokens' queries rotated
- * in the same launch.
+ * in the same call.
  *
  *   c_K[b,j,:] = Rot(positions[b]) k[b,j,:] . A_K[j]      c_V[b,:] = v[b,:] . A_V
  *   q_out[b,h,:] = Rot(positions[b]) q[b,h,:]
  *
- * The rotated key is not rounded before its code is formed (fp32 throughout, one
- * rounding to fp16); q_out is rounded to fp16 and is what starkv_paged_decode
- * and its kin take as q.
+ * A code rounds once to fp16: the rotated key goes into its sum in fp32, or for
+ * many rows as two fp16 halves (22 bits), and the sum is fp32.  q_out is rounded
+ * to fp16 and is what starkv_paged_decode and its kin take as q.
  *
  *   rope          host struct, see above
  *   q             fp16 [batch][H][d], or NULL: no queries to rotate
  *   q_out         fp16 [batch][H][d]; may be q itself (rotated in place), must
- *                 not overlap it otherwise; ignored when q is NULL
+ *                 not overlap it otherwise, nor any other buffer of the call;
+ *                 ignored when q is NULL
  *   the rest      as in starkv_compress_append
  *
  * A position outside [0, max_position) skips the row's codes (flagged
@@ -362,8 +363,11 @@ starkv_status starkv_paged_prefill(const starkv_layer_desc* desc, int32_t n_seqs
  * clamped and flagged in the status word (STARKV_FLAG_BAD_SEQ_LEN,
  * STARKV_FLAG_BAD_ROW_OFFSET, STARKV_FLAG_BAD_BLOCK_ID; the affected rows are
  * undefined).  Accumulation is fp32; attention weights enter the V contraction
- * as fp16.  Calls that share a workspace must be ordered on one stream.  At
- * most 2^20 rows.  The method pages have no counterpart to this entry point.
+ * as fp16.  Calls that share a workspace must be ordered on one stream.  A
+ * workspace for the largest counts and bounds also serves smaller ones.
+ * STARKV_ERR_UNSUPPORTED beyond 2^20 rows, for bounds above 2^30, or where rows
+ * times lengths pass the 32-bit positions of the passes' work lists.  The
+ * method pages have no counterpart to this entry point.
  */
 size_t starkv_shared_workspace_bytes(const starkv_layer_desc* desc, int32_t n_groups, int32_t batch,
                                      int32_t max_shared_len, int32_t max_own_len);

@@ -11,7 +11,8 @@
 //   M[b,h]   = max_t s          w[b,h,t] = fp16(exp2(s - M))        L = sum_t w
 //   out[b,h] = (sum_t w c_V[t] / L) . B_V[:, g(h) d : (g(h)+1) d]
 // The maximum is taken over both entries before any weight is formed, so the
-// partial sums of a row simply add up.  Launches, all on the caller's stream:
+// partial sums of a row simply add up.  Launches, all on the caller's stream (small calls
+// take group_attend between 1 and 5, with a running maximum per cluster, see there):
 //   1. group_absorb           q~ = log2(e) scale q . B_K^T in fp16 hi + lo
 //                             halves; the entry tables (one extra CTA); M = -inf
 //   2. group_kpass<maxima>    S = c_K . q~ on tcgen05, column maxima only
@@ -79,7 +80,6 @@ struct GroupGeom {
 
 constexpr int kGVTile = 256;    // V pass: columns (row, head) and rows of R per tile
 constexpr int kGVTok = 64;      // V pass: tokens per unit
-constexpr int kGNarrowCols = 128;
 constexpr int kGNarrowPer = 16;
 
 // Column tiles of an entry with `cols` (row, head) columns, and their width.
@@ -103,12 +103,10 @@ __device__ __forceinline__ int gk_tiles(int nrows, const GroupGeom& g) {
 // ================================================================= tables
 // What an item of the K pass costs, for the partition of the items over the CTAs: its
 // steps, a wide one by its columns (128 tokens by 16 columns are one accumulator block of
-// a warp), plus its start.  By number instead of cost, a call of 64 rows over 8192 shared
-// and up to 256 own tokens (32 heads) took 274 us, its last CTAs twice the median.
-#ifndef STARKV_GK_START
-#define STARKV_GK_START 8
-#endif
-constexpr int kGKStart = STARKV_GK_START;
+// a warp), plus its start.  By number instead of cost, the weights pass of 64 rows over
+// 8192 shared and up to 256 own tokens (32 heads) had CTAs of twice the median's time: 94 us
+// against 47 (with three producer warps and both teams on narrow items).
+constexpr int kGKStart = 8;
 __device__ __forceinline__ int gk_cost(const GroupEntry& en, const GroupGeom& g, int log2Hkv) {
   if (en.narrow) return (g.chunk_n >> (7 - log2Hkv)) * (2 + ((en.nrows * g.H) >> 4)) + kGKStart;
   return (g.chunk_w >> 7) * (4 + ((en.k_per << g.log2G) >> 4)) + kGKStart;
@@ -414,13 +412,16 @@ __device__ __forceinline__ int32_t entry_of(const GroupTables& t, int32_t x) {
 // of a wide entry is one KV head, one tile of rows and one chunk of tokens, its
 // tiles 128 tokens of the head (one 16-token x 64-code box per page) and its
 // columns the tile's (row, query head of the KV head) pairs.  An item of a
-// narrow entry is one chunk of tokens of all heads (see gk_narrow).  Warp 0
-// issues the copies, warp 1 the MMAs into a ring of accumulators, warps 2..9
+// narrow entry is one chunk of tokens of all heads (see gk_narrow).  Warps 0, 10
+// and 11 issue the copies, warp 1 the MMAs into a ring of accumulators, warps 2..9
 // drain them: wide, each takes one lane quarter and every other block of 16
 // columns; narrow, four of them (the two fours take turns) stage their quarter in
-// shared memory and each lane reads its own head's columns.  The weights pass forms S a second time
-// rather than keeping it: r / R of the V pass's products against 8 bytes of
-// traffic per logit.
+// shared memory and each lane reads its own head's columns.  The weights pass forms
+// S a second time rather than keeping it: r / R of the V pass's products against 8
+// bytes of traffic per logit.
+// Bound by issue, not by bytes: 64 rows over 8192 + up to 256 tokens (32 heads, r = 64,
+// 34 MB + of codes) take 45 us for the maxima (a wide step 1.0 us, eight 2 KB boxes)
+// and 47 for the weights (1.5 us a step: exp2, rounding and stores of 64 x 128 values).
 struct GroupKParams {
   GroupGeom g;
   const int32_t* tables;     // rows of g.MB entries
@@ -944,6 +945,8 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
 // U / n)).  The sum of a tile that begins in a CTA's range goes to the Z matrix
 // of its source, that of a tile carried over from the CTA before goes to the
 // CTA's carry slot, so a tile's partial sums have fixed places and order.
+// Bound by the copies into shared memory: a unit of 256 columns brings 64 KB in 0.95 us
+// (10 TB/s over the SMs), its MMAs take 0.75; 64 rows x 32 heads over 8192 tokens: 71 us.
 struct GroupVParams {
   GroupGeom g;
   const int32_t* tables;
@@ -1254,6 +1257,8 @@ group_vpass_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_consta
 // issues the Z products, 4..7 gather logits and store Z, 8..11 take maxima and form
 // weights (a thread per column, two teams on alternate parts), 12 tells the
 // other CTAs that a block of weights has been consumed here.
+// Bound by the scalar latency of the maxima and weights warps, about 3 us per block and
+// cluster of 8, 5 of 2; one row over 1500 tokens of 32 heads, R = 2048: 12 us of the call's 38.
 struct GroupAttendParams {
   GroupGeom g;
   const int32_t* tables;
@@ -1963,11 +1968,13 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 
 // ================================================================== finish
 // out^T (128 rows of d x columns) = B_V^T . (Z / L)^T for the (row, query head)
-// columns of one KV head, with Z / L formed on the fly: eight converter warps add
+// columns of one KV head, with Z / L formed on the fly: converter warps add
 // a column's partial sums (its one or two entries, in a fixed order), scale by
 // 1 / L and split into fp16 hi + lo halves (about 22 bits) in the B operand.
 // K = R is split over a cluster whose fp32 sums are added in rank order.
 // A = 64 x 64 boxes of B_V (MN-major).  A row without tokens gives zeros.
+// Bound by the converters' arithmetic and latency: 64 rows x 32 heads of R = 2048 take
+// 31 us, 616 rows x 32 heads of R = 512 with 95 MB read 42 us.
 struct GroupFinishParams {
   GroupGeom g;
   __half* out;           // [n_rows][H][d]

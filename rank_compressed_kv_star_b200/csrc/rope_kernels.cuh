@@ -1,13 +1,13 @@
 // Rotary compress-and-append: the new tokens' query and key heads are rotated by
 // their positions and the rotated keys' and the values' codes are written to the
-// paged pools, in one launch.
+// paged pools, in one launch for few rows and in three that overlap for many.
 //
 // A head vector x at position p is rotated in pairs (a, b) = (x[i], x[i + rot/2])
 // (or, interleaved, (x[2i], x[2i + 1])), i < rot / 2, by the angle whose cosine
 // and sine stand in row p of the caller's table:
 //   a' = a cos - b sin,  b' = b cos + a sin;     elements from rot on are kept.
-// q_out is the rotated query rounded to fp16.  A rotated key is kept in fp32
-// until its code c_K = k' . A_K[h] is rounded: the code rounds once.
+// q_out is the rotated query rounded to fp16.  A rotated key is kept in fp32 (many rows:
+// in 22 bits) until its code c_K = k' . A_K[h] is rounded: the code rounds once.
 #pragma once
 #include <cstdint>
 #include <cuda_fp16.h>
@@ -235,7 +235,8 @@ __device__ __forceinline__ void rope_q_item(const RopeParams& p, int item) {
                kPrepThreads);
 }
 
-// Grid columns: V-code tiles, K-code items, query items (clusters of KS along y).
+// Few rows.  Grid columns: V-code tiles, K-code items, query items (clusters of KS along y).
+// One row of 32 heads of 128, R = 2048: 6.7 us, of which the 16 MiB of A_V are 2.6.
 __global__ void __launch_bounds__(kPrepThreads, 2)
 rope_append_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap vmap, RopeParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -273,7 +274,8 @@ __global__ void __launch_bounds__(kPrepThreads, 3) rope_q_kernel(RopeParams p) {
 //   D (128 rows x r) = k' (128 x d) . A_K[h] (d x r),
 // the rotated rows written to shared memory as fp16 hi + lo halves (22 bits, so the
 // code still rounds once) in the K-major operand layout, A_K[h] by TMA boxes of 64
-// ranks x 64 rows (MN-major).
+// ranks x 64 rows (MN-major).  A block's chain takes 8 to 10 us (its loads 3 to 5, MMAs
+// 1.5, drain 1); two share an SM.  32 heads x 4096 rows: 46 us alone, 95 with the V codes.
 constexpr int kRRThreads = 512;
 struct RopeRowsParams {
   RopeTable rope;
@@ -431,6 +433,8 @@ rope_vrows_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constan
 // codes.
 //   warp 0: TMA (v K-major, A_V MN-major boxes of 64 x 64); warp 1: MMAs;
 //   warps 4..11: epilogue.
+// 4096 rows, HD = 4096, R = 2048: 53 us on 128 SMs, 1.30 PFLOP/s (0.79 of the measured
+// cuBLAS burst rate), bound by 64 KB of copies per 64-deep step.
 constexpr int kRVThreads = 384;
 struct RopeVParams {
   AppendTarget tgt;

@@ -1629,7 +1629,7 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
   const int64_t cap = static_cast<int64_t>(d->max_blocks_per_seq) * 16;
   if (n_groups < 0 || n_rows < 0 || max0 < 0 || max1 < 0) return STARKV_ERR_INVALID_ARG;
   if ((shared ? max0 / 16 * 16 : max0) > cap || max1 > cap) return STARKV_ERR_INVALID_ARG;   // whole pages are shared
-  if (n_rows > (1 << 20) || n_groups > (1 << 20)) return STARKV_ERR_UNSUPPORTED;
+  if (n_rows > (1 << 20) || n_groups > (1 << 20) || max0 > (1 << 30) || max1 > (1 << 30)) return STARKV_ERR_UNSUPPORTED;
   GroupPlan& p = *gp;
   std::memset(&p, 0, sizeof(p));
   GroupGeom& g = p.g;

@@ -279,3 +279,42 @@ def test_rope_graph_and_stream():
     c.call(g, stream=s)
     s.synchronize()
     c.verify(g)
+
+
+@pytest.mark.parametrize("n,R,Hkv", [(700, 512, 8), (2561, 2048, 2)])
+def test_rope_many_rows_captured_and_chained(n, R, Hkv):
+    """The launches of one call overlap; what follows on the stream sees all of them: a copy, and a call that rotates
+    the first one's result."""
+    L = Layer(33, 16, Hkv, 128, 64, R)
+    c = Case(L, n, 128, False, max_position=4096, form="store")
+    g = c.device()
+    c.call(g)
+    c.verify(g)
+    again = dict(g, q_in=g["q_out"], q_2=torch.empty_like(g["q"]))
+    c.call(again, q="q_in", q_out="q_2")
+    torch.cuda.synchronize()
+    want = [x.clone() for x in (g["q_out"], g["k_cache"], g["v_cache"], again["q_2"])]
+    graph = torch.cuda.CUDAGraph()
+    outs = [torch.empty_like(x) for x in want]
+    with torch.cuda.graph(graph):
+        c.call(g)
+        outs[0].copy_(g["q_out"]), outs[1].copy_(g["k_cache"]), outs[2].copy_(g["v_cache"])
+        c.call(again, q="q_in", q_out="q_2")
+        outs[3].copy_(again["q_2"])
+    for _ in range(5):
+        for x in outs:
+            x.zero_()
+        g["k_cache"].copy_(dev(c.k0)), g["v_cache"].copy_(dev(c.v0)), g["q_out"].zero_(), again["q_2"].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(outs, want):
+            assert torch.equal(x, y)
+    s = torch.cuda.Stream()
+    for _ in range(5):
+        g["q_out"].zero_(), again["q_2"].zero_()
+        torch.cuda.synchronize()
+        c.call(g, stream=s)
+        c.call(again, q="q_in", q_out="q_2", stream=s)
+        s.synchronize()
+        assert torch.equal(again["q_2"], want[3])
+    c.verify(g)

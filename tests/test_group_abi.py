@@ -1,5 +1,7 @@
 """Refusals of the rotary append, shared-prefix decode and cross attention entry
 points: every one is answered on the host, before any launch (no GPU needed)."""
+import random
+
 import pytest
 
 import rank_compressed_kv_star_b200 as S
@@ -78,6 +80,34 @@ def test_group_workspace_bytes():
     assert S.starkv_shared_workspace_bytes(d, 1, 64, 8192, 512) >= a
     assert S.starkv_shared_workspace_bytes(d, 1, 80, 8192, 256) > a
     assert S.starkv_cross_workspace_bytes(d, 8, 64, 1500) > S.starkv_cross_workspace_bytes(d, 8, 32, 1500) > 0
+
+
+@pytest.mark.parametrize("layer", [dict(), dict(num_kv_heads=8, v_rank=512), dict(k_rank=256, head_dim=256, num_heads=16, num_kv_heads=4),
+                                   dict(v_rank=4096), dict(num_heads=64, num_kv_heads=1, v_rank=128)])
+def test_workspace_of_larger_calls_serves_smaller_ones(layer):
+    d = _desc(max_blocks_per_seq=1 << 14, **layer)
+    rng = random.Random(1)
+    size = lambda hi: int(2 ** rng.uniform(0, hi))
+    for _ in range(300):
+        groups, rows, shared, own = size(7), size(10), size(17.5), size(17.5)
+        more = [x + rng.choice((0, 0, 1, 16, x)) for x in (groups, rows, shared, own)]
+        more[2:] = [min(x, 1 << 18) for x in more[2:]]
+        small = S.starkv_shared_workspace_bytes(d, groups, rows, shared, own)
+        large = S.starkv_shared_workspace_bytes(d, *more)
+        assert small > 0 and (large >= small or large == 0)
+        small = S.starkv_cross_workspace_bytes(d, groups, rows, shared)
+        large = S.starkv_cross_workspace_bytes(d, *more[:3])
+        assert small > 0 and (large >= small or large == 0)
+
+
+def test_bounds_past_the_limits_are_refused():
+    d = _desc(max_blocks_per_seq=(1 << 27) - 1)
+    top = ((1 << 27) - 1) * 16
+    for n in (top, (1 << 30) + 1):
+        assert S.starkv_shared_workspace_bytes(d, 1, 4, n, 16) == 0
+        assert S.starkv_shared_workspace_bytes(d, 1, 4, 16, n) == 0
+        assert S.starkv_cross_workspace_bytes(d, 1, 4, n) == 0
+    assert S.starkv_cross_workspace_bytes(d, 1, (1 << 20) + 1, 16) == 0
 
 
 def _rope(max_position=1024, rot_dim=128, interleaved=0, cos_sin=FAKE):
