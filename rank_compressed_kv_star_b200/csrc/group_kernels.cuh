@@ -1992,6 +1992,7 @@ struct GroupFinishParams {
   int k_per_cta;         // rows of R per CTA, a multiple of 64
   int stages;
   int log2cg;            // converter groups: the warps split into 1 << log2cg groups that take stages in turn
+  int log2sub;           // attend: lanes that share an item's segments (16 rows, 4099 tokens: 69 us of the call without, 66 with)
   uint32_t stage_bytes, tmem_cols;
 };
 
@@ -2148,51 +2149,74 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
         if (k < n0 + s_n[1][c]) s_off[x] = k < n0 ? seg_off(0, c, k) : seg_off(1, c, k - n0);
       }
     };
+    int log2t = 0;   // lanes per column in what follows
+    while (log2t < 5 && (ncols << (log2t + 1)) <= conv_threads) ++log2t;
     if (attend) {
       places();
       if (!group_sync(cbar, phase)) ok = false;
-      // M, 1 / L and each segment's exp2(m - M): a warp per column, a lane per segment
-      for (int c = warp - 2; c < ncols; c += (conv_threads >> 5)) {
+      // M, 1 / L and each segment's exp2(m - M): as many lanes per column as there are threads
+      // for, two segments at a time each
+      const int t = 1 << log2t;
+      for (int c0 = 0; c0 < ncols; c0 += conv_threads >> log2t) {
+        const int c = c0 + (et >> log2t), i0 = et & (t - 1);
         const int row = row0 + (c >> g.log2G), h = (j << g.log2G) + (c & ((1 << g.log2G) - 1));
         const size_t o = static_cast<size_t>(row) * g.H + h;
-        const int n0 = s_n[0][c], n = n0 + s_n[1][c];
-        float M = -INFINITY, L = 0.f;
-        for (int b = 0; b < n; b += 32) {   // a further round only for more than 32 segments
-          const int i = b + lane;
-          float m = -INFINITY, l = 0.f;
-          if (i < n) {
-            const int sr = i >= n0 ? 1 : 0, k = i - (sr ? n0 : 0);
-            const size_t oc = static_cast<size_t>(s_i0[sr][c] + k) * kGACols + s_col[sr][c];
-            m = k == 0 ? p.m[sr][o] : p.mcarry[oc];
-            const float* lp = k == 0 ? p.l[sr] + o * g.C : p.lcarry + oc * g.C;
-            float l8[8];
+        const int n0 = c < ncols ? s_n[0][c] : 0, n = c < ncols ? n0 + s_n[1][c] : 0;
+        auto place = [&](int i) {   // of segment i in the carries; the first of a source has its own
+          const int sr = i >= n0 ? 1 : 0;
+          return static_cast<size_t>(s_i0[sr][c] + i - (sr ? n0 : 0)) * kGACols + s_col[sr][c];
+        };
+        auto seg_m = [&](int i) {
+          const int sr = i >= n0 ? 1 : 0;
+          return i == (sr ? n0 : 0) ? p.m[sr][o] : p.mcarry[place(i)];
+        };
+        float M = -INFINITY, L = 0.f, first[2] = {-INFINITY, -INFINITY};
+        for (int b = i0; b < n; b += 2 * t) {
+          float m[2] = {-INFINITY, -INFINITY}, l8[2][8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) l8[u] = u < g.C ? lp[u] : 0.f;
+          for (int v = 0; v < 2; ++v) {
+            const int i = b + v * t;
+            if (i < n) {
+              const int sr = i >= n0 ? 1 : 0;
+              m[v] = seg_m(i);
+              const float* lp = i == (sr ? n0 : 0) ? p.l[sr] + o * g.C : p.lcarry + place(i) * g.C;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) l += l8[u];
+              for (int u = 0; u < 8; ++u) l8[v][u] = u < g.C ? lp[u] : 0.f;
+            } else {
+#pragma unroll
+              for (int u = 0; u < 8; ++u) l8[v][u] = 0.f;
+            }
           }
-          float Mb = m;
-#pragma unroll
-          for (int q = 16; q > 0; q >>= 1) Mb = fmaxf(Mb, __shfl_xor_sync(0xffffffffu, Mb, q));
-          const float Mn = fmaxf(M, Mb);
+          const float Mn = fmaxf(M, fmaxf(m[0], m[1]));
+          L = M > -INFINITY ? L * ex2_approx(M - Mn) : L;
           // a segment whose logits are all NaN or -inf has m = -inf and l = NaN
-          float Lb = i < n ? (m > -INFINITY ? l * ex2_approx(m - Mn) : l) : 0.f;
 #pragma unroll
-          for (int q = 16; q > 0; q >>= 1) Lb += __shfl_xor_sync(0xffffffffu, Lb, q);
-          L = (M > -INFINITY ? L * ex2_approx(M - Mn) : L) + Lb;
+          for (int v = 0; v < 2; ++v) {
+            float l = 0.f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) l += l8[v][u];
+            L += m[v] > -INFINITY ? l * ex2_approx(m[v] - Mn) : l;
+            if (b == i0) first[v] = m[v];
+          }
           M = Mn;
-          if (n <= 32 && i < n && i < 1 << p.log2cap) s_fac[(c << p.log2cap) + i] = m > -INFINITY ? ex2_approx(m - M) : 1.f;
         }
-        if (lane == 0) {
+        float top = M;
+        for (int q = t >> 1; q > 0; q >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, q));
+        L = M > -INFINITY ? L * ex2_approx(M - top) : L;
+        for (int q = t >> 1; q > 0; q >>= 1) L += __shfl_xor_sync(0xffffffffu, L, q);
+        if (n <= 32)
+          for (int i = i0, v = 0; i < n && i < 1 << p.log2cap; i += t, ++v) {
+            const float m = v == 0 ? first[0] : v == 1 ? first[1] : seg_m(i);
+            s_fac[(c << p.log2cap) + i] = m > -INFINITY ? ex2_approx(m - top) : 1.f;
+          }
+        if (c < ncols && i0 == 0) {
           s_il[c] = L == 0.f ? 0.f : 1.f / L;   // no token at all: L = 0 and the result is 0
-          s_M[c] = M;
+          s_M[c] = top;
         }
       }
     } else {
       // 1 / L of every column: its chunks' sums by as many lanes as there are threads for, four
       // loads in flight each
-      int log2t = 0;
-      while (log2t < 5 && (ncols << (log2t + 1)) <= conv_threads) ++log2t;
       const int t = 1 << log2t;
       for (int c0 = 0; c0 < ncols; c0 += conv_threads >> log2t) {
         const int c = c0 + (et >> log2t), i0 = et & (t - 1);
@@ -2220,7 +2244,12 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
       }
     }
     if (!group_sync(cbar, phase)) ok = false;
-    const int cthr = conv_threads >> p.log2cg, cgrp = et / cthr;   // threads of a group, this thread's group
+    // threads of a group, counted without the sub lanes (which share an item's segments); this
+    // thread's group, its number in the group and its sub lane
+    const int log2sub = kAttend ? p.log2sub : 0;
+    const int cthr = conv_threads >> (p.log2cg + log2sub), cgrp = et / (conv_threads >> p.log2cg);
+    const int sub = (et >> 3) & ((1 << log2sub) - 1);
+    const int eg = et & ((conv_threads >> p.log2cg) - 1), en = (eg & 7) | (eg >> (3 + log2sub) << 3);
     for (int i = 0; i < n_stages && ok; ++i) {
       const int s = i % S;
       const int kr = k0 + i * 64;
@@ -2238,7 +2267,7 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
       // where a thread has them (a call of 1024 rows, 256 columns a block: 120 us with NI = 1)
       auto convert = [&](auto ni) {
         constexpr int NI = decltype(ni)::value, NS = 4 / NI;
-        for (int it0 = et & (cthr - 1); it0 < p.npad * 8; it0 += cthr * NI) {
+        for (int it0 = en; it0 < p.npad * 8; it0 += cthr * NI) {
           float z[NI][8];
           int n[NI], most = 0;
 #pragma unroll
@@ -2250,7 +2279,8 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
             for (int u = 0; u < 8; ++u) z[v][u] = 0.f;
           }
           most = min(most, 1 << p.log2cap);
-          for (int u0 = 0; u0 < most; u0 += NS) {
+          for (int us = 0; us < most; us += NS << log2sub) {
+            const int u0 = us + sub * NS;
             float4 a[NI][NS], b[NI][NS];
 #pragma unroll
             for (int v = 0; v < NI; ++v)
@@ -2280,7 +2310,7 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
           for (int v = 0; v < NI; ++v) {
             const int it = it0 + v * cthr, bl = it >> 3, c = it & 7;
             if (it >= p.npad * 8) break;
-            for (int u = most; u < n[v]; ++u) {   // more segments than the list holds
+            for (int u = most + sub; u < n[v]; u += 1 << log2sub) {   // more segments than the list holds
               const int n0 = s_n[0][bl];
               const float4* src = reinterpret_cast<const float4*>(p.base + kr + c * 8 + (u < n0 ? seg_off(0, bl, u) : seg_off(1, bl, u - n0)));
               const float4 x = src[0], y = src[1];
@@ -2288,6 +2318,10 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
               z[v][0] += x.x * f; z[v][1] += x.y * f; z[v][2] += x.z * f; z[v][3] += x.w * f;
               z[v][4] += y.x * f; z[v][5] += y.y * f; z[v][6] += y.z * f; z[v][7] += y.w * f;
             }
+            for (int q = 8; q < 8 << log2sub; q <<= 1)   // uniform: p.npad * 8 items in whole rounds
+#pragma unroll
+              for (int u = 0; u < 8; ++u) z[v][u] += __shfl_xor_sync(0xffffffffu, z[v][u], q);
+            if (sub != 0) continue;
             const float il = n[v] > 0 ? s_il[bl] : 0.f;
             uint4 hv, lv;
             uint32_t* hw = reinterpret_cast<uint32_t*>(&hv);

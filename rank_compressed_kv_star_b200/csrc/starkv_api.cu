@@ -1577,7 +1577,7 @@ struct GroupPlan {
   int v_stages, v_ctas;
   size_t v_smem;
   // finish
-  int f_mt, f_rows, f_tiles, f_npad, f_ks, f_kpc, f_stages, f_conv, f_log2cg, f_log2cap;
+  int f_mt, f_rows, f_tiles, f_npad, f_ks, f_kpc, f_stages, f_conv, f_log2cg, f_log2sub, f_log2cap;
   uint32_t f_stage_bytes, f_tmem;
   size_t f_smem;
   // attend (g.a_rows > 0)
@@ -1767,9 +1767,11 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
   // more converters where each block has an SM to itself: clusters of eight fill three quarters of
   // the SMs at best (128 blocks of 576 threads took a second wave: 30 us against 22)
   p.f_conv = f_per_sm == 1 || static_cast<int64_t>(g.Hkv) * p.f_mt * p.f_tiles * p.f_ks <= sms * 3 / 4 ? kGFConvOne : kGFConvTwo;
-  // few columns: groups of converter warps take the stages in turn
-  while ((p.f_conv >> (p.f_log2cg + 1)) >= p.f_npad * 8) ++p.f_log2cg;
   p.f_kpc = (g.R + p.f_ks * 64 - 1) / (p.f_ks * 64) * 64;
+  // few columns: groups of converter warps take the stages in turn; with few stages of the cluster
+  // kernel's sums lanes share a column's segments (whole warps: 16 columns are 128 items)
+  while ((p.f_conv >> (p.f_log2cg + 1)) >= p.f_npad * 8 && 2 << p.f_log2cg <= p.f_kpc / 64) ++p.f_log2cg;
+  while (p.f_log2sub < 2 && (p.f_conv >> (p.f_log2cg + p.f_log2sub + 1)) >= p.f_npad * 8) ++p.f_log2sub;
   p.f_tmem = static_cast<uint32_t>(pow2_ceil(p.f_npad < 32 ? 32 : p.f_npad));
 
   // rows per absorption item: few while two waves of four blocks per SM hold them (545 items of 4
@@ -2007,7 +2009,7 @@ starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_g
   fp.g = g;
   fp.out = static_cast<__half*>(out);
   fp.n_mt = pl.f_mt; fp.rows_tile = pl.f_rows; fp.npad = pl.f_npad; fp.k_per_cta = pl.f_kpc;
-  fp.stages = pl.f_stages; fp.log2cg = pl.f_log2cg; fp.log2cap = pl.f_log2cap; fp.stage_bytes = pl.f_stage_bytes; fp.tmem_cols = pl.f_tmem;
+  fp.stages = pl.f_stages; fp.log2cg = pl.f_log2cg; fp.log2sub = pl.f_log2sub; fp.log2cap = pl.f_log2cap; fp.stage_bytes = pl.f_stage_bytes; fp.tmem_cols = pl.f_tmem;
   const auto finish = g.a_rows > 0 ? group_finish_kernel<true> : group_finish_kernel<false>;
   if (!set_smem(finish, pl.f_smem)) return STARKV_ERR_CUDA;
   return launch(finish, dim3(g.Hkv * pl.f_mt * pl.f_tiles, pl.f_ks), dim3(pl.f_conv + 64), pl.f_smem, s, pl.f_ks, bvmap, fp) ==
