@@ -1774,7 +1774,7 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
   while (p.f_log2sub < 2 && (p.f_conv >> (p.f_log2cg + p.f_log2sub + 1)) >= p.f_npad * 8) ++p.f_log2sub;
   p.f_tmem = static_cast<uint32_t>(pow2_ceil(p.f_npad < 32 ? 32 : p.f_npad));
 
-  // rows per absorption item: few while two waves of four blocks per SM hold them (545 items of 4
+  // rows per absorption item: few while four waves of two blocks per SM hold them (545 items of 4
   // rows 8.0 us against 11.7 of 16; 4928 items 45 us against 33 of 32 rows)
   p.abs_tile = static_cast<int64_t>(g.H) * ((n_rows + kGAbsRows - 1) / kGAbsRows) <= 8 * sms ? kGAbsRows
                : g.H * ((n_rows + 15) / 16) <= 2 * sms ? 16 : kAbsBT;
