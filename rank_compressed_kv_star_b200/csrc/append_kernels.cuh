@@ -70,7 +70,8 @@ struct AppendVParams {
   __half* v_cache;         // [NB][16][R]
   int B, HD, R;
   int k_per_cta;           // rows of H*d per CTA (multiple of 64)
-  int npad;                // UMMA N: batch tile padded to a multiple of 16 (<= 256)
+  int rows;                // sequences per batch tile (256, or 128)
+  int npad;                // UMMA N: batch tile padded to a multiple of 16 (<= rows)
   int stages;
   uint32_t tmem_cols;
 };
@@ -99,7 +100,7 @@ __device__ __forceinline__ void append_v_tile(const CUtensorMap* amap, const CUt
   __shared__ uint32_t taddr_s;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int b0 = bt * 256;
+  const int b0 = bt * p.rows;
   const int k0 = ks * p.k_per_cta;
   const int k1 = min(p.HD, k0 + p.k_per_cta);
   const int n_stages = k1 > k0 ? (k1 - k0 + kAppKC - 1) / kAppKC : 0;

@@ -61,9 +61,6 @@
 #ifndef STARKV_ROPE_MACS
 #define STARKV_ROPE_MACS (24 << 20)   // rotary append: from so many key-code products on, tensor cores and three launches
 #endif
-#ifndef STARKV_ROPE_SPLIT
-#define STARKV_ROPE_SPLIT 12     // rotary append of many rows: V codes split over a cluster when that saves a block so many steps
-#endif
 #ifndef STARKV_V_RING_BYTES
 #define STARKV_V_RING_BYTES (105 * 1024)
 #endif
@@ -613,7 +610,7 @@ struct AppendPlan {
 
 starkv_status plan_append(const starkv_layer_desc* desc, int32_t batch, const void* k, const void* v,
                           const void* A_K, const void* A_V, AppendTarget tgt, void* k_cache, void* v_cache,
-                          AppendPlan* ap, int ks_max = STARKV_APP_KS_MAX) {
+                          AppendPlan* ap, int ks_max = STARKV_APP_KS_MAX, int rows = 256) {
   if (!k || !v || !A_K || !A_V || !k_cache || !v_cache) return STARKV_ERR_INVALID_ARG;
   if (!tgt.slots && (!tgt.tables || !tgt.positions)) return STARKV_ERR_INVALID_ARG;
   if (!aligned16(k) || !aligned16(v) || !aligned16(A_K) || !aligned16(A_V) || !aligned16(k_cache) ||
@@ -623,8 +620,8 @@ starkv_status plan_append(const starkv_layer_desc* desc, int32_t batch, const vo
   const int H = kv_heads(desc), d = desc->head_dim, r = desc->k_rank, R = desc->v_rank;   // codes per KV head
   const int HD = H * d;
   // joint V codes: tcgen05 GEMM, split-K over a cluster
-  const int n_bt = (batch + 255) / 256;
-  const int bt_rows = batch < 256 ? batch : 256;
+  const int n_bt = (batch + rows - 1) / rows;
+  const int bt_rows = batch < rows ? batch : rows;
   const int npad = (bt_rows + 15) / 16 * 16;
   if (!encode_2d_map(&ap->amap, A_V, static_cast<uint64_t>(R), static_cast<uint64_t>(HD), 64, kAppKC) ||
       !encode_2d_map(&ap->vmap, v, static_cast<uint64_t>(HD), static_cast<uint64_t>(batch), 64,
@@ -644,6 +641,7 @@ starkv_status plan_append(const starkv_layer_desc* desc, int32_t batch, const vo
   vp.v_cache = static_cast<__half*>(v_cache);
   vp.B = batch; vp.HD = HD; vp.R = R;
   vp.k_per_cta = ((HD + KS * kAppKC - 1) / (KS * kAppKC)) * kAppKC;
+  vp.rows = rows;
   vp.npad = npad;
   vp.stages = 4;
   vp.tmem_cols = static_cast<uint32_t>(pow2_ceil(npad < 32 ? 32 : npad));
@@ -1440,7 +1438,10 @@ starkv_status rope_impl(const starkv_layer_desc* desc, const starkv_rope* rope, 
   tgt.rope_positions = positions;
   tgt.rope_max = rope->max_position;
   AppendPlan ap{};
-  st = plan_append(desc, n, k, v, A_K, A_V, tgt, k_cache, v_cache, &ap, kRopeKS);
+  // batch tiles of 128 rows while a tile's depth can still be split in two (half the sums to
+  // exchange: 400 rows of 32 heads, R = 2048, 24 us against 29 of 256; 777 rows 41 against 34)
+  const bool half = n > 256 && static_cast<int64_t>((desc->v_rank + 127) / 128) * ((n + 127) / 128) * 2 <= device_sm_count();
+  st = plan_append(desc, n, k, v, A_K, A_V, tgt, k_cache, v_cache, &ap, kRopeKS, half ? 128 : 256);
   if (st != STARKV_OK) return st;
   RopeParams rp{};
   rp.rope.cos_sin = rope->cos_sin;
@@ -1456,7 +1457,9 @@ starkv_status rope_impl(const starkv_layer_desc* desc, const starkv_rope* rope, 
   rp.H = desc->num_heads;
   rp.d = desc->head_dim;
   if (static_cast<int64_t>(n) * ap.kp.H * rp.d * ap.kp.r >= STARKV_ROPE_MACS) {
-    // many rows: V-code tiles, and beside them the queries and the rotated keys' codes
+    // many rows (single launch : three, in us: 8 KV heads of 128, r = 64, R = 512: 256 rows 9.5 : 13,
+    // 400 rows 15 : 12; 32 heads, R = 2048: 64 rows 8.9 : 12.7, 96 14 : 14, 128 16.5 : 15): V-code
+    // tiles, and beside them the queries and the rotated keys' codes
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const int sms = device_sm_count(), rows256 = (n + 255) / 256;
     // rank tiles of 256 or 128: the one whose waves move fewer bytes into an SM
@@ -1466,7 +1469,10 @@ starkv_status rope_impl(const starkv_layer_desc* desc, const starkv_rope* rope, 
     while (ap.KS < kRopeKS && ap.v_cols * ap.KS * 2 <= (ap.KS == 1 ? sms : sms * 3 / 4) &&
            ap.vp.HD / kAppKC >= ap.KS * 2)
       ap.KS *= 2;
-    if (ap.vp.HD / kAppKC * (ap.KS - 1) / ap.KS < STARKV_ROPE_SPLIT) {
+    // the split's exchange of sums costs about so many steps (8 KV heads, R = 512, split : persistent
+    // tiles: 777 rows 15 : 17 us, 2048 17.6 : 18.1, 3000 (256-row tiles) 26 : 20; 32 heads, R = 2048:
+    // 777 rows 34 : 41, 1024 37 : 42)
+    if (ap.vp.HD / kAppKC * (ap.KS - 1) / ap.KS < (half ? 8 : 12)) {
       RopeVParams pv{};
       pv.tgt = ap.vp.tgt;
       pv.v_cache = ap.vp.v_cache;
