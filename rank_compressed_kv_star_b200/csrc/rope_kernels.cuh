@@ -162,7 +162,7 @@ struct RopeParams {
   int q_items;             // query items of kRopeQUnits units
 };
 
-constexpr int kRopeKB = 32;                       // rows per K-code item
+constexpr int kRopeKB = 32;                       // rows per K-code item, at most
 // Blocks of a cluster that share a V-code tile's depth: eight beat four (one row, 32
 // heads of 128, R = 2048: 6.7 against 9.0 us; 64 rows: 8.9 against 11.2).
 constexpr int kRopeKS = 8;

@@ -1520,14 +1520,23 @@ starkv_status rope_impl(const starkv_layer_desc* desc, const starkv_rope* rope, 
     return STARKV_OK;
   }
   const int KS = ap.KS;
-  rp.k.tile = kRopeKB;
   rp.v_mt = ap.v_mt;
   rp.v_cols = ap.v_cols;
-  rp.k_items = rp.k.H * ((n + rp.k.tile - 1) / rp.k.tile);
-  rp.k_cols = (rp.k_items + KS - 1) / KS;
+  // rows per key item: the fewest whose items still fit beside the V-code tiles, in clusters that
+  // fill four fifths of the SMs at best (in us with 8 / 16 / 32 rows: 8 KV heads, R = 512: 32 rows
+  // 5.7 / 5.9 / 7.0, 96 rows 10 / 6.4 / 7.1; 32 heads, R = 2048: 48 rows 12.5 / 8.0 / 8.2, 64 rows
+  // 17 / 12 / 8.9)
+  auto k_smem_of = [&](int tile) { return static_cast<size_t>(rp.d) * rp.k.r * 2 + static_cast<size_t>(tile) * rp.d * 4; };
+  for (rp.k.tile = 8;; rp.k.tile *= 2) {
+    rp.k_items = rp.k.H * ((n + rp.k.tile - 1) / rp.k.tile);
+    rp.k_cols = (rp.k_items + KS - 1) / KS;
+    const size_t most = ap.v_smem > k_smem_of(rp.k.tile) ? ap.v_smem : k_smem_of(rp.k.tile);
+    const int per_sm = most + 4096 <= 113 * 1024 ? 2 : 1;
+    if (rp.k.tile == kRopeKB || (rp.v_cols + rp.k_cols) * KS * 5 <= per_sm * device_sm_count() * 4) break;
+  }
   const int64_t units = static_cast<int64_t>(n) * rp.H * rope_units(rp.d, rp.rope.rot, rp.rope.interleaved);
   rp.q_items = q ? static_cast<int>((units + kRopeQUnits - 1) / kRopeQUnits) : 0;
-  const size_t k_smem = static_cast<size_t>(rp.d) * rp.k.r * 2 + static_cast<size_t>(rp.k.tile) * rp.d * 4;
+  const size_t k_smem = k_smem_of(rp.k.tile);
   const size_t smem = (ap.v_smem > k_smem ? ap.v_smem : k_smem) + 1024;
   if (!set_smem(rope_append_kernel, smem)) return STARKV_ERR_CUDA;
   const dim3 grid(rp.v_cols + rp.k_cols + (rp.q_items + KS - 1) / KS, KS);
