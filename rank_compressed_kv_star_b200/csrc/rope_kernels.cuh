@@ -166,6 +166,11 @@ constexpr int kRopeKB = 32;                       // rows per K-code item, at mo
 // Blocks of a cluster that share a V-code tile's depth: eight beat four (one row, 32
 // heads of 128, R = 2048: 6.7 against 9.0 us; 64 rows: 8.9 against 11.2).
 constexpr int kRopeKS = 8;
+// Three launches instead of one where the items of one do not fit one wave, from so many rows
+// on (us, one : three; 32 heads of 128, r = 64: R = 2048: 96 rows 15.5 : 13.9, 128 22 : 15;
+// R = 8192: 1 row 10 : 17, 64 rows 18 : 20, 128 33 : 24; 8 KV heads, R = 512: 280 rows 12.8 :
+// 10.8; 64 heads of 32, r = 16, R = 1024: 128 rows 12.4 : 10.0, 1000 rows 69 : 20).
+constexpr int kRopeRows = 80;
 constexpr int kRopeQUnits = kPrepThreads * kRopeBatch;
 
 // One K-code item: KV head h, rows [b0, b0 + tile).  The rotated rows stand in

@@ -58,9 +58,6 @@
 #ifndef STARKV_APP_KS_MAX
 #define STARKV_APP_KS_MAX 4     // largest cluster splitting the V-code GEMM's K range
 #endif
-#ifndef STARKV_ROPE_MACS
-#define STARKV_ROPE_MACS (24 << 20)   // rotary append: from so many key-code products on, tensor cores and three launches
-#endif
 #ifndef STARKV_V_RING_BYTES
 #define STARKV_V_RING_BYTES (105 * 1024)
 #endif
@@ -1456,10 +1453,25 @@ starkv_status rope_impl(const starkv_layer_desc* desc, const starkv_rope* rope, 
   rp.n = n;
   rp.H = desc->num_heads;
   rp.d = desc->head_dim;
-  if (static_cast<int64_t>(n) * ap.kp.H * rp.d * ap.kp.r >= STARKV_ROPE_MACS) {
-    // many rows (single launch : three, in us: 8 KV heads of 128, r = 64, R = 512: 256 rows 9.5 : 13,
-    // 400 rows 15 : 12; 32 heads, R = 2048: 64 rows 8.9 : 12.7, 96 14 : 14, 128 16.5 : 15): V-code
-    // tiles, and beside them the queries and the rotated keys' codes
+  const int KS = ap.KS;
+  rp.v_mt = ap.v_mt;
+  rp.v_cols = ap.v_cols;
+  // rows per key item: the fewest whose items still fit beside the V-code tiles, in clusters that
+  // fill four fifths of the SMs at best (in us with 8 / 16 / 32 rows: 8 KV heads, R = 512: 32 rows
+  // 5.7 / 5.9 / 7.0, 96 rows 10 / 6.4 / 7.1; 32 heads, R = 2048: 48 rows 12.5 / 8.0 / 8.2, 64 rows
+  // 17 / 12 / 8.9)
+  auto k_smem_of = [&](int tile) { return static_cast<size_t>(rp.d) * rp.k.r * 2 + static_cast<size_t>(tile) * rp.d * 4; };
+  bool fits = false;
+  for (rp.k.tile = 8;; rp.k.tile *= 2) {
+    rp.k_items = rp.k.H * ((n + rp.k.tile - 1) / rp.k.tile);
+    rp.k_cols = (rp.k_items + KS - 1) / KS;
+    const size_t most = ap.v_smem > k_smem_of(rp.k.tile) ? ap.v_smem : k_smem_of(rp.k.tile);
+    const int per_sm = most + 4096 <= 113 * 1024 ? 2 : 1;
+    fits = static_cast<int64_t>(rp.v_cols + rp.k_cols) * KS * 5 <= static_cast<int64_t>(per_sm) * device_sm_count() * 4;
+    if (fits || rp.k.tile == kRopeKB) break;
+  }
+  if (!fits && n >= kRopeRows) {
+    // many rows: V-code tiles, and beside them the queries and the rotated keys' codes
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const int sms = device_sm_count(), rows256 = (n + 255) / 256;
     // rank tiles of 256 or 128: the one whose waves move fewer bytes into an SM
@@ -1518,21 +1530,6 @@ starkv_status rope_impl(const starkv_layer_desc* desc, const starkv_rope* rope, 
         return STARKV_ERR_CUDA;
     }
     return STARKV_OK;
-  }
-  const int KS = ap.KS;
-  rp.v_mt = ap.v_mt;
-  rp.v_cols = ap.v_cols;
-  // rows per key item: the fewest whose items still fit beside the V-code tiles, in clusters that
-  // fill four fifths of the SMs at best (in us with 8 / 16 / 32 rows: 8 KV heads, R = 512: 32 rows
-  // 5.7 / 5.9 / 7.0, 96 rows 10 / 6.4 / 7.1; 32 heads, R = 2048: 48 rows 12.5 / 8.0 / 8.2, 64 rows
-  // 17 / 12 / 8.9)
-  auto k_smem_of = [&](int tile) { return static_cast<size_t>(rp.d) * rp.k.r * 2 + static_cast<size_t>(tile) * rp.d * 4; };
-  for (rp.k.tile = 8;; rp.k.tile *= 2) {
-    rp.k_items = rp.k.H * ((n + rp.k.tile - 1) / rp.k.tile);
-    rp.k_cols = (rp.k_items + KS - 1) / KS;
-    const size_t most = ap.v_smem > k_smem_of(rp.k.tile) ? ap.v_smem : k_smem_of(rp.k.tile);
-    const int per_sm = most + 4096 <= 113 * 1024 ? 2 : 1;
-    if (rp.k.tile == kRopeKB || (rp.v_cols + rp.k_cols) * KS * 5 <= per_sm * device_sm_count() * 4) break;
   }
   const int64_t units = static_cast<int64_t>(n) * rp.H * rope_units(rp.d, rp.rope.rot, rp.rope.interleaved);
   rp.q_items = q ? static_cast<int>((units + kRopeQUnits - 1) / kRopeQUnits) : 0;

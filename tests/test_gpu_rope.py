@@ -160,6 +160,17 @@ def test_rope_many_rows_and_ranks(H, Hkv, d, r, R, n, inter):
     c.verify(g, q_rows=np.zeros(n, bool))
 
 
+@pytest.mark.parametrize("H,Hkv,d,r,R", [(64, 64, 32, 16, 1024), (8, 8, 64, 32, 8192), (16, 16, 256, 96, 512), (4, 1, 128, 256, 64)])
+@pytest.mark.parametrize("n", [8, 79, 80, 130, 257])
+def test_rope_forms_at_other_layers(H, Hkv, d, r, R, n):
+    """Layers whose items fill a wave early or never: both sides of the choice between one launch and three."""
+    L = Layer(30, H, Hkv, d, r, R)
+    c = Case(L, n, d, n % 2 == 1, form="append" if n < 100 else "store")
+    g = c.device()
+    c.call(g)
+    c.verify(g)
+
+
 def test_rope_many_rows_skipped():
     L = Layer(31, 2, 2, 32, 16, 2048)
     c = Case(L, 2561, 32, False, max_position=4096, form="store")
