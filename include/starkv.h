@@ -362,7 +362,8 @@ starkv_status starkv_paged_prefill(const starkv_layer_desc* desc, int32_t n_seqs
  * empty groups and shared lengths of 0 are allowed.  Values out of range are
  * clamped and flagged in the status word (STARKV_FLAG_BAD_SEQ_LEN,
  * STARKV_FLAG_BAD_ROW_OFFSET, STARKV_FLAG_BAD_BLOCK_ID; the affected rows are
- * undefined).  Accumulation is fp32; attention weights enter the V contraction
+ * undefined): lengths to their bounds, block ids to page 0, row_offsets to
+ * [0, batch] and, where they fall, to the largest before.  Accumulation is fp32; attention weights enter the V contraction
  * as fp16.  Calls that share a workspace must be ordered on one stream.  A
  * workspace for the largest counts and bounds also serves smaller ones.
  * STARKV_ERR_UNSUPPORTED beyond 2^20 rows, for bounds above 2^30, or where rows

@@ -16,7 +16,8 @@ ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 LIB = os.path.join(PKG, "libstarkv.so")
 SOURCES = [os.path.join(PKG, "csrc", "starkv_api.cu")]
 DEPS = SOURCES + [os.path.join(PKG, "csrc", f) for f in
-                  ("ptx.cuh", "decode_kernels.cuh", "append_kernels.cuh", "rope_kernels.cuh", "group_kernels.cuh")] + [
+                  ("ptx.cuh", "decode_kernels.cuh", "append_kernels.cuh", "rope_kernels.cuh", "group_tables.cuh",
+                   "group_kernels.cuh")] + [
     os.path.join(ROOT, "include", "starkv.h")]
 
 

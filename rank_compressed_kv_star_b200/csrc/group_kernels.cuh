@@ -30,88 +30,12 @@
 #include "ptx.cuh"
 #include "append_kernels.cuh"
 #include "decode_kernels.cuh"
+#include "group_tables.cuh"
 #include "../../include/starkv.h"
 
 namespace starkv {
 
-// One run of rows over one list of pages: rows row0 .. row0 + nrows - 1 over
-// tokens 0 .. len - 1, token t in slot t % 16 of page tables[tab][page0 + t / 16].
-// Its columns are the (row, query head) pairs in that order.
-struct alignas(16) GroupEntry {
-  int32_t row0, nrows, len, page0;
-  int32_t tab;
-  int32_t psrc, zsrc;  // which P and Z matrices it uses: 0 a group's (or sequence's), 1 a row's own
-  int32_t tile0;       // V tiles before it
-  // what the passes' walks would have to divide for
-  int32_t narrow;      // gk_narrow
-  int32_t k_nt, k_per; // wide: row tiles, rows per tile
-  int32_t v_units;     // 64-token units per V tile
-  int32_t v_width;     // columns per V tile
-  int32_t a_nt, a_per; // attend: row tiles, rows per tile
-  int32_t a_tile0;     // attend tiles before it
-};
-static_assert(sizeof(GroupEntry) == 64, "loaded as four 16-byte words");
-
-struct GroupGeom {
-  int H, Hkv, log2G, d, r, R, MB, NB;
-  int n_rows, n_groups, E;     // E = n_groups entries, plus n_rows own entries when shared
-  int shared;                  // 1: shared-prefix decode, 0: cross attention
-  int ncol;                    // K pass: query columns per tile
-  int chunk_w, chunk_n;        // K pass: tokens per item of a wide / narrow entry
-  int n_rt;                    // V pass: 256-row tiles of R
-  int t_pad[2];                // P row length, a multiple of 128
-  int n_ch[2];                 // chunks per row of the sums of weights
-  int max_len[2];              // host bounds of the entries' lengths
-  GroupEntry* ent;             // [E]
-  int32_t* kpre;               // [E + 1] cost of the K items before each entry
-  int32_t* vpre;               // [E + 1] V units before each entry
-  int32_t* apre;               // [E + 1] attend blocks before each entry
-  int a_rows;                  // attend: rows per tile at most (0: the call does not use it)
-  int C, nch;                  // attend: CTAs per cluster, 64-code blocks of R per CTA
-  int32_t* row_ent;            // [n_rows] the row's group, or -1
-  int32_t* row_use;            // [n_rows] 1: the row attends over its group's pages
-  int32_t* n_used;             // rows that belong to groups (row_offsets[n_groups])
-  int32_t* tfirst;             // [V tiles] first CTA of each tile
-  int32_t* tlast;              // [V tiles] last CTA
-  float* mrow;                 // [n_rows][H] maxima
-  float* lpart[2];             // by zsrc, [n_rows][H][n_ch] sums of weights per chunk
-  int32_t* status;
-};
-
-constexpr int kGVTile = 256;    // V pass: columns (row, head) and rows of R per tile
-constexpr int kGVTok = 64;      // V pass: tokens per unit
-constexpr int kGNarrowPer = 16;
-
-// Column tiles of an entry with `cols` (row, head) columns, and their width.
-__device__ __forceinline__ int gv_tiles(int cols) { return (cols + kGVTile - 1) / kGVTile; }
-__device__ __forceinline__ int gv_width(int cols, int nt) { return ((cols + nt - 1) / nt + 15) / 16 * 16; }
-
-// A narrow entry has so few columns that one tile holds those of all heads: its K
-// tiles are 128 code rows in page order (128 / Hkv tokens x Hkv heads, large
-// contiguous copies), and each row uses the columns of its own head; the
-// tensor cores compute the others too, which costs less than the copies.  A wide
-// entry's K tiles are 128 tokens of one head.
-__device__ __forceinline__ bool gk_narrow(int nrows, const GroupGeom& g) {
-  return nrows * g.H <= g.ncol && (nrows << g.log2G) <= kGNarrowPer;
-}
-// Row tiles of a wide entry.
-__device__ __forceinline__ int gk_tiles(int nrows, const GroupGeom& g) {
-  const int per = g.ncol >> g.log2G;
-  return (nrows + per - 1) / per;
-}
-
 // ================================================================= tables
-// What an item of the K pass costs, for the partition of the items over the CTAs: its
-// steps, a wide one by its columns (128 tokens by 16 columns are one accumulator block of
-// a warp), plus its start.  By number instead of cost, the weights pass of 64 rows over
-// 8192 shared and up to 256 own tokens (32 heads) had CTAs of twice the median's time: 94 us
-// against 47 (with three producer warps and both teams on narrow items).
-constexpr int kGKStart = 8;
-__device__ __forceinline__ int gk_cost(const GroupEntry& en, const GroupGeom& g, int log2Hkv) {
-  if (en.narrow) return (g.chunk_n >> (7 - log2Hkv)) * (2 + ((en.nrows * g.H) >> 4)) + kGKStart;
-  return (g.chunk_w >> 7) * (4 + ((en.k_per << g.log2G) >> 4)) + kGKStart;
-}
-
 struct GroupSetupParams {
   GroupGeom g;
   const int32_t* row_offsets;  // [n_groups + 1]
@@ -125,99 +49,98 @@ __device__ __forceinline__ int clamp_flag(int x, int lo, int hi, int32_t* bad, i
   return x;
 }
 
-// Group of row b, or -1: behind the last group, or the offsets are out of order.
-__device__ __forceinline__ int group_of_row(const GroupSetupParams& p, int b) {
-  if (b >= p.row_offsets[p.g.n_groups]) return -1;
-  int lo = 0, hi = p.g.n_groups - 1;
+// Group of row b, or -1: before the first group or behind the last.
+__device__ __forceinline__ int group_of_row(const GroupGeom& g, int b) {
+  int lo = 0, hi = g.n_groups - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (p.row_offsets[mid] <= b) lo = mid; else hi = mid - 1;
+    if (g.ent[mid].row0 <= b) lo = mid; else hi = mid - 1;
   }
-  return b >= p.row_offsets[lo] && b < p.row_offsets[lo + 1] ? lo : -1;
+  const int x = b - g.ent[lo].row0;
+  return x >= 0 && x < g.ent[lo].nrows ? lo : -1;
 }
 
 // One CTA of 256 threads.  Every value read from the caller's arrays is clamped
-// (and flagged) here, so that the later kernels index in range whatever they hold.
+// (and flagged) here, and the groups' rows are disjoint whatever the offsets hold
+// (group_rows), so that the later kernels index in range and the tables hold what
+// the host has sized them for.
 __device__ __forceinline__ void group_setup(const GroupSetupParams& p) {
   const GroupGeom& g = p.g;
   __shared__ int32_t bad;
-  __shared__ int32_t warp_sum[5][8];
+  __shared__ int32_t warp_sum[5][8], warp_max[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) bad = 0;
-  __syncthreads();
-  if (tid == 0) *g.n_used = clamp_flag(p.row_offsets[g.n_groups], 0, g.n_rows, &bad, STARKV_FLAG_BAD_ROW_OFFSET);
   // thread t makes the entries [t per, (t + 1) per)
   const int per = (g.E + 255) / 256;
-  const int e0 = tid * per, e1 = min(g.E, e0 + per);
+  const int e0 = tid * per, e1 = min(g.E, e0 + per), eg = min(e1, g.n_groups);
   int32_t mine[5] = {0, 0, 0, 0, 0};   // cost of the K items, V units, V tiles, attend blocks, attend tiles
-  auto counts = [&](const GroupEntry& en, int32_t (&c)[5]) {
-    c[0] = c[1] = c[2] = c[3] = c[4] = 0;
-    if (en.nrows == 0 || en.len == 0) return;
-    const int nt = gv_tiles(en.nrows * g.H) * g.n_rt;
-    c[0] = en.narrow ? (en.len + g.chunk_n - 1) / g.chunk_n
-                     : en.k_nt * g.Hkv * ((en.len + g.chunk_w - 1) / g.chunk_w);
-    c[0] *= gk_cost(en, g, 31 - __clz(g.Hkv));
-    c[1] = nt * ((en.len + kGVTok - 1) / kGVTok);
-    c[2] = nt;
-    c[3] = en.a_nt * en.v_units;
-    c[4] = en.a_nt;
-  };
-  for (int e = e0; e < e1; ++e) {
-    GroupEntry en{};
-    if (e < g.n_groups) {
-      const int a = p.row_offsets[e], b = p.row_offsets[e + 1];
-      if (a < 0 || a > b || b > g.n_rows || (e == 0 && a != 0)) atomicOr(&bad, STARKV_FLAG_BAD_ROW_OFFSET);
-      en.row0 = min(max(a, 0), g.n_rows);
-      en.nrows = max(0, min(max(b, 0), g.n_rows) - en.row0);
-      const int len =
-          clamp_flag(g.shared ? p.shared_lens[e] : p.seq_lens[e], 0, g.max_len[0], &bad, STARKV_FLAG_BAD_SEQ_LEN);
-      en.len = g.shared ? len / kBlock * kBlock : len;   // whole pages are shared
-      en.tab = g.shared ? min(en.row0, g.n_rows - 1) : e;
-    } else {
-      const int b = e - g.n_groups;
-      const int grp = group_of_row(p, b);
-      en.row0 = b;
-      en.psrc = en.zsrc = 1;
-      en.tab = b;
-      int use = 0;
-      if (grp >= 0) {
-        const int common = min(max(p.shared_lens[grp], 0), g.max_len[0]) / kBlock * kBlock;
-        const int T = clamp_flag(p.seq_lens[b], 0, g.MB * kBlock, &bad, STARKV_FLAG_BAD_SEQ_LEN);
-        en.nrows = 1;
-        if (T >= common) {
-          use = common > 0;
-          en.page0 = common / kBlock;
-          en.len = clamp_flag(T - common, 0, g.max_len[1], &bad, STARKV_FLAG_BAD_SEQ_LEN);
-        } else {
-          // shorter than the shared pages: the row reads all of its tokens by
-          // itself and keeps its weights in its unused row of the group's P
-          en.len = T;
-          en.psrc = 0;
-        }
-      }
-      g.row_ent[b] = grp;
-      g.row_use[b] = use;
-    }
-    if (en.nrows > 0) {
-      const int cols = en.nrows * g.H;
-      en.narrow = gk_narrow(en.nrows, g);
-      en.k_nt = gk_tiles(en.nrows, g);
-      en.k_per = (en.nrows + en.k_nt - 1) / en.k_nt;
-      en.v_units = (en.len + kGVTok - 1) / kGVTok;
-      en.v_width = gv_width(cols, gv_tiles(cols));
-      if (g.a_rows > 0) {
-        en.a_nt = (en.nrows + g.a_rows - 1) / g.a_rows;
-        en.a_per = (en.nrows + en.a_nt - 1) / en.a_nt;
-      }
-    }
+  const int log2Hkv = 31 - __clz(g.Hkv);
+  auto put = [&](int e, GroupEntry& en) {
+    group_entry_shape(en, g);
     g.ent[e] = en;
     int32_t c[5];
-    counts(en, c);
+    group_counts(en, g, log2Hkv, c);
     for (int i = 0; i < 5; ++i) mine[i] += c[i];
+  };
+  // the largest offset before the thread's first group
+  int32_t from = 0;
+  for (int e = e0; e < eg; ++e) from = max(from, group_offset(p.row_offsets[e], g.n_rows));
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t y = __shfl_up_sync(0xffffffffu, from, o);
+    if (lane >= o) from = max(from, y);
+  }
+  if (lane == 31) warp_max[warp] = from;
+  from = __shfl_up_sync(0xffffffffu, from, 1);
+  if (lane == 0) from = 0;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) from = max(from, warp_max[w]);
+  for (int e = e0; e < eg; ++e) {
+    GroupEntry en{};
+    const int a = p.row_offsets[e], b = p.row_offsets[e + 1];
+    if (a < 0 || a > b || b > g.n_rows || (e == 0 && a != 0)) atomicOr(&bad, STARKV_FLAG_BAD_ROW_OFFSET);
+    const GroupRows rows = group_rows(from, a, b, g.n_rows);
+    from = rows.row0;
+    en.row0 = rows.row0;
+    en.nrows = rows.end - rows.row0;
+    const int len =
+        clamp_flag(g.shared ? p.shared_lens[e] : p.seq_lens[e], 0, g.max_len[0], &bad, STARKV_FLAG_BAD_SEQ_LEN);
+    en.len = g.shared ? len / kBlock * kBlock : len;   // whole pages are shared
+    en.tab = g.shared ? min(en.row0, g.n_rows - 1) : e;
+    put(e, en);
+    if (e == g.n_groups - 1) *g.n_used = rows.end;
+  }
+  __syncthreads();   // group_of_row reads the groups' entries
+  for (int e = max(e0, g.n_groups); e < e1; ++e) {
+    const int b = e - g.n_groups;
+    const int grp = group_of_row(g, b);
+    GroupEntry en{};
+    en.row0 = b;
+    en.psrc = en.zsrc = 1;
+    en.tab = b;
+    int use = 0;
+    if (grp >= 0) {
+      const int common = min(max(p.shared_lens[grp], 0), g.max_len[0]) / kBlock * kBlock;
+      const int T = clamp_flag(p.seq_lens[b], 0, g.MB * kBlock, &bad, STARKV_FLAG_BAD_SEQ_LEN);
+      en.nrows = 1;
+      if (T >= common) {
+        use = common > 0;
+        en.page0 = common / kBlock;
+        en.len = clamp_flag(T - common, 0, g.max_len[1], &bad, STARKV_FLAG_BAD_SEQ_LEN);
+      } else {
+        // shorter than the shared pages: the row reads all of its tokens by
+        // itself and keeps its weights in its unused row of the group's P
+        en.len = T;
+        en.psrc = 0;
+      }
+    }
+    g.row_ent[b] = grp;
+    g.row_use[b] = use;
+    put(e, en);
   }
   if (!g.shared)
     for (int b = tid; b < g.n_rows; b += 256) {
-      const int grp = group_of_row(p, b);
+      const int grp = group_of_row(g, b);
       g.row_ent[b] = grp;
       g.row_use[b] = grp >= 0 ? 1 : 0;
     }
@@ -240,7 +163,7 @@ __device__ __forceinline__ void group_setup(const GroupSetupParams& p) {
   }
   for (int e = e0; e < e1; ++e) {
     int32_t c[5];
-    counts(g.ent[e], c);
+    group_counts(g.ent[e], g, log2Hkv, c);
     g.kpre[e] = at[0];
     g.vpre[e] = at[1];
     g.ent[e].tile0 = at[2];

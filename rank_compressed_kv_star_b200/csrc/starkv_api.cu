@@ -1679,9 +1679,8 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
              (2 * p.k_stages + 4 + 2 * kGKAcc + 2) * sizeof(uint64_t) + staging;
   p.k_tmem = static_cast<uint32_t>(kGKAcc * g.ncol);
   p.k_ctas = sms;
-  const int64_t runs = n_groups < n_rows ? n_groups : n_rows;   // entries of several rows at most
-  const int own_max = max0 > max1 ? max0 : max1;                // a row's own pages: also those of a row shorter than its group's
-  const int64_t wide_tiles = runs + static_cast<int64_t>(n_rows) * G / g.ncol * 2 + 1;
+  const int64_t runs = group_runs_most(g), wide_tiles = group_wide_tiles_most(g);
+  const int own_max = group_own_most(g);
   {
     // steps of 128 tokens per wide item: an item costs about two steps beside its own
     const int64_t steps = g.t_pad[0] / 128;
@@ -1724,13 +1723,8 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
   p.v_stages = 3;
   p.v_ctas = sms;
   p.v_smem = 1024 + static_cast<size_t>(p.v_stages) * (kGVABytes + kGVBBytes) + (2 * p.v_stages + 8) * sizeof(uint64_t);
-  const int64_t v_tiles = g.n_rt * (runs + static_cast<int64_t>(n_rows) * g.H / kGVTile + 1 + (shared ? n_rows : 0));
   // positions in the K items' costs and in the V units are 32-bit
-  const int64_t k_cost =
-      wide_tiles * g.Hkv * ((g.t_pad[0] + g.chunk_w - 1) / g.chunk_w) * ((g.chunk_w >> 7) * (4 + g.ncol / 16) + kGKStart) +
-      (runs + (shared ? n_rows : 0)) * static_cast<int64_t>((own_max + g.chunk_n) / g.chunk_n + 1) *
-          (static_cast<int64_t>(g.chunk_n) * g.Hkv / 128 * (2 + g.ncol / 16) + kGKStart);
-  if (k_cost > (1 << 30) || v_tiles * ((own_max + kGVTok) / kGVTok + 1) > (1 << 30)) return STARKV_ERR_UNSUPPORTED;
+  if (group_k_cost_most(g) > (1 << 30) || group_v_units_most(g) > (1 << 30)) return STARKV_ERR_UNSUPPORTED;
 
   // finish
   p.f_mt = (g.d + 127) / 128;
@@ -1825,8 +1819,10 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
     const int64_t own_b = shared ? static_cast<int64_t>(n_rows) * ((max1 + kGATok - 1) / kGATok) : 0;
     const int64_t about = n_rows / rows + runs / 2, once = runs * b0 + own_b,
                   read = (about > runs ? about : runs) * b0 + own_b;
-    if (p.at_v_stages >= 3 && 2 * read - 3 * once <= 11 * static_cast<int64_t>(most)) {
-      g.a_rows = rows;
+    g.a_rows = rows;
+    if (p.at_v_stages < 3 || 2 * read - 3 * once > 11 * static_cast<int64_t>(most) || group_a_blocks_most(g) > (1 << 30)) {
+      g.a_rows = 0;
+    } else {
       p.at_clusters = blocks < 1 ? 1 : (blocks < most ? static_cast<int>(blocks) : most);
     }
   }
@@ -1844,7 +1840,7 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
     p.row_ent_off = take(N * 4);
     p.row_use_off = take(N * 4);
     p.used_off = take(4);
-    const int64_t tiles = attend ? runs + n_rows / g.a_rows + 1 + (shared ? n_rows : 0) : v_tiles;
+    const int64_t tiles = attend ? group_a_tiles_most(g) : group_v_tiles_most(g);
     p.tfirst_off = take(static_cast<size_t>(tiles) * 4);
     p.tlast_off = take(static_cast<size_t>(tiles) * 4);
     p.mrow_off = take(rh * 4);

@@ -206,3 +206,55 @@ def test_rows_in_no_group_and_empty_calls():
     c = make_shared(L, [(0, [0, 0])])
     g, got = check_case(L, c)
     assert (got == 0).all()
+
+
+@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("kind", ["shared", "cross"])
+def test_offsets_that_rise_again_are_flagged_and_stay_in_the_tables(kind, far):
+    """Every second group would have all rows, were the offsets taken one by one: the first group keeps them, the others are
+    empty, and neither the workspace's neighbour nor a row is disturbed."""
+    L = Layer(15, 8, 2, 64, 48, 320)
+    n, groups = 24, 40
+    if kind == "shared":
+        c = make_shared(L, [(70, [1 + b % 30 for b in range(n)])], pad_rows=3)
+    else:
+        c = make_cross(L, [(90, n)], pad_rows=3)
+        c["tables"] = np.repeat(c["tables"], groups, 0)
+        c["seq_lens"] = np.repeat(c["seq_lens"], groups)
+    if kind == "shared":
+        c["shared_lens"] = np.repeat(c["shared_lens"], groups)
+    if far:   # the separate passes
+        wide = np.full((c["tables"].shape[0], 2500), c["tables"][0, -1], np.int32)
+        wide[:, :c["tables"].shape[1]] = c["tables"]
+        c["tables"] = wide
+        c["max_shared" if kind == "shared" else "max_len"] = 40000
+    c["n_groups"] = groups
+    c["row_offsets"] = np.array([0, n] * (groups // 2) + [n], np.int32)
+    g = to_device(L, c)
+    guard = 1 << 16
+    ws = torch.full((g["bytes"] + guard,), 0xA5, dtype=torch.uint8, device="cuda")
+    g["ws"] = ws
+    call(L, c, g)
+    assert S.starkv_decode_check(ws)[1] == S.FLAG_BAD_ROW_OFFSET
+    assert bool((ws[g["bytes"]:] == 0xA5).all())
+    one = dict(c, n_groups=1, row_offsets=np.array([0, n], np.int32))
+    ref, bound = reference(L, one)
+    got = g["out"].float().cpu().numpy()
+    for b in range(n):
+        assert (np.abs(got[b] - ref[b]) <= bound[b]).all(), b
+    assert (got[n:] == UNTOUCHED).all()
+
+
+def test_more_groups_than_rows_with_falling_offsets():
+    L = Layer(16, *LAYERS["gqa32"])
+    c = make_cross(L, [(130, 8)])
+    groups = 300
+    c.update(n_groups=groups, tables=np.repeat(c["tables"], groups, 0), seq_lens=np.repeat(c["seq_lens"], groups),
+             row_offsets=np.array([0, 8] * (groups // 2) + [5], np.int32))
+    g = to_device(L, c)
+    call(L, c, g)
+    assert S.starkv_decode_check(g["ws"])[1] == S.FLAG_BAD_ROW_OFFSET
+    ref, bound = reference(L, dict(c, n_groups=1, row_offsets=np.array([0, 8], np.int32)))
+    got = g["out"].float().cpu().numpy()
+    for b in range(8):
+        assert (np.abs(got[b] - ref[b]) <= bound[b]).all(), b
