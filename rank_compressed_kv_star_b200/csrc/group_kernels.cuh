@@ -506,7 +506,7 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int s = 0; s < S; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int s = 0; s < S; ++s) { mbar_init(&full[s], kGKProd); mbar_init(&empty[s], 1); }
     for (int a = 0; a < 2; ++a) { mbar_init(&qfull[a], 1); mbar_init(&qempty[a], 1); }
     for (int a = 0; a < kGKAcc; ++a) { mbar_init(&tfull[a], 1); mbar_init(&tempty[a], kGKEpi / 32); }
     mbar_init(mmadone, 1);
@@ -540,8 +540,9 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
   if (warp == 0 || warp >= 2 + kGKEpi / 32) {
     // ----------------------------------------------------------- producers
     // A step's boxes are dealt out to the producer warps (one lane's issue of eight boxes takes
-    // 2 us, as long as everything else of a step together); the first also brings the queries
-    // and arrives for all: a box that lands before the arrival is counted all the same.
+    // 2 us, as long as everything else of a step together); the first also brings the queries.
+    // Each arrives for every step, with or without a box in it: the ring cannot pass one that
+    // lags, whose parity waits would then be for phases long gone.
     const int pid = warp == 0 ? 0 : warp - (1 + kGKEpi / 32);
     const uint64_t keep = policy_evict_last();
     RingPos k;
@@ -592,7 +593,8 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
         uint8_t* st = smem + static_cast<size_t>(k.s) * p.a_bytes;
         if (lane == 0) {
           if (k.u > 0 && !mbar_wait(&empty[k.s], (k.u - 1) & 1)) ok = false;
-          else if (pid == 0) mbar_arrive_expect_tx(&full[k.s], static_cast<uint32_t>(nb * p.kb) * box);
+          else if (pid < nb) mbar_arrive_expect_tx(&full[k.s], static_cast<uint32_t>((nb - pid + kGKProd - 1) / kGKProd * p.kb) * box);
+          else mbar_arrive(&full[k.s]);
         }
         for (int c = pid; c < nb; c += kGKProd) {
           const int tk = t + c * tb;
