@@ -172,8 +172,9 @@ typedef struct {
  *   q_out[b,h,:] = Rot(positions[b]) q[b,h,:]
  *
  * A code rounds once to fp16: the rotated key goes into its sum in fp32, or for
- * many rows as two fp16 halves (22 bits), and the sum is fp32.  q_out is rounded
- * to fp16 and is what starkv_paged_decode and its kin take as q.
+ * many rows as two fp16 halves (22 bits, or to 2^-35 for a key below 2^-13), and
+ * the sum is fp32.  q_out is rounded to fp16 and is what starkv_paged_decode and
+ * its kin take as q.
  *
  *   rope          host struct, see above
  *   q             fp16 [batch][H][d], or NULL: no queries to rotate

@@ -277,9 +277,10 @@ __global__ void __launch_bounds__(kPrepThreads, 3) rope_q_kernel(RopeParams p) {
 
 // Key codes: a block is one KV head's 128 rows, on tcgen05,
 //   D (128 rows x r) = k' (128 x d) . A_K[h] (d x r),
-// the rotated rows written to shared memory as fp16 hi + lo halves (22 bits, so the
-// code still rounds once) in the K-major operand layout, A_K[h] by TMA boxes of 64
-// ranks x 64 rows (MN-major).  A block's chain takes 8 to 10 us (its loads 3 to 5, MMAs
+// the rotated rows written to shared memory as two fp16 halves, hi and 2^11 lo (22 bits,
+// or to 2^-35 for keys below 2^-13, so the code still rounds once), in the K-major operand
+// layout, A_K[h] by TMA boxes of 64 ranks x 64 rows (MN-major).  Each half has its own
+// accumulator; the drain joins them.  A block's chain takes 8 to 10 us (its loads 3 to 5, MMAs
 // 1.5, drain 1); two share an SM.  32 heads x 4096 rows: 46 us alone, 95 with the V codes.
 constexpr int kRRThreads = 512;
 struct RopeRowsParams {
@@ -287,8 +288,9 @@ struct RopeRowsParams {
   AppendKParams k;
   int kc, nc;              // 64-element chunks of d, 64-rank chunks of r
   int b_slots;             // chunks of A_K[h] in shared memory at a time
-  uint32_t tmem_cols;
+  uint32_t lo_col;         // tensor memory column of the low half's accumulator
 };
+constexpr float kRRLow = 2048.f;   // scale of the low half
 
 __global__ void __launch_bounds__(kRRThreads, 2)
 rope_rows_kernel(const __grid_constant__ CUtensorMap akmap, RopeRowsParams p) {
@@ -312,7 +314,7 @@ rope_rows_kernel(const __grid_constant__ CUtensorMap akmap, RopeRowsParams p) {
     prefetch_tensormap(&akmap);
   }
   if (warp == 0) {
-    tmem_alloc(&taddr_s, p.tmem_cols);
+    tmem_alloc(&taddr_s, 2 * p.lo_col);
     tmem_relinquish();
     tc_fence_before();
   }
@@ -342,9 +344,11 @@ rope_rows_kernel(const __grid_constant__ CUtensorMap akmap, RopeRowsParams p) {
       const float e = 0.5f * y[2 * u], o2 = 0.5f * y[2 * u + 1];   // a rotation grows a value by up to sqrt(2)
       const __half2 hh = __floats2half2_rn(e, o2);
       const float2 f = __half22float2(hh);
-      // at most half a step of 2^15; an infinity less itself is no number, and -64 keeps it an infinity
-      lo[2 * u] = fmaxf(e - f.x, -64.f);
-      lo[2 * u + 1] = fmaxf(o2 - f.y, -64.f);
+      // scaled so that the rest of a small key is no subnormal (unscaled, a key of 2^-10 kept 14
+      // bits); at most half a step of 2^15 before; an infinity less itself is no number, and a
+      // finite low half keeps it an infinity
+      lo[2 * u] = fmaxf((e - f.x) * kRRLow, -16.f * kRRLow);
+      lo[2 * u + 1] = fmaxf((o2 - f.y) * kRRLow, -16.f * kRRLow);
       hw[u] = *reinterpret_cast<const uint32_t*>(&hh);
     }
     const uint32_t at = static_cast<uint32_t>(o >> 6) * a_chunk + b * 128u + ((((o & 63) >> 3) ^ (b & 7)) << 4);
@@ -376,7 +380,7 @@ rope_rows_kernel(const __grid_constant__ CUtensorMap akmap, RopeRowsParams p) {
       for (int kk = 0; kk < min(64, d - c * 64) / 16; ++kk) {
         const uint64_t bd = smem_desc(sb + kk * 2048u, 8192u, 1024u, kSwizzle128B);
         umma_f16_ss(taddr, smem_desc(sh + kk * 32u, 16u, 1024u, kSwizzle128B), bd, idesc, on);
-        umma_f16_ss(taddr, smem_desc(sl + kk * 32u, 16u, 1024u, kSwizzle128B), bd, idesc, 1u);
+        umma_f16_ss(taddr + p.lo_col, smem_desc(sl + kk * 32u, 16u, 1024u, kSwizzle128B), bd, idesc, on);
         on = 1;
       }
       umma_commit(&bfree[s]);
@@ -400,15 +404,17 @@ rope_rows_kernel(const __grid_constant__ CUtensorMap akmap, RopeRowsParams p) {
     __half* out = kp.k_cache + (row < 0 ? 0 : (row * kp.H + h) * r);
     for (int c0 = (warp >> 2) * 16; c0 < r; c0 += kRRThreads / 8) {
       __syncwarp();
-      uint32_t v[32];
+      uint32_t v[32], w[32];
       tmem_ld_32x32b_x16(taddr + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0, v);
+      tmem_ld_32x32b_x16(taddr + (static_cast<uint32_t>((warp & 3) * 32) << 16) + p.lo_col + c0, w);
       tmem_ld_wait();
       if (row >= 0) {
         float y[8];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
 #pragma unroll
-          for (int u = 0; u < 8; ++u) y[u] = 2.f * __uint_as_float(v[8 * g + u]);
+          for (int u = 0; u < 8; ++u)
+            y[u] = fmaf(__uint_as_float(w[8 * g + u]), 2.f / kRRLow, 2.f * __uint_as_float(v[8 * g + u]));
           *reinterpret_cast<uint4*>(out + c0 + 8 * g) = pack8(y);
         }
       }
@@ -420,7 +426,7 @@ rope_rows_kernel(const __grid_constant__ CUtensorMap akmap, RopeRowsParams p) {
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(taddr, p.tmem_cols);
+    tmem_dealloc(taddr, 2 * p.lo_col);
   }
   if (blockIdx.x == gridDim.x - 1) griddep_wait();
 }

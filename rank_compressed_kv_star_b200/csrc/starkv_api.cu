@@ -1516,7 +1516,7 @@ starkv_status rope_impl(const starkv_layer_desc* desc, const starkv_rope* rope, 
     const size_t a_bytes = static_cast<size_t>(pr.kc) * 2 * 16384, b_chunk = static_cast<size_t>(pr.nc) * 8192;
     pr.b_slots = pr.kc;
     while (pr.b_slots > 1 && a_bytes + pr.b_slots * b_chunk > 200 * 1024) --pr.b_slots;
-    pr.tmem_cols = static_cast<uint32_t>(pow2_ceil(ap.kp.r < 32 ? 32 : ap.kp.r));
+    pr.lo_col = static_cast<uint32_t>(pow2_ceil(ap.kp.r < 32 ? 32 : ap.kp.r));
     CUtensorMap akmap;
     const size_t smem = 1024 + a_bytes + pr.b_slots * b_chunk;
     if (!encode_2d_map(&akmap, A_K, static_cast<uint64_t>(ap.kp.r), static_cast<uint64_t>(ap.kp.H) * rp.d, 64, 64) ||

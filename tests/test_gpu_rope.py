@@ -203,6 +203,33 @@ def test_rope_large_values(n, R):
     c.verify(g, keep)
 
 
+@pytest.mark.parametrize("size", [2.0 ** -10, 1e-4, 2.0 ** -20])
+@pytest.mark.parametrize("H,Hkv,d,r,R,n", [(2, 2, 32, 16, 2048, 2561), (32, 8, 128, 64, 512, 777), (2, 2, 256, 256, 2048, 1300),
+                                           (32, 8, 128, 64, 512, 5)])
+def test_rope_small_keys(H, Hkv, d, r, R, n, size):
+    """Keys down to fp16's subnormals, with projections that bring their codes back to its normal range: however many rows the
+    call has, a rotated key keeps its bits relative to its own size.
+
+    The bound of a code is the module's, plus what two fp16 halves cannot hold of a small key k': hi is k'/2 rounded to fp16
+    and the rest, at most 2^-12 |k'/2| or half the smallest step, 2^-25, is kept times 2^11 in fp16: off by at most 2^-24 of
+    |k'/2| (counted in the module's 2^-21) where the scaled rest is normal, else by half the smallest step, 2^-25 2^-11 of
+    k'/2, that is 2^-35 of k' per element."""
+    L = Layer(36, H, Hkv, d, r, R)
+    L.A_K = (L.A_K.astype(np.float64) * min(0.25 / size, 2.0 ** 14)).astype(np.float16)
+    c = Case(L, n, d // 2, False, max_position=4096, form="store")
+    c.k = (c.k.astype(np.float64) * size).astype(np.float16)
+    g = c.device()
+    c.call(g)
+    assert S.starkv_decode_check(g["status"])[1] == 0
+    kr, km = rotate(c.k, c.cs, c.pos, c.inter)
+    aK = L.A_K.astype(np.float64)
+    ck, mk = np.einsum("njd,jdr->njr", kr, aK), np.einsum("njd,jdr->njr", km, np.abs(aK))
+    got = g["k_cache"].cpu().numpy().reshape(-1, Hkv, r)[c.slots].astype(np.float64)
+    bound = 2.0 ** -11 * np.abs(ck) + 2.0 ** -25 + ((d + 8) * 2.0 ** -23 + 2.0 ** -21) * mk + 2.0 ** -35 * np.abs(aK).sum(1)
+    over = np.abs(got - ck) - bound
+    assert (over <= 0).all(), (float(over.max()), float(np.abs(got - ck).max()))
+
+
 @pytest.mark.parametrize("inter", [False, True])
 def test_rope_in_place_and_without_queries(inter):
     L = Layer(24, 8, 2, 128, 64, 256)
