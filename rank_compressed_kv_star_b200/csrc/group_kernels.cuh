@@ -13,8 +13,9 @@
 // The maximum is taken over both entries before any weight is formed, so the
 // partial sums of a row simply add up.  Launches, all on the caller's stream (small calls
 // take group_attend between 1 and 5, with a running maximum per cluster, see there):
-//   1. group_absorb           q~ = log2(e) scale q . B_K^T in fp16 hi + lo
-//                             halves; the entry tables (one extra CTA); M = -inf
+//   1. group_absorb           q~ = log2(e) scale q . B_K^T, scaled per (row, head) by a
+//                             power of two, in fp16 hi + lo halves; the entry tables
+//                             (one extra CTA); M = -inf
 //   2. group_kpass<maxima>    S = c_K . q~ on tcgen05, column maxima only
 //   3. group_kpass<weights>   S again, w to the P matrix, L per token chunk
 //   4. group_vpass            Z = P . c_V on tcgen05, partial sums per (tile, CTA)
@@ -184,11 +185,32 @@ struct GroupAbsorbParams {
   GroupSetupParams su;
   const __half* q;     // [n_rows][H][d]
   const __half* B_K;   // [Hkv][r][d]
-  __half* qh;          // [n_rows * H][r] fp16 of q~
+  __half* qh;          // [n_rows * H][r] fp16 of q~ / g.qf
   __half* ql;          // [n_rows * H][r] fp16 of its remainder
   float coef;          // scale * log2(e)
   int tile;            // rows per item
 };
+
+// q~ is kept as f x (hi + lo) with a power of two f per (row, head) that holds the halves
+// below 2^15: they keep 22 bits of every value down to 2^-17 of that, whatever q~'s own size.
+// The logits are scaled back where they are used.
+// 2^x and 2^-x, x held in [-120, 120].
+__device__ __forceinline__ float pow2_pair(int x, float* inverse) {
+  x = min(max(x, -120), 120);
+  *inverse = __uint_as_float(static_cast<uint32_t>(127 - x) << 23);
+  return __uint_as_float(static_cast<uint32_t>(127 + x) << 23);
+}
+// e with |v| < 2^(e + 1) (128 of an infinity or a NaN: any power of two will do for its row).
+__device__ __forceinline__ int exponent_of(float v) {
+  return static_cast<int>((__float_as_uint(v) >> 23) & 255u) - 127;
+}
+__device__ __forceinline__ float half_of(uint32_t bits) { return __half2float(__ushort_as_half(static_cast<unsigned short>(bits))); }
+// The largest of eight fp16 magnitudes, as bits.
+__device__ __forceinline__ uint32_t abs_top8(const uint4& v) {
+  const uint32_t m = 0x7fff7fffu;
+  const uint32_t t = __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+  return max(t & 0xffffu, t >> 16);
+}
 
 // A few rows (<= kGAbsRows): a warp per rank index, the lanes along d, eight rank
 // indices at a time.  B_K is read in its own order, one round of loads per eight
@@ -205,7 +227,14 @@ __device__ __forceinline__ void absorb_few(const GroupAbsorbParams& p, int h, in
     for (int u = 0; u < EPL; ++u)
       q[b][u] = b < nb ? __half2float(p.q[(static_cast<size_t>(b0 + b) * g.H + h) * D + lane * EPL + u]) : 0.f;
   const __half* bk = p.B_K + static_cast<size_t>(h >> g.log2G) * r * D + lane * EPL;
-  for (int i0 = warp * 8; i0 < r; i0 += kPrepThreads / 32 * 8) {
+  constexpr int kRound = kPrepThreads / 32 * 8;
+  static_assert(4 * kRound == 256, "r <= 256: a lane keeps the values of round lane & 3");
+  __shared__ uint32_t s_top[kPrepThreads / 32][kGAbsRows];
+  float val[kGAbsRows];            // of index mine
+  const int mine = (lane & 3) * kRound + warp * 8 + (lane >> 2);
+#pragma unroll
+  for (int b = 0; b < kGAbsRows; ++b) val[b] = 0.f;
+  for (int it = 0, i0 = warp * 8; i0 < r; ++it, i0 += kRound) {
     __half w[8][EPL];
 #pragma unroll
     for (int x = 0; x < 8; ++x) {   // r is a multiple of 16
@@ -225,7 +254,7 @@ __device__ __forceinline__ void absorb_few(const GroupAbsorbParams& p, int h, in
 #pragma unroll
         for (int u = 0; u < EPL; ++u) a[x] += q[b][u] * __half2float(w[x][u]);
       }
-      // eight sums over the lanes: lane l ends with index l >> 2
+      // eight sums over the lanes: lanes 4 x to 4 x + 3 end with index x
 #pragma unroll
       for (int o = 16, n = 4; o >= 4; o >>= 1, n >>= 1) {
         const bool up = (lane & o) != 0;
@@ -237,13 +266,30 @@ __device__ __forceinline__ void absorb_few(const GroupAbsorbParams& p, int h, in
       }
       a[0] += __shfl_xor_sync(0xffffffffu, a[0], 2);
       a[0] += __shfl_xor_sync(0xffffffffu, a[0], 1);
-      if ((lane & 3) == 0) {
-        const float v = a[0] * p.coef;
-        const size_t o = (static_cast<size_t>(b0 + b) * g.H + h) * r + i0 + (lane >> 2);
-        const __half hi = __float2half_rn(v);
-        p.qh[o] = hi;
-        p.ql[o] = __float2half_rn(v - __half2float(hi));
-      }
+      if ((lane & 3) == it) val[b] = a[0] * p.coef;
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < kGAbsRows; ++b) {
+    const uint32_t t = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(val[b])));
+    if (lane == 0) s_top[warp][b] = t;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int b = 0; b < kGAbsRows; ++b) {
+    if (b >= nb) break;
+    uint32_t t = s_top[0][b];
+#pragma unroll
+    for (int w = 1; w < kPrepThreads / 32; ++w) t = max(t, s_top[w][b]);
+    float inv;
+    const float f = pow2_pair(exponent_of(__uint_as_float(t)) - 14, &inv);
+    const size_t rh = static_cast<size_t>(b0 + b) * g.H + h;
+    if (threadIdx.x == 0) g.qf[rh] = f;
+    if (mine < r) {
+      const float v = val[b] * inv;
+      const __half hi = __float2half_rn(v);
+      p.qh[rh * r + mine] = hi;
+      p.ql[rh * r + mine] = __float2half_rn(v - __half2float(hi));
     }
   }
 }
@@ -274,22 +320,48 @@ group_absorb_kernel(GroupAbsorbParams p) {
     return;
   }
   const __half* bk = p.B_K + static_cast<size_t>(h >> g.log2G) * r * D;
+  __shared__ float s_inv[kAbsBT];                     // coef over the row's scale
+  __shared__ uint32_t s_qtop[kAbsBT], s_btop[kPrepThreads / 32];
+  uint32_t top = 0;
   for (int x = tid; x < r * (D / 8); x += kPrepThreads) {
     const int i = x % r, jb = x / r;
     const uint4 v = *reinterpret_cast<const uint4*>(bk + static_cast<size_t>(i) * D + jb * 8);
     const __half* hv = reinterpret_cast<const __half*>(&v);
 #pragma unroll
     for (int u = 0; u < 8; ++u) Ws[(jb * 8 + u) * r + i] = hv[u];
+    top = max(top, abs_top8(v));
   }
-  for (int x = tid; x < nb * (D / 8); x += kPrepThreads) {
-    const int bb = x / (D / 8), c = x % (D / 8);
-    reinterpret_cast<uint4*>(qs)[x] =
-        reinterpret_cast<const uint4*>(p.q + (static_cast<size_t>(b0 + bb) * g.H + h) * D)[c];
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((tid & 31) == 0) s_btop[tid >> 5] = top;
+  const int lpr = D / 8;                              // lanes per row of q: 4 to 32
+  for (int x0 = 0; x0 < nb * lpr; x0 += kPrepThreads) {
+    const int x = x0 + tid, bb = x / lpr, c = x & (lpr - 1);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (bb < nb) {
+      v = reinterpret_cast<const uint4*>(p.q + (static_cast<size_t>(b0 + bb) * g.H + h) * D)[c];
+      reinterpret_cast<uint4*>(qs)[x] = v;
+    }
+    uint32_t t = abs_top8(v);
+    for (int o = lpr >> 1; o > 0; o >>= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
+    if (bb < nb && c == 0) s_qtop[bb] = t;
+  }
+  __syncthreads();
+  if (tid < nb) {
+    // |q~| <= coef d max|q| max|B_K|, each factor below twice its power of two (a zero counts as
+    // the smallest fp16 value)
+    uint32_t bt = 0;
+    for (int w = 0; w < kPrepThreads / 32; ++w) bt = max(bt, s_btop[w]);
+    const int e = exponent_of(p.coef * D) + max(exponent_of(half_of(s_qtop[tid])), -24) +
+                  max(exponent_of(half_of(bt)), -24) + 3;
+    float inv;
+    g.qf[static_cast<size_t>(b0 + tid) * g.H + h] = pow2_pair(e - 15, &inv);
+    s_inv[tid] = p.coef * inv;
   }
   __syncthreads();
   small_proj(Ws, qs, nb, D, r, [&](int bb, int i, float v0, float v1) {
-    v0 *= p.coef;
-    v1 *= p.coef;
+    const float k = s_inv[bb];
+    v0 *= k;
+    v1 *= k;
     const size_t o = (static_cast<size_t>(b0 + bb) * g.H + h) * r + i;
     const __half2 hi = __floats2half2_rn(v0, v1);
     const float2 hf = __half22float2(hi);
@@ -501,7 +573,7 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
   __shared__ GroupTablesSmem s_tab;
   __shared__ int64_t s_off[128];   // P row of each column, or -1
   __shared__ int32_t s_rh[128];    // its (row, query head), or -1
-  __shared__ float s_m[128];
+  __shared__ float2 s_fm[128];     // the column's scale, and its negated maximum (weights)
   __shared__ float s_red[8][128];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -687,22 +759,23 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
     while (ok && walk.next(&x)) {
       const int t_pad = g.t_pad[x.en.psrc];
       __half* P = kWeights ? p.P[x.en.psrc] : nullptr;
-      // per column: its P row (-1: the row does not attend over these pages) and maximum
+      // per column: its P row (-1: the row does not attend over these pages), scale and maximum
       if (!group_sync(ebar, phase)) { ok = false; break; }
       if (et < 128) {
         int32_t rh = -1;
-        float m = 0.f;
+        float2 fm = make_float2(1.f, 0.f);
         if (et < x.cols) {
           const int row = x.row0 + (x.en.narrow ? et / g.H : et >> g.log2G);
           const int h = x.en.narrow ? et & (g.H - 1) : (x.j << g.log2G) + (et & (G - 1));
           rh = row * g.H + h;
           const int use = x.en.zsrc ? 1 : g.row_use[row];
-          if (kWeights) m = g.mrow[rh];
+          fm.x = g.qf[rh];
+          if (kWeights) fm.y = -g.mrow[rh];
           if (!use) rh = -1;
         }
         s_rh[et] = rh;
         s_off[et] = rh < 0 ? -1 : static_cast<int64_t>(rh) * t_pad;
-        s_m[et] = m;
+        s_fm[et] = fm;
         for (int u = 0; u < 8; ++u) s_red[u][et] = kWeights ? 0.f : -INFINITY;
       }
       if (!group_sync(ebar, phase)) { ok = false; break; }
@@ -748,7 +821,8 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
                 if (i < ng && col >= cg && col < ce) {
                   const float s = st[col - cg];
                   if constexpr (kWeights) {
-                    const __half w = __float2half_rn(in ? ex2_approx(s - s_m[col]) : 0.f);
+                    const float2 fm = s_fm[col];
+                    const __half w = __float2half_rn(in ? ex2_approx(fmaf(s, fm.x, fm.y)) : 0.f);
                     run[i] += __half2float(w);
                     if (page && s_off[col] >= 0) P[s_off[col] + t] = w;
                   } else {
@@ -800,7 +874,8 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
               for (int u = 0; u < 16; ++u) {
                 const int c = cb * 16 + u;
                 if constexpr (kWeights) {
-                  const float e = ex2_approx(__uint_as_float(v[u]) - s_m[c]);
+                  const float2 fm = s_fm[c];
+                  const float e = ex2_approx(fmaf(__uint_as_float(v[u]), fm.x, fm.y));
                   const __half w = __float2half_rn(__uint_as_float(__float_as_uint(e) & in));
                   run[i][u] += __half2float(w);
                   const int64_t off = s_off[c];
@@ -841,7 +916,7 @@ group_kpass_kernel(const __grid_constant__ CUtensorMap kwmap, const __grid_const
           float m = s_red[0][et];
 #pragma unroll
           for (int u = 1; u < 8; ++u) m = fmaxf(m, s_red[u][et]);
-          if (m > -INFINITY) atomic_max_f32(&g.mrow[s_rh[et]], m);
+          if (m > -INFINITY) atomic_max_f32(&g.mrow[s_rh[et]], m * s_fm[et].x);
         }
       } else {
         if (et < x.cols && s_rh[et] >= 0) {
@@ -1173,6 +1248,7 @@ group_vpass_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_consta
 // the SMs and no phase waits for a grid.
 //   S      = c_K . (q~ hi + q~ lo) for 128 code rows in page order at a time (see
 //            gk_narrow); each row keeps its own head's columns
+//            A column's logits are scaled back (g.qf) where maxima and weights are taken.
 //   m      = max of the first block's logits, per column; raised, with Z and l
 //            rescaled, when a later block exceeds it by more than 15 (weights
 //            then stay below 2^15 and keep fp16's relative precision)
@@ -1706,6 +1782,7 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     uint32_t nr = 0, nw = 0;
     while (ok && walk.next(&x)) {
       const int len = x.en.len;
+      const float fq = col < x.ncols ? g.qf[static_cast<size_t>(x.row0) * g.H + col] : 1.f;   // scale of the column's logits
       float ref = 0.f, ref_o = 0.f, l = 0.f;
       int os = first_own(x.b0 * ppb, c, C), ow = os;   // next own part to take maxima, weights of
       // the maxima of the CTA's own parts of block b, to every CTA
@@ -1729,7 +1806,7 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
               }
             }
             float* at = s_mx + (ms.s * 4 + pi) * kGACols + col;
-            *at = m;
+            *at = m * fq;
             if (C > 1) {
               fence_proxy_async_smem();
               __syncwarp();
@@ -1826,7 +1903,7 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
               // weights of eight tokens, rounded to fp16 for the products; the sum takes the rounded weights
               float e[8];
 #pragma unroll
-              for (int u = 0; u < 8; ++u) e[u] = ex2_approx(src[u * p.lstride] - base);
+              for (int u = 0; u < 8; ++u) e[u] = ex2_approx(fmaf(src[u * p.lstride], fq, -base));
               if (t0 + t8 + 8 > len) {
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
@@ -1895,7 +1972,8 @@ group_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 // out^T (128 rows of d x columns) = B_V^T . (Z / L)^T for the (row, query head)
 // columns of one KV head, with Z / L formed on the fly: converter warps add
 // a column's partial sums (its one or two entries, in a fixed order), scale by
-// 1 / L and split into fp16 hi + lo halves (about 22 bits) in the B operand.
+// 1 / L and split into fp16 hi + lo halves (22 bits, or to 2^-25, the step of a value code
+// itself, for sums below 2^-3) in the B operand.
 // K = R is split over a cluster whose fp32 sums are added in rank order.
 // A = 64 x 64 boxes of B_V (MN-major).  A row without tokens gives zeros.
 // Bound by the converters' arithmetic and latency: 64 rows x 32 heads of R = 2048 take

@@ -52,6 +52,7 @@ struct GroupGeom {
   int32_t* tfirst;             // [V tiles] first CTA of each tile
   int32_t* tlast;              // [V tiles] last CTA
   float* mrow;                 // [n_rows][H] maxima
+  float* qf;                   // [n_rows][H] q~ is qf times what its halves hold
   float* lpart[2];             // by zsrc, [n_rows][H][n_ch] sums of weights per chunk
   int32_t* status;
 };

@@ -1599,7 +1599,7 @@ struct GroupPlan {
   // absorption
   int abs_tile;
   // workspace
-  size_t apre_off, m_off[2], l_off[2], mcarry_off, lcarry_off, ent_off, kpre_off, vpre_off, row_ent_off, row_use_off, used_off, tfirst_off, tlast_off, mrow_off, lpart_off[2],
+  size_t apre_off, m_off[2], l_off[2], mcarry_off, lcarry_off, ent_off, kpre_off, vpre_off, row_ent_off, row_use_off, used_off, tfirst_off, tlast_off, mrow_off, qf_off, lpart_off[2],
       qh_off, ql_off, p_off[2], z_off[2], carry_off, total;
 };
 
@@ -1844,6 +1844,7 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
     p.tfirst_off = take(static_cast<size_t>(tiles) * 4);
     p.tlast_off = take(static_cast<size_t>(tiles) * 4);
     p.mrow_off = take(rh * 4);
+    p.qf_off = take(rh * 4);
     p.qh_off = take(rh * g.r * 2);
     p.ql_off = take(rh * g.r * 2);
     for (int s = 0; s < (shared ? 2 : 1); ++s) {
@@ -1917,6 +1918,7 @@ starkv_status group_impl(const starkv_layer_desc* desc, bool shared, int32_t n_g
   g.tfirst = i32(pl.tfirst_off);
   g.tlast = i32(pl.tlast_off);
   g.mrow = f32(pl.mrow_off);
+  g.qf = f32(pl.qf_off);
   const int second = shared ? 1 : 0;   // an unused second source stands for the first
   const int src[2] = {0, second};
   for (int i = 0; i < 2; ++i) g.lpart[i] = f32(pl.lpart_off[src[i]]);

@@ -258,3 +258,45 @@ def test_more_groups_than_rows_with_falling_offsets():
     got = g["out"].float().cpu().numpy()
     for b in range(8):
         assert (np.abs(got[b] - ref[b]) <= bound[b]).all(), b
+
+
+@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("rows", [1, 4, 23, 90])   # 90 rows of 64 heads: absorbed 16 or 32 at a time
+@pytest.mark.parametrize("kind", ["large", "small", "mixed"])
+def test_absorbed_queries_of_any_size(kind, rows, far):
+    """q~ past fp16's largest value, or far below its normal range, with codes that bring the logits back to a few: the rows are
+    those of the formula, and of starkv_paged_decode, which keeps a multi-head layer's q~ in fp32."""
+    L = Layer(17, *LAYERS["mha4" if rows < 20 else "gqa32" if rows < 90 else "mqa64"])
+    up, down = (2.0 ** 14, 2.0 ** -17), (2.0 ** -20, 2.0 ** 15)
+    L.B_K = (L.B_K.astype(np.float64) * (2.0 ** 6 if kind == "large" else 2.0 ** 3)).astype(np.float16)
+    c = make_cross(L, [(150, rows), (77, 2)])
+    q, k = up if kind == "large" else down
+    if kind == "mixed":   # rows and heads of very different sizes in one tile
+        q = 2.0 ** L.rng.integers(-20, 1, (c["n"], L.H, 1))
+        k = 1.0
+    top = 65504.0
+    c["q"] = np.clip(c["q"].astype(np.float64) * q, -top, top).astype(np.float16)
+    c["k"] = np.clip(c["k"].astype(np.float64) * k, -top, top).astype(np.float16)
+    if kind != "large":
+        c["q"][-1] = 0
+    if far:
+        wide = np.full((2, 2500), c["tables"][0, -1], np.int32)
+        wide[:, :c["tables"].shape[1]] = c["tables"]
+        c.update(tables=wide, max_len=40000)
+    g, got = check_case(L, c)
+    if kind == "large":
+        coef = L.scale / np.log(2)
+        G = L.H // L.Hkv
+        qt = np.abs(coef * np.einsum("nhd,hrd->nhr", c["q"].astype(np.float64), np.repeat(L.B_K.astype(np.float64), G, 0)))
+        assert (qt.max(2) > 65504).all()
+    if L.H == L.Hkv:
+        one = np.repeat(np.arange(2), [rows, 2])
+        t, T = dev(c["tables"][one]), dev(c["seq_lens"][one])
+        wsb = S.starkv_decode_workspace_bytes(g["desc"], c["n"], 150)
+        ws = torch.empty(wsb, dtype=torch.uint8, device="cuda")
+        out = torch.empty_like(g["out"])
+        S.starkv_paged_decode(g["desc"], c["n"], 150, g["q"], g["B_K"], g["B_V"], g["k"], g["v"], t, T, L.scale, ws, wsb, out)
+        _, bound = reference(L, c)
+        want = out.float().cpu().numpy()
+        for b in bound:
+            assert (np.abs(got[b] - want[b]) <= 2 * bound[b]).all()
