@@ -2192,7 +2192,7 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
           }
           const float Mn = fmaxf(M, fmaxf(m[0], m[1]));
           L = M > -INFINITY ? L * ex2_approx(M - Mn) : L;
-          // a segment whose logits are all NaN or -inf has m = -inf and l = NaN
+          // m = -inf: a segment whose logits are all -inf (l = 0) or NaN (l = NaN)
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
             float l = 0.f;
@@ -2213,7 +2213,8 @@ group_finish_kernel(const __grid_constant__ CUtensorMap bvmap, GroupFinishParams
             s_fac[(c << p.log2cap) + i] = m > -INFINITY ? ex2_approx(m - top) : 1.f;
           }
         if (c < ncols && i0 == 0) {
-          s_il[c] = L == 0.f ? 0.f : 1.f / L;   // no token at all: L = 0 and the result is 0
+          // no token at all: the result is 0; tokens whose logits are all -inf: NaN, as in the passes
+          s_il[c] = n == 0 ? 0.f : top > -INFINITY ? 1.f / L : __uint_as_float(0x7fc00000u);
           s_M[c] = top;
         }
       }

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import rank_compressed_kv_star_b200 as S
-from group_common import (Layer, UNTOUCHED, call, check_case, dev, make_cross, make_shared, reference, to_device)
+from group_common import (PAGE, Layer, UNTOUCHED, call, check_case, dev, make_cross, make_shared, reference, to_device)
 from gpu_common import load
 
 pytestmark = pytest.mark.gpu
@@ -214,7 +214,7 @@ def test_offsets_that_rise_again_are_flagged_and_stay_in_the_tables(kind, far):
     """Every second group would have all rows, were the offsets taken one by one: the first group keeps them, the others are
     empty, and neither the workspace's neighbour nor a row is disturbed."""
     L = Layer(15, 8, 2, 64, 48, 320)
-    n, groups = 24, 40
+    n, groups = 200 if far else 24, 40
     if kind == "shared":
         c = make_shared(L, [(70, [1 + b % 30 for b in range(n)])], pad_rows=3)
     else:
@@ -300,3 +300,64 @@ def test_absorbed_queries_of_any_size(kind, rows, far):
         want = out.float().cpu().numpy()
         for b in bound:
             assert (np.abs(got[b] - want[b]) <= 2 * bound[b]).all()
+
+
+def _minus_infinity(L, c, tokens_of):
+    """Queries and projections with one absorbed value, positive in both of its halves, so that codes of -inf at its rank are
+    logits of -inf; tokens_of: (table row, tokens) whose codes get them."""
+    L.B_K[:] = 0
+    L.B_K[:, 3, 0] = 1
+    coef = np.float32(np.float32(L.scale) * np.float32(1.4426950408889634))
+    for x in np.arange(1.0, 2.0, 2.0 ** -10):
+        v = np.float32(coef * np.float32(np.float16(x)))
+        if 0 < v - np.float32(np.float16(v)) and 0 < np.float16(v - np.float32(np.float16(v))):
+            break
+    c["q"][:] = 0
+    c["q"][:, :, 0] = x
+    for table, tokens in tokens_of:
+        c["k"][table[tokens // PAGE], tokens % PAGE, :, 3] = -np.inf
+
+
+@pytest.mark.parametrize("far", [False, True])
+def test_rows_whose_logits_are_all_minus_infinity(far):
+    """NaN, not the zeros of a row without tokens, whichever kernels a call takes."""
+    L = Layer(18, *LAYERS["gqa32"])
+    m = 30 if far else 3     # enough rows for the separate passes
+    c = make_cross(L, [(70, m), (90, m), (0, 1)])
+    _minus_infinity(L, c, [(c["tables"][0], np.arange(70)), (c["tables"][1], np.arange(64))])
+    if far:
+        wide = np.full((3, 2500), c["tables"][0, -1], np.int32)
+        wide[:, :c["tables"].shape[1]] = c["tables"]
+        c.update(tables=wide, max_len=40000)
+    g = to_device(L, c)
+    call(L, c, g)
+    assert S.starkv_decode_check(g["ws"]) == (0, 0)
+    got = g["out"].float().cpu().numpy()
+    assert np.isnan(got[:m]).all()
+    assert (got[2 * m] == 0).all()
+    # the first 64 tokens of the second sequence weigh nothing beside the others
+    rest = dict(c, tables=c["tables"][:, 4:], seq_lens=c["seq_lens"] - 64)
+    ref, bound = reference(L, rest, rows=range(m, 2 * m))
+    for b in ref:
+        assert (np.abs(got[b] - ref[b]) <= bound[b]).all()
+
+
+@pytest.mark.parametrize("far", [False, True])
+def test_shared_pages_of_minus_infinity_leave_the_own_tokens(far):
+    L = Layer(19, *LAYERS["gqa32"])
+    m = 13 if far else 1
+    c = make_shared(L, [(64, [10, 0, 33] * m)])
+    _minus_infinity(L, c, [(c["tables"][0], np.arange(64))])
+    if far:
+        wide = np.full((3 * m, 2500), c["tables"][0, -1], np.int32)
+        wide[:, :c["tables"].shape[1]] = c["tables"]
+        c.update(tables=wide, max_shared=40000)
+    g = to_device(L, c)
+    call(L, c, g)
+    assert S.starkv_decode_check(g["ws"]) == (0, 0)
+    got = g["out"].float().cpu().numpy()
+    assert np.isnan(got[1::3]).all()
+    own = dict(c, tables=c["tables"][:, 4:], seq_lens=c["seq_lens"] - 64)
+    ref, bound = reference(L, own, rows=[b for b in range(3 * m) if b % 3 != 1])
+    for b in ref:
+        assert (np.abs(got[b] - ref[b]) <= bound[b]).all()
