@@ -361,3 +361,67 @@ def test_shared_pages_of_minus_infinity_leave_the_own_tokens(far):
     ref, bound = reference(L, own, rows=[b for b in range(3 * m) if b % 3 != 1])
     for b in ref:
         assert (np.abs(got[b] - ref[b]) <= bound[b]).all()
+
+
+@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("kind", ["shared", "cross"])
+def test_arrays_of_any_values_stay_inside_their_buffers(kind, far):
+    """Offsets, lengths and block ids of any values: flagged, and nothing outside the workspace and the rows is written."""
+    L = Layer(20, 8, 2, 64, 48, 320)
+    rng = L.rng
+    groups, n, guard = 9, 150 if far else 20, 4096
+    width = 2500 if far else 20
+    bound = 39000 if far else 300
+    wild = lambda size, top: np.where(rng.random(size) < 0.5, rng.integers(0, top + 1, size),
+                                      rng.choice([-1, top + 1, -(1 << 31), (1 << 31) - 1, 1 << 20], size)).astype(np.int32)
+    nb = 40
+    k, v = dev(L.f(nb, PAGE, L.Hkv, L.r)), dev(L.f(nb, PAGE, L.R))
+    desc = S.layer_desc(L.H, L.d, L.r, L.R, nb, width, num_kv_heads=L.Hkv)
+    B_K, B_V, q = dev(L.B_K), dev(L.B_V), dev(L.f(n, L.H, L.d))
+    nbytes = (S.starkv_shared_workspace_bytes(desc, groups, n, bound, 60) if kind == "shared"
+              else S.starkv_cross_workspace_bytes(desc, groups, n, bound))
+    ws = torch.empty(nbytes + guard, dtype=torch.uint8, device="cuda")
+    out = torch.empty(n + 2, L.H, L.d, dtype=torch.float16, device="cuda")
+    for _ in range(12):
+        tables = dev(wild((n if kind == "shared" else groups, width), nb - 1))
+        seq, off = wild(n if kind == "shared" else groups, 300), wild(groups + 1, n)
+        ws.fill_(0xA5), out.fill_(UNTOUCHED)
+        if kind == "shared":
+            S.starkv_paged_decode_shared(desc, groups, n, bound, 60, q, B_K, B_V, k, v, tables, dev(seq), dev(wild(groups, 250)),
+                                         dev(off), L.scale, ws, nbytes, out)
+        else:
+            S.starkv_paged_cross(desc, groups, n, bound, q, B_K, B_V, k, v, tables, dev(seq), dev(off), L.scale, ws, nbytes, out)
+        status, flags = S.starkv_decode_check(ws)
+        assert status in (0, 5) and not flags & S.FLAG_TIMEOUT
+        if off[0] != 0 or (np.diff(off.astype(np.int64)) < 0).any() or off.max() > n:
+            assert flags & S.FLAG_BAD_ROW_OFFSET
+        assert bool((ws[nbytes:] == 0xA5).all()) and bool((out[n:] == UNTOUCHED).all())
+        used = min(n, max(0, int(off.max())))
+        assert bool((out[used:] == UNTOUCHED).all())
+
+
+@pytest.mark.parametrize("far", [False, True])
+def test_pages_past_the_32_bit_offsets_of_a_pool(far):
+    """Pools of more than 2^32 codes whose last pages are used, and (far) weights of more than 2^31 places."""
+    L = Layer(22, 64, 64, 64, 64, 4096)
+    rows = 40 if far else 2
+    c = make_cross(L, [(150, rows), (33, 1)])
+    g = to_device(L, c)
+    pages = 66000
+    shift = pages - c["nb"]
+    for name, width in (("k", (L.Hkv, L.r)), ("v", (L.R,))):
+        pool = torch.zeros(pages, PAGE, *width, dtype=torch.float16, device="cuda")
+        assert pool.numel() > 1 << 32
+        pool[shift:] = g[name]
+        g[name] = pool
+    wide = 60000 if far else c["tables"].shape[1]
+    t = np.full((2, wide), pages - 1, np.int32)
+    t[:, :c["tables"].shape[1]] = c["tables"] + shift
+    g["tables"] = dev(t)
+    g["desc"] = S.layer_desc(L.H, L.d, L.r, L.R, pages, wide, num_kv_heads=L.Hkv)
+    if far:
+        c["max_len"] = wide * PAGE
+        assert c["n"] * L.H * c["max_len"] > 1 << 31
+    g["bytes"] = S.starkv_cross_workspace_bytes(g["desc"], 2, c["n"], c["max_len"])
+    g["ws"] = torch.empty(g["bytes"], dtype=torch.uint8, device="cuda")
+    check_case(L, c, g, rows=[0, rows - 1, rows])

@@ -356,3 +356,26 @@ def test_rope_many_rows_captured_and_chained(n, R, Hkv):
         s.synchronize()
         assert torch.equal(again["q_2"], want[3])
     c.verify(g)
+
+
+@pytest.mark.parametrize("n", [5, 300])
+def test_rope_slots_past_the_32_bit_offsets_of_a_pool(n):
+    L = Layer(37, 64, 64, 64, 64, 4096)
+    c = Case(L, n, 64, False, form="store")
+    g = c.device()
+    pages = 66000
+    shift = pages - c.nb
+    small = {}
+    for name in ("k_cache", "v_cache"):
+        small[name] = g[name]
+        pool = torch.zeros(pages, *g[name].shape[1:], dtype=torch.float16, device="cuda")
+        assert pool.numel() > 1 << 32
+        pool[shift:] = g[name]
+        g[name] = pool
+    g["desc"] = S.layer_desc(L.H, L.d, L.r, L.R, pages, c.MB, num_kv_heads=L.Hkv)
+    g["where"] += shift * PAGE
+    c.call(g)
+    for name in small:
+        assert not bool(g[name][:shift].any())
+        g[name] = g[name][shift:].clone()
+    c.verify(g)
