@@ -350,8 +350,9 @@ starkv_status starkv_paged_prefill(const starkv_layer_desc* desc, int32_t n_seqs
  *                 read); tokens from 16 s on are read through each row's own
  *                 table.
  *   row_offsets   int32 [n_groups + 1] (device), non-decreasing from 0.  Rows
- *                 from row_offsets[n_groups] on belong to no group: nothing of
- *                 theirs is read and their out rows are left as they were.
+ *                 from row_offsets[n_groups] on belong to no group: what q,
+ *                 seq_lens and block_tables hold of them does not matter and
+ *                 their out rows are left as they were.
  *   max_shared_len  host-side upper bound of every shared_lens[g]
  *   max_own_len     host-side upper bound of every seq_lens[b] - 16 s
  *   workspace     at least starkv_shared_workspace_bytes(desc, n_groups, batch,
@@ -370,6 +371,13 @@ starkv_status starkv_paged_prefill(const starkv_layer_desc* desc, int32_t n_seqs
  * STARKV_ERR_UNSUPPORTED beyond 2^20 rows, for bounds above 2^30, or where rows
  * times lengths pass the 32-bit positions of the passes' work lists.  The
  * method pages have no counterpart to this entry point.
+ *
+ * When it pays, against starkv_paged_decode of the same rows (one B200, us): for
+ * few rows (4 over 1000 tokens, 8 KV heads, R 512: 32 against 55) and for many
+ * over a long prefix (64 over 8192, 32 heads, R 2048: 205 against 543).  In
+ * between the two come close, and several groups of a few rows each over pages
+ * that fit the L2 cache are better decoded plainly (20 rows in 4 groups over 2050
+ * tokens, 32 heads, R 2048: 139 against 106).
  */
 size_t starkv_shared_workspace_bytes(const starkv_layer_desc* desc, int32_t n_groups, int32_t batch,
                                      int32_t max_shared_len, int32_t max_own_len);
@@ -461,9 +469,9 @@ starkv_status starkv_paged_decode_static(const starkv_layer_desc* desc, int32_t 
 
 /*
  * starkv_decode_check -- synchronise `stream` and read the device status word
- * at `workspace` (the first int32 of a decode or prefill workspace, or an
- * append `status` word).  For a workspace it is the status of the last decode
- * or prefill call that returned STARKV_OK with that workspace, calls with
+ * at `workspace` (the first int32 of a decode, prefill, shared-prefix or cross
+ * workspace, or an append `status` word).  For a workspace it is the status of
+ * the last attention call that returned STARKV_OK with that workspace, calls with
  * nothing to compute (batch 0, max_seq_len 0, n_rows 0) included: those clear
  * the word.  *flags_out receives STARKV_FLAG_* bits (0 when clean).  Returns
  * STARKV_OK when clean, STARKV_ERR_TIMEOUT when the timeout bit is set,

@@ -81,7 +81,7 @@ constexpr int kAppKC = 64;         // rows of H*d per pipeline stage
 
 // One tile of the V-code GEMM: rows [128 mt, 128 mt + 128) of R, the ks-th of
 // KS K ranges (the CTA's rank in its (1, KS, 1) cluster), batch tile bt of
-// 256 sequences.  Warp 0 issues the TMA copies, warp 1 the MMAs, warps 2..5
+// p.rows sequences.  Warp 0 issues the TMA copies, warp 1 the MMAs, warps 2..5
 // drain the accumulator; all kPrepThreads threads take part in the
 // cluster-wide reduction.  `smem` is the 1024-aligned dynamic shared memory.
 __device__ __forceinline__ void append_v_tile(const CUtensorMap* amap, const CUtensorMap* vmap,

@@ -281,7 +281,8 @@ __global__ void __launch_bounds__(kPrepThreads, 3) rope_q_kernel(RopeParams p) {
 // or to 2^-35 for keys below 2^-13, so the code still rounds once), in the K-major operand
 // layout, A_K[h] by TMA boxes of 64 ranks x 64 rows (MN-major).  Each half has its own
 // accumulator; the drain joins them.  A block's chain takes 8 to 10 us (its loads 3 to 5, MMAs
-// 1.5, drain 1); two share an SM.  32 heads x 4096 rows: 46 us alone, 95 with the V codes.
+// 1.5, drain 1); two share an SM.  32 heads x 4096 rows: 40 us by itself; the whole call,
+// with the V codes and the queries, 104 (93 where the same inputs come again, from L2).
 constexpr int kRRThreads = 512;
 struct RopeRowsParams {
   RopeTable rope;

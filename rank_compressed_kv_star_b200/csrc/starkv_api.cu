@@ -628,9 +628,10 @@ starkv_status plan_append(const starkv_layer_desc* desc, int32_t batch, const vo
   ap->v_cols = ap->v_mt * n_bt;
   const int sms = device_sm_count();
   int KS = 1;
-  // <= one wave at 2 CTAs/SM, and clusters of at most 4: the whole prep grid
-  // (K-code and absorption items too) is launched in clusters of KS, and with
-  // 8 some of them found no free GPC slots until the V tiles had ended
+  // <= one wave at 2 CTAs/SM, and clusters of at most ks_max: 4 for the prep
+  // grid, which is launched in clusters of KS as a whole (K-code and absorption
+  // items too; with 8 some of them found no free GPC slots until the V tiles had
+  // ended), kRopeKS for the rotary append's
   while (KS < ks_max && ap->v_cols * KS * 2 <= 2 * sms && (HD / kAppKC) >= KS * 2) KS *= 2;
   ap->KS = KS;
   AppendVParams& vp = ap->vp;
@@ -1781,7 +1782,7 @@ starkv_status make_group_plan(const starkv_layer_desc* d, bool shared, int32_t n
   p.f_tmem = static_cast<uint32_t>(pow2_ceil(p.f_npad < 32 ? 32 : p.f_npad));
 
   // rows per absorption item: few while four waves of two blocks per SM hold them (545 items of 4
-  // rows 8.0 us against 11.7 of 16; 4928 items 45 us against 33 of 32 rows)
+  // rows 8.7 us against 12.7 of 16; 4928 items 51 us against 36 of 32 rows)
   p.abs_tile = static_cast<int64_t>(g.H) * ((n_rows + kGAbsRows - 1) / kGAbsRows) <= 8 * sms ? kGAbsRows
                : g.H * ((n_rows + 15) / 16) <= 2 * sms ? 16 : kAbsBT;
 
