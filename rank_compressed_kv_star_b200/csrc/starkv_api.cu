@@ -10,6 +10,7 @@
 #include <map>
 #include <tuple>
 #include <mutex>
+#include <new>
 #include <utility>
 
 #include "../../include/starkv.h"
@@ -156,7 +157,10 @@ bool set_smem(K kernel, size_t bytes) {
     cudaGetLastError();
     return false;
   }
-  set_bytes[key] = static_cast<int>(bytes);
+  try {
+    set_bytes[key] = static_cast<int>(bytes);
+  } catch (const std::bad_alloc&) {   // not remembered: the next call sets it again
+  }
   return true;
 }
 
@@ -1631,7 +1635,10 @@ int max_attend_clusters(int C, size_t smem) {
     cudaGetLastError();
     return device_sm_count() / C;   // no device: the host-side sizes only
   }
-  known[key] = n;
+  try {
+    known[key] = n;
+  } catch (const std::bad_alloc&) {   // not remembered: the next call asks again
+  }
   return n;
 }
 
