@@ -264,3 +264,39 @@ def test_prompt_then_steps_then_shared_decode_and_cross():
              row_offsets=np.array([0, 5], np.int32), max_len=P, q=L.f(5, L.H, L.d, a=2.0))
     check_case(L, x)
     assert S.starkv_decode_check(status)[1] == 0
+
+
+def test_wait_bounds_do_not_count_the_kernel_before():
+    """Several milliseconds of V pass whose narrow entries end long before its wide ones, every wait held to 200 us: blocks of the
+    last step that start early wait for the pass's end without their bounds running."""
+    L = Layer(54, *LAYERS["gqa32"])
+    T, wide, rows, narrow = 2048, 200, 64, 1700
+    nb, seqs, n = T // PAGE, wide + narrow, wide * rows + narrow
+    k, v = dev(L.f(nb, PAGE, L.Hkv, L.r)), dev(L.f(nb, PAGE, L.R))
+    off = dev(np.concatenate([np.arange(wide) * rows, wide * rows + np.arange(narrow + 1)]).astype(np.int32))
+    q = torch.randn(n, L.H, L.d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).half()
+    tables = dev(np.tile(np.arange(nb, dtype=np.int32), (seqs, 1)))
+    lens = torch.full((seqs,), T, dtype=torch.int32, device="cuda")
+    desc = S.layer_desc(L.H, L.d, L.r, L.R, nb, nb, num_kv_heads=L.Hkv)
+    nbytes = S.starkv_cross_workspace_bytes(desc, seqs, n, T)
+    ws, out = torch.empty(nbytes, dtype=torch.uint8, device="cuda"), torch.empty_like(q)
+    B_K, B_V = dev(L.B_K), dev(L.B_V)
+
+    def run():
+        S.starkv_paged_cross(desc, seqs, n, T, q, B_K, B_V, k, v, tables, lens, off, L.scale, ws, nbytes, out)
+        return S.starkv_decode_check(ws)
+    assert run() == (0, 0)
+    want = out.clone()
+    try:
+        S.starkv_set_wait_test_hook(200, -1)
+        held = [run() for _ in range(3)]
+    finally:
+        S.starkv_set_wait_test_hook(0, -1)
+    assert held == [(0, 0)] * 3
+    assert torch.equal(out, want)
+    # a row of each kind against the formula
+    for seq, b in ((3, 3 * rows + 5), (wide + 9, wide * rows + 9)):
+        c = dict(n=1, used=1, tables=np.arange(nb, dtype=np.int32)[None], k=k.cpu().numpy(), v=v.cpu().numpy(), n_groups=1,
+                 seq_lens=np.array([T], np.int32), row_offsets=np.array([0, 1], np.int32), q=q[b:b + 1].cpu().numpy())
+        ref, bound = reference(L, c)
+        assert (np.abs(want[b].float().cpu().numpy() - ref[0]) <= bound[0]).all()
